@@ -12,6 +12,10 @@ The functions keep the C names:
 * :func:`nvfp4_dequantize` -- codes + scales + alpha -> float32 or bfloat16
 * :func:`nvfp4_gemm`       -- D = alpha_a * alpha_b * A * B^T of two NVFP4 operands (tiled scales)
 * :func:`nvfp4_strerror`
+
+The operators around the linear layer (include/nvfp4_layer.h) are in
+:mod:`.layer` and exported here too: :func:`nvfp4_layernorm`,
+:func:`nvfp4_layernorm_backward`, :func:`nvfp4_linear`, :func:`nvfp4_act_backward`.
 """
 from __future__ import annotations
 
@@ -22,11 +26,15 @@ from typing import Optional
 
 from .build import LIB as _LIB_PATH
 from .build import build
+from .layer import (ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU, ActGrads, LinearOut, Normed, NormGrads,
+                    layer_lib, nvfp4_act_backward, nvfp4_layernorm, nvfp4_layernorm_backward, nvfp4_linear)
 
 __all__ = [
     "ROWWISE", "COLWISE", "TWO_D", "RHT_ROW", "RHT_COL", "SR", "FOUR_SIX",
     "SEL_MAE", "SEL_MSE", "SEL_MAXERR", "Nvfp4Error", "Quantized", "lib", "build",
     "nvfp4_amax", "nvfp4_quantize", "nvfp4_dequantize", "nvfp4_gemm", "nvfp4_strerror", "output_shapes",
+    "ACT_NONE", "ACT_RELU", "ACT_GELU", "ACT_GELU_TANH", "ACT_SILU", "Normed", "NormGrads", "LinearOut", "ActGrads",
+    "layer_lib", "nvfp4_layernorm", "nvfp4_layernorm_backward", "nvfp4_linear", "nvfp4_act_backward",
 ]
 
 ROWWISE, COLWISE, TWO_D, RHT_ROW, RHT_COL, SR, FOUR_SIX, SF_SWIZZLED = 1, 2, 4, 8, 16, 32, 64, 128

@@ -1,7 +1,11 @@
 """Build the CUDA libraries in-tree with plain nvcc (one -gencode, sm_103a):
 
-* nvfp4_bit_block_gb300/_build/libnvfp4.so -- the product library (the C ABI
-  of include/nvfp4.h and its kernels);
+* nvfp4_bit_block_gb300/_build/libnvfp4.so -- the quantizer and its GEMM (the
+  C ABI of include/nvfp4.h and its kernels);
+* nvfp4_bit_block_gb300/_build/libnvfp4_layer.so -- the operators around the
+  linear layer (the C ABI of include/nvfp4_layer.h and its kernels), a library
+  of its own because the quantizer's arithmetic is compiled without fused
+  multiply-adds and theirs with them;
 * tests/selftest/_build/libnvfp4_selftest.so -- device self-checks used only
   by the tests (build_selftest); it holds no product entry point.
 
@@ -18,6 +22,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libnvfp4.so")
+LAYER_BUILD = os.path.join(BUILD, "layer")
+LAYER_LIB = os.path.join(BUILD, "libnvfp4_layer.so")
 INCLUDE = os.path.join(ROOT, "include")
 SELFTEST_DIR = os.path.join(ROOT, "tests", "selftest")
 SELFTEST_BUILD = os.path.join(SELFTEST_DIR, "_build")
@@ -25,6 +31,7 @@ SELFTEST_LIB = os.path.join(SELFTEST_BUILD, "libnvfp4_selftest.so")
 
 SOURCES = ["api.cu", "tmap.cu", "amax.cu", "quant1d.cu", "quant1d_sr.cu", "quant1d_46mae.cu", "quant1d_46mse.cu", "quant1d_46max.cu",
            "quant2d.cu", "dequant.cu", "analysis.cu", "gemm.cu"]
+LAYER_SOURCES = ["layer_api.cu", "layernorm.cu", "act_backward.cu", "linear.cu", "tmap.cu"]
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
     "-O3", "-lineinfo", "-std=c++17",
@@ -32,6 +39,7 @@ NVCC_FLAGS = [
     "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
     "--expt-relaxed-constexpr",
 ]
+LAYER_NVCC_FLAGS = ["-fmad=true" if f == "-fmad=false" else f for f in NVCC_FLAGS]
 
 
 def _nvcc() -> str:
@@ -49,7 +57,7 @@ def _stale(target: str, deps) -> bool:
 
 def _headers():
     hs = [os.path.join(CSRC, h) for h in os.listdir(CSRC) if h.endswith((".cuh", ".h"))]
-    hs.append(os.path.join(INCLUDE, "nvfp4.h"))
+    hs += [os.path.join(INCLUDE, h) for h in ("nvfp4.h", "nvfp4_layer.h")]
     return hs
 
 
@@ -61,7 +69,7 @@ def _run(cmd, verbose=False):
         print(r.stdout, r.stderr)
 
 
-def _build_lib(sources, build_dir, lib, force, verbose, extra_flags=()):
+def _build_lib(sources, build_dir, lib, force, verbose, flags=NVCC_FLAGS):
     """Compile `sources` (absolute paths) to objects in build_dir and link `lib`."""
     os.makedirs(build_dir, exist_ok=True)
     headers = _headers()
@@ -71,7 +79,7 @@ def _build_lib(sources, build_dir, lib, force, verbose, extra_flags=()):
         o = os.path.join(build_dir, os.path.basename(s).replace(".cu", ".o"))
         objs.append(o)
         if force or _stale(o, [s] + headers):
-            jobs.append([nvcc, *NVCC_FLAGS, *extra_flags, "-I", INCLUDE, "-I", CSRC, "-c", s, "-o", o])
+            jobs.append([nvcc, *flags, "-I", INCLUDE, "-I", CSRC, "-c", s, "-o", o])
     if jobs:
         with ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
             list(ex.map(lambda c: _run(c, verbose), jobs))
@@ -84,8 +92,13 @@ def _build_lib(sources, build_dir, lib, force, verbose, extra_flags=()):
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """The product library; returns its path."""
-    return _build_lib([os.path.join(CSRC, s) for s in SOURCES], BUILD, LIB, force, verbose)
+    """The product libraries, side by side; returns the path of libnvfp4.so."""
+    with ThreadPoolExecutor(max_workers=2) as ex:
+        main = ex.submit(_build_lib, [os.path.join(CSRC, s) for s in SOURCES], BUILD, LIB, force, verbose)
+        layer = ex.submit(_build_lib, [os.path.join(CSRC, s) for s in LAYER_SOURCES], LAYER_BUILD, LAYER_LIB, force,
+                          verbose, LAYER_NVCC_FLAGS)
+        layer.result()
+        return main.result()
 
 
 def build_selftest(force: bool = False, verbose: bool = False) -> str:
