@@ -447,7 +447,9 @@ def check_linear(a, b, K, r, bias=None, act=0, residual=None, dtype=BF):
 LINEAR = [(1, 1, 32), (1, 40, 64), (1, 5120, 1024), (3, 130, 96), (8, 256, 256), (16, 200, 2080), (17, 1000, 1056),
           (24, 513, 4096), (33, 128, 544), (64, 640, 512), (65, 257, 288), (127, 384, 320), (128, 128, 256),
           (129, 1111, 992), (200, 96, 7200), (256, 512, 1024), (333, 1000, 1056), (300, 2600, 1536),
-          (2048, 1280, 768), (1000, 31, 64)]
+          (2048, 1280, 768), (1000, 31, 64),
+          # whole output tiles over the GPU, with every edge: tokens, features, K % 64, a second band that is not there
+          (1000, 2600, 544), (2050, 2177, 96), (4000, 1000, 1312), (1500, 1921, 32)]
 
 
 @pytest.mark.parametrize("M,N,K", LINEAR)
