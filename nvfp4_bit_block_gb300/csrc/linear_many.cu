@@ -1,11 +1,14 @@
 // linear_many.cu -- nvfp4_linear for many tokens: persistent blocks walk tiles
 // of 128 tokens x BN features.
 //
-// Warp 0 loads (TMA), warp 1 copies each stage's scales to TMEM and issues the
-// MMAs, warps 2-9 are the epilogue: two warps per TMEM lane quarter, each with
-// half of the tile's columns.  They take the whole accumulator into registers
-// and hand it back before they compute, so that the next tile's MMAs wait for
-// the read-out alone and the epilogue's arithmetic and traffic run beside them.
+// Warp 0 loads (TMA), warp 1 issues the MMAs, warps 4-7 move each stage's scales
+// from shared memory to TMEM (tcgen05.cp from the MMA's thread would run in the
+// tensor pipe's order, 12 copies per stage: 970 instead of 645 us for 16384 x 5120
+// x 20480), warps 8-15 are the epilogue: two warps per TMEM lane quarter, each
+// with half of the tile's columns.  They take the whole accumulator into
+// registers and hand it back before they compute, so that the next tile's MMAs
+// wait for the read-out alone and the epilogue's arithmetic and traffic run
+// beside them; registers are moved to them from the other warps (setmaxnreg).
 #include "linear_launch.h"
 #include "linear_tc.cuh"
 
@@ -13,15 +16,19 @@ namespace nvfp4 {
 namespace lin {
 namespace {
 
-constexpr int kThreads = 320;
-constexpr int kEpiWarp0 = 2, kEpiWarps = 8;
+constexpr int kThreads = 512;
+constexpr int kSfWarp0 = 4, kSfWarps = 4, kEpiWarp0 = 8, kEpiWarps = 8;
+// Registers per thread: 512 * 128 at launch, shared out as 256 * 48 + 256 * 208.
+constexpr int kFewRegs = 48, kEpiRegs = 208;
+static_assert(256 * kFewRegs + 256 * kEpiRegs == kThreads * 128, "register split");
 constexpr int64_t kGroupM = 8;  // token tiles walked together, so that blocks in flight share operand tiles in L2
 
 template <int BN>
 struct Cfg {
   static constexpr int kBands = BN / 128;
-  static constexpr int kStageBytes = kLaneTile + BN * kBK / 2 + kSfStage * (1 + kBands);  // 54 or 36 KB
-  static constexpr int kStages = BN == 256 ? 4 : 6;
+  static constexpr int kSfAt = kLaneTile + BN * kBK / 2;
+  static constexpr int kStageBytes = kSfAt + kSfStage * (1 + kBands);  // 54 KB
+  static constexpr int kStages = 4;
   static constexpr int kHalf = BN / 2;  // columns of an epilogue warp
   static constexpr int kSmem = kStages * kStageBytes + BN * 4 /* bias */ + 256 /* barriers */ + 1024 /* alignment */;
   static constexpr uint32_t kSfCols = 16 + 16 * kBands;
@@ -155,19 +162,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   float* bias_s = reinterpret_cast<float*>(smem + kStages * C::kStageBytes);
   uint64_t* bars = reinterpret_cast<uint64_t*>(bias_s + BN);
-  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages, accf = empty0 + 8 * kStages, acce = accf + 8,
-                 drain = accf + 16;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 3);
-  volatile int* stop = reinterpret_cast<int*>(bars + 2 * kStages + 4);
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages, sfr0 = empty0 + 8 * kStages;
+  const uint32_t accf = sfr0 + 8 * kStages, acce = accf + 8, drain = accf + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * kStages + 3);
+  volatile int* stop = reinterpret_cast<int*>(bars + 3 * kStages + 4);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int nk = (int)((a.K + kBK - 1) / kBK);
+  const Steps K(a.K);
   const int64_t tm = (a.M + kLaneRows - 1) / kLaneRows, tn = (a.N + BN - 1) / BN, tiles = tm * tn;
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       tma::mbar_init(full0 + 8 * s, 1);
       tma::mbar_init(empty0 + 8 * s, 1);
+      tma::mbar_init(sfr0 + 8 * s, kSfWarps);  // the stage has arrived and its scales are in TMEM
     }
     tma::mbar_init(accf, 1);
     tma::mbar_init(acce, kEpiWarps);
@@ -185,61 +193,79 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   uint32_t top = 0;
 
-  if (warp == 0) {
-    if (lane == 0) {
-      const int64_t sf_row = (a.K + 63) / 64 * kSfBlock;  // scale bytes of a 128-row band
-      int64_t g = 0;
-      for (int64_t t = blockIdx.x; t < tiles && !*stop; t += gridDim.x) {
-        int64_t m, n;
-        tile_at(t, tm, tn, m, n);
-        const int64_t rows = a.N - n * BN;
-        const int bands = BN == 256 && rows > 128 ? 2 : 1;  // 128-row bands of scales that exist
-        const uint8_t* sfx = a.sfa + m * sf_row;
-        const uint8_t* sfw = a.sfb + n * C::kBands * sf_row;
-        for (int kb = 0; kb < nk; ++kb, ++g) {
-          const int s = (int)(g % kStages);
-          if (g >= kStages && !tma::wait(empty0 + 8 * s, (uint32_t)(g / kStages - 1) & 1u)) {
+  if (warp < kEpiWarp0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+    if (warp == 0) {
+      if (lane == 0) {
+        const int64_t sf_row = (a.K + 63) / 64 * kSfBlock;  // scale bytes of a 128-row band
+        Ring<kStages> r;
+        int64_t g = 0;
+        for (int64_t t = blockIdx.x; t < tiles && !*stop; t += gridDim.x) {
+          int64_t m, n;
+          tile_at(t, tm, tn, m, n);
+          const int bands = a.N - n * BN > 128 ? C::kBands : 1;  // 128-row bands of scales that exist
+          const uint8_t* sfx = a.sfa + m * sf_row;
+          const uint8_t* sfw = a.sfb + n * C::kBands * sf_row;
+          for (int kb = 0; kb < K.n; ++kb, ++g, r.next()) {
+            if (g >= kStages && !tma::wait(empty0 + 8 * r.slot, r.phase ^ 1u)) {
+              *stop = 1;
+              break;
+            }
+            const uint32_t st = smem_u32(smem + r.slot * C::kStageBytes), full = full0 + 8 * r.slot;
+            const int groups = K.groups(kb);
+            tma::arrive_expect_tx(full, (uint32_t)(C::kSfAt + (1 + bands) * groups * kSfBlock));
+            load_codes<BN>(st, full, &xmap, &wmap, (int)(m * kLaneRows), (int)(n * BN), kb);
+            load_scales(st + C::kSfAt, full, sfx, sfw, sf_row, kb, groups, bands);
+          }
+        }
+        // no copy may land after the block has gone: wait for the last fill of every stage
+        for (int64_t j = g > kStages ? g - kStages : 0; j < g; ++j)
+          tma::wait(full0 + 8 * (int)(j % kStages), (uint32_t)(j / kStages) & 1u);
+      }
+    } else if (warp == 1) {
+      if (lane == 0) {
+        Ring<kStages> r;
+        int li = 0;
+        for (int64_t t = blockIdx.x; t < tiles && !*stop; t += gridDim.x, ++li) {
+          // the epilogue has taken the previous tile out
+          if (li > 0 && !tma::wait(acce, (uint32_t)(li - 1) & 1u)) {
             *stop = 1;
             break;
           }
-          load_stage<BN>(smem_u32(smem + s * C::kStageBytes), full0 + 8 * s, &xmap, &wmap, sfx, sfw, sf_row,
-                         (int)(m * kLaneRows), (int)(n * BN), kb, groups_of(a.K, kb), bands);
+          for (int kb = 0; kb < K.n; ++kb, r.next()) {
+            if (!tma::wait(sfr0 + 8 * r.slot, r.phase)) {  // the scale warps have waited for the stage
+              *stop = 1;
+              break;
+            }
+            tc5::fence_after_thread_sync();
+            mma_stage<BN>(tmem, tmem + BN + (uint32_t)r.slot * C::kSfCols,
+                          StageDesc(smem_u32(smem + r.slot * C::kStageBytes)), K.groups(kb), kb == 0);
+            tc5::commit(empty0 + 8 * r.slot);
+          }
+          if (*stop) break;
+          tc5::commit(accf);
+        }
+        tc5::commit(drain);  // arrives when every MMA issued above has completed
+      }
+    } else if (warp >= kSfWarp0) {
+      const uint32_t quarter = (uint32_t)(32 * (warp & 3)) << 16;
+      Ring<kStages> r;
+      bool quit = false;
+      for (int64_t t = blockIdx.x; t < tiles && !quit; t += gridDim.x) {
+        for (int kb = 0; kb < K.n; ++kb, r.next()) {
+          quit = !__all_sync(0xFFFFFFFFu, tma::wait(full0 + 8 * r.slot, r.phase) && *stop == 0);
+          if (quit) break;
+          put_scales<C::kBands>(tmem + quarter + BN + (uint32_t)r.slot * C::kSfCols,
+                                smem + r.slot * C::kStageBytes + C::kSfAt, K.groups(kb), kb == K.n - 1 && K.tail, lane);
+          tc5::fence_before_thread_sync();
+          __syncwarp();
+          if (lane == 0) arrive(sfr0 + 8 * r.slot);
         }
       }
-      // no copy may land after the block has gone: wait for the last fill of every stage
-      for (int64_t j = g > kStages ? g - kStages : 0; j < g; ++j)
-        tma::wait(full0 + 8 * (int)(j % kStages), (uint32_t)(j / kStages) & 1u);
+      if (quit && lane == 0) *stop = 1;
     }
-  } else if (warp == 1) {
-    int64_t g = 0;
-    int li = 0;
-    bool quit = false;
-    for (int64_t t = blockIdx.x; t < tiles && !quit; t += gridDim.x, ++li) {
-      // the epilogue has taken the previous tile out
-      quit = !__all_sync(0xFFFFFFFFu, (li == 0 || tma::wait(acce, (uint32_t)(li - 1) & 1u)) && !*stop);
-      if (quit) break;
-      tc5::fence_after_thread_sync();
-      for (int kb = 0; kb < nk; ++kb, ++g) {
-        const int s = (int)(g % kStages);
-        quit = !__all_sync(0xFFFFFFFFu, tma::wait(full0 + 8 * s, (uint32_t)(g / kStages) & 1u));
-        if (quit) break;
-        const int groups = groups_of(a.K, kb);
-        uint8_t* st = smem + s * C::kStageBytes;
-        if (kb == nk - 1 && a.K % 64) clear_tail(st + kLaneTile + BN * kBK / 2, 1 + C::kBands, groups - 1, lane);
-        tc5::fence_after_thread_sync();
-        if (lane == 0) {
-          mma_stage<BN>(tmem, tmem + BN + (uint32_t)s * C::kSfCols, smem_u32(st), groups, kb == 0);
-          tc5::commit(empty0 + 8 * s);
-        }
-        __syncwarp();
-      }
-      if (quit) break;
-      if (lane == 0) tc5::commit(accf);
-      __syncwarp();
-    }
-    if (quit && lane == 0) *stop = 1;
-    if (lane == 0) tc5::commit(drain);  // arrives when every MMA issued above has completed
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
     const int e = warp - kEpiWarp0, q = warp & 3, half = e >> 2;  // lane quarter, column half
     const float scale = a.alpha_a[0] * a.alpha_b[0];
     float* bias = bias_s + half * C::kHalf;  // shared by the half's four warps
@@ -266,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc5::wait_ld();
       tc5::fence_before_thread_sync();
       __syncwarp();
-      if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(acce) : "memory");
+      if (lane == 0) arrive(acce);
       if (row < a.M) {
 #pragma unroll
         for (int c = 0; c < C::kHalf; c += 32)

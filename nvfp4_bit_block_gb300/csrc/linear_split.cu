@@ -75,8 +75,9 @@ __global__ void __launch_bounds__(kThreads)
   const uint32_t rank = cluster_rank();
   const int64_t f0 = (int64_t)(blockIdx.x / S) * kLaneRows;  // first feature
   const int64_t t0 = (int64_t)blockIdx.y * BN;               // first token
-  const int nk = (int)((a.K + kBK - 1) / kBK);
-  const int k0 = (int)((int64_t)nk * rank / S), k1 = (int)((int64_t)nk * (rank + 1) / S);
+  const Steps K(a.K);
+  const int k0 = (int)((int64_t)K.n * rank / S), k1 = (int)((int64_t)K.n * (rank + 1) / S);
+  constexpr int kColTile = BN * kBK / 2;
 
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -101,35 +102,40 @@ __global__ void __launch_bounds__(kThreads)
       const int64_t sf_row = (a.K + 63) / 64 * kSfBlock;  // scale bytes of a 128-row band
       const uint8_t* sfw = a.sfb + f0 / 128 * sf_row;
       const uint8_t* sfx = a.sfa + t0 / 128 * sf_row;
-      int g = 0;
-      for (int kb = k0; kb < k1; ++kb, ++g) {
-        const int s = g % C::kStages;
-        if (g >= C::kStages && !tma::wait(empty0 + 8 * s, (uint32_t)(g / C::kStages - 1) & 1u)) {
+      Ring<C::kStages> r;
+      int kb = k0;
+      for (; kb < k1; ++kb, r.next()) {
+        if (kb - k0 >= C::kStages && !tma::wait(empty0 + 8 * r.slot, r.phase ^ 1u)) {
           *stop = 1;
           break;
         }
-        load_stage<BN>(smem_u32(smem + s * C::kStageBytes), full0 + 8 * s, &wmap, &xmap, sfw, sfx, sf_row, (int)f0,
-                       (int)t0, kb, groups_of(a.K, kb), 1);
+        const uint32_t st = smem_u32(smem + r.slot * C::kStageBytes), full = full0 + 8 * r.slot;
+        const int groups = K.groups(kb);
+        tma::arrive_expect_tx(full, (uint32_t)(kLaneTile + kColTile + 2 * groups * kSfBlock));
+        load_codes<BN>(st, full, &wmap, &xmap, (int)f0, (int)t0, kb);
+        load_scales(st + kLaneTile + kColTile, full, sfw, sfx, sf_row, kb, groups, 1);
       }
       // no copy may land after the block has gone: wait for the last fill of every stage
+      const int g = kb - k0;
       for (int j = g > C::kStages ? g - C::kStages : 0; j < g; ++j)
         tma::wait(full0 + 8 * (j % C::kStages), (uint32_t)(j / C::kStages) & 1u);
     }
   } else if (warp == 5) {
-    int g = 0;
-    for (int kb = k0; kb < k1; ++kb, ++g) {
-      const int s = g % C::kStages;
-      if (!__all_sync(0xFFFFFFFFu, tma::wait(full0 + 8 * s, (uint32_t)(g / C::kStages) & 1u))) {
+    Ring<C::kStages> r;
+    for (int kb = k0; kb < k1; ++kb, r.next()) {
+      if (!__all_sync(0xFFFFFFFFu, tma::wait(full0 + 8 * r.slot, r.phase))) {
         if (lane == 0) *stop = 1;
         break;
       }
-      const int groups = groups_of(a.K, kb);
-      uint8_t* st = smem + s * C::kStageBytes;
-      if (kb == nk - 1 && a.K % 64) clear_tail(st + kLaneTile + BN * kBK / 2, 2, groups - 1, lane);
+      const int groups = K.groups(kb);
+      uint8_t* st = smem + r.slot * C::kStageBytes;
+      if (kb == K.n - 1 && K.tail) clear_tail(st + kLaneTile + kColTile, 2, groups - 1, lane);
       tc5::fence_after_thread_sync();
       if (lane == 0) {
-        mma_stage<BN>(tmem, tmem + BN + (uint32_t)s * C::kSfCols, smem_u32(st), groups, g == 0);
-        tc5::commit(empty0 + 8 * s);
+        const uint32_t sf_tmem = tmem + BN + (uint32_t)r.slot * C::kSfCols;
+        copy_stage_scales<BN>(sf_tmem, smem_u32(st + kLaneTile + kColTile), groups);
+        mma_stage<BN>(tmem, sf_tmem, StageDesc(smem_u32(st)), groups, kb == k0);
+        tc5::commit(empty0 + 8 * r.slot);
       }
       __syncwarp();
     }

@@ -46,28 +46,48 @@ __device__ __forceinline__ void ld_32x32b_x16(uint32_t taddr, uint32_t* r) {
       : "r"(taddr));
 }
 
-// Number of 64-value groups of K in stage kb (the last stage may be short).
-__device__ __forceinline__ int groups_of(int64_t K, int kb) {
-  const int64_t left = (K - (int64_t)kb * kBK + 63) / 64;
-  return left < 4 ? (int)left : 4;
+// K in stages of 256 values: how many, the 64-value groups of the last one, and
+// whether its last group is half padding (K % 64 == 32).
+struct Steps {
+  int n, last;
+  bool tail;
+  __device__ __forceinline__ explicit Steps(int64_t K)
+      : n((int)((K + kBK - 1) / kBK)), last((int)((K - (int64_t)(n - 1) * kBK + 63) / 64)), tail(K % 64 != 0) {}
+  __device__ __forceinline__ int groups(int kb) const { return kb == n - 1 ? last : 4; }
+};
+
+// A position in a ring of N slots: the slot and the parity of the use that it is in.
+template <int N>
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+__device__ __forceinline__ void arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// Issue one stage's loads: codes by TMA (rows and values beyond the operand
-// arrive as zeros), the scale blocks that exist by bulk copies.  `bands` is the
-// number of 128-row scale bands of the column operand in this tile.
+// Issue the loads of one stage's codes (rows and values beyond the operand
+// arrive as zeros) and of the scale blocks that exist: the lane operand's 128
+// rows, then `bands` bands of the column operand.
 template <int BN>
-__device__ __forceinline__ void load_stage(uint32_t st, uint32_t full, const CUtensorMap* lmap, const CUtensorMap* cmap,
-                                           const uint8_t* sfl, const uint8_t* sfc, int64_t sf_row, int lrow, int crow,
-                                           int kb, int groups, int bands) {
-  constexpr int kColTile = BN * kBK / 2;
-  const uint32_t sf_bytes = (uint32_t)(groups * kSfBlock);
-  tma::arrive_expect_tx(full, (uint32_t)(kLaneTile + kColTile) + sf_bytes * (uint32_t)(1 + bands));
+__device__ __forceinline__ void load_codes(uint32_t st, uint32_t full, const CUtensorMap* lmap, const CUtensorMap* cmap,
+                                           int lrow, int crow, int kb) {
   tma::load_2d(st, lmap, kb * (kBK / 2), lrow, full);
   tma::load_2d(st + kLaneTile, cmap, kb * (kBK / 2), crow, full);
-  tc5::bulk_g2s(st + kLaneTile + kColTile, sfl + (int64_t)kb * kSfStage, sf_bytes, full);
+}
+__device__ __forceinline__ void load_scales(uint32_t sf, uint32_t full, const uint8_t* sfl, const uint8_t* sfc,
+                                            int64_t sf_row, int kb, int groups, int bands) {
+  const uint32_t bytes = (uint32_t)(groups * kSfBlock);
+  tc5::bulk_g2s(sf, sfl + (int64_t)kb * kSfStage, bytes, full);
   for (int h = 0; h < bands; ++h)
-    tc5::bulk_g2s(st + kLaneTile + kColTile + kSfStage * (1 + h), sfc + h * sf_row + (int64_t)kb * kSfStage, sf_bytes,
-                  full);
+    tc5::bulk_g2s(sf + kSfStage * (1 + h), sfc + h * sf_row + (int64_t)kb * kSfStage, bytes, full);
 }
 
 // K % 64 == 32: the last group's scales 2 and 3 are padding, whose bytes may be
@@ -87,15 +107,37 @@ __device__ __forceinline__ void clear_tail(uint8_t* sf, int bands, int group, in
   __syncwarp();
 }
 
-// One stage's tensor-core work, issued by one thread: scales to TMEM, then an
-// MMA per 64 values of K.  Each stage has TMEM columns of its own for its
-// scales: 16 for the lane operand, then 4 per band and group.
+// One stage's scales by the four warps of TMEM's lane quarters: each lane holds
+// the 16 bytes of its row of a block, and every quarter gets the same ones.
+// `tail`: the last group's scales 2 and 3 are padding and become zeros.
+template <int BANDS>
+__device__ __forceinline__ void put_scales(uint32_t sf_tmem, const uint8_t* sf, int groups, bool tail, int lane) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint4 v[1 + BANDS];
+#pragma unroll
+    for (int h = 0; h < 1 + BANDS; ++h)
+      v[h] = *reinterpret_cast<const uint4*>(sf + h * kSfStage + j * kSfBlock + 16 * lane);
+    if (tail && j == groups - 1) {
+#pragma unroll
+      for (int h = 0; h < 1 + BANDS; ++h) {
+        v[h].x &= 0xFFFFu;
+        v[h].y &= 0xFFFFu;
+        v[h].z &= 0xFFFFu;
+        v[h].w &= 0xFFFFu;
+      }
+    }
+    tc5::st_32x32b_x4(sf_tmem + 4u * j, v[0]);
+#pragma unroll
+    for (int h = 0; h < BANDS; ++h) tc5::st_32x32b_x4(sf_tmem + 16u + 4u * BANDS * j + 4u * h, v[1 + h]);
+  }
+  tc5::wait_st();
+}
+
+// The same by tensor-core copies, issued in order with the MMAs by their thread.
 template <int BN>
-__device__ __forceinline__ void mma_stage(uint32_t acc, uint32_t sf_tmem, uint32_t st, int groups, bool fresh) {
-  constexpr uint32_t idesc = tc5::idesc_e2m1_e4m3(kLaneRows, BN);
+__device__ __forceinline__ void copy_stage_scales(uint32_t sf_tmem, uint32_t sf, int groups) {
   constexpr int kBands = (BN + 127) / 128;
-  constexpr int kColTile = BN * kBK / 2;
-  const uint32_t sf = st + kLaneTile + kColTile;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     if (j < groups) {
@@ -105,14 +147,35 @@ __device__ __forceinline__ void mma_stage(uint32_t acc, uint32_t sf_tmem, uint32
         copy_scales(sf_tmem + 16u + 4u * kBands * j + 4u * h, sf + kSfStage * (1 + h) + j * kSfBlock);
     }
   }
+}
+
+// Shared-memory descriptors of a stage's two tiles; 64 values of K are 32 bytes
+// (2 descriptor units) into each 128-byte swizzled row.
+struct StageDesc {
+  uint64_t lane, col;
+  __device__ __forceinline__ explicit StageDesc(uint32_t st)
+      : lane(tc5::smem_desc(st, 16, 1024, tc5::kLayoutSwizzle128B)),
+        col(tc5::smem_desc(st + kLaneTile, 16, 1024, tc5::kLayoutSwizzle128B)) {}
+};
+
+// One stage's tensor-core work, issued by one thread: an MMA per 64 values of K.
+// Each stage has TMEM columns of its own for its scales: 16 for the lane
+// operand, then 4 per band and group.  A whole stage is straight-line code: a
+// branch before each MMA kept the tensor pipe waiting for its next instruction
+// (16384 x 5120 x 20480: 714 us with, 627 us without).
+template <int BN>
+__device__ __forceinline__ void mma_step(uint32_t acc, uint32_t sf_tmem, StageDesc d, int j, bool add) {
+  constexpr uint32_t idesc = tc5::idesc_e2m1_e4m3(kLaneRows, BN);
+  constexpr int kBands = (BN + 127) / 128;
+  tc5::mma_nvf4(acc, d.lane + 2 * j, d.col + 2 * j, idesc, sf_tmem + 4u * j, sf_tmem + 16u + 4u * kBands * j, add);
+}
+template <int BN>
+__device__ __forceinline__ void mma_stage(uint32_t acc, uint32_t sf_tmem, StageDesc d, int groups, bool fresh) {
+  if (groups == 4) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (j < groups) {
-      // 64 values = 32 bytes into each 128-byte swizzled row
-      const uint64_t ad = tc5::smem_desc(st + 32 * j, 16, 1024, tc5::kLayoutSwizzle128B);
-      const uint64_t bd = tc5::smem_desc(st + kLaneTile + 32 * j, 16, 1024, tc5::kLayoutSwizzle128B);
-      tc5::mma_nvf4(acc, ad, bd, idesc, sf_tmem + 4u * j, sf_tmem + 16u + 4u * kBands * j, !(fresh && j == 0));
-    }
+    for (int j = 0; j < 4; ++j) mma_step<BN>(acc, sf_tmem, d, j, j > 0 || !fresh);
+  } else {
+    for (int j = 0; j < groups; ++j) mma_step<BN>(acc, sf_tmem, d, j, j > 0 || !fresh);
   }
 }
 
