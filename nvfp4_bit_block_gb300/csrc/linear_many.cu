@@ -1,14 +1,24 @@
-// linear_many.cu -- nvfp4_linear for many tokens: persistent blocks walk tiles
-// of 128 tokens x BN features.
+// linear_many.cu -- nvfp4_linear for many tokens: pairs of blocks walk tiles of
+// 256 tokens x 256 features.
 //
-// Warp 0 loads (TMA), warp 1 issues the MMAs, warps 4-7 move each stage's scales
-// from shared memory to TMEM (tcgen05.cp from the MMA's thread would run in the
-// tensor pipe's order, 12 copies per stage: 970 instead of 645 us for 16384 x 5120
-// x 20480), warps 8-15 are the epilogue: two warps per TMEM lane quarter, each
-// with half of the tile's columns.  They take the whole accumulator into
-// registers and hand it back before they compute, so that the next tile's MMAs
-// wait for the read-out alone and the epilogue's arithmetic and traffic run
-// beside them; registers are moved to them from the other warps (setmaxnreg).
+// What bounds the product is the rate at which an SM takes operands from L2 (64
+// bytes per clock): a stage of 256 values of K feeds 512 clocks of MMAs, and a
+// block on its own with a 128 x 256 tile needs 54 KB for it.  In a pair
+// (cta_group::2) each block holds its 128 tokens and half of the weight's rows,
+// 38 KB: 256 x 256 outputs from the bytes of two 128 x 128 tiles.
+//
+// In each block: warp 0 loads its part of a stage (TMA); warps 4-7 wait for the
+// stage, move its scales from shared memory to TMEM (tcgen05.cp from the MMA's
+// thread would run in the tensor pipe's order, 12 copies per stage: 970 instead
+// of 650 us for 16384 x 5120 x 20480) and tell the leader block, whose warp 1
+// issues the pair's MMAs.  Warps 8-15 are the epilogue: two warps per TMEM lane
+// quarter, each with half of the tile's columns.  They take the whole
+// accumulator into registers and hand it back before they compute, so that the
+// next tile's MMAs wait for the read-out alone; registers are moved to them
+// from the other warps (setmaxnreg).  Outputs are staged in shared memory, 32
+// rows of 128 bytes per warp, and stored by TMA as whole lines (16-byte pieces
+// of 32 rows at once cost 3 us per tile); the residual comes in by TMA before the
+// product is done.
 #include "linear_launch.h"
 #include "linear_tc.cuh"
 
@@ -16,6 +26,7 @@ namespace nvfp4 {
 namespace lin {
 namespace {
 
+constexpr int kBN = 256;
 constexpr int kThreads = 512;
 constexpr int kSfWarp0 = 4, kSfWarps = 4, kEpiWarp0 = 8, kEpiWarps = 8;
 // Registers per thread: 512 * 128 at launch, shared out as 256 * 48 + 256 * 208.
@@ -23,19 +34,19 @@ constexpr int kFewRegs = 48, kEpiRegs = 208;
 static_assert(256 * kFewRegs + 256 * kEpiRegs == kThreads * 128, "register split");
 constexpr int64_t kGroupM = 8;  // token tiles walked together, so that blocks in flight share operand tiles in L2
 
-template <int BN>
-struct Cfg {
-  static constexpr int kBands = BN / 128;
-  static constexpr int kSfAt = kLaneTile + BN * kBK / 2;
-  static constexpr int kStageBytes = kSfAt + kSfStage * (1 + kBands);  // 54 KB
-  static constexpr int kStages = 4;
-  static constexpr int kHalf = BN / 2;  // columns of an epilogue warp
-  static constexpr int kSmem = kStages * kStageBytes + BN * 4 /* bias */ + 256 /* barriers */ + 1024 /* alignment */;
-  static constexpr uint32_t kSfCols = 16 + 16 * kBands;
-  static constexpr uint32_t kTmemCols = 512;
-  static_assert(BN + kStages * kSfCols <= kTmemCols, "TMEM columns");
-  static_assert(kSmem <= 232448, "shared memory");
-};
+constexpr int kBands = 2;                                    // 128-row scale bands of the features
+constexpr int kSfAt = 2 * kLaneTile;                         // codes of 128 tokens and 128 features
+constexpr int kStageBytes = kSfAt + kSfStage * (1 + kBands);  // 38 KB
+constexpr int kStages = 4;
+constexpr int kHalf = kBN / 2;  // columns of an epilogue warp
+constexpr int kBox = 32 * 128;  // staging buffer: 32 rows of 128 bytes
+constexpr int kStageOut = kEpiWarps * 2 * kBox;
+constexpr int kBars = 3 * kStages + 3 + 2 * kEpiWarps;
+constexpr int kSmem = kStages * kStageBytes + kStageOut + kBN * 4 /* bias */ + 512 /* barriers */ + 1024 /* alignment */;
+constexpr uint32_t kSfCols = 16 + 16 * kBands;
+constexpr uint32_t kTmemCols = 512;
+static_assert(kBN + kStages * kSfCols <= kTmemCols, "TMEM columns");
+static_assert(kStageBytes % 1024 == 0 && 8 * (kBars + 2) <= 512 && kSmem <= 232448, "shared memory");
 
 // Named barrier of `threads` threads; true if `v` holds in all of them.
 __device__ __forceinline__ bool bar_all(int id, int threads, bool v) {
@@ -57,8 +68,8 @@ __device__ __forceinline__ void tile_at(int64_t t, int64_t tm, int64_t tn, int64
   n = r / rows;
 }
 
-// 8 consecutive outputs; `p` is 16-byte aligned.
-__device__ __forceinline__ void store8(bf16* p, const float* v) {
+// 16 bytes of outputs: 8 bf16 or 4 fp32 values, rounded.
+__device__ __forceinline__ uint4 pack16(const float* v, bf16) {
   uint4 w;
   __nv_bfloat162 h[4];
 #pragma unroll
@@ -67,14 +78,12 @@ __device__ __forceinline__ void store8(bf16* p, const float* v) {
   w.y = *reinterpret_cast<uint32_t*>(&h[1]);
   w.z = *reinterpret_cast<uint32_t*>(&h[2]);
   w.w = *reinterpret_cast<uint32_t*>(&h[3]);
-  *reinterpret_cast<uint4*>(p) = w;
+  return w;
 }
-__device__ __forceinline__ void store8(float* p, const float* v) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ uint4 pack16(const float* v, float) {
+  return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
 }
-__device__ __forceinline__ void add8(const bf16* p, float* v) {
-  const uint4 w = *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ void add16(uint4 w, float* v, bf16) {
   v[0] += bf16_lo(w.x);
   v[1] += bf16_hi(w.x);
   v[2] += bf16_lo(w.y);
@@ -84,22 +93,29 @@ __device__ __forceinline__ void add8(const bf16* p, float* v) {
   v[6] += bf16_lo(w.w);
   v[7] += bf16_hi(w.w);
 }
-__device__ __forceinline__ void add8(const float* p, float* v) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] += a.x;
-  v[1] += a.y;
-  v[2] += a.z;
-  v[3] += a.w;
-  v[4] += b.x;
-  v[5] += b.y;
-  v[6] += b.z;
-  v[7] += b.w;
+__device__ __forceinline__ void add16(uint4 w, float* v, float) {
+  v[0] += __uint_as_float(w.x);
+  v[1] += __uint_as_float(w.y);
+  v[2] += __uint_as_float(w.z);
+  v[3] += __uint_as_float(w.w);
 }
 
-// Epilogue of 32 consecutive features of one token, `v` holding the products.
+// Largest magnitude of 32 values after rounding; only the first `cols` are outputs.
 template <typename T>
-__device__ __forceinline__ uint32_t put32(const LinearArgs& a, int64_t m, int64_t n, float* v, const float* bias,
-                                          float scale, bool vec) {
+__device__ __forceinline__ uint32_t top32(const float* v, int64_t cols, uint32_t top) {
+  if (cols >= 32) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) top = max(top, abs_bits(to_f32(from_f32<T>(v[i]))));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i < cols) top = max(top, abs_bits(to_f32(from_f32<T>(v[i]))));
+  }
+  return top;
+}
+
+// v = product * scale + bias, 32 values.
+__device__ __forceinline__ void affine32(float* v, const float* bias, float scale) {
 #pragma unroll
   for (int i = 0; i < 32; i += 4) {
     const float4 b = *reinterpret_cast<const float4*>(bias + i);
@@ -108,87 +124,80 @@ __device__ __forceinline__ uint32_t put32(const LinearArgs& a, int64_t m, int64_
     v[i + 2] = fmaf(v[i + 2], scale, b.z);
     v[i + 3] = fmaf(v[i + 3], scale, b.w);
   }
-  uint32_t top = 0;
-  if (vec && n + 32 <= a.N) {
-    if (a.z) {
-      T* p = static_cast<T*>(a.z) + m * a.ldz + n;
+}
+
+// Outputs that cannot go through a tensor map (rows that are not 16-byte
+// aligned), or a z beside a residual: 32 consecutive features of one token.
+template <typename T>
+__device__ __forceinline__ uint32_t put32(const LinearArgs& a, int64_t m, int64_t n, float* v, uint32_t top) {
+  const int cols = a.N - n < 32 ? (int)(a.N - n) : 32;
+  if (a.z) {
+    T* p = static_cast<T*>(a.z) + m * a.ldz + n;
 #pragma unroll
-      for (int i = 0; i < 32; i += 8) store8(p + i, v + i);
-    }
-    act_all<32>(v, a.act);
-    if (a.residual) {
-      const T* p = static_cast<const T*>(a.residual) + m * a.ldr + n;
+    for (int i = 0; i < 32; ++i)
+      if (i < cols) p[i] = from_f32<T>(v[i]);
+  }
+  act_all<32>(v, a.act);
+  const T* res = a.residual ? static_cast<const T*>(a.residual) + m * a.ldr + n : nullptr;
+  T* p = static_cast<T*>(a.d) + m * a.ldd + n;
 #pragma unroll
-      for (int i = 0; i < 32; i += 8) add8(p + i, v + i);
-    }
-    T* p = static_cast<T*>(a.d) + m * a.ldd + n;
-#pragma unroll
-    for (int i = 0; i < 32; i += 8) store8(p + i, v + i);
-    if (a.amax) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) top = max(top, abs_bits(to_f32(from_f32<T>(v[i]))));
-    }
-  } else {
-    const int cols = a.N - n < 32 ? (int)(a.N - n) : 32;
-    if (a.z) {
-      T* p = static_cast<T*>(a.z) + m * a.ldz + n;
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (i < cols) p[i] = from_f32<T>(v[i]);
-    }
-    act_all<32>(v, a.act);
-    const T* res = a.residual ? static_cast<const T*>(a.residual) + m * a.ldr + n : nullptr;
-    T* p = static_cast<T*>(a.d) + m * a.ldd + n;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      if (i < cols) {
-        const T o = from_f32<T>(v[i] + (res ? to_f32(res[i]) : 0.0f));
-        p[i] = o;
-        top = max(top, abs_bits(to_f32(o)));
-      }
+  for (int i = 0; i < 32; ++i) {
+    if (i < cols) {
+      const T o = from_f32<T>(v[i] + (res ? to_f32(res[i]) : 0.0f));
+      p[i] = o;
+      top = max(top, abs_bits(to_f32(o)));
     }
   }
   return top;
 }
 
-template <int BN, typename T>
+// This lane's row of a staging buffer in the 128-byte swizzle: 16-byte piece i.
+__device__ __forceinline__ uint4* piece(uint8_t* buf, int lane, int i) {
+  return reinterpret_cast<uint4*>(buf + lane * 128 + ((i ^ (lane & 7)) << 4));
+}
+
+template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_many_kernel(const LinearArgs a, const __grid_constant__ CUtensorMap xmap,
-                       const __grid_constant__ CUtensorMap wmap, int vec) {
-  using C = Cfg<BN>;
-  constexpr int kStages = C::kStages;
+                       const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap dmap,
+                       const __grid_constant__ CUtensorMap zmap, const __grid_constant__ CUtensorMap rmap, int staged) {
   extern __shared__ uint8_t raw[];
   // 1024-byte alignment for the 128-byte swizzle
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  float* bias_s = reinterpret_cast<float*>(smem + kStages * C::kStageBytes);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(bias_s + BN);
+  uint8_t* out_s = smem + kStages * kStageBytes;
+  float* bias_s = reinterpret_cast<float*>(out_s + kStageOut);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(bias_s + kBN);
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages, sfr0 = empty0 + 8 * kStages;
-  const uint32_t accf = sfr0 + 8 * kStages, acce = accf + 8, drain = accf + 16;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * kStages + 3);
-  volatile int* stop = reinterpret_cast<int*>(bars + 3 * kStages + 4);
+  const uint32_t accf = sfr0 + 8 * kStages, acce = accf + 8, drain = accf + 16, res0 = accf + 24;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
+  volatile int* stop = reinterpret_cast<int*>(bars + kBars + 1);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();  // 0: the leader
   const Steps K(a.K);
-  const int64_t tm = (a.M + kLaneRows - 1) / kLaneRows, tn = (a.N + BN - 1) / BN, tiles = tm * tn;
+  const int64_t tm = (a.M + 2 * kLaneRows - 1) / (2 * kLaneRows), tn = (a.N + kBN - 1) / kBN, tiles = tm * tn;
+  const int64_t first = blockIdx.x / 2, step = gridDim.x / 2;
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       tma::mbar_init(full0 + 8 * s, 1);
       tma::mbar_init(empty0 + 8 * s, 1);
-      tma::mbar_init(sfr0 + 8 * s, kSfWarps);  // the stage has arrived and its scales are in TMEM
+      tma::mbar_init(sfr0 + 8 * s, 2 * kSfWarps);  // leader's: the stage is there in both blocks, its scales in TMEM
     }
     tma::mbar_init(accf, 1);
-    tma::mbar_init(acce, kEpiWarps);
+    tma::mbar_init(acce, 2 * kEpiWarps);  // leader's: both blocks have taken the tile out
     tma::mbar_init(drain, 1);
+    for (int i = 0; i < 2 * kEpiWarps; ++i) tma::mbar_init(res0 + 8 * i, 1);
     *stop = 0;
     tma::fence_barrier_init();
   }
   if (warp == 1) {
-    tc5::alloc(smem_u32(tmem_slot), C::kTmemCols);
-    tc5::relinquish_alloc_permit();
+    alloc2(smem_u32(tmem_slot), kTmemCols);
+    relinquish2();
   }
   tc5::fence_before_thread_sync();
   __syncthreads();
+  cluster_sync();  // both blocks' barriers are set up
   tc5::fence_after_thread_sync();
   const uint32_t tmem = *tmem_slot;
   uint32_t top = 0;
@@ -200,22 +209,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t sf_row = (a.K + 63) / 64 * kSfBlock;  // scale bytes of a 128-row band
         Ring<kStages> r;
         int64_t g = 0;
-        for (int64_t t = blockIdx.x; t < tiles && !*stop; t += gridDim.x) {
+        for (int64_t t = first; t < tiles && !*stop; t += step) {
           int64_t m, n;
           tile_at(t, tm, tn, m, n);
-          const int bands = a.N - n * BN > 128 ? C::kBands : 1;  // 128-row bands of scales that exist
-          const uint8_t* sfx = a.sfa + m * sf_row;
-          const uint8_t* sfw = a.sfb + n * C::kBands * sf_row;
+          const int64_t row = (2 * m + rank) * kLaneRows, col = n * kBN + rank * kLaneRows;
+          const int bands = a.N - n * kBN > 128 ? 2 : 1;  // 128-row bands of scales that exist
+          const int tok = row < a.M ? 1 : 0;              // and of the tokens'
+          const uint8_t* sfx = a.sfa + (2 * m + rank) * sf_row;
+          const uint8_t* sfw = a.sfb + n * kBands * sf_row;
           for (int kb = 0; kb < K.n; ++kb, ++g, r.next()) {
             if (g >= kStages && !tma::wait(empty0 + 8 * r.slot, r.phase ^ 1u)) {
               *stop = 1;
               break;
             }
-            const uint32_t st = smem_u32(smem + r.slot * C::kStageBytes), full = full0 + 8 * r.slot;
-            const int groups = K.groups(kb);
-            tma::arrive_expect_tx(full, (uint32_t)(C::kSfAt + (1 + bands) * groups * kSfBlock));
-            load_codes<BN>(st, full, &xmap, &wmap, (int)(m * kLaneRows), (int)(n * BN), kb);
-            load_scales(st + C::kSfAt, full, sfx, sfw, sf_row, kb, groups, bands);
+            const uint32_t st = smem_u32(smem + r.slot * kStageBytes), full = full0 + 8 * r.slot;
+            const uint32_t bytes = (uint32_t)(K.groups(kb) * kSfBlock);
+            tma::arrive_expect_tx(full, (uint32_t)kSfAt + bytes * (uint32_t)(tok + bands));
+            // rows beyond the operand arrive as zeros
+            tma::load_2d(st, &xmap, kb * (kBK / 2), (int)row, full);
+            tma::load_2d(st + kLaneTile, &wmap, kb * (kBK / 2), (int)col, full);
+            const int64_t at = (int64_t)kb * kSfStage;
+            if (tok) tc5::bulk_g2s(st + kSfAt, sfx + at, bytes, full);
+            tc5::bulk_g2s(st + kSfAt + kSfStage, sfw + at, bytes, full);
+            if (bands == 2) tc5::bulk_g2s(st + kSfAt + 2 * kSfStage, sfw + sf_row + at, bytes, full);
           }
         }
         // no copy may land after the block has gone: wait for the last fill of every stage
@@ -223,83 +239,149 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma::wait(full0 + 8 * (int)(j % kStages), (uint32_t)(j / kStages) & 1u);
       }
     } else if (warp == 1) {
-      if (lane == 0) {
+      if (lane == 0 && rank == 0) {
         Ring<kStages> r;
         int li = 0;
-        for (int64_t t = blockIdx.x; t < tiles && !*stop; t += gridDim.x, ++li) {
-          // the epilogue has taken the previous tile out
-          if (li > 0 && !tma::wait(acce, (uint32_t)(li - 1) & 1u)) {
+        for (int64_t t = first; t < tiles && !*stop; t += step, ++li) {
+          // both epilogues have taken the previous tile out
+          if (li > 0 && !wait_cluster(acce, (uint32_t)(li - 1) & 1u)) {
             *stop = 1;
             break;
           }
           for (int kb = 0; kb < K.n; ++kb, r.next()) {
-            if (!tma::wait(sfr0 + 8 * r.slot, r.phase)) {  // the scale warps have waited for the stage
+            if (!wait_cluster(sfr0 + 8 * r.slot, r.phase)) {  // the scale warps have waited for the stage
               *stop = 1;
               break;
             }
             tc5::fence_after_thread_sync();
-            mma_stage<BN>(tmem, tmem + BN + (uint32_t)r.slot * C::kSfCols,
-                          StageDesc(smem_u32(smem + r.slot * C::kStageBytes)), K.groups(kb), kb == 0);
-            tc5::commit(empty0 + 8 * r.slot);
+            mma2_stage<kBN>(tmem, tmem + kBN + (uint32_t)r.slot * kSfCols, StageDesc(smem_u32(smem + r.slot * kStageBytes)),
+                            K.groups(kb), kb == 0);
+            commit2(empty0 + 8 * r.slot);
           }
           if (*stop) break;
-          tc5::commit(accf);
+          commit2(accf);
         }
-        tc5::commit(drain);  // arrives when every MMA issued above has completed
+        commit2(drain);  // arrives in both blocks when every MMA issued above has completed
       }
     } else if (warp >= kSfWarp0) {
       const uint32_t quarter = (uint32_t)(32 * (warp & 3)) << 16;
       Ring<kStages> r;
       bool quit = false;
-      for (int64_t t = blockIdx.x; t < tiles && !quit; t += gridDim.x) {
+      for (int64_t t = first; t < tiles && !quit; t += step) {
         for (int kb = 0; kb < K.n; ++kb, r.next()) {
           quit = !__all_sync(0xFFFFFFFFu, tma::wait(full0 + 8 * r.slot, r.phase) && *stop == 0);
           if (quit) break;
-          put_scales<C::kBands>(tmem + quarter + BN + (uint32_t)r.slot * C::kSfCols,
-                                smem + r.slot * C::kStageBytes + C::kSfAt, K.groups(kb), kb == K.n - 1 && K.tail, lane);
+          put_scales<kBands>(tmem + quarter + kBN + (uint32_t)r.slot * kSfCols, smem + r.slot * kStageBytes + kSfAt,
+                             K.groups(kb), kb == K.n - 1 && K.tail, lane);
           tc5::fence_before_thread_sync();
           __syncwarp();
-          if (lane == 0) arrive(sfr0 + 8 * r.slot);
+          if (lane == 0) arrive_at(sfr0 + 8 * r.slot, 0);
         }
       }
       if (quit && lane == 0) *stop = 1;
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
+    constexpr int kCols = 128 / (int)sizeof(T);  // columns of a staging buffer
+    constexpr int kChunks = kHalf / kCols;
+    constexpr int kPer = 16 / (int)sizeof(T);    // values in 16 bytes
     const int e = warp - kEpiWarp0, q = warp & 3, half = e >> 2;  // lane quarter, column half
     const float scale = a.alpha_a[0] * a.alpha_b[0];
-    float* bias = bias_s + half * C::kHalf;  // shared by the half's four warps
-    int li = 0;
-    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, ++li) {
+    float* bias = bias_s + half * kHalf;  // shared by the half's four warps
+    uint8_t* buf = out_s + e * 2 * kBox;
+    const uint32_t res = res0 + 16 * e;
+    int li = 0, slot = 0;
+    uint32_t res_phase = 0;
+    for (int64_t t = first; t < tiles; t += step, ++li) {
       int64_t m, n;
       tile_at(t, tm, tn, m, n);
-      const int64_t row = m * kLaneRows + 32 * q + lane, col = n * BN + half * C::kHalf;
+      const int64_t row0 = (2 * m + rank) * kLaneRows + 32 * q, row = row0 + lane, col = n * kBN + half * kHalf;
+      const bool rows = row0 < a.M;  // warp-uniform: some row of this warp exists
+      auto load_res = [&](int c) {   // the residual of chunk c into its buffer, once earlier stores have left it
+        if (lane == 0 && rows && col + c * kCols < a.N) {
+          stores_read<0>();
+          tma::arrive_expect_tx(res + 8 * (c & 1), kBox);
+          tma::load_2d(smem_u32(buf + (c & 1) * kBox), &rmap, (int)(col + c * kCols), (int)row0, res + 8 * (c & 1));
+        }
+      };
+      if (staged && a.residual) {
+        load_res(0);
+        load_res(1);
+      }
       // the four warps of this half have read the previous tile's bias; load this tile's
       bar_all(1 + half, 128, true);
-      for (int i = 32 * q + lane; i < C::kHalf; i += 128)
+      for (int i = 32 * q + lane; i < kHalf; i += 128)
         bias[i] = a.bias && col + i < a.N ? load_as_f32(a.bias, col + i, a.bias_bf16) : 0.0f;
       const bool ready = tma::wait(accf, (uint32_t)li & 1u);
       // the barrier orders the bias, and the four warps go on or stop together
       if (!bar_all(1 + half, 128, ready && *stop == 0)) {
         if (lane == 0) *stop = 1;
+        if (staged && a.residual && rows)  // the copies issued above land before the block goes
+          for (int c = 0; c < 2 && col + c * kCols < a.N; ++c) tma::wait(res + 8 * c, (res_phase >> c) & 1u);
         break;
       }
       tc5::fence_after_thread_sync();
-      const uint32_t acc = tmem + (uint32_t)(half * C::kHalf) + ((uint32_t)(32 * q) << 16);
-      uint32_t r[C::kHalf];
+      const uint32_t acc = tmem + (uint32_t)(half * kHalf) + ((uint32_t)(32 * q) << 16);
+      uint32_t raw_r[kHalf];
+      float* r = reinterpret_cast<float*>(raw_r);
 #pragma unroll
-      for (int c = 0; c < C::kHalf; c += 32) tc5::ld_32x32b_x32(acc + (uint32_t)c, r + c);
+      for (int c = 0; c < kHalf; c += 32) tc5::ld_32x32b_x32(acc + (uint32_t)c, raw_r + c);
       tc5::wait_ld();
       tc5::fence_before_thread_sync();
       __syncwarp();
-      if (lane == 0) arrive(acce);
-      if (row < a.M) {
+      if (lane == 0) arrive_at(acce, 0);
+      if (!rows) continue;
+      if (staged) {
 #pragma unroll
-        for (int c = 0; c < C::kHalf; c += 32)
-          if (col + c < a.N)
-            top = max(top, put32<T>(a, row, col + c, reinterpret_cast<float*>(r + c), bias + c, scale, vec != 0));
+        for (int c = 0; c < kChunks; ++c) {
+          if (col + c * kCols >= a.N) break;
+          float* v = r + c * kCols;
+#pragma unroll
+          for (int h = 0; h < kCols; h += 32) affine32(v + h, bias + c * kCols + h, scale);
+          auto put = [&](const CUtensorMap* map, uint8_t* b) {  // v, rounded, through buffer b
+#pragma unroll
+            for (int i = 0; i < 8; ++i) *piece(b, lane, i) = pack16(v + i * kPer, T());
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) store_2d(map, (int)(col + c * kCols), (int)row0, smem_u32(b));
+          };
+          auto next_buffer = [&]() {  // the buffer of two stores ago
+            if (lane == 0) stores_read<1>();
+            __syncwarp();
+            slot ^= 1;
+            return buf + slot * kBox;
+          };
+          if (a.z) put(&zmap, next_buffer());
+#pragma unroll
+          for (int h = 0; h < kCols; h += 32) act_all<32>(v + h, a.act);
+          if (a.residual) {
+            uint8_t* b = buf + (c & 1) * kBox;
+            const uint32_t bit = 1u << (c & 1);
+            if (!__all_sync(0xFFFFFFFFu, tma::wait(res + 8 * (c & 1), (res_phase & bit) ? 1u : 0u)) && lane == 0) *stop = 1;
+            res_phase ^= bit;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) add16(*piece(b, lane, i), v + i * kPer, T());
+            put(&dmap, b);
+            if (c + 2 < kChunks) load_res(c + 2);
+          } else {
+            put(&dmap, next_buffer());
+          }
+          if (a.amax && row < a.M) {
+#pragma unroll
+            for (int h = 0; h < kCols; h += 32) top = top32<T>(v + h, a.N - col - c * kCols - h, top);
+          }
+        }
+      } else if (row < a.M) {
+#pragma unroll
+        for (int c = 0; c < kHalf; c += 32) {
+          if (col + c < a.N) {
+            affine32(r + c, bias + c, scale);
+            top = put32<T>(a, row, col + c, r + c, top);
+          }
+        }
       }
     }
+    if (lane == 0) stores_done();
   }
   __syncwarp();
   __syncthreads();
@@ -308,35 +390,49 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0 && (*stop || !drained) && a.status) atomicExch(a.status, kStatusPipeline);
   tc5::fence_before_thread_sync();
   __syncthreads();
-  if (warp == 1) tc5::dealloc(tmem, C::kTmemCols);
+  cluster_sync();  // neither block leaves while the pair's MMAs may read it or its peer arrives on its barriers
+  if (warp == 1) dealloc2(tmem, kTmemCols);
 }
 
-template <int BN, typename T>
+template <typename T>
 cudaError_t launch(const LinearArgs& a, cudaStream_t s) {
-  using C = Cfg<BN>;
-  auto kern = linear_many_kernel<BN, T>;
+  auto kern = linear_many_kernel<T>;
   static std::atomic<int> cache[64] = {};
   int cap = 0;
-  cudaError_t e = resident_grid(kern, kThreads, C::kSmem, cache, cap);
-  if (e != cudaSuccess) return e;
-  CUtensorMap xmap, wmap;
-  e = make_codes_map(&xmap, a.qa, a.M, a.K / 2, kBK / 2, kLaneRows);
-  if (e != cudaSuccess) return e;
-  e = make_codes_map(&wmap, a.qb, a.N, a.K / 2, kBK / 2, BN);
+  cudaError_t e = resident_grid(kern, kThreads, kSmem, cache, cap);
   if (e != cudaSuccess) return e;
   auto ok16 = [](const void* p, int64_t ld) {
     return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * (int64_t)sizeof(T) % 16 == 0);
   };
-  const int vec = ok16(a.d, a.ldd) && ok16(a.z, a.ldz) && ok16(a.residual, a.ldr);
-  const int64_t tiles = ((a.M + kLaneRows - 1) / kLaneRows) * ((a.N + BN - 1) / BN);
-  kern<<<(unsigned)(tiles < cap ? tiles : cap), kThreads, C::kSmem, s>>>(a, xmap, wmap, vec);
-  return cudaGetLastError();
+  const bool staged = ok16(a.d, a.ldd) && ok16(a.z, a.ldz) && ok16(a.residual, a.ldr) && !(a.z && a.residual);
+  CUtensorMap xmap, wmap, dmap, zmap, rmap;
+  e = make_codes_map(&xmap, a.qa, a.M, a.K / 2, kBK / 2, kLaneRows);
+  if (e == cudaSuccess) e = make_codes_map(&wmap, a.qb, a.N, a.K / 2, kBK / 2, kLaneRows);
+  const bool b16 = sizeof(T) == 2;
+  if (e == cudaSuccess) e = make_out_map(&dmap, staged ? a.d : nullptr, b16, a.M, a.N, a.ldd, 32);
+  if (e == cudaSuccess) e = make_out_map(&zmap, staged ? a.z : nullptr, b16, a.M, a.N, a.ldz, 32);
+  if (e == cudaSuccess) e = make_out_map(&rmap, staged ? a.residual : nullptr, b16, a.M, a.N, a.ldr, 32);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = ((a.M + 255) / 256) * ((a.N + kBN - 1) / kBN);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * (tiles < cap / 2 ? tiles : cap / 2)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a, xmap, wmap, dmap, zmap, rmap, staged ? 1 : 0);
 }
 
 }  // namespace
 
 cudaError_t launch_many(const LinearArgs& a, cudaStream_t s) {
-  return a.out_bf16 ? launch<256, bf16>(a, s) : launch<256, float>(a, s);
+  return a.out_bf16 ? launch<bf16>(a, s) : launch<float>(a, s);
 }
 
 }  // namespace lin

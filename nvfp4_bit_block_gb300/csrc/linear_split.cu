@@ -31,14 +31,6 @@ struct Cfg {
   static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two blocks per SM");
 };
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 __device__ __forceinline__ float ld_rank(uint32_t saddr, uint32_t rank) {
   uint32_t a;
   float v;

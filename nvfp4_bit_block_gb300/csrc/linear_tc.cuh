@@ -38,6 +38,86 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
+// ---- pairs of blocks (cta_group::2): the two blocks of a cluster of two form one
+// MMA of 256 rows; each holds its 128 rows of the lane operand, half of the column
+// operand's rows, its 128 rows of the accumulator, and all of the column scales.
+__device__ __forceinline__ void alloc2(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
+               : "memory");
+}
+__device__ __forceinline__ void relinquish2() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void dealloc2(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void mma2_nvf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t sfa_tmem, uint32_t sfb_tmem, bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(
+          d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+// The mbarrier at this offset in both blocks receives an arrival when the pair's MMAs issued so far are done.
+__device__ __forceinline__ void commit2(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Arrival on the barrier at this offset in block `rank` of the cluster, and the
+// wait for such arrivals.  What they order is tensor-core work (TMEM accesses,
+// fenced by tcgen05.fence, and tiles whose copies have completed), no ordinary
+// memory, so the arrival has the default scope: a release at cluster scope made
+// a stage of the pair kernel take 1930 instead of 930 clocks.
+__device__ __forceinline__ void arrive_at(uint32_t bar, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(bar), "r"(rank));
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(a) : "memory");
+}
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 0; i < tma::kWaitLimitPolls; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (i == 0) t0 = tma::globaltimer();
+    if ((i & 255u) == 255u && tma::globaltimer() - t0 > tma::kWaitLimitNs) return false;
+  }
+  return false;
+}
+
+// ---- stores of staged tiles by TMA, tracked in bulk groups of the issuing thread.
+__device__ __forceinline__ void store_2d(const CUtensorMap* map, int x, int y, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(src)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+template <int LEFT>
+__device__ __forceinline__ void stores_read() {  // all but the LEFT latest stores have read shared memory
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(LEFT) : "memory");
+}
+__device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
 __device__ __forceinline__ void ld_32x32b_x16(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
@@ -103,7 +183,7 @@ __device__ __forceinline__ void clear_tail(uint8_t* sf, int bands, int group, in
     v.w &= 0xFFFFu;
     *p = v;
   }
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  fence_async_smem();
   __syncwarp();
 }
 
@@ -176,6 +256,23 @@ __device__ __forceinline__ void mma_stage(uint32_t acc, uint32_t sf_tmem, StageD
     for (int j = 0; j < 4; ++j) mma_step<BN>(acc, sf_tmem, d, j, j > 0 || !fresh);
   } else {
     for (int j = 0; j < groups; ++j) mma_step<BN>(acc, sf_tmem, d, j, j > 0 || !fresh);
+  }
+}
+
+// The same for a pair of blocks: 256 rows of lanes, BN columns of which each block holds half.
+template <int BN>
+__device__ __forceinline__ void mma2_step(uint32_t acc, uint32_t sf_tmem, StageDesc d, int j, bool add) {
+  constexpr uint32_t idesc = tc5::idesc_e2m1_e4m3(2 * kLaneRows, BN);
+  constexpr int kBands = (BN + 127) / 128;
+  mma2_nvf4(acc, d.lane + 2 * j, d.col + 2 * j, idesc, sf_tmem + 4u * j, sf_tmem + 16u + 4u * kBands * j, add);
+}
+template <int BN>
+__device__ __forceinline__ void mma2_stage(uint32_t acc, uint32_t sf_tmem, StageDesc d, int groups, bool fresh) {
+  if (groups == 4) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) mma2_step<BN>(acc, sf_tmem, d, j, j > 0 || !fresh);
+  } else {
+    for (int j = 0; j < groups; ++j) mma2_step<BN>(acc, sf_tmem, d, j, j > 0 || !fresh);
   }
 }
 
