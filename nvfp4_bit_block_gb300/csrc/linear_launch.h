@@ -14,7 +14,7 @@ cudaError_t launch_split(const LinearArgs& a, int bn, int S, cudaStream_t s);
 // Many tokens: pairs of blocks walk tiles of 256 tokens x 256 features.
 cudaError_t launch_many(const LinearArgs& a, cudaStream_t s);
 
-// rows x cols elements (row stride ld; 16-byte aligned rows) in boxes of 128 bytes x box_rows, 128-byte swizzle.
+// rows x cols elements (row stride ld; 16-byte aligned rows) in boxes of 64 bytes x box_rows, 64-byte swizzle.
 // NULL gives an empty map.
 cudaError_t make_out_map(CUtensorMap* map, const void* p, bool is_bf16, int64_t rows, int64_t cols, int64_t ld,
                          int box_rows);

@@ -16,7 +16,7 @@
 // accumulator into registers and hand it back before they compute, so that the
 // next tile's MMAs wait for the read-out alone; registers are moved to them
 // from the other warps (setmaxnreg).  Outputs are staged in shared memory, 32
-// rows of 128 bytes per warp, and stored by TMA as whole lines (16-byte pieces
+// rows of 64 bytes per warp, and stored by TMA as whole sectors (16-byte pieces
 // of 32 rows at once cost 3 us per tile); the residual comes in by TMA before the
 // product is done.
 #include "linear_launch.h"
@@ -37,9 +37,10 @@ constexpr int64_t kGroupM = 8;  // token tiles walked together, so that blocks i
 constexpr int kBands = 2;                                    // 128-row scale bands of the features
 constexpr int kSfAt = 2 * kLaneTile;                         // codes of 128 tokens and 128 features
 constexpr int kStageBytes = kSfAt + kSfStage * (1 + kBands);  // 38 KB
-constexpr int kStages = 4;
+constexpr int kStages = 5;
 constexpr int kHalf = kBN / 2;  // columns of an epilogue warp
-constexpr int kBox = 32 * 128;  // staging buffer: 32 rows of 128 bytes
+constexpr int kRow = 64;         // staging buffers: 32 rows of 64 bytes, two per epilogue warp
+constexpr int kBox = 32 * kRow;
 constexpr int kStageOut = kEpiWarps * 2 * kBox;
 constexpr int kBars = 3 * kStages + 3 + 2 * kEpiWarps;
 constexpr int kSmem = kStages * kStageBytes + kStageOut + kBN * 4 /* bias */ + 512 /* barriers */ + 1024 /* alignment */;
@@ -100,24 +101,25 @@ __device__ __forceinline__ void add16(uint4 w, float* v, float) {
   v[3] += __uint_as_float(w.w);
 }
 
-// Largest magnitude of 32 values after rounding; only the first `cols` are outputs.
-template <typename T>
-__device__ __forceinline__ uint32_t top32(const float* v, int64_t cols, uint32_t top) {
-  if (cols >= 32) {
+// Largest magnitude of NV values after rounding; only the first `cols` are outputs.
+template <int NV, typename T>
+__device__ __forceinline__ uint32_t top_of(const float* v, int64_t cols, uint32_t top) {
+  if (cols >= NV) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) top = max(top, abs_bits(to_f32(from_f32<T>(v[i]))));
+    for (int i = 0; i < NV; ++i) top = max(top, abs_bits(to_f32(from_f32<T>(v[i]))));
   } else {
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
+    for (int i = 0; i < NV; ++i)
       if (i < cols) top = max(top, abs_bits(to_f32(from_f32<T>(v[i]))));
   }
   return top;
 }
 
-// v = product * scale + bias, 32 values.
-__device__ __forceinline__ void affine32(float* v, const float* bias, float scale) {
+// v = product * scale + bias.
+template <int NV>
+__device__ __forceinline__ void affine(float* v, const float* bias, float scale) {
 #pragma unroll
-  for (int i = 0; i < 32; i += 4) {
+  for (int i = 0; i < NV; i += 4) {
     const float4 b = *reinterpret_cast<const float4*>(bias + i);
     v[i] = fmaf(v[i], scale, b.x);
     v[i + 1] = fmaf(v[i + 1], scale, b.y);
@@ -151,9 +153,9 @@ __device__ __forceinline__ uint32_t put32(const LinearArgs& a, int64_t m, int64_
   return top;
 }
 
-// This lane's row of a staging buffer in the 128-byte swizzle: 16-byte piece i.
+// This lane's row of a staging buffer in the 64-byte swizzle: 16-byte piece i.
 __device__ __forceinline__ uint4* piece(uint8_t* buf, int lane, int i) {
-  return reinterpret_cast<uint4*>(buf + lane * 128 + ((i ^ (lane & 7)) << 4));
+  return reinterpret_cast<uint4*>(buf + lane * kRow + ((i ^ ((lane >> 1) & 3)) << 4));
 }
 
 template <typename T>
@@ -282,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
-    constexpr int kCols = 128 / (int)sizeof(T);  // columns of a staging buffer
+    constexpr int kCols = kRow / (int)sizeof(T);   // columns of a staging buffer
     constexpr int kChunks = kHalf / kCols;
     constexpr int kPer = 16 / (int)sizeof(T);    // values in 16 bytes
     const int e = warp - kEpiWarp0, q = warp & 3, half = e >> 2;  // lane quarter, column half
@@ -336,11 +338,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < kChunks; ++c) {
           if (col + c * kCols >= a.N) break;
           float* v = r + c * kCols;
-#pragma unroll
-          for (int h = 0; h < kCols; h += 32) affine32(v + h, bias + c * kCols + h, scale);
+          affine<kCols>(v, bias + c * kCols, scale);
           auto put = [&](const CUtensorMap* map, uint8_t* b) {  // v, rounded, through buffer b
 #pragma unroll
-            for (int i = 0; i < 8; ++i) *piece(b, lane, i) = pack16(v + i * kPer, T());
+            for (int i = 0; i < kRow / 16; ++i) *piece(b, lane, i) = pack16(v + i * kPer, T());
             fence_async_smem();
             __syncwarp();
             if (lane == 0) store_2d(map, (int)(col + c * kCols), (int)row0, smem_u32(b));
@@ -352,30 +353,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             return buf + slot * kBox;
           };
           if (a.z) put(&zmap, next_buffer());
-#pragma unroll
-          for (int h = 0; h < kCols; h += 32) act_all<32>(v + h, a.act);
+          act_all<kCols>(v, a.act);
           if (a.residual) {
             uint8_t* b = buf + (c & 1) * kBox;
             const uint32_t bit = 1u << (c & 1);
             if (!__all_sync(0xFFFFFFFFu, tma::wait(res + 8 * (c & 1), (res_phase & bit) ? 1u : 0u)) && lane == 0) *stop = 1;
             res_phase ^= bit;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) add16(*piece(b, lane, i), v + i * kPer, T());
+            for (int i = 0; i < kRow / 16; ++i) add16(*piece(b, lane, i), v + i * kPer, T());
             put(&dmap, b);
             if (c + 2 < kChunks) load_res(c + 2);
           } else {
             put(&dmap, next_buffer());
           }
-          if (a.amax && row < a.M) {
-#pragma unroll
-            for (int h = 0; h < kCols; h += 32) top = top32<T>(v + h, a.N - col - c * kCols - h, top);
-          }
+          if (a.amax && row < a.M) top = top_of<kCols, T>(v, a.N - col - c * kCols, top);
         }
       } else if (row < a.M) {
 #pragma unroll
         for (int c = 0; c < kHalf; c += 32) {
           if (col + c < a.N) {
-            affine32(r + c, bias + c, scale);
+            affine<32>(r + c, bias + c, scale);
             top = put32<T>(a, row, col + c, r + c, top);
           }
         }
