@@ -31,7 +31,7 @@ SELFTEST_LIB = os.path.join(SELFTEST_BUILD, "libnvfp4_selftest.so")
 
 SOURCES = ["api.cu", "tmap.cu", "amax.cu", "quant1d.cu", "quant1d_sr.cu", "quant1d_46mae.cu", "quant1d_46mse.cu", "quant1d_46max.cu",
            "quant2d.cu", "dequant.cu", "analysis.cu", "gemm.cu"]
-LAYER_SOURCES = ["layer_api.cu", "layernorm.cu", "act_backward.cu", "linear.cu", "linear_split.cu", "linear_many.cu", "out_tmap.cu",
+LAYER_SOURCES = ["layer_api.cu", "layernorm.cu", "layernorm_backward.cu", "act_backward.cu", "linear.cu", "linear_split.cu", "linear_many.cu", "out_tmap.cu",
                  "tmap.cu"]
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

@@ -1,135 +1,210 @@
-// layernorm.cu -- layer norm over the rows of a matrix and its gradient.
-#include "layer_device.cuh"
+// layernorm.cu -- layer norm over the rows of a matrix.
+//
+// y = (x - mean) * rstd * gamma + beta: 2 reads and writes per element and nine
+// operations, so HBM bounds it.  A row is read once and stays in registers; the
+// mean is summed first and the squares about it second (two reductions: no
+// cancellation however far the mean is from zero).
+#include <atomic>
+
 #include "layer_internal.h"
+#include "norm_common.cuh"
+#include "nvfp4_internal.h"
 
 namespace nvfp4 {
+namespace norm {
 namespace {
 
-using namespace layer;
+constexpr int kMaxThreads = 1024;
+constexpr int kWarpThreads = 256;  // block of the one-warp-per-row kernels
 
-constexpr int kThreads = 256;
-
-// y = (x - mean) * rstd * gamma + beta, one block per row: the mean, then the
-// squares about it (no cancellation however large the mean is), then y.
-template <typename XT, typename YT>
-__global__ void __launch_bounds__(kThreads) norm_kernel(const NormArgs a) {
-  __shared__ float buf[32];
-  const int64_t r = blockIdx.x;
-  const XT* x = static_cast<const XT*>(a.x) + r * a.ldx;
-  YT* y = static_cast<YT*>(a.y) + r * a.ldy;
-  float t = 0.0f;
-  for (int64_t c = threadIdx.x; c < a.N; c += kThreads) t += to_f32(x[c]);
-  const float mean = block_sum(t, buf) / (float)a.N;
-  t = 0.0f;
-  for (int64_t c = threadIdx.x; c < a.N; c += kThreads) {
-    const float d = to_f32(x[c]) - mean;
-    t += d * d;
-  }
-  const float rstd = 1.0f / sqrtf(block_sum(t, buf) / (float)a.N + a.eps);
-  uint32_t top = 0;
-  for (int64_t c = threadIdx.x; c < a.N; c += kThreads) {
-    float v = (to_f32(x[c]) - mean) * rstd;
-    if (a.gamma) v *= load_as_f32(a.gamma, c, a.w_bf16);
-    if (a.beta) v += load_as_f32(a.beta, c, a.w_bf16);
-    const YT o = from_f32<YT>(v);
-    y[c] = o;
-    top = max(top, abs_bits(to_f32(o)));
-  }
-  if (threadIdx.x == 0) {
-    if (a.mean) a.mean[r] = mean;
-    if (a.rstd) a.rstd[r] = rstd;
-  }
-  if (a.amax) {
-    top = __reduce_max_sync(0xFFFFFFFFu, top);
-    if ((threadIdx.x & 31) == 0) {
-      atomicMax(reinterpret_cast<uint32_t*>(a.amax), top);
-      atomicMax(reinterpret_cast<uint32_t*>(a.amax) + 1, top);
-    }
-  }
-}
-
-template <typename DT, typename XT>
-__global__ void __launch_bounds__(kThreads) norm_grad_kernel(const NormGradArgs a) {
-  __shared__ float buf[32];
-  const int64_t r = blockIdx.x;
-  const DT* dy = static_cast<const DT*>(a.dy) + r * a.lddy;
-  const XT* x = static_cast<const XT*>(a.x) + r * a.ldx;
-  const XT* dres = a.dres ? static_cast<const XT*>(a.dres) + r * a.lddres : nullptr;
-  XT* dx = static_cast<XT*>(a.dx) + r * a.lddx;
-  const float mean = a.mean[r], rstd = a.rstd[r];
-  float t0 = 0.0f, t1 = 0.0f;
-  for (int64_t c = threadIdx.x; c < a.N; c += kThreads) {
-    const float g = to_f32(dy[c]) * (a.gamma ? load_as_f32(a.gamma, c, a.w_bf16) : 1.0f);
-    t0 += g;
-    t1 += g * ((to_f32(x[c]) - mean) * rstd);
-  }
-  const float m0 = block_sum(t0, buf) / (float)a.N;
-  const float m1 = block_sum(t1, buf) / (float)a.N;
-  for (int64_t c = threadIdx.x; c < a.N; c += kThreads) {
-    const float g = to_f32(dy[c]) * (a.gamma ? load_as_f32(a.gamma, c, a.w_bf16) : 1.0f);
-    float v = rstd * (g - m0 - (to_f32(x[c]) - mean) * rstd * m1);
-    if (dres) v += to_f32(dres[c]);
-    dx[c] = from_f32<XT>(v);
-  }
-}
-
-// dgamma and dbeta: a block of 32 columns x 8 row lanes, joined in shared memory.
-template <typename DT, typename XT>
-__global__ void __launch_bounds__(kThreads) norm_weight_grad_kernel(const NormGradArgs a) {
-  __shared__ float s0[8][32], s1[8][32];
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const int64_t c = (int64_t)blockIdx.x * 32 + tx;
-  float t0 = 0.0f, t1 = 0.0f;
-  if (c < a.N) {
-    for (int64_t r = ty; r < a.M; r += 8) {
-      const float dy = to_f32(static_cast<const DT*>(a.dy)[r * a.lddy + c]);
-      t0 += dy;
-      t1 += dy * ((to_f32(static_cast<const XT*>(a.x)[r * a.ldx + c]) - a.mean[r]) * a.rstd[r]);
-    }
-  }
-  s0[ty][tx] = t0;
-  s1[ty][tx] = t1;
+// The block's largest magnitude into both amax entries: by one block alone
+// stored, by several joined (the pair is zeroed before the launch).
+__device__ __forceinline__ void put_amax(const NormArgs& a, uint32_t top, uint32_t* buf) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  top = __reduce_max_sync(0xFFFFFFFFu, top);
+  if (lane == 0) buf[warp] = top;
   __syncthreads();
-  if (ty == 0 && c < a.N) {
-    for (int i = 1; i < 8; ++i) {
-      t0 += s0[i][tx];
-      t1 += s1[i][tx];
+  if (warp == 0) {
+    top = __reduce_max_sync(0xFFFFFFFFu, lane < warps ? buf[lane] : 0u);
+    if (lane < 2) {
+      uint32_t* p = reinterpret_cast<uint32_t*>(a.amax) + lane;
+      if (gridDim.x == 1)
+        *p = top;
+      else
+        atomicMax(p, top);
     }
-    if (a.dbeta) a.dbeta[c] = t0;
-    if (a.dgamma) a.dgamma[c] = t1;
   }
 }
 
-template <typename DT, typename XT>
-void launch_grad(const NormGradArgs& a, cudaStream_t s) {
-  // the weight's gradient first: dx may take dy's place
-  if (a.dgamma || a.dbeta) norm_weight_grad_kernel<DT, XT><<<(unsigned)((a.N + 31) / 32), kThreads, 0, s>>>(a);
-  norm_grad_kernel<DT, XT><<<(unsigned)a.M, kThreads, 0, s>>>(a);
+// R rows at a time per group, so that R rows share the loads of gamma and beta and
+// the barriers of the reductions.
+template <typename XT, typename YT, int V, int NC, int R, bool WARP, int THREADS>
+__global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a) {
+  __shared__ float buf[2][R * 32];
+  __shared__ uint32_t top_s[32];
+  const int N = (int)a.N;
+  const int lane = WARP ? threadIdx.x & 31 : threadIdx.x, group = WARP ? 32 : blockDim.x;
+  const int64_t groups = WARP ? (int64_t)gridDim.x * (kWarpThreads / 32) : gridDim.x;
+  const int64_t first = WARP ? (int64_t)blockIdx.x * (kWarpThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
+  const float inv = 1.0f / (float)N;
+  uint32_t top = 0;
+  for (int64_t r0 = first * R; r0 < a.M; r0 += groups * R) {
+    Raw<XT, V> x[R][NC];
+#pragma unroll
+    for (int q = 0; q < R; ++q)
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+        x[q][i] = load_chunk<XT, V>(static_cast<const XT*>(a.x) + (r0 + q) * a.ldx, V * (lane + i * group),
+                                    r0 + q < a.M ? N : 0);
+    float mean[R], t[R];
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      mean[q] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        float f[V];
+        unpack(x[q][i], f);
+#pragma unroll
+        for (int j = 0; j < V; ++j) mean[q] += f[j];
+      }
+    }
+    group_sums<WARP, R>(mean, buf[0]);
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      mean[q] *= inv;
+      t[q] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        if (V * (lane + i * group) < N) {
+          float f[V];
+          unpack(x[q][i], f);
+#pragma unroll
+          for (int j = 0; j < V; ++j) t[q] += (f[j] - mean[q]) * (f[j] - mean[q]);
+        }
+      }
+    }
+    group_sums<WARP, R>(t, buf[1]);
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      t[q] = 1.0f / sqrtf(t[q] * inv + a.eps);
+      if (lane == 0 && r0 + q < a.M) {
+        if (a.mean) a.mean[r0 + q] = mean[q];
+        if (a.rstd) a.rstd[r0 + q] = t[q];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = V * (lane + i * group);
+      if (c >= N) break;
+      float g[V], b[V];
+      load_weights<V>(a.gamma, a.w_bf16, c, N, 1.0f, g);
+      load_weights<V>(a.beta, a.w_bf16, c, N, 0.0f, b);
+#pragma unroll
+      for (int q = 0; q < R; ++q) {
+        if (r0 + q >= a.M) break;
+        float f[V];
+        unpack(x[q][i], f);
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[j] = (f[j] - mean[q]) * t[q] * g[j] + b[j];
+        Raw<YT, V> o = pack(f, Raw<YT, V>());
+        *reinterpret_cast<Raw<YT, V>*>(static_cast<YT*>(a.y) + (r0 + q) * a.ldy + c) = o;
+        if (a.amax) {
+          unpack(o, f);
+#pragma unroll
+          for (int j = 0; j < V; ++j) top = max(top, abs_bits(f[j]));
+        }
+      }
+    }
+  }
+  if (a.amax) put_amax(a, top, top_s);
+}
+
+// Rows too long for the registers of a block: three passes over the row.
+template <typename XT, typename YT>
+__global__ void __launch_bounds__(kMaxThreads) norm_long_kernel(const NormArgs a) {
+  __shared__ float buf[2][32];
+  __shared__ uint32_t top_s[32];
+  uint32_t top = 0;
+  for (int64_t r = blockIdx.x; r < a.M; r += gridDim.x) {
+    const XT* x = static_cast<const XT*>(a.x) + r * a.ldx;
+    YT* y = static_cast<YT*>(a.y) + r * a.ldy;
+    float s[1] = {0.0f}, t[1] = {0.0f};
+    for (int64_t c = threadIdx.x; c < a.N; c += kMaxThreads) s[0] += to_f32(x[c]);
+    group_sums<false, 1>(s, buf[0]);
+    const float mean = s[0] / (float)a.N;
+    for (int64_t c = threadIdx.x; c < a.N; c += kMaxThreads) {
+      const float d = to_f32(x[c]) - mean;
+      t[0] += d * d;
+    }
+    group_sums<false, 1>(t, buf[1]);
+    const float rstd = 1.0f / sqrtf(t[0] / (float)a.N + a.eps);
+    for (int64_t c = threadIdx.x; c < a.N; c += kMaxThreads) {
+      float v = (to_f32(x[c]) - mean) * rstd;
+      if (a.gamma) v *= load_as_f32(a.gamma, c, a.w_bf16);
+      if (a.beta) v += load_as_f32(a.beta, c, a.w_bf16);
+      const YT o = from_f32<YT>(v);
+      y[c] = o;
+      top = max(top, abs_bits(to_f32(o)));
+    }
+    if (threadIdx.x == 0) {
+      if (a.mean) a.mean[r] = mean;
+      if (a.rstd) a.rstd[r] = rstd;
+    }
+  }
+  if (a.amax) put_amax(a, top, top_s);
+}
+
+// Grid of `kern` over `work` groups' worth of blocks; the amax pair is zeroed unless one block alone writes it.
+template <typename Kernel>
+cudaError_t run(Kernel kern, const NormArgs& a, int64_t blocks, int threads, cudaStream_t s) {
+  int dev = 0, sms = 0, per_sm = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess && blocks > sms) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, 0);
+  if (e != cudaSuccess) return e;
+  if (blocks > sms && blocks > (int64_t)sms * per_sm) blocks = (int64_t)sms * (per_sm > 0 ? per_sm : 1);
+  if (a.amax && blocks > 1) {
+    e = cudaMemsetAsync(a.amax, 0, 2 * sizeof(float), s);
+    if (e != cudaSuccess) return e;
+  }
+  kern<<<(unsigned)blocks, threads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+int round32(int64_t v) { return (int)((v + 31) / 32 * 32); }
+
+template <typename XT, typename YT>
+cudaError_t launch(const NormArgs& a, cudaStream_t s) {
+  const bool vec = a.N % 8 == 0 && rows16(a.x, a.ldx, sizeof(XT)) && rows16(a.y, a.ldy, sizeof(YT)) &&
+                   rows16(a.gamma, 0, 4) && rows16(a.beta, 0, 4);
+  const int64_t chunks = vec ? a.N / 8 : a.N;
+  const int64_t per_warp_block = kWarpThreads / 32;
+  if (vec) {
+    if (chunks <= 128) {  // a warp holds the row
+      const int64_t blocks = (a.M + 2 * per_warp_block - 1) / (2 * per_warp_block);
+      return chunks <= 32 ? run(norm_kernel<XT, YT, 8, 1, 2, true, kWarpThreads>, a, blocks, kWarpThreads, s)
+                          : run(norm_kernel<XT, YT, 8, 4, 2, true, kWarpThreads>, a, blocks, kWarpThreads, s);
+    }
+    if (chunks <= 1024 && a.M <= 608)  // few rows: all the threads that a row can use
+      return run(norm_kernel<XT, YT, 8, 1, 1, false, 1024>, a, a.M, round32(chunks), s);
+    if (chunks <= 2048)
+      return run(norm_kernel<XT, YT, 8, 4, 2, false, 512>, a, (a.M + 1) / 2, round32((chunks + 3) / 4), s);
+    if (chunks <= 4096) return run(norm_kernel<XT, YT, 8, 4, 1, false, 1024>, a, a.M, round32((chunks + 3) / 4), s);
+  } else {
+    if (chunks <= 512)
+      return run(norm_kernel<XT, YT, 1, 16, 1, true, kWarpThreads>, a, (a.M + per_warp_block - 1) / per_warp_block, kWarpThreads, s);
+    if (chunks <= 8192) return run(norm_kernel<XT, YT, 1, 8, 1, false, 1024>, a, a.M, round32((chunks + 7) / 8), s);
+    if (chunks <= 32768) return run(norm_kernel<XT, YT, 1, 32, 1, false, 1024>, a, a.M, round32((chunks + 31) / 32), s);
+  }
+  return run(norm_long_kernel<XT, YT>, a, a.M, kMaxThreads, s);
 }
 
 }  // namespace
+}  // namespace norm
 
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
-  if (a.amax) {
-    const cudaError_t e = cudaMemsetAsync(a.amax, 0, 2 * sizeof(float), s);
-    if (e != cudaSuccess) return e;
-  }
-  const unsigned grid = (unsigned)a.M;
-  if (a.x_bf16 && a.y_bf16) norm_kernel<bf16, bf16><<<grid, kThreads, 0, s>>>(a);
-  if (a.x_bf16 && !a.y_bf16) norm_kernel<bf16, float><<<grid, kThreads, 0, s>>>(a);
-  if (!a.x_bf16 && a.y_bf16) norm_kernel<float, bf16><<<grid, kThreads, 0, s>>>(a);
-  if (!a.x_bf16 && !a.y_bf16) norm_kernel<float, float><<<grid, kThreads, 0, s>>>(a);
-  return cudaGetLastError();
-}
-
-int64_t norm_grad_workspace(int64_t, int64_t) { return 0; }
-
-cudaError_t launch_norm_grad(const NormGradArgs& a, cudaStream_t s) {
-  if (a.dy_bf16 && a.x_bf16) launch_grad<bf16, bf16>(a, s);
-  if (a.dy_bf16 && !a.x_bf16) launch_grad<bf16, float>(a, s);
-  if (!a.dy_bf16 && a.x_bf16) launch_grad<float, bf16>(a, s);
-  if (!a.dy_bf16 && !a.x_bf16) launch_grad<float, float>(a, s);
-  return cudaGetLastError();
+  if (a.x_bf16) return a.y_bf16 ? norm::launch<layer::bf16, layer::bf16>(a, s) : norm::launch<layer::bf16, float>(a, s);
+  return a.y_bf16 ? norm::launch<float, layer::bf16>(a, s) : norm::launch<float, float>(a, s);
 }
 
 }  // namespace nvfp4
