@@ -14,6 +14,12 @@ namespace nvfp4 {
 namespace norm {
 namespace {
 
+#ifndef NORM_NC
+#define NORM_NC 4
+#define NORM_KB true
+#define NORM_S 3
+#define NORM_KEEP true
+#endif
 constexpr int kMaxThreads = 1024;
 constexpr int kWarpThreads = 256;  // block of the one-warp-per-row kernels
 
@@ -40,7 +46,7 @@ __device__ __forceinline__ void put_amax(const NormArgs& a, uint32_t top, uint32
 // the barriers of the reductions.
 template <typename XT, typename YT, int V, int NC, int R, bool WARP, int THREADS>
 __global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a) {
-  __shared__ float buf[2][R * 32];
+  __shared__ __align__(16) float buf[2][R * 32];
   __shared__ uint32_t top_s[32];
   const int N = (int)a.N;
   const int lane = WARP ? threadIdx.x & 31 : threadIdx.x, group = WARP ? 32 : blockDim.x;
@@ -119,10 +125,102 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a) {
   if (a.amax) put_amax(a, top, top_s);
 }
 
+// The same for 16-byte rows and many of them: S rows of each group on their way in
+// shared memory, packed fp32 arithmetic.  KEEP: gamma and beta stay in registers.
+template <typename XT, typename YT, int NC, int S, bool WARP, bool KEEP, int THREADS>
+__global__ void __launch_bounds__(THREADS) norm_stream_kernel(const NormArgs a) {
+  extern __shared__ uint4 ring[];
+  __shared__ __align__(16) float buf[2][32];
+  __shared__ uint32_t top_s[32];
+  const int N = (int)a.N;
+  const int lane = WARP ? threadIdx.x & 31 : threadIdx.x, group = WARP ? 32 : blockDim.x;
+  const int64_t groups = WARP ? (int64_t)gridDim.x * (THREADS / 32) : gridDim.x;
+  const int64_t first = WARP ? (int64_t)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5) : blockIdx.x;
+  const float inv = 1.0f / (float)N;
+  // this thread's slots: [stage][chunk], blockDim.x apart
+  Raw<XT, 8>* mine = reinterpret_cast<Raw<XT, 8>*>(ring) + threadIdx.x;
+  const uint32_t mine_s = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
+  auto copy_row = [&](int64_t r, int stage) {
+    if (r < a.M) {
+      const XT* row = static_cast<const XT*>(a.x) + r * a.ldx;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int c = 8 * (lane + i * group);
+        copy_chunk<XT>(mine_s + (uint32_t)((stage * NC + i) * (int)blockDim.x * (int)sizeof(Raw<XT, 8>)), row, c, c < N);
+      }
+    }
+    copies_commit();
+  };
+  float2 g[KEEP ? NC : 1][4], b[KEEP ? NC : 1][4];
+  if (KEEP) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      load_weights2(a.gamma, a.w_bf16, 8 * (lane + i * group), N, 1.0f, g[i]);
+      load_weights2(a.beta, a.w_bf16, 8 * (lane + i * group), N, 0.0f, b[i]);
+    }
+  }
+  uint32_t top = 0;
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s) copy_row(first + s * groups, s);
+  int stage = 0;
+  for (int64_t r = first; r < a.M; r += groups) {
+    copy_row(r + (S - 1) * groups, stage == 0 ? S - 1 : stage - 1);  // the slot read in the previous round
+    copies_wait<S - 1>();
+    float2 x[NC][4];
+    float2 sum = splat(0.0f);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      unpack2(mine[(stage * NC + i) * (int)blockDim.x], x[i]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum = add2(sum, x[i][j]);
+    }
+    stage = stage == S - 1 ? 0 : stage + 1;
+    float m[1] = {sum.x + sum.y};
+    group_sums<WARP, 1>(m, buf[0]);
+    const float mean = m[0] * inv;
+    const float2 shift = splat(-mean);
+    sum = splat(0.0f);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      if (8 * (lane + i * group) < N) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x[i][j] = add2(x[i][j], shift);
+          sum = fma2(x[i][j], x[i][j], sum);
+        }
+      }
+    }
+    float t[1] = {sum.x + sum.y};
+    group_sums<WARP, 1>(t, buf[1]);
+    const float rstd = 1.0f / sqrtf(t[0] * inv + a.eps);
+    if (lane == 0) {
+      if (a.mean) a.mean[r] = mean;
+      if (a.rstd) a.rstd[r] = rstd;
+    }
+    YT* y = static_cast<YT*>(a.y) + r * a.ldy;
+    const float2 scale = splat(rstd);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = 8 * (lane + i * group);
+      if (c >= N) break;
+      if (!KEEP) {
+        load_weights2(a.gamma, a.w_bf16, c, N, 1.0f, g[0]);
+        load_weights2(a.beta, a.w_bf16, c, N, 0.0f, b[0]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[i][j] = fma2(mul2(x[i][j], scale), g[KEEP ? i : 0][j], b[KEEP ? i : 0][j]);
+      const Raw<YT, 8> o = pack2(x[i], Raw<YT, 8>());
+      *reinterpret_cast<Raw<YT, 8>*>(y + c) = o;
+      if (a.amax) top = top_of(o, top);
+    }
+  }
+  if (a.amax) put_amax(a, top, top_s);
+}
+
 // Rows too long for the registers of a block: three passes over the row.
 template <typename XT, typename YT>
 __global__ void __launch_bounds__(kMaxThreads) norm_long_kernel(const NormArgs a) {
-  __shared__ float buf[2][32];
+  __shared__ __align__(16) float buf[2][32];
   __shared__ uint32_t top_s[32];
   uint32_t top = 0;
   for (int64_t r = blockIdx.x; r < a.M; r += gridDim.x) {
@@ -156,18 +254,19 @@ __global__ void __launch_bounds__(kMaxThreads) norm_long_kernel(const NormArgs a
 
 // Grid of `kern` over `work` groups' worth of blocks; the amax pair is zeroed unless one block alone writes it.
 template <typename Kernel>
-cudaError_t run(Kernel kern, const NormArgs& a, int64_t blocks, int threads, cudaStream_t s) {
+cudaError_t run(Kernel kern, const NormArgs& a, int64_t blocks, int threads, cudaStream_t s, int smem = 0) {
   int dev = 0, sms = 0, per_sm = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess && blocks > sms) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, 0);
+  if (e == cudaSuccess && smem > 40 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess && blocks > sms) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
   if (e != cudaSuccess) return e;
   if (blocks > sms && blocks > (int64_t)sms * per_sm) blocks = (int64_t)sms * (per_sm > 0 ? per_sm : 1);
   if (a.amax && blocks > 1) {
     e = cudaMemsetAsync(a.amax, 0, 2 * sizeof(float), s);
     if (e != cudaSuccess) return e;
   }
-  kern<<<(unsigned)blocks, threads, 0, s>>>(a);
+  kern<<<(unsigned)blocks, threads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -179,6 +278,20 @@ cudaError_t launch(const NormArgs& a, cudaStream_t s) {
                    rows16(a.gamma, 0, 4) && rows16(a.beta, 0, 4);
   const int64_t chunks = vec ? a.N / 8 : a.N;
   const int64_t per_warp_block = kWarpThreads / 32;
+  if (vec && a.M > 608) {
+    const int slot = 8 * (int)sizeof(XT);  // bytes of a thread's chunk in flight
+    if (chunks <= 128)
+      return chunks <= 32 ? run(norm_stream_kernel<XT, YT, 1, 4, true, true, 256>, a, (a.M + 7) / 8, 256, s, 256 * 4 * slot)
+                          : run(norm_stream_kernel<XT, YT, 4, 3, true, NORM_KEEP, 256>, a, (a.M + 7) / 8, 256, s, 256 * 12 * slot);
+    if (chunks <= 1024) {
+      const int t = round32((chunks + NORM_NC - 1) / NORM_NC);
+      return run(norm_stream_kernel<XT, YT, NORM_NC, NORM_S, false, NORM_KB, 1024 / NORM_NC / 32 * 32>, a, a.M, t, s, t * NORM_NC * NORM_S * slot);
+    }
+    if (chunks <= 4096) {
+      const int t = round32((chunks + 3) / 4);
+      return run(norm_stream_kernel<XT, YT, 4, 2, false, false, 1024>, a, a.M, t, s, t * 8 * slot);
+    }
+  }
   if (vec) {
     if (chunks <= 128) {  // a warp holds the row
       const int64_t blocks = (a.M + 2 * per_warp_block - 1) / (2 * per_warp_block);

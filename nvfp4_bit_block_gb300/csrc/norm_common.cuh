@@ -99,9 +99,88 @@ __device__ __forceinline__ void load_weights(const void* w, int is_bf16, int c, 
   }
 }
 
+// ---- rows streamed through shared memory: a thread copies its own chunks ahead
+// (cp.async) into slots that it alone reads, so that no barrier is needed and a
+// group keeps several rows in flight while it works on one.
+template <typename T>
+__device__ __forceinline__ void copy_chunk(uint32_t dst, const T* row, int c, bool there) {
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 16u * (uint32_t)i),
+                 "l"(there ? row + c + i * (16 / (int)sizeof(T)) : row), "r"(there ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() {  // all but the LEFT latest groups of this thread have landed
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+// 8 values as pairs for the packed fp32 instructions.
+__device__ __forceinline__ void unpack2(const Raw<bf16, 8>& r, float2* f) {
+  f[0] = bf16x2_to_f32x2(r.v.x);
+  f[1] = bf16x2_to_f32x2(r.v.y);
+  f[2] = bf16x2_to_f32x2(r.v.z);
+  f[3] = bf16x2_to_f32x2(r.v.w);
+}
+__device__ __forceinline__ void unpack2(const Raw<float, 8>& r, float2* f) {
+  f[0] = make_float2(r.v[0].x, r.v[0].y);
+  f[1] = make_float2(r.v[0].z, r.v[0].w);
+  f[2] = make_float2(r.v[1].x, r.v[1].y);
+  f[3] = make_float2(r.v[1].z, r.v[1].w);
+}
+__device__ __forceinline__ Raw<bf16, 8> pack2(const float2* f, Raw<bf16, 8>) {
+  Raw<bf16, 8> r;
+  __nv_bfloat162 h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = __float22bfloat162_rn(f[i]);
+  r.v.x = *reinterpret_cast<uint32_t*>(&h[0]);
+  r.v.y = *reinterpret_cast<uint32_t*>(&h[1]);
+  r.v.z = *reinterpret_cast<uint32_t*>(&h[2]);
+  r.v.w = *reinterpret_cast<uint32_t*>(&h[3]);
+  return r;
+}
+__device__ __forceinline__ Raw<float, 8> pack2(const float2* f, Raw<float, 8>) {
+  Raw<float, 8> r;
+  r.v[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+  r.v[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+  return r;
+}
+__device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
+
+// Weights at column c as pairs, as load_weights.
+__device__ __forceinline__ void load_weights2(const void* w, int is_bf16, int c, int N, float none, float2* f) {
+  if (!w || c >= N) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = splat(none);
+  } else if (is_bf16) {
+    unpack2(*reinterpret_cast<const Raw<bf16, 8>*>(static_cast<const bf16*>(w) + c), f);
+  } else {
+    unpack2(*reinterpret_cast<const Raw<float, 8>*>(static_cast<const float*>(w) + c), f);
+  }
+}
+
+// Largest magnitude in 8 outputs, joined to `top` (bits of the value, NaN the largest).
+__device__ __forceinline__ uint32_t top_of(const Raw<bf16, 8>& r, uint32_t top) {
+  uint32_t m;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(r.v.x), "r"(r.v.y));
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(r.v.z));
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(r.v.w));
+  m &= 0x7FFF7FFFu;
+  return max(top, max(m << 16, m & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint32_t top_of(const Raw<float, 8>& r, uint32_t top) {
+  float f[8];
+  unpack(r, f);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) top = max(top, abs_bits(f[j]));
+  return top;
+}
+
 // Sums of K values over the row's group, the same bits in every thread.  For a
-// block, `buf` is K * 32 floats of shared memory; calls alternate between two
-// of them, so that one barrier per call is enough.
+// block, `buf` is K * 32 floats of shared memory, 16-byte aligned; calls alternate
+// between two of them, so that one barrier per call is enough.  The warps' parts
+// are read back four at a time and added in order.
 template <bool WARP, int K>
 __device__ __forceinline__ void group_sums(float (&v)[K], float* buf) {
 #pragma unroll
@@ -114,7 +193,17 @@ __device__ __forceinline__ void group_sums(float (&v)[K], float* buf) {
   }
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < K; ++k) v[k] = warp_sum(lane < warps ? buf[k * 32 + lane] : 0.0f);
+  for (int k = 0; k < K; ++k) v[k] = 0.0f;
+  for (int w = 0; w < warps; w += 4) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const float4 p = *reinterpret_cast<const float4*>(buf + k * 32 + w);
+      v[k] += p.x;
+      if (w + 1 < warps) v[k] += p.y;
+      if (w + 2 < warps) v[k] += p.z;
+      if (w + 3 < warps) v[k] += p.w;
+    }
+  }
 }
 
 inline bool rows16(const void* p, int64_t ld, int size) {
