@@ -5,7 +5,8 @@
 * nvfp4_bit_block_gb300/_build/libnvfp4_layer.so -- the operators around the
   linear layer (the C ABI of include/nvfp4_layer.h and its kernels), a library
   of its own because the quantizer's arithmetic is compiled without fused
-  multiply-adds and theirs with them;
+  multiply-adds and theirs with them; _build/_nvfp4_layer.so is its Python
+  binding (a CPython extension against torch's C++ interface);
 * tests/selftest/_build/libnvfp4_selftest.so -- device self-checks used only
   by the tests (build_selftest); it holds no product entry point.
 
@@ -24,6 +25,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libnvfp4.so")
 LAYER_BUILD = os.path.join(BUILD, "layer")
 LAYER_LIB = os.path.join(BUILD, "libnvfp4_layer.so")
+LAYER_EXT = os.path.join(BUILD, "_nvfp4_layer.so")
 INCLUDE = os.path.join(ROOT, "include")
 SELFTEST_DIR = os.path.join(ROOT, "tests", "selftest")
 SELFTEST_BUILD = os.path.join(SELFTEST_DIR, "_build")
@@ -92,13 +94,44 @@ def _build_lib(sources, build_dir, lib, force, verbose, flags=NVCC_FLAGS):
     return lib
 
 
+def _build_ext(force: bool, verbose: bool) -> tuple:
+    """Compile the layer's binding; returns (object, whether it is new)."""
+    import sysconfig
+
+    from torch.utils.cpp_extension import include_paths
+    os.makedirs(LAYER_BUILD, exist_ok=True)
+    src, o = os.path.join(CSRC, "layer_binding.cpp"), os.path.join(LAYER_BUILD, "layer_binding.o")
+    stale = force or _stale(o, [src] + [h for h in _headers() if h.startswith(INCLUDE)])
+    if stale:
+        cuda = os.path.dirname(os.path.dirname(_nvcc()))
+        inc = [*include_paths(), sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
+        _run([os.environ.get("CXX", "g++"), "-O1", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-w",
+              *[x for i in inc for x in ("-I", i)], "-c", src, "-o", o], verbose)
+    return o, stale
+
+
+def _link_ext(o: str, force: bool, verbose: bool) -> None:
+    from torch.utils.cpp_extension import library_paths
+    if not force and not _stale(LAYER_EXT, [o]):
+        return
+    libs = library_paths()
+    tmp = LAYER_EXT + f".tmp{os.getpid()}"
+    _run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, o, LAYER_LIB, *[f"-L{p}" for p in libs],
+          *[f"-Wl,-rpath,{p}" for p in ["$ORIGIN", *libs]], "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"],
+         verbose)
+    os.replace(tmp, LAYER_EXT)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """The product libraries, side by side; returns the path of libnvfp4.so."""
-    with ThreadPoolExecutor(max_workers=2) as ex:
+    """The product libraries and the layer's binding, side by side; returns the path of libnvfp4.so."""
+    with ThreadPoolExecutor(max_workers=3) as ex:
+        ext = ex.submit(_build_ext, force, verbose)
         main = ex.submit(_build_lib, [os.path.join(CSRC, s) for s in SOURCES], BUILD, LIB, force, verbose)
         layer = ex.submit(_build_lib, [os.path.join(CSRC, s) for s in LAYER_SOURCES], LAYER_BUILD, LAYER_LIB, force,
                           verbose, LAYER_NVCC_FLAGS)
         layer.result()
+        o, fresh = ext.result()
+        _link_ext(o, fresh, verbose)
         return main.result()
 
 
