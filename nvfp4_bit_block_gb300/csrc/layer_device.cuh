@@ -32,49 +32,88 @@ __device__ __forceinline__ float load_as_f32(const void* p, int64_t i, int is_bf
 }
 
 // ---------------------------------------------------------------- activations
-// 1 / (1 + exp(-t)): the exponential overflows to +Inf for t below -88, where
-// the quotient is the 0 that it should be.
-__device__ __forceinline__ float sigmoid(float t) { return __fdividef(1.0f, 1.0f + __expf(-t)); }
+// The hardware's base-2 exponential and reciprocal (about 2 and 1 units in the
+// last place; subnormal results are 0, which is far below what is kept here).
+__device__ __forceinline__ float ex2(float t) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
+  return r;
+}
+__device__ __forceinline__ float rcp(float t) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
+  return r;
+}
 
-constexpr float kGeluC = 0.7978845608028654f;     // sqrt(2 / pi)
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kGeluC = 2.0f * 0.7978845608028654f;  // 2 sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 constexpr float kRsqrt2 = 0.7071067811865476f;
 constexpr float kRsqrt2Pi = 0.3989422804014327f;  // 1 / sqrt(2 pi)
 
-// 0.5 (1 + tanh u) = sigmoid(2u), so tanh GELU is z * sigmoid(2u): one
-// exponential and one division, without the cancellation of 1 + tanh u.
+// 1 / (1 + exp(-t)) of t = s / log2(e): the exponential overflows to Inf far below
+// zero, where the quotient is the 0 that it should be.
+__device__ __forceinline__ float sigmoid_log2(float s) { return rcp(1.0f + ex2(-s)); }
+
+// 0.5 (1 + tanh u) = sigmoid(2u), so tanh GELU is z * sigmoid(2u): one exponential
+// and one reciprocal, without the cancellation of 1 + tanh u.
+__device__ __forceinline__ float gelu_tanh_gate(float z) {
+  return sigmoid_log2(z * fmaf(z * z, kLog2e * kGeluC * kGeluA, kLog2e * kGeluC));
+}
+
+// The Gaussian distribution function and density at z, the latter without its
+// 1 / sqrt(2 pi).  With x = |z| / sqrt 2, erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2),
+// t = 1 / (1 + p x): Abramowitz and Stegun, Handbook of Mathematical Functions,
+// 7.1.26, off by 1.5e-7 at most; exp(-x^2) is the density that the derivative
+// needs as well.  (erff and expf took 554 us for the gradient at 16384 x 20480,
+// this takes the time of the tanh form.)
+__device__ __forceinline__ void gauss(float z, float& cdf, float& density) {
+  const float x = fabsf(z) * kRsqrt2;
+  const float t = rcp(fmaf(0.3275911f, x, 1.0f));
+  density = ex2(-kLog2e * x * x);
+  float q = fmaf(1.061405429f, t, -1.453152027f);
+  q = fmaf(q, t, 1.421413741f);
+  q = fmaf(q, t, -0.284496736f);
+  q = fmaf(q, t, 0.254829592f);
+  q = 0.5f * q * t * density;
+  cdf = z < 0.0f ? q : 1.0f - q;
+}
+
 __device__ __forceinline__ float act_value(float z, int act) {
   switch (act) {
     case NVFP4_ACT_RELU: return z > 0.0f || z != z ? z : 0.0f;
-    case NVFP4_ACT_GELU: return 0.5f * z * (1.0f + erff(z * kRsqrt2));
-    case NVFP4_ACT_GELU_TANH: return z * sigmoid(2.0f * kGeluC * (z + kGeluA * z * z * z));
-    case NVFP4_ACT_SILU: return z * sigmoid(z);
+    case NVFP4_ACT_GELU: {
+      float p, e;
+      gauss(z, p, e);
+      return z * p;
+    }
+    case NVFP4_ACT_GELU_TANH: return z * gelu_tanh_gate(z);
+    case NVFP4_ACT_SILU: return z * sigmoid_log2(z * kLog2e);
     default: return z;
   }
 }
 
-// v limited to [-c, c]; NaN stays NaN.
-__device__ __forceinline__ float clamp_abs(float v, float c) { return v > c ? c : (v < -c ? -c : v); }
+// v limited to [-c, c] (NaN becomes a limit: what it multiplies is NaN then).
+__device__ __forceinline__ float limit(float v, float c) { return fminf(fmaxf(v, -c), c); }
 
 // The derivative; with p = sigmoid(u(z)) that of z p is p + z p (1 - p) u'(z).
-// Beyond the clamps p (or the Gaussian) is 0 or 1 in fp32, so limiting z changes
-// no finite result and keeps 0 * Inf out.
+// Beyond the limits p (or the density) is 0 or 1 to fp32's precision, so that
+// limiting z in the second term changes no finite result and keeps 0 * Inf out.
 __device__ __forceinline__ float act_slope(float z, int act) {
   switch (act) {
     case NVFP4_ACT_RELU: return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
     case NVFP4_ACT_GELU: {
-      const float c = clamp_abs(z, 16.0f);
-      return 0.5f * (1.0f + erff(c * kRsqrt2)) + c * kRsqrt2Pi * __expf(-0.5f * c * c);
+      float p, e;
+      gauss(z, p, e);
+      return fmaf(limit(z, 16.0f) * kRsqrt2Pi, e, p);
     }
     case NVFP4_ACT_GELU_TANH: {
-      const float c = clamp_abs(z, 16.0f), c2 = c * c;
-      const float p = sigmoid(2.0f * kGeluC * (c + kGeluA * c2 * c));
-      return p + c * p * (1.0f - p) * (2.0f * kGeluC * (1.0f + 3.0f * kGeluA * c2));
+      const float p = gelu_tanh_gate(z), c = limit(z, 16.0f);
+      return fmaf(c * fmaf(-p, p, p), fmaf(c * c, 3.0f * kGeluA * kGeluC, kGeluC), p);
     }
     case NVFP4_ACT_SILU: {
-      const float c = clamp_abs(z, 128.0f);
-      const float p = sigmoid(c);
-      return p * (1.0f + c * (1.0f - p));
+      const float p = sigmoid_log2(z * kLog2e);
+      return fmaf(limit(z, 128.0f), fmaf(-p, p, p), p);
     }
     default: return 1.0f;
   }
