@@ -90,10 +90,8 @@ int nvfp4_layernorm_backward(const void* dy_dev, int64_t lddy, int dy_is_bf16, c
     const int st = zero(dgamma_dev, N * 4, s);
     return st ? st : zero(dbeta_dev, N * 4, s);
   }
-  if (dgamma_dev || dbeta_dev) {
-    const int st = check_workspace(workspace_dev, workspace_bytes, nvfp4::norm_grad_workspace(M, N));
-    if (st) return st;
-  }
+  const int st = check_workspace(workspace_dev, workspace_bytes, nvfp4::norm_grad_workspace(M, N));
+  if (st) return st;
   nvfp4::NormGradArgs a;
   a.dy = dy_dev;
   a.x = x_dev;

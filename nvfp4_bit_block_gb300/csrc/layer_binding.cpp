@@ -236,8 +236,7 @@ PyObject* layernorm_backward(PyObject* const* a) {
   Floats f(dev);
   const int64_t ag = dgamma ? f.add(N) : 0, ab = dbeta ? f.add(N) : 0;
   f.make();
-  Workspace ws;
-  if (dgamma || dbeta) ws = Workspace(nvfp4_layernorm_backward_workspace(M, N), "nvfp4_layernorm_backward_workspace", dev);
+  const Workspace ws(nvfp4_layernorm_backward_workspace(M, N), "nvfp4_layernorm_backward_workspace", dev);
   check(nvfp4_layernorm_backward(dm.p, dm.ld, dyb, xm.p, xm.ld, xb, M, N, static_cast<float*>(mp),
                                  static_cast<float*>(sp), gp, wb, rm.p, rm.ld, om.p, om.ld,
                                  dgamma ? f.ptr(ag) : nullptr, dbeta ? f.ptr(ab) : nullptr, ws.p, ws.n, stream_of(dev)),
