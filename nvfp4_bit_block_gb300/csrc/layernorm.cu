@@ -252,21 +252,20 @@ __global__ void __launch_bounds__(kMaxThreads) norm_long_kernel(const NormArgs a
   if (a.amax) put_amax(a, top, top_s);
 }
 
-// Grid of `kern` over `work` groups' worth of blocks; the amax pair is zeroed unless one block alone writes it.
-template <typename Kernel>
-cudaError_t run(Kernel kern, const NormArgs& a, int64_t blocks, int threads, cudaStream_t s, int smem = 0) {
-  int dev = 0, sms = 0, per_sm = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess && smem > 40 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess && blocks > sms) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
+// `blocks` blocks of a kernel, or as many as the GPU holds at once; the amax pair
+// is zeroed unless one block alone writes it.
+template <auto KERN>
+cudaError_t run(const NormArgs& a, int64_t blocks, int threads, cudaStream_t s, int smem = 0) {
+  static BlocksPerSm cache;
+  int sms = 0, per_sm = 0;
+  cudaError_t e = cache.get(KERN, threads, smem, sms, per_sm);
   if (e != cudaSuccess) return e;
-  if (blocks > sms && blocks > (int64_t)sms * per_sm) blocks = (int64_t)sms * (per_sm > 0 ? per_sm : 1);
+  blocks = blocks < (int64_t)sms * per_sm ? blocks : (int64_t)sms * per_sm;
   if (a.amax && blocks > 1) {
     e = cudaMemsetAsync(a.amax, 0, 2 * sizeof(float), s);
     if (e != cudaSuccess) return e;
   }
-  kern<<<(unsigned)blocks, threads, smem, s>>>(a);
+  KERN<<<(unsigned)blocks, threads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -281,35 +280,35 @@ cudaError_t launch(const NormArgs& a, cudaStream_t s) {
   if (vec && a.M > 608) {
     const int slot = 8 * (int)sizeof(XT);  // bytes of a thread's chunk in flight
     if (chunks <= 128)
-      return chunks <= 32 ? run(norm_stream_kernel<XT, YT, 1, 4, true, true, 256>, a, (a.M + 7) / 8, 256, s, 256 * 4 * slot)
-                          : run(norm_stream_kernel<XT, YT, 4, 3, true, NORM_KEEP, 256>, a, (a.M + 7) / 8, 256, s, 256 * 12 * slot);
+      return chunks <= 32 ? run<norm_stream_kernel<XT, YT, 1, 4, true, true, 256>>(a, (a.M + 7) / 8, 256, s, 256 * 4 * slot)
+                          : run<norm_stream_kernel<XT, YT, 4, 3, true, NORM_KEEP, 256>>(a, (a.M + 7) / 8, 256, s, 256 * 12 * slot);
     if (chunks <= 1024) {
       const int t = round32((chunks + NORM_NC - 1) / NORM_NC);
-      return run(norm_stream_kernel<XT, YT, NORM_NC, NORM_S, false, NORM_KB, 1024 / NORM_NC / 32 * 32>, a, a.M, t, s, t * NORM_NC * NORM_S * slot);
+      return run<norm_stream_kernel<XT, YT, NORM_NC, NORM_S, false, NORM_KB, 1024 / NORM_NC / 32 * 32>>(a, a.M, t, s, t * NORM_NC * NORM_S * slot);
     }
     if (chunks <= 4096) {
       const int t = round32((chunks + 3) / 4);
-      return run(norm_stream_kernel<XT, YT, 4, 2, false, false, 1024>, a, a.M, t, s, t * 8 * slot);
+      return run<norm_stream_kernel<XT, YT, 4, 2, false, false, 1024>>(a, a.M, t, s, t * 8 * slot);
     }
   }
   if (vec) {
     if (chunks <= 128) {  // a warp holds the row
       const int64_t blocks = (a.M + 2 * per_warp_block - 1) / (2 * per_warp_block);
-      return chunks <= 32 ? run(norm_kernel<XT, YT, 8, 1, 2, true, kWarpThreads>, a, blocks, kWarpThreads, s)
-                          : run(norm_kernel<XT, YT, 8, 4, 2, true, kWarpThreads>, a, blocks, kWarpThreads, s);
+      return chunks <= 32 ? run<norm_kernel<XT, YT, 8, 1, 2, true, kWarpThreads>>(a, blocks, kWarpThreads, s)
+                          : run<norm_kernel<XT, YT, 8, 4, 2, true, kWarpThreads>>(a, blocks, kWarpThreads, s);
     }
     if (chunks <= 1024 && a.M <= 608)  // few rows: all the threads that a row can use
-      return run(norm_kernel<XT, YT, 8, 1, 1, false, 1024>, a, a.M, round32(chunks), s);
+      return run<norm_kernel<XT, YT, 8, 1, 1, false, 1024>>(a, a.M, round32(chunks), s);
     if (chunks <= 2048)
-      return run(norm_kernel<XT, YT, 8, 4, 2, false, 512>, a, (a.M + 1) / 2, round32((chunks + 3) / 4), s);
-    if (chunks <= 4096) return run(norm_kernel<XT, YT, 8, 4, 1, false, 1024>, a, a.M, round32((chunks + 3) / 4), s);
+      return run<norm_kernel<XT, YT, 8, 4, 2, false, 512>>(a, (a.M + 1) / 2, round32((chunks + 3) / 4), s);
+    if (chunks <= 4096) return run<norm_kernel<XT, YT, 8, 4, 1, false, 1024>>(a, a.M, round32((chunks + 3) / 4), s);
   } else {
     if (chunks <= 512)
-      return run(norm_kernel<XT, YT, 1, 16, 1, true, kWarpThreads>, a, (a.M + per_warp_block - 1) / per_warp_block, kWarpThreads, s);
-    if (chunks <= 8192) return run(norm_kernel<XT, YT, 1, 8, 1, false, 1024>, a, a.M, round32((chunks + 7) / 8), s);
-    if (chunks <= 32768) return run(norm_kernel<XT, YT, 1, 32, 1, false, 1024>, a, a.M, round32((chunks + 31) / 32), s);
+      return run<norm_kernel<XT, YT, 1, 16, 1, true, kWarpThreads>>(a, (a.M + per_warp_block - 1) / per_warp_block, kWarpThreads, s);
+    if (chunks <= 8192) return run<norm_kernel<XT, YT, 1, 8, 1, false, 1024>>(a, a.M, round32((chunks + 7) / 8), s);
+    if (chunks <= 32768) return run<norm_kernel<XT, YT, 1, 32, 1, false, 1024>>(a, a.M, round32((chunks + 31) / 32), s);
   }
-  return run(norm_long_kernel<XT, YT>, a, a.M, kMaxThreads, s);
+  return run<norm_long_kernel<XT, YT>>(a, a.M, kMaxThreads, s);
 }
 
 }  // namespace

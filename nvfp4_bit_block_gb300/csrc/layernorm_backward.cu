@@ -22,64 +22,66 @@ namespace nvfp4 {
 namespace norm {
 namespace {
 
-constexpr int kMaxBlocks = 304;  // two per SM: rows of partial sums in the workspace
+constexpr int kMaxBlocks = 608;          // rows of partial sums in the workspace
+constexpr int64_t kRing = 216 * 1024;    // shared memory for rows on their way
 
 // Barrier of a row's group (its threads are whole warps of one block).
 __device__ __forceinline__ void group_sync(int id, int threads) {
   asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// Two sums over a group of `warps` warps, the same bits in all its threads;
+// K sums (2 or 4) over a group of `warps` warps, the same bits in all its threads;
 // `buf` (16-byte aligned) is the group's, calls alternate between two of them.
-__device__ __forceinline__ void group_sums2(float& a, float& b, float* buf, int warps, int group) {
-  a = warp_sum(a);
-  b = warp_sum(b);
+template <int K>
+__device__ __forceinline__ void group_sums_k(float (&v)[K], float* buf, int warps, int group) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) v[k] = warp_sum(v[k]);
   if (warps == 1) return;
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - group * warps;
   if (lane == 0) {
-    buf[2 * warp] = a;
-    buf[2 * warp + 1] = b;
+#pragma unroll
+    for (int k = 0; k < K; ++k) buf[K * warp + k] = v[k];
   }
   group_sync(1 + group, warps * 32);
-  a = b = 0.0f;
-  for (int w = 0; w < warps; w += 2) {
-    const float4 p = *reinterpret_cast<const float4*>(buf + 2 * w);
-    a += p.x;
-    b += p.y;
-    if (w + 1 < warps) {
-      a += p.z;
-      b += p.w;
+#pragma unroll
+  for (int k = 0; k < K; ++k) v[k] = 0.0f;
+  constexpr int W = 4 / K;  // warps per read
+  for (int w = 0; w < warps; w += W) {
+    const float4 p = *reinterpret_cast<const float4*>(buf + K * w);
+    v[0] += p.x;
+    v[1] += p.y;
+    if constexpr (K == 4) {
+      v[2] += p.z;
+      v[3] += p.w;
+    } else if (w + 1 < warps) {
+      v[0] += p.z;
+      v[1] += p.w;
     }
   }
 }
 
-// A thread's NC chunks of V values of a row as pairs: neighbours for V = 8,
-// values of two chunks for V = 1.
-template <typename T, int V, int NC>
-struct Row {
-  Raw<T, V> raw[NC];
-  __device__ __forceinline__ float2 pair(int p) const {
-    float2 f[4];
-    if constexpr (V == 8) {
-      unpack2(raw[p / 4], f);
-      return f[p % 4];
-    } else {
-      return make_float2(to_f32(raw[2 * p].v[0]), to_f32(raw[2 * p + 1].v[0]));
-    }
-  }
-};
-// A read of shared memory that the compiler does not merge with an earlier one of the same place.
-template <typename R>
-__device__ __forceinline__ R reread(const uint8_t* p) {
-  R r;
-  uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(p));
+// 16-byte pieces of shared memory at a 32-bit address, read anew each time.
+template <typename T>
+__device__ __forceinline__ Raw<T, 8> slot_read(uint32_t at) {
+  Raw<T, 8> r;
 #pragma unroll
-  for (int i = 0; i < (int)sizeof(R) / 16; ++i) {
+  for (int i = 0; i < (int)sizeof(r) / 16; ++i) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at + 16u * i));
     reinterpret_cast<uint4*>(&r)[i] = v;
   }
   return r;
+}
+// Chunks of a thread as pairs: neighbours for V = 8, values of two chunks for V = 1.
+template <typename T, int NC>
+__device__ __forceinline__ void to_pairs(const Raw<T, 8> (&raw)[NC], float2 (&f)[NC * 4]) {
+#pragma unroll
+  for (int i = 0; i < NC; ++i) unpack2(raw[i], f + 4 * i);
+}
+template <typename T, int NC>
+__device__ __forceinline__ void to_pairs(const Raw<T, 1> (&raw)[NC], float2 (&f)[NC / 2]) {
+#pragma unroll
+  for (int i = 0; i < NC / 2; ++i) f[i] = make_float2(to_f32(raw[2 * i].v[0]), to_f32(raw[2 * i + 1].v[0]));
 }
 // Column of element e of a thread.
 template <int V>
@@ -87,41 +89,51 @@ __device__ __forceinline__ int column(int t, int group, int e) {
   return V == 8 ? 8 * (t + (e / 8) * group) + e % 8 : t + e * group;
 }
 
-// S > 0: S rows of each group on their way in shared memory (16-byte rows, V = 8); S = 0: plain loads.
-template <typename DT, typename XT, int V, int NC, int S, int THREADS, int BLOCKS>
+// R neighbouring rows at a time.  S > 0: S times R rows of each group on their way in
+// shared memory (16-byte rows, V = 8); S = 0: plain loads.  REREAD: dy and x are
+// read from shared memory again after the sums instead of kept in registers.
+template <typename DT, typename XT, int V, int NC, int R, int S, bool RES, bool REREAD, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_kernel(const NormGradArgs a, int group_threads) {
-  constexpr int P = NC * V / 2;
+  constexpr int P = NC * V / 2, K = 2 * R;
   extern __shared__ uint4 ring[];
-  __shared__ __align__(16) float buf[2][THREADS / 32 * 4];
+  __shared__ __align__(16) float buf[2][THREADS / 32 * 2 * K];
   const int N = (int)a.N;
   const int warps = group_threads >> 5, group = (int)threadIdx.x / group_threads, ngroups = (int)blockDim.x / group_threads;
   const int t = (int)threadIdx.x - group * group_threads;
-  const int64_t step = (int64_t)gridDim.x * ngroups, first = (int64_t)blockIdx.x * ngroups + group;
+  const int64_t step = (int64_t)gridDim.x * ngroups * R, first = ((int64_t)blockIdx.x * ngroups + group) * R;
   const float inv = 1.0f / (float)N;
-  const DT* dy = static_cast<const DT*>(a.dy);
-  const XT* x = static_cast<const XT*>(a.x);
-  const XT* dres = static_cast<const XT*>(a.dres);
-  // this thread's slots: stage by stage NC chunks of dy, of x and of dres, each blockDim.x apart
-  constexpr int kDy = (int)sizeof(Raw<DT, V>), kX = (int)sizeof(Raw<XT, V>);
-  const int stage_bytes = NC * (int)blockDim.x * (kDy + kX * (dres ? 2 : 1));
-  uint8_t* slots = reinterpret_cast<uint8_t*>(ring);
-  auto slot_dy = [&](int s, int i) { return slots + s * stage_bytes + (i * (int)blockDim.x + (int)threadIdx.x) * kDy; };
-  auto slot_x = [&](int s, int i, int which) {
-    return slots + s * stage_bytes + NC * (int)blockDim.x * (kDy + which * kX) +
-           (i * (int)blockDim.x + (int)threadIdx.x) * kX;
-  };
-  auto smem = [](const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); };
-  auto copy_row = [&](int64_t r, int s) {
+  // this thread's slots: per stage and row NC chunks of dy, of x and of dres, each blockDim.x apart
+  constexpr uint32_t kDy = sizeof(Raw<DT, V>), kX = sizeof(Raw<XT, V>);
+  const uint32_t threads = blockDim.x, at_x = NC * threads * kDy, at_res = at_x + NC * threads * kX;
+  const uint32_t row_bytes = at_x + NC * threads * kX * (RES ? 2 : 1), stage_bytes = R * row_bytes;
+  const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+  const uint32_t my_dy = base + threadIdx.x * kDy, my_x = base + at_x + threadIdx.x * kX;
+  // global positions: the rows being copied, the rows being worked on
+  const DT* dy = static_cast<const DT*>(a.dy) + first * a.lddy + V * t;
+  const XT* x = static_cast<const XT*>(a.x) + first * a.ldx + V * t;
+  const XT* res = RES ? static_cast<const XT*>(a.dres) + first * a.lddres + V * t : nullptr;
+  XT* dx = static_cast<XT*>(a.dx) + first * a.lddx + V * t;
+  int64_t ahead = first;  // row that dy, x and res point at
+  auto copy_rows = [&](uint32_t stage) {
     if constexpr (S > 0) {
-      if (r < a.M) {
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-          const int c = V * (t + i * group_threads);
-          copy_chunk<DT>(smem(slot_dy(s, i)), dy + r * a.lddy, c, c < N);
-          copy_chunk<XT>(smem(slot_x(s, i, 0)), x + r * a.ldx, c, c < N);
-          if (dres) copy_chunk<XT>(smem(slot_x(s, i, 1)), dres + r * a.lddres, c, c < N);
+      for (int q = 0; q < R; ++q) {
+        if (ahead + q < a.M) {
+          const uint32_t at = stage + q * row_bytes;
+#pragma unroll
+          for (int i = 0; i < NC; ++i) {
+            const int off = V * i * group_threads;
+            const bool there = V * t + off < N;
+            copy_chunk<DT>(my_dy + at + i * threads * kDy, dy + q * a.lddy, off, there);
+            copy_chunk<XT>(my_x + at + i * threads * kX, x + q * a.ldx, off, there);
+            if constexpr (RES) copy_chunk<XT>(my_x + (at_res - at_x) + at + i * threads * kX, res + q * a.lddres, off, there);
+          }
         }
       }
+      dy += step * a.lddy;
+      x += step * a.ldx;
+      if constexpr (RES) res += step * a.lddres;
+      ahead += step;
       copies_commit();
     }
   };
@@ -134,80 +146,119 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_kernel(const NormGr
     dg[p] = db[p] = splat(0.0f);
   }
 #pragma unroll
-  for (int s = 0; s < S - 1; ++s) copy_row(first + s * step, s);
-  float mean = first < a.M ? a.mean[first] : 0.0f, rstd = first < a.M ? a.rstd[first] : 0.0f;
-  int stage = 0, parity = 0;
-  float* mine = buf[0] + group * ((warps + 1) & ~1) * 2;
-  for (int64_t r = first; r < a.M; r += step) {
-    Row<DT, V, NC> rd;
-    Row<XT, V, NC> rx, rr;
-    auto read = [&]() {  // dy and x of this row (from its slot, they are read again after the sums: registers)
+  for (int s = 0; s < S - 1; ++s) copy_rows((uint32_t)s * stage_bytes);
+  float mean[R], rstd[R];
+  auto load_stats = [&](int64_t r) {
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        rd.raw[i] = reread<Raw<DT, V>>(slot_dy(stage, i));
-        rx.raw[i] = reread<Raw<XT, V>>(slot_x(stage, i, 0));
+    for (int q = 0; q < R; ++q) {
+      mean[q] = r + q < a.M ? a.mean[r + q] : 0.0f;
+      rstd[q] = r + q < a.M ? a.rstd[r + q] : 0.0f;
+    }
+  };
+  load_stats(first);
+  uint32_t stage = 0;
+  int parity = 0;
+  float* mine = buf[0] + group * (K == 2 ? (warps + 1) & ~1 : warps) * K;
+  for (int64_t r = first; r < a.M; r += step, dx += step * a.lddx) {
+    float2 d[R][P], xh[R][P];
+    Raw<XT, V> raw_r[NC];
+    auto read = [&](int q) {  // row q's dy and x from its slots
+      if constexpr (S > 0) {
+        Raw<DT, V> raw_d[NC];
+        Raw<XT, V> raw_x[NC];
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          raw_d[i] = slot_read<DT>(my_dy + stage + q * row_bytes + i * threads * kDy);
+          raw_x[i] = slot_read<XT>(my_x + stage + q * row_bytes + i * threads * kX);
+        }
+        to_pairs(raw_d, d[q]);
+        to_pairs(raw_x, xh[q]);
       }
     };
     if constexpr (S > 0) {
-      copy_row(r + (S - 1) * step, stage == 0 ? S - 1 : stage - 1);  // the slot read in the previous round
+      copy_rows(stage == 0 ? (S - 1) * stage_bytes : stage - stage_bytes);  // the slots read in the previous round
       copies_wait<S - 1>();
-      read();
-    } else {
+    } else {  // R = 1
+      Raw<DT, V> raw_d[NC];
+      Raw<XT, V> raw_x[NC];
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
-        const int c = V * (t + i * group_threads);
-        rd.raw[i] = load_chunk<DT, V>(dy + r * a.lddy, c, N);
-        rx.raw[i] = load_chunk<XT, V>(x + r * a.ldx, c, N);
-        if (dres) rr.raw[i] = load_chunk<XT, V>(dres + r * a.lddres, c, N);
+        const int off = V * i * group_threads, c = V * t + off;
+        raw_d[i] = load_chunk<DT, V>(dy - V * t, c, N);
+        raw_x[i] = load_chunk<XT, V>(x - V * t, c, N);
+        if constexpr (RES) raw_r[i] = load_chunk<XT, V>(res - V * t, c, N);
       }
+      to_pairs(raw_d, d[0]);
+      to_pairs(raw_x, xh[0]);
+      dy += step * a.lddy;
+      x += step * a.ldx;
+      if constexpr (RES) res += step * a.lddres;
     }
-    const float2 scale = splat(rstd), shift = splat(-mean);
-    const float rs = rstd;
-    if (r + step < a.M) {  // the next row's, long before they are needed
-      mean = a.mean[r + step];
-      rstd = a.rstd[r + step];
-    }
-    float2 s0 = splat(0.0f), s1 = splat(0.0f);
+    float2 scale[R], shift[R];
+    float sums[K];
 #pragma unroll
-    for (int p = 0; p < P; ++p) {  // beyond the row dy is 0, so that nothing is added
-      const float2 d = rd.pair(p), xh = mul2(add2(rx.pair(p), shift), scale), g = mul2(d, gamma[p]);
-      db[p] = add2(db[p], d);
-      dg[p] = fma2(d, xh, dg[p]);
-      s0 = add2(s0, g);
-      s1 = fma2(g, xh, s1);
+    for (int q = 0; q < R; ++q) {
+      scale[q] = splat(rstd[q]);
+      shift[q] = splat(-mean[q]);
     }
-    float m0 = s0.x + s0.y, m1 = s1.x + s1.y;
-    group_sums2(m0, m1, mine + parity * (THREADS / 32 * 4), warps, group);
+    load_stats(r + step);  // the next rows', long before they are needed
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      float2 s0 = splat(0.0f), s1 = splat(0.0f);
+      if constexpr (S > 0) read(q);
+      if (R == 1 || r + q < a.M) {  // slots of a row that is not there hold old values
+#pragma unroll
+        for (int p = 0; p < P; ++p) {  // beyond the row dy is 0, so that nothing is added
+          xh[q][p] = mul2(add2(xh[q][p], shift[q]), scale[q]);
+          db[p] = add2(db[p], d[q][p]);
+          dg[p] = fma2(d[q][p], xh[q][p], dg[p]);
+          d[q][p] = mul2(d[q][p], gamma[p]);
+          s0 = add2(s0, d[q][p]);
+          s1 = fma2(d[q][p], xh[q][p], s1);
+        }
+      }
+      sums[2 * q] = s0.x + s0.y;
+      sums[2 * q + 1] = s1.x + s1.y;
+    }
+    group_sums_k<K>(sums, mine + parity * (THREADS / 32 * 2 * K), warps, group);
     parity ^= 1;
-    const float2 k1 = splat(-m1 * inv), k0 = splat(-m0 * inv * rs), sc = splat(rs);
-    XT* dx = static_cast<XT*>(a.dx) + r * a.lddx;
-    if constexpr (S > 0) {
-      read();
-      if (dres) {
 #pragma unroll
-        for (int i = 0; i < NC; ++i) rr.raw[i] = *reinterpret_cast<Raw<XT, V>*>(slot_x(stage, i, 1));
+    for (int q = 0; q < R; ++q) {
+      if (R > 1 && r + q >= a.M) break;
+      if constexpr (S > 0 && REREAD) {
+        read(q);
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          xh[q][p] = mul2(add2(xh[q][p], shift[q]), scale[q]);
+          d[q][p] = mul2(d[q][p], gamma[p]);
+        }
       }
-      stage = stage == S - 1 ? 0 : stage + 1;
+      const float2 k0 = splat(-sums[2 * q] * inv * scale[q].x), k1 = splat(-sums[2 * q + 1] * inv);
+#pragma unroll
+      for (int p = 0; p < P; ++p) d[q][p] = fma2(fma2(xh[q][p], k1, d[q][p]), scale[q], k0);
+      if constexpr (RES) {
+        if constexpr (S > 0) {
+#pragma unroll
+          for (int i = 0; i < NC; ++i)
+            raw_r[i] = slot_read<XT>(my_x + (at_res - at_x) + stage + q * row_bytes + i * threads * kX);
+        }
+        to_pairs(raw_r, xh[q]);
+#pragma unroll
+        for (int p = 0; p < P; ++p) d[q][p] = add2(d[q][p], xh[q][p]);
+      }
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int off = V * i * group_threads;
+        if (V * t + off < N) {
+          XT* o = dx + q * a.lddx + off;
+          if constexpr (V == 8)
+            *reinterpret_cast<Raw<XT, 8>*>(o) = pack2(d[q] + 4 * i, Raw<XT, 8>());
+          else
+            *o = from_f32<XT>(i % 2 ? d[q][i / 2].y : d[q][i / 2].x);
+        }
+      }
     }
-#pragma unroll
-    for (int i = 0; i < (V == 8 ? NC : NC / 2); ++i) {
-      constexpr int Q = V == 8 ? 4 : 1;  // pairs stored together
-      float2 o[Q];
-#pragma unroll
-      for (int j = 0; j < Q; ++j) {
-        const int p = i * Q + j;
-        const float2 xh = mul2(add2(rx.pair(p), shift), scale);
-        o[j] = fma2(fma2(xh, k1, mul2(rd.pair(p), gamma[p])), sc, k0);
-        if (dres) o[j] = add2(o[j], rr.pair(p));
-      }
-      const int c = column<V>(t, group_threads, 2 * i * Q);
-      if constexpr (V == 8) {
-        if (c < N) *reinterpret_cast<Raw<XT, 8>*>(dx + c) = pack2(o, Raw<XT, 8>());
-      } else {
-        if (c < N) dx[c] = from_f32<XT>(o[0].x);
-        if (c + group_threads < N) dx[c + group_threads] = from_f32<XT>(o[0].y);
-      }
-    }
+    if (S > 0) stage = stage == (S - 1) * stage_bytes ? 0 : stage + stage_bytes;
   }
   if (!a.dgamma && !a.dbeta) return;
   // one row of column sums per block; alone it is the result
@@ -308,22 +359,23 @@ cudaError_t join(const NormGradArgs& a, int64_t parts, cudaStream_t s) {
   return colsum::launch_join<2>(a.ws, (int)parts, a.N, a.dgamma, a.dbeta, s);
 }
 
-template <typename DT, typename XT, int V, int NC, int S, int THREADS, int BLOCKS>
+template <typename DT, typename XT, int V, int NC, int R, int S, bool REREAD, int THREADS, int BLOCKS>
 cudaError_t run(const NormGradArgs& a, cudaStream_t s) {
-  auto kern = norm_grad_kernel<DT, XT, V, NC, S, THREADS, BLOCKS>;
+  auto kern = a.dres ? norm_grad_kernel<DT, XT, V, NC, R, S, true, REREAD, THREADS, BLOCKS>
+                     : norm_grad_kernel<DT, XT, V, NC, R, S, false, REREAD, THREADS, BLOCKS>;
+  static BlocksPerSm cache[2];
   const int group = round32((a.N + V * NC - 1) / (V * NC));
-  const int groups = (int)std::max<int64_t>(1, std::min<int64_t>(THREADS / group, (a.M + kMaxBlocks / 2 - 1) / (kMaxBlocks / 2)));
+  // groups of a block: as many as fit, fewer where that leaves SMs without a block
+  const int64_t rows_of_all = (int64_t)(kMaxBlocks / 4) * R;
+  const int groups = (int)std::max<int64_t>(1, std::min<int64_t>(THREADS / group, (a.M + rows_of_all - 1) / rows_of_all));
   const int threads = group * groups;
-  int smem = S * NC * threads * (int)(sizeof(Raw<DT, V>) + sizeof(Raw<XT, V>) * (a.dres ? 2 : 1));
+  int smem = R * S * NC * threads * (int)(sizeof(Raw<DT, V>) + sizeof(Raw<XT, V>) * (a.dres ? 2 : 1));
   if (groups > 1) smem = std::max(smem, (int)(8 * a.N));
-  int dev = 0, sms = 0, per_sm = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess && smem > 40 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
+  int sms = 0, per_sm = 0;
+  const cudaError_t e = cache[a.dres ? 1 : 0].get(kern, threads, smem, sms, per_sm);
   if (e != cudaSuccess) return e;
-  const int64_t blocks = std::min<int64_t>(std::min<int64_t>((a.M + groups - 1) / groups, kMaxBlocks),
-                                           (int64_t)sms * std::max(per_sm, 1));
+  const int64_t rows = (int64_t)groups * R;
+  const int64_t blocks = std::min<int64_t>(std::min<int64_t>((a.M + rows - 1) / rows, kMaxBlocks), (int64_t)sms * per_sm);
   kern<<<(unsigned)blocks, threads, smem, s>>>(a, group);
   return join(a, blocks, s);
 }
@@ -343,13 +395,18 @@ cudaError_t launch(const NormGradArgs& a, cudaStream_t s) {
   const bool vec = a.N % 8 == 0 && rows16(a.dy, a.lddy, sizeof(DT)) && rows16(a.x, a.ldx, sizeof(XT)) &&
                    rows16(a.dx, a.lddx, sizeof(XT)) && rows16(a.dres, a.lddres, sizeof(XT)) && rows16(a.gamma, 0, 4);
   if (vec) {
-    constexpr int S = sizeof(XT) == 2 ? 3 : 2;
-    if (a.N <= 5120) return run<DT, XT, 8, 2, S, 320, 2>(a, s);
-    if (a.N <= 10240) return run<DT, XT, 8, 2, S, 640, 1>(a, s);
+    const int64_t row = a.N * (int64_t)(sizeof(DT) + sizeof(XT) * (a.dres ? 2 : 1));
+    if (a.N <= 5120) {
+      // two rows at a time where six (or four) fit shared memory: half the barriers and loop overhead per row
+      if (6 * row <= kRing) return run<DT, XT, 8, 2, 2, 3, false, 320, 1>(a, s);
+      if (4 * row <= kRing) return run<DT, XT, 8, 2, 2, 2, false, 320, 1>(a, s);
+      return run<DT, XT, 8, 2, 1, 2, true, 320, 2>(a, s);
+    }
+    if (a.N <= 10240) return run<DT, XT, 8, 2, 1, 2, true, 640, 1>(a, s);
     return run_long<DT, XT, 8>(a, s);
   }
-  if (a.N <= 2560) return run<DT, XT, 1, 8, 0, 320, 2>(a, s);
-  if (a.N <= 5120) return run<DT, XT, 1, 8, 0, 640, 1>(a, s);
+  if (a.N <= 2560) return run<DT, XT, 1, 8, 1, 0, false, 320, 2>(a, s);
+  if (a.N <= 5120) return run<DT, XT, 1, 8, 1, 0, false, 640, 1>(a, s);
   return run_long<DT, XT, 1>(a, s);
 }
 

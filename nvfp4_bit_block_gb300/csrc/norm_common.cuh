@@ -7,6 +7,8 @@
 // neighbouring threads touch neighbouring memory.
 #pragma once
 
+#include <atomic>
+
 #include "layer_device.cuh"
 #include "nvfp4_device.cuh"
 
@@ -80,10 +82,8 @@ __device__ __forceinline__ Raw<T, 1> pack(const float* f, Raw<T, 1>) {
 template <typename T, int V>
 __device__ __forceinline__ Raw<T, V> load_chunk(const T* row, int c, int N) {
   if (c < N) return *reinterpret_cast<const Raw<T, V>*>(row + c);
-  Raw<T, V> z;
-  float zero[V] = {};
-  z = pack(zero, z);
-  return z;
+  const float zero[V] = {};
+  return pack(zero, Raw<T, V>());
 }
 
 // V weights at column c as fp32 (`one` where there are none); 16-byte aligned when V = 8.
@@ -205,6 +205,38 @@ __device__ __forceinline__ void group_sums(float (&v)[K], float* buf) {
     }
   }
 }
+
+// Blocks of a kernel that an SM holds, asked for once per (device, threads, shared
+// memory) and kept while the same are asked for again; opts the kernel in to the
+// shared memory that it needs.
+class BlocksPerSm {
+ public:
+  template <typename Kernel>
+  cudaError_t get(Kernel kern, int threads, int smem, int& sms, int& per_sm) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    // key: device (8 bits), threads / 32 (8), smem / 16 (16); value: SMs (16), blocks (16)
+    const uint64_t key = (uint64_t)(dev & 255) << 24 | (uint64_t)(threads / 32) << 16 | (uint64_t)((smem + 15) / 16);
+    const uint64_t seen = last_.load(std::memory_order_relaxed);
+    if (seen >> 32 == key && seen != 0) {
+      sms = (int)(seen >> 16 & 0xFFFF);
+      per_sm = (int)(seen & 0xFFFF);
+      return cudaSuccess;
+    }
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess && smem > 40 * 1024)
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
+    if (e != cudaSuccess) return e;
+    if (per_sm < 1) return cudaErrorInvalidConfiguration;
+    last_.store(key << 32 | (uint64_t)sms << 16 | (uint64_t)per_sm, std::memory_order_relaxed);
+    return cudaSuccess;
+  }
+
+ private:
+  std::atomic<uint64_t> last_{0};
+};
 
 inline bool rows16(const void* p, int64_t ld, int size) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * size % 16 == 0;
