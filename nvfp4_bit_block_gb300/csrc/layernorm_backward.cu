@@ -23,41 +23,51 @@ namespace norm {
 namespace {
 
 constexpr int kMaxBlocks = 608;          // rows of partial sums in the workspace
-constexpr int64_t kRing = 216 * 1024;    // shared memory for rows on their way
+constexpr int64_t kRing = 220 * 1024;    // shared memory for rows on their way
 
 // Barrier of a row's group (its threads are whole warps of one block).
 __device__ __forceinline__ void group_sync(int id, int threads) {
   asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// K sums (2 or 4) over a group of `warps` warps, the same bits in all its threads;
-// `buf` (16-byte aligned) is the group's, calls alternate between two of them.
+// K sums (2, 4 or 8) over a warp at once: in each of the first exchanges a lane
+// keeps half of its sums and gives away the other half, so that K sums take K - 1
+// exchanges and a few more instead of 5 K.  Lane l ends with sum l / (32 / K).
 template <int K>
-__device__ __forceinline__ void group_sums_k(float (&v)[K], float* buf, int warps, int group) {
+__device__ __forceinline__ float warp_sums(float (&v)[K]) {
+  const int lane = threadIdx.x & 31;
+  int o = 16;
 #pragma unroll
-  for (int k = 0; k < K; ++k) v[k] = warp_sum(v[k]);
-  if (warps == 1) return;
-  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - group * warps;
-  if (lane == 0) {
+  for (int n = K / 2; n > 0; n >>= 1, o >>= 1) {
+    const bool high = lane & o;
 #pragma unroll
-    for (int k = 0; k < K; ++k) buf[K * warp + k] = v[k];
-  }
-  group_sync(1 + group, warps * 32);
-#pragma unroll
-  for (int k = 0; k < K; ++k) v[k] = 0.0f;
-  constexpr int W = 4 / K;  // warps per read
-  for (int w = 0; w < warps; w += W) {
-    const float4 p = *reinterpret_cast<const float4*>(buf + K * w);
-    v[0] += p.x;
-    v[1] += p.y;
-    if constexpr (K == 4) {
-      v[2] += p.z;
-      v[3] += p.w;
-    } else if (w + 1 < warps) {
-      v[0] += p.z;
-      v[1] += p.w;
+    for (int k = 0; k < n; ++k) {
+      const float give = high ? v[k] : v[k + n], keep = high ? v[k + n] : v[k];
+      v[k] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
     }
   }
+  for (; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
+  return v[0];
+}
+
+// K sums over a group of `warps` warps, the same bits in all its threads; `buf` is
+// the group's, calls alternate between two of them.
+template <int K>
+__device__ __forceinline__ void group_sums_k(float (&v)[K], float* buf, int warps, int group) {
+  constexpr int L = 32 / K;  // lanes that share a sum
+  const int lane = threadIdx.x & 31, k = lane / L, l = lane % L;
+  float t = warp_sums<K>(v);
+  if (warps > 1) {
+    if (l == 0) buf[K * ((int)(threadIdx.x >> 5) - group * warps) + k] = t;
+    group_sync(1 + group, warps * 32);
+    t = 0.0f;
+#pragma unroll 1
+    for (int w = l; w < warps; w += L) t += buf[K * w + k];
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+  }
+#pragma unroll
+  for (int q = 0; q < K; ++q) v[q] = __shfl_sync(0xFFFFFFFFu, t, q * L);
 }
 
 // 16-byte pieces of shared memory at a 32-bit address, read anew each time.
@@ -89,14 +99,15 @@ __device__ __forceinline__ int column(int t, int group, int e) {
   return V == 8 ? 8 * (t + (e / 8) * group) + e % 8 : t + e * group;
 }
 
-// R neighbouring rows at a time.  S > 0: S times R rows of each group on their way in
-// shared memory (16-byte rows, V = 8); S = 0: plain loads.  REREAD: dy and x are
-// read from shared memory again after the sums instead of kept in registers.
-template <typename DT, typename XT, int V, int NC, int R, int S, bool RES, bool REREAD, int THREADS, int BLOCKS>
+// R neighbouring rows at a time, which share a barrier, the sums' exchanges and the
+// loop's overhead.  S > 0: S times R rows of each group in shared memory or on
+// their way there (16-byte rows, V = 8), where dy and x are read again after the
+// sums instead of being kept in registers; S = 0: plain loads, one row.
+template <typename DT, typename XT, int V, int NC, int R, int S, bool RES, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_kernel(const NormGradArgs a, int group_threads) {
-  constexpr int P = NC * V / 2, K = 2 * R;
+  constexpr int P = NC * V / 2, K = R == 3 ? 8 : 2 * R;  // sums of a round, a power of two
   extern __shared__ uint4 ring[];
-  __shared__ __align__(16) float buf[2][THREADS / 32 * 2 * K];
+  __shared__ float buf[2][THREADS / 32 * K];
   const int N = (int)a.N;
   const int warps = group_threads >> 5, group = (int)threadIdx.x / group_threads, ngroups = (int)blockDim.x / group_threads;
   const int t = (int)threadIdx.x - group * group_threads;
@@ -158,7 +169,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_kernel(const NormGr
   load_stats(first);
   uint32_t stage = 0;
   int parity = 0;
-  float* mine = buf[0] + group * (K == 2 ? (warps + 1) & ~1 : warps) * K;
+  float* mine = buf[0] + group * warps * K;
   for (int64_t r = first; r < a.M; r += step, dx += step * a.lddx) {
     float2 d[R][P], xh[R][P];
     Raw<XT, V> raw_r[NC];
@@ -220,12 +231,14 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_kernel(const NormGr
       sums[2 * q] = s0.x + s0.y;
       sums[2 * q + 1] = s1.x + s1.y;
     }
-    group_sums_k<K>(sums, mine + parity * (THREADS / 32 * 2 * K), warps, group);
+#pragma unroll
+    for (int k = 2 * R; k < K; ++k) sums[k] = 0.0f;
+    group_sums_k<K>(sums, mine + parity * (THREADS / 32 * K), warps, group);
     parity ^= 1;
 #pragma unroll
     for (int q = 0; q < R; ++q) {
       if (R > 1 && r + q >= a.M) break;
-      if constexpr (S > 0 && REREAD) {
+      if constexpr (S > 0) {
         read(q);
 #pragma unroll
         for (int p = 0; p < P; ++p) {
@@ -359,10 +372,10 @@ cudaError_t join(const NormGradArgs& a, int64_t parts, cudaStream_t s) {
   return colsum::launch_join<2>(a.ws, (int)parts, a.N, a.dgamma, a.dbeta, s);
 }
 
-template <typename DT, typename XT, int V, int NC, int R, int S, bool REREAD, int THREADS, int BLOCKS>
+template <typename DT, typename XT, int V, int NC, int R, int S, int THREADS, int BLOCKS>
 cudaError_t run(const NormGradArgs& a, cudaStream_t s) {
-  auto kern = a.dres ? norm_grad_kernel<DT, XT, V, NC, R, S, true, REREAD, THREADS, BLOCKS>
-                     : norm_grad_kernel<DT, XT, V, NC, R, S, false, REREAD, THREADS, BLOCKS>;
+  auto kern = a.dres ? norm_grad_kernel<DT, XT, V, NC, R, S, true, THREADS, BLOCKS>
+                     : norm_grad_kernel<DT, XT, V, NC, R, S, false, THREADS, BLOCKS>;
   static BlocksPerSm cache[2];
   const int group = round32((a.N + V * NC - 1) / (V * NC));
   // groups of a block: as many as fit, fewer where that leaves SMs without a block
@@ -395,18 +408,22 @@ cudaError_t launch(const NormGradArgs& a, cudaStream_t s) {
   const bool vec = a.N % 8 == 0 && rows16(a.dy, a.lddy, sizeof(DT)) && rows16(a.x, a.ldx, sizeof(XT)) &&
                    rows16(a.dx, a.lddx, sizeof(XT)) && rows16(a.dres, a.lddres, sizeof(XT)) && rows16(a.gamma, 0, 4);
   if (vec) {
-    const int64_t row = a.N * (int64_t)(sizeof(DT) + sizeof(XT) * (a.dres ? 2 : 1));
+    const int64_t bytes = sizeof(DT) + sizeof(XT) * (a.dres ? 2 : 1);  // of a value of the row
+    const int64_t group = round32((a.N + 15) / 16);
     if (a.N <= 5120) {
-      // two rows at a time where six (or four) fit shared memory: half the barriers and loop overhead per row
-      if (6 * row <= kRing) return run<DT, XT, 8, 2, 2, 3, false, 320, 1>(a, s);
-      if (4 * row <= kRing) return run<DT, XT, 8, 2, 2, 2, false, 320, 1>(a, s);
-      return run<DT, XT, 8, 2, 1, 2, true, 320, 2>(a, s);
+      const int64_t row = 320 / group * group * 16 * bytes;  // a row of each group of a block
+      // As many rows at a time as two sets of them fit shared memory: the loop's overhead is shared (16384 x 5120
+      // bf16 with residual: one row 160 us, two 117, three 108; without it, four rows 89 us, two 103).
+      if (8 * row <= kRing) return run<DT, XT, 8, 2, 4, 2, 320, 1>(a, s);
+      if (6 * row <= kRing) return run<DT, XT, 8, 2, 3, 2, 320, 1>(a, s);
+      if (4 * row <= kRing) return run<DT, XT, 8, 2, 2, 2, 320, 1>(a, s);
+      return run<DT, XT, 8, 2, 1, 3, 320, 1>(a, s);
     }
-    if (a.N <= 10240) return run<DT, XT, 8, 2, 1, 2, true, 640, 1>(a, s);
+    if (a.N <= 10240 && 2 * group * 16 * bytes <= kRing) return run<DT, XT, 8, 2, 1, 2, 640, 1>(a, s);
     return run_long<DT, XT, 8>(a, s);
   }
-  if (a.N <= 2560) return run<DT, XT, 1, 8, 1, 0, false, 320, 2>(a, s);
-  if (a.N <= 5120) return run<DT, XT, 1, 8, 1, 0, false, 640, 1>(a, s);
+  if (a.N <= 2560) return run<DT, XT, 1, 8, 1, 0, 320, 2>(a, s);
+  if (a.N <= 5120) return run<DT, XT, 1, 8, 1, 0, 640, 1>(a, s);
   return run_long<DT, XT, 1>(a, s);
 }
 
