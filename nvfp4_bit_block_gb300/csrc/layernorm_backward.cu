@@ -149,12 +149,17 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_kernel(const NormGr
     }
   };
   float2 gamma[P], dg[P], db[P];
+  if constexpr (V == 8) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) load_weights2(a.gamma, a.w_bf16, 8 * (t + i * group_threads), N, 1.0f, gamma + 4 * i);
+  }
 #pragma unroll
   for (int p = 0; p < P; ++p) {
+    dg[p] = db[p] = splat(0.0f);
+    if (V == 8) continue;
     const int c0 = column<V>(t, group_threads, 2 * p), c1 = column<V>(t, group_threads, 2 * p + 1);
     gamma[p].x = a.gamma && c0 < N ? load_as_f32(a.gamma, c0, a.w_bf16) : 1.0f;
     gamma[p].y = a.gamma && c1 < N ? load_as_f32(a.gamma, c1, a.w_bf16) : 1.0f;
-    dg[p] = db[p] = splat(0.0f);
   }
 #pragma unroll
   for (int s = 0; s < S - 1; ++s) copy_rows((uint32_t)s * stage_bytes);
@@ -379,7 +384,7 @@ cudaError_t run(const NormGradArgs& a, cudaStream_t s) {
   static BlocksPerSm cache[2];
   const int group = round32((a.N + V * NC - 1) / (V * NC));
   // groups of a block: as many as fit, fewer where that leaves SMs without a block
-  const int64_t rows_of_all = (int64_t)(kMaxBlocks / 4) * R;
+  const int64_t rows_of_all = (int64_t)152 * R;
   const int groups = (int)std::max<int64_t>(1, std::min<int64_t>(THREADS / group, (a.M + rows_of_all - 1) / rows_of_all));
   const int threads = group * groups;
   int smem = R * S * NC * threads * (int)(sizeof(Raw<DT, V>) + sizeof(Raw<XT, V>) * (a.dres ? 2 : 1));
@@ -414,9 +419,11 @@ cudaError_t launch(const NormGradArgs& a, cudaStream_t s) {
       const int64_t row = 320 / group * group * 16 * bytes;  // a row of each group of a block
       // As many rows at a time as two sets of them fit shared memory: the loop's overhead is shared (16384 x 5120
       // bf16 with residual: one row 160 us, two 117, three 108; without it, four rows 89 us, two 103).
-      if (8 * row <= kRing) return run<DT, XT, 8, 2, 4, 2, 320, 1>(a, s);
-      if (6 * row <= kRing) return run<DT, XT, 8, 2, 3, 2, 320, 1>(a, s);
-      if (4 * row <= kRing) return run<DT, XT, 8, 2, 2, 2, 320, 1>(a, s);
+      // With few rows one at a time, so that they spread over the SMs.
+      const bool many = a.M >= 8 * 152;
+      if (many && 8 * row <= kRing) return run<DT, XT, 8, 2, 4, 2, 320, 1>(a, s);
+      if (many && 6 * row <= kRing) return run<DT, XT, 8, 2, 3, 2, 320, 1>(a, s);
+      if (many && 4 * row <= kRing) return run<DT, XT, 8, 2, 2, 2, 320, 1>(a, s);
       return run<DT, XT, 8, 2, 1, 3, 320, 1>(a, s);
     }
     if (a.N <= 10240 && 2 * group * 16 * bytes <= kRing) return run<DT, XT, 8, 2, 1, 2, 640, 1>(a, s);
