@@ -1,13 +1,17 @@
-// linear_split.cu -- nvfp4_linear for few tokens: K split over a cluster.
+// linear_split.cu -- nvfp4_linear for few tokens: the weight streamed once, K
+// split over the SMs.
 //
-// d = act(alpha_a alpha_b A B^T + bias) + residual where the product is too
-// small to fill the GPU with whole output tiles and the weight's bytes (9/16
-// per value) are what it costs.  The weight's rows are the MMA's 128 lanes and
-// the tokens its BN columns (16 to 128), so that a tile of the weight is
-// multiplied once by all tokens.  A cluster of S blocks shares one output tile:
-// block r sums its part of K in TMEM, the partial tiles meet in shared memory,
-// and each block joins 128 / S features of all S parts (in rank order, so that
-// the sum's order is fixed), applies the epilogue and stores.
+// d = act(alpha_a alpha_b A B^T + bias) + residual where there are too few whole
+// output tiles to fill the GPU and the weight's bytes (9/16 per value) are what
+// it costs.  The weight's rows are the MMA's 128 lanes and the tokens its BN
+// columns (16 to 128), so that a tile of the weight is read once for all tokens.
+// The steps of K (256 values) of all output tiles form one row of work that is cut
+// into equal pieces, one per SM: every SM streams the same number of bytes,
+// without a pause at the tiles' borders, with a ring of stages as deep as shared
+// memory holds (200 KB on its way per SM).  A piece leaves the sums of each tile
+// that it touches (usually two) in the workspace, and a second, small kernel adds
+// the pieces of a tile in order and applies the epilogue; it is launched early
+// and waits for the first.
 #include <algorithm>
 
 #include "linear_launch.h"
@@ -17,26 +21,177 @@ namespace nvfp4 {
 namespace lin {
 namespace {
 
-constexpr int kThreads = 192;  // warps 0-3: epilogue (TMEM lane quarters), 4: loads, 5: MMA
+constexpr int kThreads = 192;  // warps 0-3: sums out of TMEM (its lane quarters), 4: loads, 5: MMA
 
 template <int BN>
 struct Cfg {
-  static constexpr int kStageBytes = kLaneTile + BN * kBK / 2 + 2 * kSfStage;  // 22 to 36 KB
-  static constexpr int kStages = BN == 16 ? 5 : (BN == 32 ? 4 : 3);            // two blocks per SM
+  static constexpr int kColTile = BN * kBK / 2;
+  static constexpr int kSfAt = kLaneTile + kColTile;
+  static constexpr int kStageBytes = kSfAt + 2 * kSfStage;  // 22 to 36 KB
+  static constexpr int kStages = BN == 16 ? 10 : (BN == 32 ? 9 : (BN == 64 ? 8 : 6));
+  static constexpr int kBars = 2 * kStages + 5;
   static constexpr int kSmem = kStages * kStageBytes + 256 /* barriers */ + 1024 /* alignment */;
   static constexpr uint32_t kSfCols = 32;  // TMEM columns of one stage's scales
-  static constexpr uint32_t kTmemCols = 256;
-  static_assert(BN + kStages * kSfCols <= kTmemCols, "TMEM columns (two blocks share 512)");
-  static_assert(BN * kLaneRows * 4 <= kStages * kStageBytes, "the partial tile takes the stages' place");
-  static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two blocks per SM");
+  static constexpr uint32_t kTmemCols = 512;
+  static_assert(2 * BN + kStages * kSfCols <= kTmemCols, "TMEM columns");
+  static_assert(8 * (kBars + 2) <= 256 && kSmem <= 232448, "shared memory");
 };
 
-__device__ __forceinline__ float ld_rank(uint32_t saddr, uint32_t rank) {
-  uint32_t a;
-  float v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a));
-  return v;
+// The work in steps of K: `steps` per output tile, `tiles` of them, cut into `pieces`.
+struct Cut {
+  int64_t tiles, tiles_f;  // output tiles; of them per token tile
+  int steps, pieces, most;  // most: tiles that a piece touches at most
+  __host__ __device__ int64_t begin(int64_t piece) const { return tiles * steps * piece / pieces; }
+  __host__ __device__ int64_t piece_of(int64_t unit) const {  // the piece that holds this step
+    int64_t p = unit * pieces / (tiles * steps);
+    while (begin(p + 1) <= unit) ++p;
+    return p;
+  }
+};
+
+template <int BN>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_split_kernel(const LinearArgs a, const __grid_constant__ CUtensorMap wmap,
+                        const __grid_constant__ CUtensorMap xmap, const Cut cut) {
+  using C = Cfg<BN>;
+  extern __shared__ uint8_t raw[];
+  // 1024-byte alignment for the 128-byte swizzle
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStageBytes);
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * C::kStages;
+  const uint32_t accf0 = empty0 + 8 * C::kStages, acce0 = accf0 + 16, drain = accf0 + 32;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
+  volatile int* stop = reinterpret_cast<int*>(bars + C::kBars + 1);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Steps K(a.K);
+  const int64_t u0 = cut.begin(blockIdx.x), u1 = cut.begin((int64_t)blockIdx.x + 1);
+
+  if (tid == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      tma::mbar_init(full0 + 8 * s, 1);
+      tma::mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      tma::mbar_init(accf0 + 8 * b, 1);
+      tma::mbar_init(acce0 + 8 * b, 4);
+    }
+    tma::mbar_init(drain, 1);
+    *stop = 0;
+    tma::fence_barrier_init();
+    if (blockIdx.x == 0 && a.amax) a.amax[0] = a.amax[1] = 0.0f;  // the second kernel joins its maxima to it
+  }
+  if (warp == 5) {
+    tc5::alloc(smem_u32(tmem_slot), C::kTmemCols);
+    tc5::relinquish_alloc_permit();
+  }
+  tc5::fence_before_thread_sync();
+  __syncthreads();
+  tc5::fence_after_thread_sync();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 4) {
+    if (lane == 0) {
+      const int64_t sf_row = (a.K + 63) / 64 * kSfBlock;  // scale bytes of a 128-row band
+      Ring<C::kStages> r;
+      int64_t tile = u0 / K.n, u = u0;
+      int kb = (int)(u0 - tile * K.n);
+      for (; u < u1; ++u, r.next()) {
+        if (u - u0 >= C::kStages && !tma::wait(empty0 + 8 * r.slot, r.phase ^ 1u)) {
+          *stop = 1;
+          break;
+        }
+        const int64_t f = tile % cut.tiles_f, tok = tile / cut.tiles_f;
+        const uint32_t st = smem_u32(smem + r.slot * C::kStageBytes), full = full0 + 8 * r.slot;
+        const int groups = K.groups(kb);
+        tma::arrive_expect_tx(full, (uint32_t)(C::kSfAt + 2 * groups * kSfBlock));
+        load_codes<BN>(st, full, &wmap, &xmap, (int)(f * kLaneRows), (int)(tok * BN), kb);
+        load_scales(st + C::kSfAt, full, a.sfb + f * sf_row, a.sfa + tok * BN / 128 * sf_row, sf_row, kb, groups, 1);
+        if (++kb == K.n) {
+          kb = 0;
+          ++tile;
+        }
+      }
+      // no copy may land after the block has gone: wait for the last fill of every stage
+      const int64_t g = u - u0;
+      for (int64_t j = g > C::kStages ? g - C::kStages : 0; j < g; ++j)
+        tma::wait(full0 + 8 * (int)(j % C::kStages), (uint32_t)(j / C::kStages) & 1u);
+    }
+  } else if (warp == 5) {
+    Ring<C::kStages> r;
+    Ring<2> acc;
+    bool quit = false;
+    int64_t u = u0;
+    int kb = (int)(u0 % K.n), n = 0;
+    while (u < u1 && !quit) {  // one tile's part
+      // its accumulator has been read out
+      quit = !__all_sync(0xFFFFFFFFu, n < 2 || tma::wait(acce0 + 8 * acc.slot, acc.phase ^ 1u));
+      bool fresh = true;
+      for (; u < u1 && !quit; r.next()) {
+        quit = !__all_sync(0xFFFFFFFFu, tma::wait(full0 + 8 * r.slot, r.phase));
+        if (quit) break;
+        const int groups = K.groups(kb);
+        uint8_t* st = smem + r.slot * C::kStageBytes;
+        if (kb == K.n - 1 && K.tail) clear_tail(st + C::kSfAt, 2, groups - 1, lane);
+        tc5::fence_after_thread_sync();
+        if (lane == 0) {
+          const uint32_t sf_tmem = tmem + 2 * BN + (uint32_t)r.slot * C::kSfCols;
+          copy_stage_scales<BN>(sf_tmem, smem_u32(st + C::kSfAt), groups);
+          mma_stage<BN>(tmem + (uint32_t)(acc.slot * BN), sf_tmem, StageDesc(smem_u32(st)), groups, fresh);
+          tc5::commit(empty0 + 8 * r.slot);
+        }
+        __syncwarp();
+        fresh = false;
+        ++u;
+        if (++kb == K.n) {
+          kb = 0;
+          r.next();
+          break;
+        }
+      }
+      if (quit) break;
+      if (lane == 0) tc5::commit(accf0 + 8 * acc.slot);
+      __syncwarp();
+      acc.next();
+      ++n;
+    }
+    if (quit && lane == 0) *stop = 1;
+    if (lane == 0) tc5::commit(drain);  // arrives when every MMA issued above has completed
+  } else {
+    Ring<2> acc;
+    const int64_t first = u0 / K.n;
+    for (int64_t tile = first; tile * K.n < u1; ++tile, acc.next()) {
+      const bool ready = tma::wait(accf0 + 8 * acc.slot, acc.phase);
+      if (!__all_sync(0xFFFFFFFFu, ready && *stop == 0)) {
+        if (lane == 0) *stop = 1;
+        break;
+      }
+      tc5::fence_after_thread_sync();
+      const int64_t t0 = tile / cut.tiles_f * BN;
+      const int tokens = (int)(a.M - t0 < BN ? a.M - t0 : BN);
+      float* out = a.ws + (((int64_t)blockIdx.x * cut.most + (tile - first)) * BN) * kLaneRows + tid;
+#pragma unroll 1
+      for (int c = 0; c < tokens; c += 16) {
+        uint32_t v[16];
+        ld_32x32b_x16(tmem + (uint32_t)(acc.slot * BN + c) + ((uint32_t)(32 * warp) << 16), v);
+        tc5::wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (c + i < tokens) out[(int64_t)(c + i) * kLaneRows] = __uint_as_float(v[i]);
+      }
+      tc5::fence_before_thread_sync();
+      __syncwarp();
+      if (lane == 0) arrive(acce0 + 8 * acc.slot);
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+  const bool drained = tma::wait(drain, 0);
+  if (tid == 0 && (*stop || !drained) && a.status) atomicExch(a.status, kStatusPipeline);
+  tc5::fence_before_thread_sync();
+  __syncthreads();
+  if (warp == 5) tc5::dealloc(tmem, C::kTmemCols);
 }
 
 // Epilogue of one output; returns the magnitude bits of the rounded d.
@@ -50,151 +205,55 @@ __device__ __forceinline__ uint32_t put(const LinearArgs& a, int64_t m, int64_t 
   return abs_bits(to_f32(o));
 }
 
-template <int BN, typename T>
-__global__ void __launch_bounds__(kThreads)
-    linear_split_kernel(const LinearArgs a, const __grid_constant__ CUtensorMap wmap,
-                        const __grid_constant__ CUtensorMap xmap, int S) {
-  using C = Cfg<BN>;
-  extern __shared__ uint8_t raw[];
-  // 1024-byte alignment for the 128-byte swizzle
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStageBytes);
-  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * C::kStages, done = full0 + 16 * C::kStages;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * C::kStages + 1);
-  volatile int* stop = reinterpret_cast<int*>(bars + 2 * C::kStages + 2);
-
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t rank = cluster_rank();
-  const int64_t f0 = (int64_t)(blockIdx.x / S) * kLaneRows;  // first feature
-  const int64_t t0 = (int64_t)blockIdx.y * BN;               // first token
-  const Steps K(a.K);
-  const int k0 = (int)((int64_t)K.n * rank / S), k1 = (int)((int64_t)K.n * (rank + 1) / S);
-  constexpr int kColTile = BN * kBK / 2;
-
-  if (tid == 0) {
-    for (int s = 0; s < C::kStages; ++s) {
-      tma::mbar_init(full0 + 8 * s, 1);
-      tma::mbar_init(empty0 + 8 * s, 1);
-    }
-    tma::mbar_init(done, 1);
-    *stop = 0;
-    tma::fence_barrier_init();
+// The pieces of output tile blockIdx.x added in order: a thread takes four features of a token.
+template <typename T>
+__global__ void __launch_bounds__(256) linear_join_kernel(const LinearArgs a, const Cut cut, int bn) {
+  const int64_t tile = blockIdx.x, f = tile % cut.tiles_f, tok = tile / cut.tiles_f;
+  const int64_t m = tok * bn + (int64_t)blockIdx.y * blockDim.y + threadIdx.y, n = f * kLaneRows + 4 * threadIdx.x;
+  const bool there = m < a.M && m < (tok + 1) * bn;
+  float bias[4] = {};
+  if (a.bias) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n + i < a.N) bias[i] = load_as_f32(a.bias, n + i, a.bias_bf16);
   }
-  if (warp == 5) {
-    tc5::alloc(smem_u32(tmem_slot), C::kTmemCols);
-    tc5::relinquish_alloc_permit();
-  }
-  tc5::fence_before_thread_sync();
-  __syncthreads();
-  tc5::fence_after_thread_sync();
-  const uint32_t tmem = *tmem_slot;
-
-  if (warp == 4) {
-    if (lane == 0) {
-      const int64_t sf_row = (a.K + 63) / 64 * kSfBlock;  // scale bytes of a 128-row band
-      const uint8_t* sfw = a.sfb + f0 / 128 * sf_row;
-      const uint8_t* sfx = a.sfa + t0 / 128 * sf_row;
-      Ring<C::kStages> r;
-      int kb = k0;
-      for (; kb < k1; ++kb, r.next()) {
-        if (kb - k0 >= C::kStages && !tma::wait(empty0 + 8 * r.slot, r.phase ^ 1u)) {
-          *stop = 1;
-          break;
-        }
-        const uint32_t st = smem_u32(smem + r.slot * C::kStageBytes), full = full0 + 8 * r.slot;
-        const int groups = K.groups(kb);
-        tma::arrive_expect_tx(full, (uint32_t)(kLaneTile + kColTile + 2 * groups * kSfBlock));
-        load_codes<BN>(st, full, &wmap, &xmap, (int)f0, (int)t0, kb);
-        load_scales(st + kLaneTile + kColTile, full, sfw, sfx, sf_row, kb, groups, 1);
-      }
-      // no copy may land after the block has gone: wait for the last fill of every stage
-      const int g = kb - k0;
-      for (int j = g > C::kStages ? g - C::kStages : 0; j < g; ++j)
-        tma::wait(full0 + 8 * (j % C::kStages), (uint32_t)(j / C::kStages) & 1u);
-    }
-  } else if (warp == 5) {
-    Ring<C::kStages> r;
-    for (int kb = k0; kb < k1; ++kb, r.next()) {
-      if (!__all_sync(0xFFFFFFFFu, tma::wait(full0 + 8 * r.slot, r.phase))) {
-        if (lane == 0) *stop = 1;
-        break;
-      }
-      const int groups = K.groups(kb);
-      uint8_t* st = smem + r.slot * C::kStageBytes;
-      if (kb == K.n - 1 && K.tail) clear_tail(st + kLaneTile + kColTile, 2, groups - 1, lane);
-      tc5::fence_after_thread_sync();
-      if (lane == 0) {
-        const uint32_t sf_tmem = tmem + BN + (uint32_t)r.slot * C::kSfCols;
-        copy_stage_scales<BN>(sf_tmem, smem_u32(st + kLaneTile + kColTile), groups);
-        mma_stage<BN>(tmem, sf_tmem, StageDesc(smem_u32(st)), groups, kb == k0);
-        tc5::commit(empty0 + 8 * r.slot);
-      }
-      __syncwarp();
-    }
-    if (lane == 0) tc5::commit(done);  // arrives when every MMA issued above has completed
-  }
-  __syncwarp();
-
-  const bool ready = tma::wait(done, 0);
-  const bool ok = __syncthreads_and(ready && *stop == 0);
-  tc5::fence_after_thread_sync();
   const float scale = a.alpha_a[0] * a.alpha_b[0];
-  const int tokens = (int)(a.M - t0 < BN ? a.M - t0 : BN);
+  const int64_t p0 = cut.piece_of(tile * cut.steps), p1 = cut.piece_of((tile + 1) * cut.steps - 1);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   uint32_t top = 0;
-  if (S == 1) {
-    if (warp < 4) {
-      const int64_t n = f0 + tid;
-      const float bias = a.bias && n < a.N ? load_as_f32(a.bias, n, a.bias_bf16) : 0.0f;
-#pragma unroll 1
-      for (int c = 0; c < BN && c < tokens; c += 16) {
-        uint32_t r[16];
-        ld_32x32b_x16(tmem + (uint32_t)c + ((uint32_t)(32 * warp) << 16), r);
-        tc5::wait_ld();
+  if (there) {
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int64_t p = p0; p <= p1; ++p) {
+      const int64_t slot = p * cut.most + (tile - cut.begin(p) / cut.steps);
+      const float4 w = *reinterpret_cast<const float4*>(a.ws + (slot * bn + (m - tok * bn)) * kLaneRows + 4 * threadIdx.x);
+      v.x += w.x;
+      v.y += w.y;
+      v.z += w.z;
+      v.w += w.w;
+    }
+    const float s[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (ok && n < a.N && c + i < tokens)
-            top = max(top, put<T>(a, t0 + c + i, n, fmaf(__uint_as_float(r[i]), scale, bias)));
-      }
-    }
-  } else {
-    // the partial tile, one row of 128 features per token, in the stages' place
-    float* part = reinterpret_cast<float*>(smem);
-    if (warp < 4) {
-#pragma unroll 1
-      for (int c = 0; c < BN && c < tokens; c += 16) {
-        uint32_t r[16];
-        ld_32x32b_x16(tmem + (uint32_t)c + ((uint32_t)(32 * warp) << 16), r);
-        tc5::wait_ld();
-#pragma unroll
-        for (int i = 0; i < 16; ++i) part[(c + i) * kLaneRows + tid] = __uint_as_float(r[i]);
-      }
-    }
-    cluster_sync();
-    const int per = kLaneRows / S;
-    const uint32_t base = smem_u32(part);
-    for (int i = tid; i < tokens * per; i += kThreads) {
-      const int c = i / per, f = (int)rank * per + i % per;
-      const int64_t n = f0 + f;
-      float v = 0.0f;
-      for (int q = 0; q < S; ++q) v += ld_rank(base + 4u * (uint32_t)(c * kLaneRows + f), (uint32_t)q);
-      if (ok && n < a.N) {
-        const float bias = a.bias ? load_as_f32(a.bias, n, a.bias_bf16) : 0.0f;
-        top = max(top, put<T>(a, t0 + c, n, fmaf(v, scale, bias)));
-      }
-    }
-    cluster_sync();  // no block leaves while another reads its part
+    for (int i = 0; i < 4; ++i)
+      if (n + i < a.N) top = max(top, put<T>(a, m, n + i, fmaf(s[i], scale, bias[i])));
   }
   if (a.amax) put_amax(a.amax, top);
-  if (tid == 0 && !ok && a.status) atomicExch(a.status, kStatusPipeline);
-  tc5::fence_before_thread_sync();
-  __syncthreads();
-  if (warp == 5) tc5::dealloc(tmem, C::kTmemCols);
 }
 
-template <int BN, typename T>
-cudaError_t launch(const LinearArgs& a, int S, cudaStream_t s) {
+Cut cut_of(int64_t M, int64_t N, int64_t K, int bn) {
+  Cut c;
+  c.tiles_f = (N + kLaneRows - 1) / kLaneRows;
+  c.tiles = c.tiles_f * ((M + bn - 1) / bn);
+  c.steps = (int)((K + kBK - 1) / kBK);
+  c.pieces = (int)std::min<int64_t>(152, c.tiles * c.steps);
+  c.most = (int)((c.tiles * c.steps + c.pieces - 1) / c.pieces + c.steps - 2) / c.steps + 1;
+  return c;
+}
+
+template <int BN>
+cudaError_t launch(const LinearArgs& a, cudaStream_t s) {
   using C = Cfg<BN>;
-  auto kern = linear_split_kernel<BN, T>;
+  auto kern = linear_split_kernel<BN>;
   static std::atomic<int> cache[64] = {};
   int cap = 0;
   cudaError_t e = resident_grid(kern, kThreads, C::kSmem, cache, cap);  // opts in to the shared memory
@@ -204,34 +263,38 @@ cudaError_t launch(const LinearArgs& a, int S, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = make_codes_map(&xmap, a.qa, a.M, a.K / 2, kBK / 2, BN);
   if (e != cudaSuccess) return e;
+  const Cut cut = cut_of(a.M, a.N, a.K, BN);
+  kern<<<(unsigned)cut.pieces, kThreads, C::kSmem, s>>>(a, wmap, xmap, cut);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int tokens = (int)std::min<int64_t>(a.M, BN);
+  const int ty = tokens >= 8 ? 8 : tokens;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((a.N + kLaneRows - 1) / kLaneRows * S), (unsigned)((a.M + BN - 1) / BN));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.gridDim = dim3((unsigned)cut.tiles, (unsigned)((tokens + ty - 1) / ty));
+  cfg.blockDim = dim3(32, (unsigned)ty);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)S;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, a, wmap, xmap, S);
-}
-
-template <int BN>
-cudaError_t launch_t(const LinearArgs& a, int S, cudaStream_t s) {
-  return a.out_bf16 ? launch<BN, bf16>(a, S, s) : launch<BN, float>(a, S, s);
+  return a.out_bf16 ? cudaLaunchKernelEx(&cfg, linear_join_kernel<bf16>, a, cut, BN)
+                    : cudaLaunchKernelEx(&cfg, linear_join_kernel<float>, a, cut, BN);
 }
 
 }  // namespace
 
-cudaError_t launch_split(const LinearArgs& a, int bn, int S, cudaStream_t s) {
+int64_t split_workspace(int64_t M, int64_t N, int64_t K, int bn) {
+  const Cut c = cut_of(M, N, K, bn);
+  return (int64_t)c.pieces * c.most * bn * kLaneRows * 4;
+}
+
+cudaError_t launch_split(const LinearArgs& a, int bn, cudaStream_t s) {
   switch (bn) {
-    case 16: return launch_t<16>(a, S, s);
-    case 32: return launch_t<32>(a, S, s);
-    case 64: return launch_t<64>(a, S, s);
-    default: return launch_t<128>(a, S, s);
+    case 16: return launch<16>(a, s);
+    case 32: return launch<32>(a, s);
+    case 64: return launch<64>(a, s);
+    default: return launch<128>(a, s);
   }
 }
 
