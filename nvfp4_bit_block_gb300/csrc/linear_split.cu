@@ -21,7 +21,10 @@ namespace nvfp4 {
 namespace lin {
 namespace {
 
-constexpr int kThreads = 192;  // warps 0-3: sums out of TMEM (its lane quarters), 4: loads, 5: MMA
+// Warps 0-3: sums out of TMEM (its lane quarters), 4-7: scales into TMEM (by
+// tensor-core copies from the MMA's thread a stage took twice its bytes' time), 8: loads, 9: MMA.
+constexpr int kThreads = 320;
+constexpr int kSfWarp0 = 4, kSfWarps = 4, kLoadWarp = 8, kMmaWarp = 9;
 
 template <int BN>
 struct Cfg {
@@ -29,23 +32,24 @@ struct Cfg {
   static constexpr int kSfAt = kLaneTile + kColTile;
   static constexpr int kStageBytes = kSfAt + 2 * kSfStage;  // 22 to 36 KB
   static constexpr int kStages = BN == 16 ? 10 : (BN == 32 ? 9 : (BN == 64 ? 8 : 6));
-  static constexpr int kBars = 2 * kStages + 5;
-  static constexpr int kSmem = kStages * kStageBytes + 256 /* barriers */ + 1024 /* alignment */;
+  static constexpr int kBars = 3 * kStages + 5;
+  static constexpr int kSmem = kStages * kStageBytes + 512 /* barriers */ + 1024 /* alignment */;
   static constexpr uint32_t kSfCols = 32;  // TMEM columns of one stage's scales
   static constexpr uint32_t kTmemCols = 512;
   static_assert(2 * BN + kStages * kSfCols <= kTmemCols, "TMEM columns");
-  static_assert(8 * (kBars + 2) <= 256 && kSmem <= 232448, "shared memory");
+  static_assert(8 * (kBars + 2) <= 512 && kSmem <= 232448, "shared memory");
 };
 
-// The work in steps of K: `steps` per output tile, `tiles` of them, cut into `pieces`.
+// The work in steps of K: `steps` per output tile, `tiles` of them, cut into `pieces`;
+// piece p begins at step floor(tiles * steps * p / pieces).
 struct Cut {
-  int64_t tiles, tiles_f;  // output tiles; of them per token tile
-  int steps, pieces, most;  // most: tiles that a piece touches at most
+  int64_t tiles, tiles_f;   // output tiles; of them per token tile
+  int steps, pieces, most;  // most: pieces that touch a tile at most
   __host__ __device__ int64_t begin(int64_t piece) const { return tiles * steps * piece / pieces; }
-  __host__ __device__ int64_t piece_of(int64_t unit) const {  // the piece that holds this step
-    int64_t p = unit * pieces / (tiles * steps);
-    while (begin(p + 1) <= unit) ++p;
-    return p;
+  // The piece that holds this step: the last p with begin(p) <= step.
+  __device__ int piece_of(int64_t step) const {
+    const uint64_t n = (uint64_t)(step + 1) * (uint32_t)pieces - 1, d = (uint64_t)tiles * (uint32_t)steps;
+    return n >> 32 ? (int)(n / d) : (int)((uint32_t)n / (uint32_t)d);
   }
 };
 
@@ -59,7 +63,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStageBytes);
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * C::kStages;
-  const uint32_t accf0 = empty0 + 8 * C::kStages, acce0 = accf0 + 16, drain = accf0 + 32;
+  const uint32_t sfr0 = empty0 + 8 * C::kStages;
+  const uint32_t accf0 = sfr0 + 8 * C::kStages, acce0 = accf0 + 16, drain = accf0 + 32;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
   volatile int* stop = reinterpret_cast<int*>(bars + C::kBars + 1);
 
@@ -71,6 +76,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < C::kStages; ++s) {
       tma::mbar_init(full0 + 8 * s, 1);
       tma::mbar_init(empty0 + 8 * s, 1);
+      tma::mbar_init(sfr0 + 8 * s, kSfWarps);  // the stage has arrived and its scales are in TMEM
     }
     for (int b = 0; b < 2; ++b) {
       tma::mbar_init(accf0 + 8 * b, 1);
@@ -81,7 +87,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma::fence_barrier_init();
     if (blockIdx.x == 0 && a.amax) a.amax[0] = a.amax[1] = 0.0f;  // the second kernel joins its maxima to it
   }
-  if (warp == 5) {
+  if (warp == kMmaWarp) {
     tc5::alloc(smem_u32(tmem_slot), C::kTmemCols);
     tc5::relinquish_alloc_permit();
   }
@@ -91,7 +97,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 4) {
+  if (warp == kLoadWarp) {
     if (lane == 0) {
       const int64_t sf_row = (a.K + 63) / 64 * kSfBlock;  // scale bytes of a 128-row band
       Ring<C::kStages> r;
@@ -118,46 +124,52 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int64_t j = g > C::kStages ? g - C::kStages : 0; j < g; ++j)
         tma::wait(full0 + 8 * (int)(j % C::kStages), (uint32_t)(j / C::kStages) & 1u);
     }
-  } else if (warp == 5) {
-    Ring<C::kStages> r;
-    Ring<2> acc;
-    bool quit = false;
-    int64_t u = u0;
-    int kb = (int)(u0 % K.n), n = 0;
-    while (u < u1 && !quit) {  // one tile's part
-      // its accumulator has been read out
-      quit = !__all_sync(0xFFFFFFFFu, n < 2 || tma::wait(acce0 + 8 * acc.slot, acc.phase ^ 1u));
-      bool fresh = true;
-      for (; u < u1 && !quit; r.next()) {
-        quit = !__all_sync(0xFFFFFFFFu, tma::wait(full0 + 8 * r.slot, r.phase));
-        if (quit) break;
-        const int groups = K.groups(kb);
-        uint8_t* st = smem + r.slot * C::kStageBytes;
-        if (kb == K.n - 1 && K.tail) clear_tail(st + C::kSfAt, 2, groups - 1, lane);
-        tc5::fence_after_thread_sync();
-        if (lane == 0) {
-          const uint32_t sf_tmem = tmem + 2 * BN + (uint32_t)r.slot * C::kSfCols;
-          copy_stage_scales<BN>(sf_tmem, smem_u32(st + C::kSfAt), groups);
-          mma_stage<BN>(tmem + (uint32_t)(acc.slot * BN), sf_tmem, StageDesc(smem_u32(st)), groups, fresh);
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) {
+      Ring<C::kStages> r;
+      Ring<2> acc;
+      int64_t u = u0;
+      int kb = (int)(u0 % K.n), n = 0;
+      while (u < u1 && !*stop) {  // one tile's part
+        // its accumulator has been read out
+        if (n >= 2 && !tma::wait(acce0 + 8 * acc.slot, acc.phase ^ 1u)) *stop = 1;
+        bool fresh = true, last = false;
+        for (; u < u1 && !last && !*stop; ++u, r.next()) {
+          if (!tma::wait(sfr0 + 8 * r.slot, r.phase)) {
+            *stop = 1;
+            break;
+          }
+          tc5::fence_after_thread_sync();
+          mma_stage<BN>(tmem + (uint32_t)(acc.slot * BN), tmem + 2 * BN + (uint32_t)r.slot * C::kSfCols,
+                        StageDesc(smem_u32(smem + r.slot * C::kStageBytes)), K.groups(kb), fresh);
           tc5::commit(empty0 + 8 * r.slot);
+          fresh = false;
+          last = ++kb == K.n;
         }
-        __syncwarp();
-        fresh = false;
-        ++u;
-        if (++kb == K.n) {
-          kb = 0;
-          r.next();
-          break;
-        }
+        if (*stop) break;
+        kb = 0;
+        tc5::commit(accf0 + 8 * acc.slot);
+        acc.next();
+        ++n;
       }
-      if (quit) break;
-      if (lane == 0) tc5::commit(accf0 + 8 * acc.slot);
-      __syncwarp();
-      acc.next();
-      ++n;
+      tc5::commit(drain);  // arrives when every MMA issued above has completed
     }
-    if (quit && lane == 0) *stop = 1;
-    if (lane == 0) tc5::commit(drain);  // arrives when every MMA issued above has completed
+  } else if (warp >= kSfWarp0) {
+    const uint32_t quarter = (uint32_t)(32 * (warp & 3)) << 16;
+    Ring<C::kStages> r;
+    int kb = (int)(u0 % K.n);
+    for (int64_t u = u0; u < u1; ++u, r.next()) {
+      if (!__all_sync(0xFFFFFFFFu, tma::wait(full0 + 8 * r.slot, r.phase) && *stop == 0)) {
+        if (lane == 0) *stop = 1;
+        break;
+      }
+      put_scales<1>(tmem + quarter + 2 * BN + (uint32_t)r.slot * C::kSfCols, smem + r.slot * C::kStageBytes + C::kSfAt,
+                    K.groups(kb), kb == K.n - 1 && K.tail, lane);
+      tc5::fence_before_thread_sync();
+      __syncwarp();
+      if (lane == 0) arrive(sfr0 + 8 * r.slot);
+      if (++kb == K.n) kb = 0;
+    }
   } else {
     Ring<2> acc;
     const int64_t first = u0 / K.n;
@@ -170,7 +182,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc5::fence_after_thread_sync();
       const int64_t t0 = tile / cut.tiles_f * BN;
       const int tokens = (int)(a.M - t0 < BN ? a.M - t0 : BN);
-      float* out = a.ws + (((int64_t)blockIdx.x * cut.most + (tile - first)) * BN) * kLaneRows + tid;
+      const int part = (int)blockIdx.x - cut.piece_of(tile * cut.steps);
+      float* out = a.ws + ((tile * cut.most + part) * BN) * kLaneRows + tid;
 #pragma unroll 1
       for (int c = 0; c < tokens; c += 16) {
         uint32_t v[16];
@@ -191,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0 && (*stop || !drained) && a.status) atomicExch(a.status, kStatusPipeline);
   tc5::fence_before_thread_sync();
   __syncthreads();
-  if (warp == 5) tc5::dealloc(tmem, C::kTmemCols);
+  if (warp == kMmaWarp) tc5::dealloc(tmem, C::kTmemCols);
 }
 
 // Epilogue of one output; returns the magnitude bits of the rounded d.
@@ -218,15 +231,15 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const LinearArgs a, co
       if (n + i < a.N) bias[i] = load_as_f32(a.bias, n + i, a.bias_bf16);
   }
   const float scale = a.alpha_a[0] * a.alpha_b[0];
-  const int64_t p0 = cut.piece_of(tile * cut.steps), p1 = cut.piece_of((tile + 1) * cut.steps - 1);
+  const int parts = cut.piece_of((tile + 1) * cut.steps - 1) - cut.piece_of(tile * cut.steps) + 1;
+  const float* in = a.ws + (tile * cut.most * bn + (m - tok * bn)) * kLaneRows + 4 * threadIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   uint32_t top = 0;
   if (there) {
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-    for (int64_t p = p0; p <= p1; ++p) {
-      const int64_t slot = p * cut.most + (tile - cut.begin(p) / cut.steps);
-      const float4 w = *reinterpret_cast<const float4*>(a.ws + (slot * bn + (m - tok * bn)) * kLaneRows + 4 * threadIdx.x);
+    for (int p = 0; p < parts; ++p) {
+      const float4 w = *reinterpret_cast<const float4*>(in + (int64_t)p * bn * kLaneRows);
       v.x += w.x;
       v.y += w.y;
       v.z += w.z;
@@ -246,7 +259,9 @@ Cut cut_of(int64_t M, int64_t N, int64_t K, int bn) {
   c.tiles = c.tiles_f * ((M + bn - 1) / bn);
   c.steps = (int)((K + kBK - 1) / kBK);
   c.pieces = (int)std::min<int64_t>(152, c.tiles * c.steps);
-  c.most = (int)((c.tiles * c.steps + c.pieces - 1) / c.pieces + c.steps - 2) / c.steps + 1;
+  // a tile's steps meet at most this many pieces of at least floor(tiles * steps / pieces) steps
+  const int64_t least = c.tiles * c.steps / c.pieces;
+  c.most = (int)((c.steps + least - 2) / least + 1);
   return c;
 }
 
@@ -286,7 +301,7 @@ cudaError_t launch(const LinearArgs& a, cudaStream_t s) {
 
 int64_t split_workspace(int64_t M, int64_t N, int64_t K, int bn) {
   const Cut c = cut_of(M, N, K, bn);
-  return (int64_t)c.pieces * c.most * bn * kLaneRows * 4;
+  return c.tiles * c.most * bn * kLaneRows * 4;
 }
 
 cudaError_t launch_split(const LinearArgs& a, int bn, cudaStream_t s) {

@@ -30,14 +30,6 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
-// 512 bytes of shared memory (32 rows of 16 bytes) to 4 TMEM columns, repeated
-// in the four lane quarters: a block of 128 rows' scales as the block-scaled
-// MMA reads them.  Runs in order with the MMAs that the same thread issues.
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
-  const uint64_t desc = tc5::smem_desc(saddr, 0, 128, 0);  // no swizzle, 8-row groups 128 bytes apart
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
-}
-
 // ---- pairs of blocks (cta_group::2): the two blocks of a cluster of two form one
 // MMA of 256 rows; each holds its 128 rows of the lane operand, half of the column
 // operand's rows, its 128 rows of the accumulator, and all of the column scales.
@@ -170,23 +162,6 @@ __device__ __forceinline__ void load_scales(uint32_t sf, uint32_t full, const ui
     tc5::bulk_g2s(sf + kSfStage * (1 + h), sfc + h * sf_row + (int64_t)kb * kSfStage, bytes, full);
 }
 
-// K % 64 == 32: the last group's scales 2 and 3 are padding, whose bytes may be
-// anything (NaN times a zero code would be NaN): set them to zero.  The whole
-// warp calls this on the stage's scale bands before the tensor cores read them.
-__device__ __forceinline__ void clear_tail(uint8_t* sf, int bands, int group, int lane) {
-  for (int h = 0; h < bands; ++h) {
-    uint4* p = reinterpret_cast<uint4*>(sf + h * kSfStage + group * kSfBlock + 16 * lane);
-    uint4 v = *p;
-    v.x &= 0xFFFFu;
-    v.y &= 0xFFFFu;
-    v.z &= 0xFFFFu;
-    v.w &= 0xFFFFu;
-    *p = v;
-  }
-  fence_async_smem();
-  __syncwarp();
-}
-
 // One stage's scales by the four warps of TMEM's lane quarters: each lane holds
 // the 16 bytes of its row of a block, and every quarter gets the same ones.
 // `tail`: the last group's scales 2 and 3 are padding and become zeros.
@@ -212,21 +187,6 @@ __device__ __forceinline__ void put_scales(uint32_t sf_tmem, const uint8_t* sf, 
     for (int h = 0; h < BANDS; ++h) tc5::st_32x32b_x4(sf_tmem + 16u + 4u * BANDS * j + 4u * h, v[1 + h]);
   }
   tc5::wait_st();
-}
-
-// The same by tensor-core copies, issued in order with the MMAs by their thread.
-template <int BN>
-__device__ __forceinline__ void copy_stage_scales(uint32_t sf_tmem, uint32_t sf, int groups) {
-  constexpr int kBands = (BN + 127) / 128;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (j < groups) {
-      copy_scales(sf_tmem + 4u * j, sf + j * kSfBlock);
-#pragma unroll
-      for (int h = 0; h < kBands; ++h)
-        copy_scales(sf_tmem + 16u + 4u * kBands * j + 4u * h, sf + kSfStage * (1 + h) + j * kSfBlock);
-    }
-  }
 }
 
 // Shared-memory descriptors of a stage's two tiles; 64 values of K are 32 bytes
