@@ -85,7 +85,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma::mbar_init(drain, 1);
     *stop = 0;
     tma::fence_barrier_init();
-    if (blockIdx.x == 0 && a.amax) a.amax[0] = a.amax[1] = 0.0f;  // the second kernel joins its maxima to it
   }
   if (warp == kMmaWarp) {
     tc5::alloc(smem_u32(tmem_slot), C::kTmemCols);
@@ -94,7 +93,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc5::fence_before_thread_sync();
   __syncthreads();
   tc5::fence_after_thread_sync();
+  // The setup above may run beside the end of the kernel before this one; what follows reads and writes memory.  The
+  // second kernel may start its own setup from here on.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid == 0 && blockIdx.x == 0 && a.amax) a.amax[0] = a.amax[1] = 0.0f;  // the second kernel joins its maxima to it
   const uint32_t tmem = *tmem_slot;
 
   if (warp == kLoadWarp) {
@@ -279,20 +282,23 @@ cudaError_t launch(const LinearArgs& a, cudaStream_t s) {
   e = make_codes_map(&xmap, a.qa, a.M, a.K / 2, kBK / 2, BN);
   if (e != cudaSuccess) return e;
   const Cut cut = cut_of(a.M, a.N, a.K, BN);
-  kern<<<(unsigned)cut.pieces, kThreads, C::kSmem, s>>>(a, wmap, xmap, cut);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  const int tokens = (int)std::min<int64_t>(a.M, BN);
-  const int ty = tokens >= 8 ? 8 : tokens;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)cut.tiles, (unsigned)((tokens + ty - 1) / ty));
-  cfg.blockDim = dim3(32, (unsigned)ty);
-  cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)cut.pieces);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, a, wmap, xmap, cut);
+  if (e != cudaSuccess) return e;
+  const int tokens = (int)std::min<int64_t>(a.M, BN);
+  const int ty = tokens >= 8 ? 8 : tokens;
+  cfg.gridDim = dim3((unsigned)cut.tiles, (unsigned)((tokens + ty - 1) / ty));
+  cfg.blockDim = dim3(32, (unsigned)ty);
+  cfg.dynamicSmemBytes = 0;
   return a.out_bf16 ? cudaLaunchKernelEx(&cfg, linear_join_kernel<bf16>, a, cut, BN)
                     : cudaLaunchKernelEx(&cfg, linear_join_kernel<float>, a, cut, BN);
 }
