@@ -217,6 +217,70 @@ __global__ void __launch_bounds__(THREADS) norm_stream_kernel(const NormArgs a) 
   if (a.amax) put_amax(a, top, top_s);
 }
 
+// Rows that are not 16-byte aligned: single values, NC of them per thread, with
+// gamma and beta in registers and the next row's values on their way while this
+// one is worked on.  Few threads with many values each: what it costs is
+// instructions, and those per row and thread are shared.
+template <typename XT, typename YT, int NC, bool WARP, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS) norm_scalar_kernel(const NormArgs a) {
+  __shared__ __align__(16) float buf[2][32];
+  __shared__ uint32_t top_s[32];
+  const int lane = WARP ? threadIdx.x & 31 : threadIdx.x, group = WARP ? 32 : blockDim.x;
+  const int64_t groups = WARP ? (int64_t)gridDim.x * (THREADS / 32) : gridDim.x;
+  const int64_t first = WARP ? (int64_t)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5) : blockIdx.x;
+  const int mine = ((int)a.N - lane + group - 1) / group;  // values of this thread: lane, lane + group, ..
+  const float inv = 1.0f / (float)a.N;
+  float g[NC], b[NC], x[NC];
+  XT next[NC];  // as they come: a conversion here would wait for them
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    g[i] = a.gamma && i < mine ? load_as_f32(a.gamma, lane + i * group, a.w_bf16) : 1.0f;
+    b[i] = a.beta && i < mine ? load_as_f32(a.beta, lane + i * group, a.w_bf16) : 0.0f;
+    next[i] = from_f32<XT>(0.0f);
+  }
+  const XT* from = static_cast<const XT*>(a.x) + first * a.ldx + lane;
+  YT* y = static_cast<YT*>(a.y) + first * a.ldy + lane;
+  auto load = [&]() {
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+      if (i < mine) next[i] = from[i * group];
+    from += groups * a.ldx;
+  };
+  if (first < a.M) load();
+  uint32_t top = 0;
+  for (int64_t r = first; r < a.M; r += groups, y += groups * a.ldy) {
+    float s[1] = {0.0f}, t[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      x[i] = to_f32(next[i]);
+      s[0] += x[i];
+    }
+    if (r + groups < a.M) load();
+    group_sums<WARP, 1>(s, buf[0]);
+    const float mean = s[0] * inv;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      x[i] -= mean;
+      if (i < mine) t[0] = fmaf(x[i], x[i], t[0]);
+    }
+    group_sums<WARP, 1>(t, buf[1]);
+    const float rstd = 1.0f / sqrtf(t[0] * inv + a.eps);
+    if (lane == 0) {
+      if (a.mean) a.mean[r] = mean;
+      if (a.rstd) a.rstd[r] = rstd;
+    }
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const YT o = from_f32<YT>(fmaf(x[i] * rstd, g[i], b[i]));
+      if (i < mine) {
+        y[i * group] = o;
+        top = max(top, abs_bits(to_f32(o)));
+      }
+    }
+  }
+  if (a.amax) put_amax(a, top, top_s);
+}
+
 // Rows too long for the registers of a block: three passes over the row.
 template <typename XT, typename YT>
 __global__ void __launch_bounds__(kMaxThreads) norm_long_kernel(const NormArgs a) {
@@ -304,8 +368,16 @@ cudaError_t launch(const NormArgs& a, cudaStream_t s) {
     if (chunks <= 4096) return run<norm_kernel<XT, YT, 8, 4, 1, false, 1024>>(a, a.M, round32((chunks + 3) / 4), s);
   } else {
     if (chunks <= 512)
-      return run<norm_kernel<XT, YT, 1, 16, 1, true, kWarpThreads>>(a, (a.M + per_warp_block - 1) / per_warp_block, kWarpThreads, s);
-    if (chunks <= 8192) return run<norm_kernel<XT, YT, 1, 8, 1, false, 1024>>(a, a.M, round32((chunks + 7) / 8), s);
+      return run<norm_scalar_kernel<XT, YT, 16, true, kWarpThreads, 3>>(
+          a, (a.M + per_warp_block - 1) / per_warp_block, kWarpThreads, s);
+    if (chunks <= 16 * 128)
+      return run<norm_scalar_kernel<XT, YT, 16, false, 128, 5>>(a, a.M, round32((chunks + 15) / 16), s);
+    if (chunks <= 24 * 128)
+      return run<norm_scalar_kernel<XT, YT, 24, false, 128, 4>>(a, a.M, round32((chunks + 23) / 24), s);
+    if (chunks <= 24 * 256)
+      return run<norm_scalar_kernel<XT, YT, 24, false, 256, 2>>(a, a.M, round32((chunks + 23) / 24), s);
+    if (chunks <= 24 * 512)
+      return run<norm_scalar_kernel<XT, YT, 24, false, 512, 1>>(a, a.M, round32((chunks + 23) / 24), s);
     if (chunks <= 32768) return run<norm_kernel<XT, YT, 1, 32, 1, false, 1024>>(a, a.M, round32((chunks + 31) / 32), s);
   }
   return run<norm_long_kernel<XT, YT>>(a, a.M, kMaxThreads, s);
