@@ -82,30 +82,20 @@ __device__ __forceinline__ Raw<T, 8> slot_read(uint32_t at) {
   }
   return r;
 }
-// Chunks of a thread as pairs: neighbours for V = 8, values of two chunks for V = 1.
+// Chunks of a thread as pairs of neighbours.
 template <typename T, int NC>
 __device__ __forceinline__ void to_pairs(const Raw<T, 8> (&raw)[NC], float2 (&f)[NC * 4]) {
 #pragma unroll
   for (int i = 0; i < NC; ++i) unpack2(raw[i], f + 4 * i);
 }
-template <typename T, int NC>
-__device__ __forceinline__ void to_pairs(const Raw<T, 1> (&raw)[NC], float2 (&f)[NC / 2]) {
-#pragma unroll
-  for (int i = 0; i < NC / 2; ++i) f[i] = make_float2(to_f32(raw[2 * i].v[0]), to_f32(raw[2 * i + 1].v[0]));
-}
-// Column of element e of a thread.
-template <int V>
-__device__ __forceinline__ int column(int t, int group, int e) {
-  return V == 8 ? 8 * (t + (e / 8) * group) + e % 8 : t + e * group;
-}
 
 // R neighbouring rows at a time, which share a barrier, the sums' exchanges and the
-// loop's overhead.  S > 0: S times R rows of each group in shared memory or on
-// their way there (16-byte rows, V = 8), where dy and x are read again after the
-// sums instead of being kept in registers; S = 0: plain loads, one row.
-template <typename DT, typename XT, int V, int NC, int R, int S, bool RES, int THREADS, int BLOCKS>
+// loop's overhead.  S times R rows of each group are in shared memory or on their
+// way there; dy and x are read from it again after the sums instead of being
+// kept in registers.  16-byte aligned rows.
+template <typename DT, typename XT, int NC, int R, int S, bool RES, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_kernel(const NormGradArgs a, int group_threads) {
-  constexpr int P = NC * V / 2, K = R == 3 ? 8 : 2 * R;  // sums of a round, a power of two
+  constexpr int P = NC * 4, K = R == 3 ? 8 : 2 * R;  // sums of a round, a power of two
   extern __shared__ uint4 ring[];
   __shared__ float buf[2][THREADS / 32 * K];
   const int N = (int)a.N;
@@ -114,53 +104,43 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_kernel(const NormGr
   const int64_t step = (int64_t)gridDim.x * ngroups * R, first = ((int64_t)blockIdx.x * ngroups + group) * R;
   const float inv = 1.0f / (float)N;
   // this thread's slots: per stage and row NC chunks of dy, of x and of dres, each blockDim.x apart
-  constexpr uint32_t kDy = sizeof(Raw<DT, V>), kX = sizeof(Raw<XT, V>);
+  constexpr uint32_t kDy = sizeof(Raw<DT, 8>), kX = sizeof(Raw<XT, 8>);
   const uint32_t threads = blockDim.x, at_x = NC * threads * kDy, at_res = at_x + NC * threads * kX;
   const uint32_t row_bytes = at_x + NC * threads * kX * (RES ? 2 : 1), stage_bytes = R * row_bytes;
   const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
   const uint32_t my_dy = base + threadIdx.x * kDy, my_x = base + at_x + threadIdx.x * kX;
   // global positions: the rows being copied, the rows being worked on
-  const DT* dy = static_cast<const DT*>(a.dy) + first * a.lddy + V * t;
-  const XT* x = static_cast<const XT*>(a.x) + first * a.ldx + V * t;
-  const XT* res = RES ? static_cast<const XT*>(a.dres) + first * a.lddres + V * t : nullptr;
-  XT* dx = static_cast<XT*>(a.dx) + first * a.lddx + V * t;
+  const DT* dy = static_cast<const DT*>(a.dy) + first * a.lddy + 8 * t;
+  const XT* x = static_cast<const XT*>(a.x) + first * a.ldx + 8 * t;
+  const XT* res = RES ? static_cast<const XT*>(a.dres) + first * a.lddres + 8 * t : nullptr;
+  XT* dx = static_cast<XT*>(a.dx) + first * a.lddx + 8 * t;
   int64_t ahead = first;  // row that dy, x and res point at
   auto copy_rows = [&](uint32_t stage) {
-    if constexpr (S > 0) {
 #pragma unroll
-      for (int q = 0; q < R; ++q) {
-        if (ahead + q < a.M) {
-          const uint32_t at = stage + q * row_bytes;
+    for (int q = 0; q < R; ++q) {
+      if (ahead + q < a.M) {
+        const uint32_t at = stage + q * row_bytes;
 #pragma unroll
-          for (int i = 0; i < NC; ++i) {
-            const int off = V * i * group_threads;
-            const bool there = V * t + off < N;
-            copy_chunk<DT>(my_dy + at + i * threads * kDy, dy + q * a.lddy, off, there);
-            copy_chunk<XT>(my_x + at + i * threads * kX, x + q * a.ldx, off, there);
-            if constexpr (RES) copy_chunk<XT>(my_x + (at_res - at_x) + at + i * threads * kX, res + q * a.lddres, off, there);
-          }
+        for (int i = 0; i < NC; ++i) {
+          const int off = 8 * i * group_threads;
+          const bool there = 8 * t + off < N;
+          copy_chunk<DT>(my_dy + at + i * threads * kDy, dy + q * a.lddy, off, there);
+          copy_chunk<XT>(my_x + at + i * threads * kX, x + q * a.ldx, off, there);
+          if constexpr (RES) copy_chunk<XT>(my_x + (at_res - at_x) + at + i * threads * kX, res + q * a.lddres, off, there);
         }
       }
-      dy += step * a.lddy;
-      x += step * a.ldx;
-      if constexpr (RES) res += step * a.lddres;
-      ahead += step;
-      copies_commit();
     }
+    dy += step * a.lddy;
+    x += step * a.ldx;
+    if constexpr (RES) res += step * a.lddres;
+    ahead += step;
+    copies_commit();
   };
   float2 gamma[P], dg[P], db[P];
-  if constexpr (V == 8) {
 #pragma unroll
-    for (int i = 0; i < NC; ++i) load_weights2(a.gamma, a.w_bf16, 8 * (t + i * group_threads), N, 1.0f, gamma + 4 * i);
-  }
+  for (int i = 0; i < NC; ++i) load_weights2(a.gamma, a.w_bf16, 8 * (t + i * group_threads), N, 1.0f, gamma + 4 * i);
 #pragma unroll
-  for (int p = 0; p < P; ++p) {
-    dg[p] = db[p] = splat(0.0f);
-    if (V == 8) continue;
-    const int c0 = column<V>(t, group_threads, 2 * p), c1 = column<V>(t, group_threads, 2 * p + 1);
-    gamma[p].x = a.gamma && c0 < N ? load_as_f32(a.gamma, c0, a.w_bf16) : 1.0f;
-    gamma[p].y = a.gamma && c1 < N ? load_as_f32(a.gamma, c1, a.w_bf16) : 1.0f;
-  }
+  for (int p = 0; p < P; ++p) dg[p] = db[p] = splat(0.0f);
 #pragma unroll
   for (int s = 0; s < S - 1; ++s) copy_rows((uint32_t)s * stage_bytes);
   float mean[R], rstd[R];
@@ -177,39 +157,20 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_kernel(const NormGr
   float* mine = buf[0] + group * warps * K;
   for (int64_t r = first; r < a.M; r += step, dx += step * a.lddx) {
     float2 d[R][P], xh[R][P];
-    Raw<XT, V> raw_r[NC];
+    Raw<XT, 8> raw_r[NC];
     auto read = [&](int q) {  // row q's dy and x from its slots
-      if constexpr (S > 0) {
-        Raw<DT, V> raw_d[NC];
-        Raw<XT, V> raw_x[NC];
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-          raw_d[i] = slot_read<DT>(my_dy + stage + q * row_bytes + i * threads * kDy);
-          raw_x[i] = slot_read<XT>(my_x + stage + q * row_bytes + i * threads * kX);
-        }
-        to_pairs(raw_d, d[q]);
-        to_pairs(raw_x, xh[q]);
-      }
-    };
-    if constexpr (S > 0) {
-      copy_rows(stage == 0 ? (S - 1) * stage_bytes : stage - stage_bytes);  // the slots read in the previous round
-      copies_wait<S - 1>();
-    } else {  // R = 1
-      Raw<DT, V> raw_d[NC];
-      Raw<XT, V> raw_x[NC];
+      Raw<DT, 8> raw_d[NC];
+      Raw<XT, 8> raw_x[NC];
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
-        const int off = V * i * group_threads, c = V * t + off;
-        raw_d[i] = load_chunk<DT, V>(dy - V * t, c, N);
-        raw_x[i] = load_chunk<XT, V>(x - V * t, c, N);
-        if constexpr (RES) raw_r[i] = load_chunk<XT, V>(res - V * t, c, N);
+        raw_d[i] = slot_read<DT>(my_dy + stage + q * row_bytes + i * threads * kDy);
+        raw_x[i] = slot_read<XT>(my_x + stage + q * row_bytes + i * threads * kX);
       }
-      to_pairs(raw_d, d[0]);
-      to_pairs(raw_x, xh[0]);
-      dy += step * a.lddy;
-      x += step * a.ldx;
-      if constexpr (RES) res += step * a.lddres;
-    }
+      to_pairs(raw_d, d[q]);
+      to_pairs(raw_x, xh[q]);
+    };
+    copy_rows(stage == 0 ? (S - 1) * stage_bytes : stage - stage_bytes);  // the slots read in the previous round
+    copies_wait<S - 1>();
     float2 scale[R], shift[R];
     float sums[K];
 #pragma unroll
@@ -221,7 +182,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_kernel(const NormGr
 #pragma unroll
     for (int q = 0; q < R; ++q) {
       float2 s0 = splat(0.0f), s1 = splat(0.0f);
-      if constexpr (S > 0) read(q);
+      read(q);
       if (R == 1 || r + q < a.M) {  // slots of a row that is not there hold old values
 #pragma unroll
         for (int p = 0; p < P; ++p) {  // beyond the row dy is 0, so that nothing is added
@@ -243,53 +204,46 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_kernel(const NormGr
 #pragma unroll
     for (int q = 0; q < R; ++q) {
       if (R > 1 && r + q >= a.M) break;
-      if constexpr (S > 0) {
-        read(q);
+      read(q);
 #pragma unroll
-        for (int p = 0; p < P; ++p) {
-          xh[q][p] = mul2(add2(xh[q][p], shift[q]), scale[q]);
-          d[q][p] = mul2(d[q][p], gamma[p]);
-        }
+      for (int p = 0; p < P; ++p) {
+        xh[q][p] = mul2(add2(xh[q][p], shift[q]), scale[q]);
+        d[q][p] = mul2(d[q][p], gamma[p]);
       }
       const float2 k0 = splat(-sums[2 * q] * inv * scale[q].x), k1 = splat(-sums[2 * q + 1] * inv);
 #pragma unroll
       for (int p = 0; p < P; ++p) d[q][p] = fma2(fma2(xh[q][p], k1, d[q][p]), scale[q], k0);
       if constexpr (RES) {
-        if constexpr (S > 0) {
 #pragma unroll
-          for (int i = 0; i < NC; ++i)
-            raw_r[i] = slot_read<XT>(my_x + (at_res - at_x) + stage + q * row_bytes + i * threads * kX);
-        }
+        for (int i = 0; i < NC; ++i)
+          raw_r[i] = slot_read<XT>(my_x + (at_res - at_x) + stage + q * row_bytes + i * threads * kX);
         to_pairs(raw_r, xh[q]);
 #pragma unroll
         for (int p = 0; p < P; ++p) d[q][p] = add2(d[q][p], xh[q][p]);
       }
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
-        const int off = V * i * group_threads;
-        if (V * t + off < N) {
+        const int off = 8 * i * group_threads;
+        if (8 * t + off < N) {
           XT* o = dx + q * a.lddx + off;
-          if constexpr (V == 8)
-            *reinterpret_cast<Raw<XT, 8>*>(o) = pack2(d[q] + 4 * i, Raw<XT, 8>());
-          else
-            *o = from_f32<XT>(i % 2 ? d[q][i / 2].y : d[q][i / 2].x);
+          *reinterpret_cast<Raw<XT, 8>*>(o) = pack2(d[q] + 4 * i, Raw<XT, 8>());
         }
       }
     }
-    if (S > 0) stage = stage == (S - 1) * stage_bytes ? 0 : stage + stage_bytes;
+    stage = stage == (S - 1) * stage_bytes ? 0 : stage + stage_bytes;
   }
   if (!a.dgamma && !a.dbeta) return;
   // one row of column sums per block; alone it is the result
   float* out_g = gridDim.x == 1 ? a.dgamma : a.ws + (int64_t)blockIdx.x * 2 * a.N;
   float* out_b = gridDim.x == 1 ? a.dbeta : a.ws + ((int64_t)blockIdx.x * 2 + 1) * a.N;
   float* join = reinterpret_cast<float*>(ring);  // [2][N]: the groups' sums, added one group after the other
-  if (S > 0) copies_wait<0>();
+  copies_wait<0>();
   for (int q = 0; q < ngroups; ++q) {
     if (ngroups > 1) __syncthreads();
     if (q != group) continue;
 #pragma unroll
-    for (int e = 0; e < NC * V; ++e) {
-      const int c = column<V>(t, group_threads, e);
+    for (int e = 0; e < NC * 8; ++e) {
+      const int c = 8 * (t + e / 8 * group_threads) + e % 8;
       if (c >= N) continue;
       float vg = e % 2 ? dg[e / 2].y : dg[e / 2].x, vb = e % 2 ? db[e / 2].y : db[e / 2].x;
       if (q > 0) {
@@ -299,6 +253,104 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_kernel(const NormGr
       if (q < ngroups - 1) {
         join[c] = vg;
         join[N + c] = vb;
+      } else {
+        if (out_g) out_g[c] = vg;
+        if (out_b) out_b[c] = vb;
+      }
+    }
+  }
+}
+
+// Rows that are not 16-byte aligned: single values, NC of them per thread, the next
+// row's on their way (unconverted: a conversion would wait for them) while this
+// one is worked on.
+template <typename DT, typename XT, int NC, bool RES, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_scalar_kernel(const NormGradArgs a, int group_threads) {
+  extern __shared__ uint4 ring[];
+  __shared__ float buf[2][THREADS / 32 * 2];
+  const int warps = group_threads >> 5, group = (int)threadIdx.x / group_threads, ngroups = (int)blockDim.x / group_threads;
+  const int t = (int)threadIdx.x - group * group_threads;
+  const int64_t step = (int64_t)gridDim.x * ngroups, first = (int64_t)blockIdx.x * ngroups + group;
+  const int mine = ((int)a.N - t + group_threads - 1) / group_threads;  // values of this thread: t, t + group_threads, ..
+  const float inv = 1.0f / (float)a.N;
+  float gamma[NC], dg[NC], db[NC];
+  DT next_d[NC];
+  XT next_x[NC], next_r[RES ? NC : 1];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    gamma[i] = a.gamma && i < mine ? load_as_f32(a.gamma, t + i * group_threads, a.w_bf16) : 1.0f;
+    dg[i] = db[i] = 0.0f;
+    next_d[i] = from_f32<DT>(0.0f);
+    next_x[i] = from_f32<XT>(0.0f);
+    if (RES) next_r[i] = from_f32<XT>(0.0f);
+  }
+  const DT* dy = static_cast<const DT*>(a.dy) + first * a.lddy + t;
+  const XT* x = static_cast<const XT*>(a.x) + first * a.ldx + t;
+  const XT* res = RES ? static_cast<const XT*>(a.dres) + first * a.lddres + t : nullptr;
+  XT* dx = static_cast<XT*>(a.dx) + first * a.lddx + t;
+  float next_mean = 0.0f, next_rstd = 0.0f;
+  auto load = [&](int64_t r) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      if (i < mine) {
+        next_d[i] = dy[i * group_threads];
+        next_x[i] = x[i * group_threads];
+        if (RES) next_r[i] = res[i * group_threads];
+      }
+    }
+    next_mean = a.mean[r];
+    next_rstd = a.rstd[r];
+    dy += step * a.lddy;
+    x += step * a.ldx;
+    if (RES) res += step * a.lddres;
+  };
+  if (first < a.M) load(first);
+  int parity = 0;
+  float* my_buf = buf[0] + group * warps * 2;
+  for (int64_t r = first; r < a.M; r += step, dx += step * a.lddx) {
+    float d[NC], xh[NC], rest[RES ? NC : 1], sums[2] = {0.0f, 0.0f};
+    const float mean = next_mean, rstd = next_rstd;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      d[i] = to_f32(next_d[i]);
+      xh[i] = to_f32(next_x[i]);
+      if (RES) rest[i] = to_f32(next_r[i]);
+    }
+    if (r + step < a.M) load(r + step);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {  // beyond the row dy is 0, so that nothing is added
+      xh[i] = (xh[i] - mean) * rstd;
+      db[i] += d[i];
+      dg[i] = fmaf(d[i], xh[i], dg[i]);
+      d[i] *= gamma[i];
+      sums[0] += d[i];
+      sums[1] = fmaf(d[i], xh[i], sums[1]);
+    }
+    group_sums_k<2>(sums, my_buf + parity * (THREADS / 32 * 2), warps, group);
+    parity ^= 1;
+    const float k0 = -sums[0] * inv * rstd, k1 = -sums[1] * inv;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      float o = fmaf(fmaf(xh[i], k1, d[i]), rstd, k0);
+      if (RES) o += rest[i];
+      if (i < mine) dx[i * group_threads] = from_f32<XT>(o);
+    }
+  }
+  if (!a.dgamma && !a.dbeta) return;
+  float* out_g = gridDim.x == 1 ? a.dgamma : a.ws + (int64_t)blockIdx.x * 2 * a.N;
+  float* out_b = gridDim.x == 1 ? a.dbeta : a.ws + ((int64_t)blockIdx.x * 2 + 1) * a.N;
+  float* join = reinterpret_cast<float*>(ring);  // [2][N], as in norm_grad_kernel
+  for (int q = 0; q < ngroups; ++q) {
+    if (ngroups > 1) __syncthreads();
+    if (q != group) continue;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = t + i * group_threads;
+      if (i >= mine) continue;
+      const float vg = dg[i] + (q > 0 ? join[c] : 0.0f), vb = db[i] + (q > 0 ? join[a.N + c] : 0.0f);
+      if (q < ngroups - 1) {
+        join[c] = vg;
+        join[a.N + c] = vb;
       } else {
         if (out_g) out_g[c] = vg;
         if (out_b) out_b[c] = vb;
@@ -377,23 +429,40 @@ cudaError_t join(const NormGradArgs& a, int64_t parts, cudaStream_t s) {
   return colsum::launch_join<2>(a.ws, (int)parts, a.N, a.dgamma, a.dbeta, s);
 }
 
-template <typename DT, typename XT, int V, int NC, int R, int S, int THREADS, int BLOCKS>
+template <typename DT, typename XT, int NC, int R, int S, int THREADS, int BLOCKS>
 cudaError_t run(const NormGradArgs& a, cudaStream_t s) {
-  auto kern = a.dres ? norm_grad_kernel<DT, XT, V, NC, R, S, true, THREADS, BLOCKS>
-                     : norm_grad_kernel<DT, XT, V, NC, R, S, false, THREADS, BLOCKS>;
+  auto kern = a.dres ? norm_grad_kernel<DT, XT, NC, R, S, true, THREADS, BLOCKS>
+                     : norm_grad_kernel<DT, XT, NC, R, S, false, THREADS, BLOCKS>;
   static BlocksPerSm cache[2];
-  const int group = round32((a.N + V * NC - 1) / (V * NC));
+  const int group = round32((a.N + 8 * NC - 1) / (8 * NC));
   // groups of a block: as many as fit, fewer where that leaves SMs without a block
   const int64_t rows_of_all = (int64_t)152 * R;
   const int groups = (int)std::max<int64_t>(1, std::min<int64_t>(THREADS / group, (a.M + rows_of_all - 1) / rows_of_all));
   const int threads = group * groups;
-  int smem = R * S * NC * threads * (int)(sizeof(Raw<DT, V>) + sizeof(Raw<XT, V>) * (a.dres ? 2 : 1));
+  int smem = R * S * NC * threads * (int)(sizeof(Raw<DT, 8>) + sizeof(Raw<XT, 8>) * (a.dres ? 2 : 1));
   if (groups > 1) smem = std::max(smem, (int)(8 * a.N));
   int sms = 0, per_sm = 0;
   const cudaError_t e = cache[a.dres ? 1 : 0].get(kern, threads, smem, sms, per_sm);
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)groups * R;
   const int64_t blocks = std::min<int64_t>(std::min<int64_t>((a.M + rows - 1) / rows, kMaxBlocks), (int64_t)sms * per_sm);
+  kern<<<(unsigned)blocks, threads, smem, s>>>(a, group);
+  return join(a, blocks, s);
+}
+
+template <typename DT, typename XT, int NC, int THREADS, int BLOCKS>
+cudaError_t run_scalar(const NormGradArgs& a, cudaStream_t s) {
+  auto kern = a.dres ? norm_grad_scalar_kernel<DT, XT, NC, true, THREADS, BLOCKS>
+                     : norm_grad_scalar_kernel<DT, XT, NC, false, THREADS, BLOCKS>;
+  static BlocksPerSm cache[2];
+  const int group = round32((a.N + NC - 1) / NC);
+  const int groups = (int)std::max<int64_t>(1, std::min<int64_t>(THREADS / group, (a.M + 303) / 304));
+  const int threads = group * groups, smem = groups > 1 ? (int)(8 * a.N) : 0;
+  int sms = 0, per_sm = 0;
+  const cudaError_t e = cache[a.dres ? 1 : 0].get(kern, threads, smem, sms, per_sm);
+  if (e != cudaSuccess) return e;
+  const int64_t blocks =
+      std::min<int64_t>(std::min<int64_t>((a.M + groups - 1) / groups, kMaxBlocks), (int64_t)sms * per_sm);
   kern<<<(unsigned)blocks, threads, smem, s>>>(a, group);
   return join(a, blocks, s);
 }
@@ -421,16 +490,19 @@ cudaError_t launch(const NormGradArgs& a, cudaStream_t s) {
       // bf16 with residual: one row 160 us, two 117, three 108; without it, four rows 89 us, two 103).
       // With few rows one at a time, so that they spread over the SMs.
       const bool many = a.M >= 8 * 152;
-      if (many && 8 * row <= kRing) return run<DT, XT, 8, 2, 4, 2, 320, 1>(a, s);
-      if (many && 6 * row <= kRing) return run<DT, XT, 8, 2, 3, 2, 320, 1>(a, s);
-      if (many && 4 * row <= kRing) return run<DT, XT, 8, 2, 2, 2, 320, 1>(a, s);
-      return run<DT, XT, 8, 2, 1, 3, 320, 1>(a, s);
+      if (many && 8 * row <= kRing) return run<DT, XT, 2, 4, 2, 320, 1>(a, s);
+      if (many && 6 * row <= kRing) return run<DT, XT, 2, 3, 2, 320, 1>(a, s);
+      if (many && 4 * row <= kRing) return run<DT, XT, 2, 2, 2, 320, 1>(a, s);
+      return run<DT, XT, 2, 1, 3, 320, 1>(a, s);
     }
-    if (a.N <= 10240 && 2 * group * 16 * bytes <= kRing) return run<DT, XT, 8, 2, 1, 2, 640, 1>(a, s);
+    if (a.N <= 10240 && 2 * group * 16 * bytes <= kRing) return run<DT, XT, 2, 1, 2, 640, 1>(a, s);
     return run_long<DT, XT, 8>(a, s);
   }
-  if (a.N <= 2560) return run<DT, XT, 1, 8, 1, 0, 320, 2>(a, s);
-  if (a.N <= 5120) return run<DT, XT, 1, 8, 1, 0, 640, 1>(a, s);
+  // few rows: more threads to a row, the latency counts; many: fewer, the instructions do (16384 x 2731 fp32 89 us
+  // with sixteen values per thread, 180 with eight; 515 x 1023 fp32 9.6 and 6.4 us)
+  if (a.M < 8 * 152 && a.N <= 8 * 256) return run_scalar<DT, XT, 8, 256, 2>(a, s);
+  if (a.N <= 16 * 192) return run_scalar<DT, XT, 16, 192, 2>(a, s);
+  if (a.N <= 16 * 320) return run_scalar<DT, XT, 16, 320, 1>(a, s);
   return run_long<DT, XT, 1>(a, s);
 }
 
