@@ -105,7 +105,7 @@ def _build_ext(force: bool, verbose: bool) -> tuple:
     if stale:
         cuda = os.path.dirname(os.path.dirname(_nvcc()))
         inc = [*include_paths(), sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
-        _run([os.environ.get("CXX", "g++"), "-O1", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-w",
+        _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-w",
               *[x for i in inc for x in ("-I", i)], "-c", src, "-o", o], verbose)
     return o, stale
 
@@ -117,7 +117,7 @@ def _link_ext(o: str, force: bool, verbose: bool) -> None:
     libs = library_paths()
     tmp = LAYER_EXT + f".tmp{os.getpid()}"
     _run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, o, LAYER_LIB, *[f"-L{p}" for p in libs],
-          *[f"-Wl,-rpath,{p}" for p in ["$ORIGIN", *libs]], "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"],
+          *[f"-Wl,-rpath,{p}" for p in ["$ORIGIN", *libs]], "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"],
          verbose)
     os.replace(tmp, LAYER_EXT)
 

@@ -8,6 +8,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -114,9 +115,11 @@ void* vector(const at::Tensor* t, const char* name, int64_t n, c10::Device dev, 
   return p;
 }
 
-at::Tensor new_matrix(int64_t M, int64_t N, at::ScalarType t, c10::Device dev) {
-  return at::empty({M, N}, at::TensorOptions().dtype(t).device(dev));
+// A new tensor on `dev` (straight from the CUDA allocator, without the dispatcher's way there).
+at::Tensor fresh(at::IntArrayRef sizes, at::ScalarType t, c10::Device dev) {
+  return at::Tensor(at::detail::empty_cuda(sizes, t, dev, std::nullopt));
 }
+at::Tensor new_matrix(int64_t M, int64_t N, at::ScalarType t, c10::Device dev) { return fresh({M, N}, t, dev); }
 
 // Small fp32 results of one call: each 16-byte aligned in one allocation that they share.
 class Floats {
@@ -128,11 +131,11 @@ class Floats {
     return at;
   }
   void make() {
-    if (total_ > 0) base_ = at::empty({total_}, at::TensorOptions().dtype(at::kFloat).device(dev_));
+    if (total_ > 0) base_ = fresh({total_}, at::kFloat, dev_);
   }
   float* ptr(int64_t at) { return base_.defined() ? base_.data_ptr<float>() + at : nullptr; }
   at::Tensor view(int64_t at, int64_t n) {
-    if (!base_.defined()) return at::empty({n}, at::TensorOptions().dtype(at::kFloat).device(dev_));
+    if (!base_.defined()) return fresh({n}, at::kFloat, dev_);
     auto t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(base_.storage()), base_.key_set(), base_.dtype());
     c10::TensorImpl* impl = t.unsafeGetTensorImpl();
     impl->set_sizes_contiguous({n});
@@ -155,7 +158,7 @@ struct Workspace {
   Workspace(int64_t bytes, const char* where, c10::Device dev) : n(bytes) {
     if (n < 0) throw Status{n, where};
     if (n > 0) {
-      t = at::empty({n}, at::TensorOptions().dtype(at::kByte).device(dev));
+      t = fresh({n}, at::kByte, dev);
       p = t.data_ptr();
     }
   }
@@ -275,7 +278,7 @@ PyObject* linear(PyObject* const* a) {
   const Matrix dm = matrix(out ? *out : made, "out", dev, M, N, ot);
   const Matrix rm = res ? matrix(*res, "residual", dev, M, N, ot) : Matrix();
   if (want_z) z = new_matrix(M, N, ot, dev);
-  if (want_amax) amax = at::empty({2}, at::TensorOptions().dtype(at::kFloat).device(dev));
+  if (want_amax) amax = fresh({2}, at::kFloat, dev);
   const Workspace ws(nvfp4_linear_workspace(M, N, K), "nvfp4_linear_workspace", dev);
   auto bytes = [](void* p) { return static_cast<const uint8_t*>(p); };
   check(nvfp4_linear(bytes(ap), bytes(sap), static_cast<float*>(aap), bytes(bp), bytes(sbp), static_cast<float*>(abp), M,
@@ -307,7 +310,7 @@ PyObject* act_backward(PyObject* const* a) {
   }
   Workspace ws;
   if (want_dbias) {
-    dbias = at::empty({N}, at::TensorOptions().dtype(at::kFloat).device(dev));
+    dbias = fresh({N}, at::kFloat, dev);
     ws = Workspace(nvfp4_act_backward_workspace(M, N), "nvfp4_act_backward_workspace", dev);
   }
   check(nvfp4_act_backward(dm.p, dm.ld, zm.p, zm.ld, M, N, b, (int)act, om.p, om.ld,

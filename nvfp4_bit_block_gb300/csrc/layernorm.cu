@@ -14,12 +14,6 @@ namespace nvfp4 {
 namespace norm {
 namespace {
 
-#ifndef NORM_NC
-#define NORM_NC 4
-#define NORM_KB true
-#define NORM_S 3
-#define NORM_KEEP true
-#endif
 constexpr int kMaxThreads = 1024;
 constexpr int kWarpThreads = 256;  // block of the one-warp-per-row kernels
 
@@ -342,18 +336,16 @@ cudaError_t launch(const NormArgs& a, cudaStream_t s) {
   const int64_t chunks = vec ? a.N / 8 : a.N;
   const int64_t per_warp_block = kWarpThreads / 32;
   if (vec && a.M > 608) {
+    // Four chunks of eight values per thread (five warps to a row of 5120 values, 58 us for 16384 x 5120 bf16; with
+    // two chunks 69 us, with one 100 us), three rows in flight; gamma and beta in registers as far as they fit (read
+    // again for each row: 92 us).
     const int slot = 8 * (int)sizeof(XT);  // bytes of a thread's chunk in flight
+    if (chunks <= 32) return run<norm_stream_kernel<XT, YT, 1, 4, true, true, 256>>(a, (a.M + 7) / 8, 256, s, 256 * 4 * slot);
     if (chunks <= 128)
-      return chunks <= 32 ? run<norm_stream_kernel<XT, YT, 1, 4, true, true, 256>>(a, (a.M + 7) / 8, 256, s, 256 * 4 * slot)
-                          : run<norm_stream_kernel<XT, YT, 4, 3, true, NORM_KEEP, 256>>(a, (a.M + 7) / 8, 256, s, 256 * 12 * slot);
-    if (chunks <= 1024) {
-      const int t = round32((chunks + NORM_NC - 1) / NORM_NC);
-      return run<norm_stream_kernel<XT, YT, NORM_NC, NORM_S, false, NORM_KB, 1024 / NORM_NC / 32 * 32>>(a, a.M, t, s, t * NORM_NC * NORM_S * slot);
-    }
-    if (chunks <= 4096) {
-      const int t = round32((chunks + 3) / 4);
-      return run<norm_stream_kernel<XT, YT, 4, 2, false, false, 1024>>(a, a.M, t, s, t * 8 * slot);
-    }
+      return run<norm_stream_kernel<XT, YT, 4, 3, true, true, 256>>(a, (a.M + 7) / 8, 256, s, 256 * 12 * slot);
+    const int t = round32((chunks + 3) / 4);
+    if (chunks <= 1024) return run<norm_stream_kernel<XT, YT, 4, 3, false, true, 256>>(a, a.M, t, s, t * 12 * slot);
+    if (chunks <= 4096) return run<norm_stream_kernel<XT, YT, 4, 2, false, false, 1024>>(a, a.M, t, s, t * 8 * slot);
   }
   if (vec) {
     if (chunks <= 128) {  // a warp holds the row
