@@ -345,7 +345,8 @@ cudaError_t launch(const NormArgs& a, cudaStream_t s) {
       return run<norm_stream_kernel<XT, YT, 4, 3, true, true, 256>>(a, (a.M + 7) / 8, 256, s, 256 * 12 * slot);
     const int t = round32((chunks + 3) / 4);
     if (chunks <= 1024) return run<norm_stream_kernel<XT, YT, 4, 3, false, true, 256>>(a, a.M, t, s, t * 12 * slot);
-    if (chunks <= 4096) return run<norm_stream_kernel<XT, YT, 4, 2, false, false, 1024>>(a, a.M, t, s, t * 8 * slot);
+    if (chunks <= 4096 && t * 8 * slot <= 224 * 1024)
+      return run<norm_stream_kernel<XT, YT, 4, 2, false, false, 1024>>(a, a.M, t, s, t * 8 * slot);
   }
   if (vec) {
     if (chunks <= 128) {  // a warp holds the row

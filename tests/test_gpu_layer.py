@@ -112,6 +112,21 @@ def test_layernorm(M, N, xt, yt):
     check_norm(x, gamma, beta, 1e-5, r, yt)
 
 
+# enough rows that each block walks over several: every kernel and width, rows of 16-byte pieces and others
+MANY_ROWS = [(5003, 64), (3001, 256), (2500, 520), (2001, 1024), (1301, 5120), (1250, 8192), (701, 20480), (650, 32768),
+             (620, 33008), (3001, 257), (3000, 1001), (1500, 2731), (1301, 5001), (900, 8191), (650, 12289)]
+
+
+@pytest.mark.parametrize("xt,yt", TYPES)
+@pytest.mark.parametrize("M,N", MANY_ROWS)
+def test_layernorm_many_rows(M, N, xt, yt):
+    x = rand((M, N), xt, M + 3 * N, 2.0, 0.5)
+    gamma, beta = rand((N,), F32, 1, 0.1, 1.0), rand((N,), F32, 2, 0.1)
+    r = nv.nvfp4_layernorm(x, gamma, beta, 1e-5, out_dtype=yt, want_amax=True)
+    check_norm(x, gamma, beta, 1e-5, r, yt)
+    assert r.amax.tolist() == [float(r.y.float().abs().max())] * 2
+
+
 @pytest.mark.parametrize("pad,offset", [(8, 0), (8, 8), (3, 1), (0, 1), (4, 2)])
 @pytest.mark.parametrize("xt,yt", TYPES)
 def test_layernorm_strides_and_alignment(xt, yt, pad, offset):
@@ -235,6 +250,28 @@ def test_layernorm_backward(M, N, xt, dt):
     check_norm_grad(dy, x, mean, rstd, gamma, dres, nv.nvfp4_layernorm_backward(dy, x, mean, rstd, gamma, dres))
 
 
+@pytest.mark.parametrize("xt,dt", TYPES)
+@pytest.mark.parametrize("M,N", MANY_ROWS + [(1217, 3000), (1300, 4104), (1303, 10240)])
+def test_layernorm_backward_many_rows(M, N, xt, dt):
+    x, dy = rand((M, N), xt, M + N, 2.0, 0.3), rand((M, N), dt, M + N + 1, 1e-3)
+    gamma = rand((N,), F32, 13, 0.2, 1.0)
+    mean, rstd = stats(x)
+    for dres in (None, rand((M, N), xt, 14, 1e-3)):
+        check_norm_grad(dy, x, mean, rstd, gamma, dres, nv.nvfp4_layernorm_backward(dy, x, mean, rstd, gamma, dres))
+
+
+@pytest.mark.parametrize("M,N", [(1301, 5120), (1300, 1001), (640, 20480)])
+def test_layernorm_backward_in_place_many_rows(M, N):
+    x, dy, dres = rand((M, N), BF, 21), rand((M, N), BF, 22), rand((M, N), BF, 23)
+    mean, rstd = stats(x)
+    want = nv.nvfp4_layernorm_backward(dy, x, mean, rstd, None, dres)
+    for k in (0, 1):
+        d, e = dy.clone(), dres.clone()
+        got = nv.nvfp4_layernorm_backward(d, x, mean, rstd, None, e, out=(d, e)[k])
+        assert torch.equal(got.dx, want.dx) and torch.equal(got.dgamma, want.dgamma)
+        assert torch.equal(got.dbeta, want.dbeta)
+
+
 @pytest.mark.parametrize("pad,offset", [(8, 0), (8, 8), (3, 1), (0, 1)])
 @pytest.mark.parametrize("xt,dt", TYPES)
 def test_layernorm_backward_strides_and_alignment(xt, dt, pad, offset):
@@ -343,7 +380,8 @@ def check_act_grad(dy, z, act, r):
 @pytest.mark.parametrize("act", range(5))
 @pytest.mark.parametrize("dt", [BF, F32])
 def test_act_backward(act, dt):
-    for M, N in ((1, 1), (3, 7), (67, 1001), (1, 20480), (300, 33), (129, 1024), (1000, 264), (2, 33001), (517, 2056)):
+    for M, N in ((1, 1), (3, 7), (67, 1001), (1, 20480), (300, 33), (129, 1024), (1000, 264), (2, 33001), (517, 2056),
+                 (5000, 72), (4001, 2048), (3000, 1001)):
         dy, z = rand((M, N), dt, M + N, 1e-3), rand((M, N), dt, N, 2.0)
         check_act_grad(dy, z, act, nv.nvfp4_act_backward(dy, z, act))
 
@@ -467,7 +505,7 @@ def test_linear(M, N, K):
     check_linear(a, b, K, r, residual=res, dtype=F32)
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 300, 512), (20, 300, 512), (140, 300, 512)])
+@pytest.mark.parametrize("M,N,K", [(1, 300, 512), (20, 300, 512), (140, 300, 512), (1300, 2056, 96)])
 @pytest.mark.parametrize("act", range(5))
 def test_linear_every_epilogue(M, N, K, act):
     a, b = operand(M, K, 50), operand(N, K, 51, 0.05)
@@ -481,7 +519,7 @@ def test_linear_every_epilogue(M, N, K, act):
 @pytest.mark.parametrize("pad,offset", [(8, 0), (8, 8), (3, 1), (0, 1), (2, 0)])
 @pytest.mark.parametrize("dt", [BF, F32])
 def test_linear_strides_and_alignment(dt, pad, offset):
-    for M, N, K in ((2, 200, 128), (40, 257, 160), (150, 264, 512)):
+    for M, N, K in ((2, 200, 128), (40, 257, 160), (150, 264, 512), (1100, 2600, 96)):
         a, b, res = operand(M, K, 60), operand(N, K, 61), rand((M, N), dt, 62)
         base, out = strided(torch.zeros((M, N), dtype=dt, device="cuda"), pad, offset)
         r = nv.nvfp4_linear(*a, *b, residual=strided(res, pad, offset)[1], out=out)
@@ -502,10 +540,10 @@ def test_linear_equals_the_gemm():
         within(got, want.double(), 2 * TGEMM * (xa @ xb.t()) * a[2].double() * b[2].double(), "d")
 
 
-@pytest.mark.parametrize("M", [1, 30, 300])
-def test_linear_zero_and_extreme_operands(M):
+@pytest.mark.parametrize("M,N", [(1, 200), (30, 200), (300, 200), (1100, 2600)])
+def test_linear_zero_and_extreme_operands(M, N):
     """All-zero operands give act(bias) + residual; the largest codes and scales do not overflow."""
-    N, K = 200, 320
+    K = 320
     a, b = operand(M, K, 80), operand(N, K, 81)
     za = (torch.zeros_like(a[0]), a[1], a[2])
     bias, res = rand((N,), F32, 82), rand((M, N), BF, 83)
@@ -518,8 +556,8 @@ def test_linear_zero_and_extreme_operands(M):
 
 def test_linear_nan_scale_stays_in_its_row():
     """An E4M3 NaN scale of one token (or one weight row) makes that row (column) NaN and no other."""
-    for M in (4, 200):
-        N, K = 300, 512
+    for M, N in ((4, 300), (200, 300), (1100, 2600)):
+        K = 512
         a, b = operand(M, K, 84, garbage=False), operand(N, K, 85, garbage=False)
         clean = nv.nvfp4_linear(*a, *b, out_dtype=F32).d
         sa, sb = a[1].clone(), b[1].clone()
@@ -564,8 +602,8 @@ def everything(seed):
     f = nv.nvfp4_layernorm(x, want_amax=True)
     g = nv.nvfp4_layernorm_backward(dy, x, f.mean, f.rstd)
     out = [f.y, f.mean, f.rstd, f.amax, g.dx, g.dgamma, g.dbeta]
-    for M in (1, 40, 300):
-        a, b = operand(M, 1536, seed + 2), operand(640, 1536, seed + 3)
+    for M, N in ((1, 640), (40, 640), (300, 640), (1100, 2600)):
+        a, b = operand(M, 1536, seed + 2), operand(N, 1536, seed + 3)
         r = nv.nvfp4_linear(*a, *b, act=nv.ACT_GELU, want_z=True, want_amax=True)
         out += [r.d, r.z, r.amax]
     t = nv.nvfp4_act_backward(dy, x, nv.ACT_GELU)
