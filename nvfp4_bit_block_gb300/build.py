@@ -7,8 +7,9 @@
   of its own because the quantizer's arithmetic is compiled without fused
   multiply-adds and theirs with them; _build/_nvfp4_layer.so is its Python
   binding (a CPython extension against torch's C++ interface);
-* tests/selftest/_build/libnvfp4_selftest.so -- device self-checks used only
-  by the tests (build_selftest); it holds no product entry point.
+* tests/selftest/_build/libnvfp4_selftest.so and libnvfp4_layer_selftest.so --
+  device self-checks used only by the tests (build_selftest,
+  build_layer_selftest); they hold no product entry point.
 
 Translation units compile in parallel; the CUDA runtime is linked statically.
 """
@@ -30,6 +31,7 @@ INCLUDE = os.path.join(ROOT, "include")
 SELFTEST_DIR = os.path.join(ROOT, "tests", "selftest")
 SELFTEST_BUILD = os.path.join(SELFTEST_DIR, "_build")
 SELFTEST_LIB = os.path.join(SELFTEST_BUILD, "libnvfp4_selftest.so")
+LAYER_SELFTEST_LIB = os.path.join(SELFTEST_BUILD, "libnvfp4_layer_selftest.so")
 
 SOURCES = ["api.cu", "tmap.cu", "amax.cu", "quant1d.cu", "quant1d_sr.cu", "quant1d_46mae.cu", "quant1d_46mse.cu", "quant1d_46max.cu",
            "quant2d.cu", "dequant.cu", "analysis.cu", "gemm.cu"]
@@ -135,6 +137,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return main.result()
 
 
+def build_layer_selftest(force: bool = False, verbose: bool = False) -> str:
+    """The test-only build of nvfp4_linear whose copies are never issued; returns its path."""
+    srcs = [os.path.join(SELFTEST_DIR, "nvfp4_layer_selftest.cu")]
+    srcs += [os.path.join(CSRC, s) for s in ("linear.cu", "linear_split.cu", "linear_many.cu", "out_tmap.cu", "tmap.cu")]
+    return _build_lib(srcs, os.path.join(SELFTEST_BUILD, "layer"), LAYER_SELFTEST_LIB, force, verbose,
+                      [*LAYER_NVCC_FLAGS, "-DNVFP4_TEST_NO_COPIES"])
+
+
 def build_selftest(force: bool = False, verbose: bool = False) -> str:
     """The test-only self-check library (its own copy of the tensor-map
     helper); returns its path."""
@@ -145,3 +155,4 @@ def build_selftest(force: bool = False, verbose: bool = False) -> str:
 if __name__ == "__main__":
     print(build(verbose=True))
     print(build_selftest(verbose=True))
+    print(build_layer_selftest(verbose=True))

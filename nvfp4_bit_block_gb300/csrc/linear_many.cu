@@ -227,9 +227,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t st = smem_u32(smem + r.slot * kStageBytes), full = full0 + 8 * r.slot;
             const uint32_t bytes = (uint32_t)(K.groups(kb) * kSfBlock);
             tma::arrive_expect_tx(full, (uint32_t)kSfAt + bytes * (uint32_t)(tok + bands));
-            // rows beyond the operand arrive as zeros
-            tma::load_2d(st, &xmap, kb * (kBK / 2), (int)row, full);
-            tma::load_2d(st + kLaneTile, &wmap, kb * (kBK / 2), (int)col, full);
+            if (!kCopies) continue;
+            load_codes(st, full, &xmap, &wmap, (int)row, (int)col, kb);
             const int64_t at = (int64_t)kb * kSfStage;
             if (tok) tc5::bulk_g2s(st + kSfAt, sfx + at, bytes, full);
             tc5::bulk_g2s(st + kSfAt + kSfStage, sfw + at, bytes, full);
@@ -237,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // no copy may land after the block has gone: wait for the last fill of every stage
-        for (int64_t j = g > kStages ? g - kStages : 0; j < g; ++j)
+        for (int64_t j = g > kStages ? g - kStages : 0; j < g && kCopies; ++j)
           tma::wait(full0 + 8 * (int)(j % kStages), (uint32_t)(j / kStages) & 1u);
       }
     } else if (warp == 1) {

@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t st = smem_u32(smem + r.slot * C::kStageBytes), full = full0 + 8 * r.slot;
         const int groups = K.groups(kb);
         tma::arrive_expect_tx(full, (uint32_t)(C::kSfAt + 2 * groups * kSfBlock));
-        load_codes<BN>(st, full, &wmap, &xmap, (int)(f * kLaneRows), (int)(tok * BN), kb);
+        load_codes(st, full, &wmap, &xmap, (int)(f * kLaneRows), (int)(tok * BN), kb);
         load_scales(st + C::kSfAt, full, a.sfb + f * sf_row, a.sfa + tok * BN / 128 * sf_row, sf_row, kb, groups, 1);
         if (++kb == K.n) {
           kb = 0;
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // no copy may land after the block has gone: wait for the last fill of every stage
       const int64_t g = u - u0;
-      for (int64_t j = g > C::kStages ? g - C::kStages : 0; j < g; ++j)
+      for (int64_t j = g > C::kStages ? g - C::kStages : 0; j < g && kCopies; ++j)
         tma::wait(full0 + 8 * (int)(j % C::kStages), (uint32_t)(j / C::kStages) & 1u);
     }
   } else if (warp == kMmaWarp) {

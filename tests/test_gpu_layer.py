@@ -593,6 +593,34 @@ def test_linear_empty_and_refusals():
         nv.nvfp4_linear(q, s, a[2], q, s, a[2])
 
 
+@pytest.mark.parametrize("M,N", [(5, 300), (1100, 2600)])
+def test_linear_wait_timeout_is_reported_and_the_context_stays_usable(M, N):
+    """Both kernels in a build whose copies are never issued (test-only
+    library): every bounded wait runs out, the kernel reports
+    NVFP4_ERR_PIPELINE and gives its tensor memory back, and the next call on the
+    same context is correct."""
+    import ctypes
+    from nvfp4_bit_block_gb300.build import build_layer_selftest
+    L = ctypes.CDLL(build_layer_selftest())
+    p, i64 = ctypes.c_void_p, ctypes.c_int64
+    L.nvfp4_test_linear_no_copies.argtypes = [p] * 6 + [i64] * 3 + [p] * 5
+    L.nvfp4_test_linear_no_copies_workspace.argtypes = [i64] * 3
+    L.nvfp4_test_linear_no_copies_workspace.restype = i64
+    K = 2048
+    a, b = operand(M, K, 120), operand(N, K, 121)
+    ws = torch.empty(max(16, L.nvfp4_test_linear_no_copies_workspace(M, N, K)), dtype=torch.uint8, device="cuda")
+    d, res = torch.zeros((M, N), dtype=BF, device="cuda"), rand((M, N), BF, 122)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert L.nvfp4_test_linear_no_copies(*[t.data_ptr() for t in (*a, *b)], M, N, K, res.data_ptr(), d.data_ptr(),
+                                         ws.data_ptr(), status.data_ptr(), None) == 0
+    torch.cuda.synchronize()
+    assert int(status.item()) == -8
+    status.zero_()
+    r = nv.nvfp4_linear(*a, *b, residual=res, status=status)
+    assert int(status.item()) == 0
+    check_linear(a, b, K, r, residual=res)
+
+
 # ---------------------------------------------------------------- all of them
 
 
