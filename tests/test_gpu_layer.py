@@ -712,3 +712,22 @@ def test_offsets_beyond_32_bits():
     a, b = operand(M, 64, 100), operand(N, 64, 101)
     d = nv.nvfp4_linear(*a, *b, residual=x)
     assert torch.equal(nv.nvfp4_linear(*a, *b, residual=xv, out=ov).d, d.d)
+
+
+# ---------------------------------------------------------------- together
+
+
+def test_feed_forward_example():
+    """All operators with the quantizer in one block, forward, backward and for
+    one token, against the same block in fp32.  Rounding to the E2M1 grid costs a
+    normal operand about a tenth of its norm, a product of two of them 0.14, and
+    the deepest gradient here has three such products behind it: below 0.14 *
+    sqrt(3) + the norms' own; a wrong operand, layout or gradient is off by 1."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "feed_forward.py")
+    spec = importlib.util.spec_from_file_location("feed_forward", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    for name, v in m.run(288, 640, 1536).items():
+        assert v <= 0.35, (name, v)
