@@ -72,7 +72,33 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Steps K(a.K);
   const int64_t u0 = cut.begin(blockIdx.x), u1 = cut.begin((int64_t)blockIdx.x + 1);
 
-  if (tid == 0) {
+  // The loads of this piece, continued by the loading thread from where it left off.
+  int64_t u = u0, f = u0 / K.n, tok = f / cut.tiles_f;
+  int kb = (int)(u0 - f * K.n);
+  f -= tok * cut.tiles_f;
+  Ring<C::kStages> fill;
+  const int64_t sf_row = (a.K + 63) / 64 * kSfBlock;  // scale bytes of a 128-row band
+  auto load_next = [&]() {
+    const uint32_t st = smem_u32(smem + fill.slot * C::kStageBytes), full = full0 + 8 * fill.slot;
+    const int groups = K.groups(kb);
+    tma::arrive_expect_tx(full, (uint32_t)(C::kSfAt + 2 * groups * kSfBlock));
+    load_codes(st, full, &wmap, &xmap, (int)(f * kLaneRows), (int)(tok * BN), kb);
+    load_scales(st + C::kSfAt, full, a.sfb + f * sf_row, a.sfa + tok * BN / 128 * sf_row, sf_row, kb, groups, 1);
+    if (++kb == K.n) {
+      kb = 0;
+      if (++f == cut.tiles_f) {
+        f = 0;
+        ++tok;
+      }
+    }
+    ++u;
+    fill.next();
+  };
+
+  // The setup may run beside the end of the kernel before this one; from griddepcontrol.wait on memory is read and
+  // written, and the second kernel may start its own setup.  The first two stages are on their way before the rest of
+  // the block is ready (more would keep it waiting).
+  if (warp == kLoadWarp && lane == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       tma::mbar_init(full0 + 8 * s, 1);
       tma::mbar_init(empty0 + 8 * s, 1);
@@ -85,6 +111,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma::mbar_init(drain, 1);
     *stop = 0;
     tma::fence_barrier_init();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    while (u < u1 && u - u0 < 2) load_next();
   }
   if (warp == kMmaWarp) {
     tc5::alloc(smem_u32(tmem_slot), C::kTmemCols);
@@ -93,8 +121,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc5::fence_before_thread_sync();
   __syncthreads();
   tc5::fence_after_thread_sync();
-  // The setup above may run beside the end of the kernel before this one; what follows reads and writes memory.  The
-  // second kernel may start its own setup from here on.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0 && blockIdx.x == 0 && a.amax) a.amax[0] = a.amax[1] = 0.0f;  // the second kernel joins its maxima to it
@@ -102,25 +128,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kLoadWarp) {
     if (lane == 0) {
-      const int64_t sf_row = (a.K + 63) / 64 * kSfBlock;  // scale bytes of a 128-row band
-      Ring<C::kStages> r;
-      int64_t tile = u0 / K.n, u = u0;
-      int kb = (int)(u0 - tile * K.n);
-      for (; u < u1; ++u, r.next()) {
-        if (u - u0 >= C::kStages && !tma::wait(empty0 + 8 * r.slot, r.phase ^ 1u)) {
+      while (u < u1) {
+        if (u - u0 >= C::kStages && !tma::wait(empty0 + 8 * fill.slot, fill.phase ^ 1u)) {
           *stop = 1;
           break;
         }
-        const int64_t f = tile % cut.tiles_f, tok = tile / cut.tiles_f;
-        const uint32_t st = smem_u32(smem + r.slot * C::kStageBytes), full = full0 + 8 * r.slot;
-        const int groups = K.groups(kb);
-        tma::arrive_expect_tx(full, (uint32_t)(C::kSfAt + 2 * groups * kSfBlock));
-        load_codes(st, full, &wmap, &xmap, (int)(f * kLaneRows), (int)(tok * BN), kb);
-        load_scales(st + C::kSfAt, full, a.sfb + f * sf_row, a.sfa + tok * BN / 128 * sf_row, sf_row, kb, groups, 1);
-        if (++kb == K.n) {
-          kb = 0;
-          ++tile;
-        }
+        load_next();
       }
       // no copy may land after the block has gone: wait for the last fill of every stage
       const int64_t g = u - u0;
