@@ -101,18 +101,18 @@ __device__ __forceinline__ void add16(uint4 w, float* v, float) {
   v[3] += __uint_as_float(w.w);
 }
 
-// Largest magnitude of NV values after rounding; only the first `cols` are outputs.
-template <int NV, typename T>
-__device__ __forceinline__ uint32_t top_of(const float* v, int64_t cols, uint32_t top) {
-  if (cols >= NV) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) top = max(top, abs_bits(to_f32(from_f32<T>(v[i]))));
-  } else {
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (i < cols) top = max(top, abs_bits(to_f32(from_f32<T>(v[i]))));
-  }
-  return top;
+// Largest magnitude among 16 bytes of outputs, joined to `top` (NaN is the largest).
+__device__ __forceinline__ uint32_t top16(uint4 w, uint32_t top, bf16) {
+  uint32_t m;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(w.x), "r"(w.y));
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(w.z));
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(w.w));
+  m &= 0x7FFF7FFFu;
+  return max(top, max(m << 16, m & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint32_t top16(uint4 w, uint32_t top, float) {
+  const uint32_t k = 0x7FFFFFFFu;
+  return max(max(top, max(w.x & k, w.y & k)), max(w.z & k, w.w & k));
 }
 
 // v = product * scale + bias.
@@ -121,10 +121,12 @@ __device__ __forceinline__ void affine(float* v, const float* bias, float scale)
 #pragma unroll
   for (int i = 0; i < NV; i += 4) {
     const float4 b = *reinterpret_cast<const float4*>(bias + i);
-    v[i] = fmaf(v[i], scale, b.x);
-    v[i + 1] = fmaf(v[i + 1], scale, b.y);
-    v[i + 2] = fmaf(v[i + 2], scale, b.z);
-    v[i + 3] = fmaf(v[i + 3], scale, b.w);
+    const float2 lo = fma2(make_float2(v[i], v[i + 1]), splat2(scale), make_float2(b.x, b.y));
+    const float2 hi = fma2(make_float2(v[i + 2], v[i + 3]), splat2(scale), make_float2(b.z, b.w));
+    v[i] = lo.x;
+    v[i + 1] = lo.y;
+    v[i + 2] = hi.x;
+    v[i + 3] = hi.y;
   }
 }
 
@@ -338,9 +340,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (col + c * kCols >= a.N) break;
           float* v = r + c * kCols;
           affine<kCols>(v, bias + c * kCols, scale);
+          uint32_t most = 0;
           auto put = [&](const CUtensorMap* map, uint8_t* b) {  // v, rounded, through buffer b
 #pragma unroll
-            for (int i = 0; i < kRow / 16; ++i) *piece(b, lane, i) = pack16(v + i * kPer, T());
+            for (int i = 0; i < kRow / 16; ++i) {
+              const uint4 w = pack16(v + i * kPer, T());
+              *piece(b, lane, i) = w;
+              most = top16(w, i == 0 ? 0u : most, T());
+            }
             fence_async_smem();
             __syncwarp();
             if (lane == 0) store_2d(map, (int)(col + c * kCols), (int)row0, smem_u32(b));
@@ -365,7 +372,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             put(&dmap, next_buffer());
           }
-          if (a.amax && row < a.M) top = top_of<kCols, T>(v, a.N - col - c * kCols, top);
+          if (a.amax && row < a.M) {
+            const int64_t left = a.N - col - c * kCols;
+            if (left < kCols) {  // only these are outputs
+              most = 0;
+#pragma unroll
+              for (int i = 0; i < kCols; ++i)
+                if (i < left) most = max(most, abs_bits(to_f32(from_f32<T>(v[i]))));
+            }
+            top = max(top, most);
+          }
         }
       } else if (row < a.M) {
 #pragma unroll

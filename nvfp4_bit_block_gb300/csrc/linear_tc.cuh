@@ -244,26 +244,53 @@ __device__ __forceinline__ void mma2_stage(uint32_t acc, uint32_t sf_tmem, Stage
   }
 }
 
+// act on pairs with the packed fp32 instructions: the operations of act_value in
+// its order, so with its results.
+__device__ __forceinline__ float2 splat2(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 gate2(float2 z, float2 neg) {  // z / (1 + 2^neg)
+  const float2 e = add2(make_float2(ex2(neg.x), ex2(neg.y)), splat2(1.0f));
+  return mul2(z, make_float2(rcp(e.x), rcp(e.y)));
+}
+template <int ACT>
+__device__ __forceinline__ float2 act_pair(float2 z) {
+  if constexpr (ACT == NVFP4_ACT_RELU) {
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(z.x) : "f"(z.x));
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(z.y) : "f"(z.y));
+    return z;
+  } else if constexpr (ACT == NVFP4_ACT_GELU_TANH) {
+    return gate2(z, mul2(z, fma2(mul2(z, z), splat2(-kLog2e * kGeluC * kGeluA), splat2(-kLog2e * kGeluC))));
+  } else if constexpr (ACT == NVFP4_ACT_SILU) {
+    return gate2(z, mul2(z, splat2(-kLog2e)));
+  } else {
+    const float2 x = mul2(make_float2(fabsf(z.x), fabsf(z.y)), splat2(kRsqrt2));
+    const float2 d = fma2(splat2(0.3275911f), x, splat2(1.0f)), y = mul2(mul2(splat2(-kLog2e), x), x);
+    const float2 t = make_float2(rcp(d.x), rcp(d.y)), e = make_float2(ex2(y.x), ex2(y.y));
+    float2 q = fma2(splat2(1.061405429f), t, splat2(-1.453152027f));
+    q = fma2(q, t, splat2(1.421413741f));
+    q = fma2(q, t, splat2(-0.284496736f));
+    q = fma2(q, t, splat2(0.254829592f));
+    q = mul2(mul2(mul2(splat2(0.5f), q), t), e);
+    const float2 r = sub2(splat2(1.0f), q);
+    return mul2(z, make_float2(z.x < 0.0f ? q.x : r.x, z.y < 0.0f ? q.y : r.y));
+  }
+}
+template <int NV, int ACT>
+__device__ __forceinline__ void act_each(float* v) {
+#pragma unroll
+  for (int i = 0; i < NV; i += 2) {
+    const float2 r = act_pair<ACT>(make_float2(v[i], v[i + 1]));
+    v[i] = r.x;
+    v[i + 1] = r.y;
+  }
+}
 // act over a register array, the choice taken once.
 template <int NV>
 __device__ __forceinline__ void act_all(float* v, int act) {
   switch (act) {
-    case NVFP4_ACT_RELU:
-#pragma unroll
-      for (int i = 0; i < NV; ++i) v[i] = act_value(v[i], NVFP4_ACT_RELU);
-      break;
-    case NVFP4_ACT_GELU:
-#pragma unroll
-      for (int i = 0; i < NV; ++i) v[i] = act_value(v[i], NVFP4_ACT_GELU);
-      break;
-    case NVFP4_ACT_GELU_TANH:
-#pragma unroll
-      for (int i = 0; i < NV; ++i) v[i] = act_value(v[i], NVFP4_ACT_GELU_TANH);
-      break;
-    case NVFP4_ACT_SILU:
-#pragma unroll
-      for (int i = 0; i < NV; ++i) v[i] = act_value(v[i], NVFP4_ACT_SILU);
-      break;
+    case NVFP4_ACT_RELU: act_each<NV, NVFP4_ACT_RELU>(v); break;
+    case NVFP4_ACT_GELU: act_each<NV, NVFP4_ACT_GELU>(v); break;
+    case NVFP4_ACT_GELU_TANH: act_each<NV, NVFP4_ACT_GELU_TANH>(v); break;
+    case NVFP4_ACT_SILU: act_each<NV, NVFP4_ACT_SILU>(v); break;
     default: break;
   }
 }
