@@ -9,9 +9,10 @@
 namespace nvfp4 {
 namespace lin {
 
-// Few tokens: tiles of 128 features x bn tokens (16, 32 or 64 for at most as many tokens, else 128), K split over the
-// SMs; split_workspace bytes at a.ws.
-cudaError_t launch_split(const LinearArgs& a, int bn, cudaStream_t s);
+// Few tokens: tiles of 128 features x bn tokens.  Either K is split over the SMs (bn 16, 32 or 64 for at most as many
+// tokens, else 128; split_workspace bytes at a.ws; amax), or the tiles are whole (bn 16 or 32 for at most as many
+// tokens, else 64; no workspace, no amax).
+cudaError_t launch_split(const LinearArgs& a, int bn, bool whole, cudaStream_t s);
 int64_t split_workspace(int64_t M, int64_t N, int64_t K, int bn);
 // Many tokens: pairs of blocks walk tiles of 256 tokens x 256 features.
 cudaError_t launch_many(const LinearArgs& a, cudaStream_t s);

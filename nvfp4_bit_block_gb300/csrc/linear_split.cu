@@ -11,8 +11,11 @@
 // memory holds (200 KB on its way per SM).  A piece leaves the sums of each tile
 // that it touches (usually two) in the workspace, and a second, small kernel adds
 // the pieces of a tile in order and applies the epilogue; it is launched early
-// and waits for the first.
+// and waits for the first.  Where the product is so small that whole tiles take
+// an SM no longer than that second kernel does, the cuts are between tiles, the
+// first kernel applies the epilogue and there is no second.
 #include <algorithm>
+#include <type_traits>
 
 #include "linear_launch.h"
 #include "linear_tc.cuh"
@@ -41,11 +44,15 @@ struct Cfg {
 };
 
 // The work in steps of K: `steps` per output tile, `tiles` of them, cut into `pieces`;
-// piece p begins at step floor(tiles * steps * p / pieces).
+// piece p begins at step floor(tiles * steps * p / pieces), or with whole tiles
+// at tile floor(tiles * p / pieces).
 struct Cut {
   int64_t tiles, tiles_f;   // output tiles; of them per token tile
   int steps, pieces, most;  // most: pieces that touch a tile at most
-  __host__ __device__ int64_t begin(int64_t piece) const { return tiles * steps * piece / pieces; }
+  int whole;                // cuts between tiles only
+  __host__ __device__ int64_t begin(int64_t piece) const {
+    return whole ? tiles * piece / pieces * steps : tiles * steps * piece / pieces;
+  }
   // The piece that holds this step: the last p with begin(p) <= step.
   __device__ int piece_of(int64_t step) const {
     const uint64_t n = (uint64_t)(step + 1) * (uint32_t)pieces - 1, d = (uint64_t)tiles * (uint32_t)steps;
@@ -53,7 +60,33 @@ struct Cut {
   }
 };
 
-template <int BN>
+// Epilogue of feature n of `count` (at most 16) tokens from m on, `v` holding the products.
+template <typename T>
+__device__ __forceinline__ void put_tokens(const LinearArgs& a, int64_t m, int64_t n, int count, float* v, float scale,
+                                           float bias) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = fmaf(v[i], scale, bias);
+  if (a.z) {
+    T* z = static_cast<T*>(a.z) + m * a.ldz + n;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < count) z[i * a.ldz] = from_f32<T>(v[i]);
+  }
+  act_all<16>(v, a.act);
+  if (a.residual) {
+    const T* r = static_cast<const T*>(a.residual) + m * a.ldr + n;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < count) v[i] += to_f32(r[i * a.ldr]);
+  }
+  T* d = static_cast<T*>(a.d) + m * a.ldd + n;
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (i < count) d[i * a.ldd] = from_f32<T>(v[i]);
+}
+
+// T: type of d where the tiles are whole; void where their sums go to the workspace.
+template <int BN, typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_split_kernel(const LinearArgs a, const __grid_constant__ CUtensorMap wmap,
                         const __grid_constant__ CUtensorMap xmap, const Cut cut) {
@@ -123,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc5::fence_after_thread_sync();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (tid == 0 && blockIdx.x == 0 && a.amax) a.amax[0] = a.amax[1] = 0.0f;  // the second kernel joins its maxima to it
+  if (std::is_void<T>::value && tid == 0 && blockIdx.x == 0 && a.amax) a.amax[0] = a.amax[1] = 0.0f;  // the second kernel joins its maxima to it
   const uint32_t tmem = *tmem_slot;
 
   if (warp == kLoadWarp) {
@@ -144,9 +177,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       Ring<C::kStages> r;
       Ring<2> acc;
-      int64_t u = u0;
-      int kb = (int)(u0 % K.n), n = 0;
+      int64_t u = u0, tile = u0 / K.n;
+      int kb = (int)(u0 - tile * K.n), n = 0;
       while (u < u1 && !*stop) {  // one tile's part
+        const uint32_t shift = (uint32_t)(tile / cut.tiles_f * BN % 128 / 32);
         // its accumulator has been read out
         if (n >= 2 && !tma::wait(acce0 + 8 * acc.slot, acc.phase ^ 1u)) *stop = 1;
         bool fresh = true, last = false;
@@ -156,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           tc5::fence_after_thread_sync();
-          mma_stage<BN>(tmem + (uint32_t)(acc.slot * BN), tmem + 2 * BN + (uint32_t)r.slot * C::kSfCols,
+          mma_stage<BN>(tmem + (uint32_t)(acc.slot * BN), tmem + 2 * BN + (uint32_t)r.slot * C::kSfCols, shift,
                         StageDesc(smem_u32(smem + r.slot * C::kStageBytes)), K.groups(kb), fresh);
           tc5::commit(empty0 + 8 * r.slot);
           fresh = false;
@@ -164,6 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (*stop) break;
         kb = 0;
+        ++tile;
         tc5::commit(accf0 + 8 * acc.slot);
         acc.next();
         ++n;
@@ -198,16 +233,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc5::fence_after_thread_sync();
       const int64_t t0 = tile / cut.tiles_f * BN;
       const int tokens = (int)(a.M - t0 < BN ? a.M - t0 : BN);
-      const int part = (int)blockIdx.x - cut.piece_of(tile * cut.steps);
-      float* out = a.ws + ((tile * cut.most + part) * BN) * kLaneRows + tid;
+      float* out = nullptr;
+      const int64_t n = tile % cut.tiles_f * kLaneRows + tid;
+      float scale = 0.0f, bias = 0.0f;
+      if constexpr (std::is_void<T>::value) {
+        const int part = (int)blockIdx.x - cut.piece_of(tile * cut.steps);
+        out = a.ws + ((tile * cut.most + part) * BN) * kLaneRows + tid;
+      } else {
+        scale = a.alpha_a[0] * a.alpha_b[0];
+        if (a.bias && n < a.N) bias = load_as_f32(a.bias, n, a.bias_bf16);
+      }
 #pragma unroll 1
       for (int c = 0; c < tokens; c += 16) {
         uint32_t v[16];
         ld_32x32b_x16(tmem + (uint32_t)(acc.slot * BN + c) + ((uint32_t)(32 * warp) << 16), v);
         tc5::wait_ld();
+        if constexpr (std::is_void<T>::value) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (c + i < tokens) out[(int64_t)(c + i) * kLaneRows] = __uint_as_float(v[i]);
+          for (int i = 0; i < 16; ++i)
+            if (c + i < tokens) out[(int64_t)(c + i) * kLaneRows] = __uint_as_float(v[i]);
+        } else if (n < a.N) {
+          put_tokens<T>(a, t0 + c, n, tokens - c, reinterpret_cast<float*>(v), scale, bias);
+        }
       }
       tc5::fence_before_thread_sync();
       __syncwarp();
@@ -269,22 +316,24 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const LinearArgs a, co
   if (a.amax) put_amax(a.amax, top);
 }
 
-Cut cut_of(int64_t M, int64_t N, int64_t K, int bn) {
+Cut cut_of(int64_t M, int64_t N, int64_t K, int bn, bool whole) {
   Cut c;
   c.tiles_f = (N + kLaneRows - 1) / kLaneRows;
   c.tiles = c.tiles_f * ((M + bn - 1) / bn);
   c.steps = (int)((K + kBK - 1) / kBK);
-  c.pieces = (int)std::min<int64_t>(152, c.tiles * c.steps);
+  c.pieces = (int)std::min<int64_t>(152, whole ? c.tiles : c.tiles * c.steps);
   // a tile's steps meet at most this many pieces of at least floor(tiles * steps / pieces) steps
   const int64_t least = c.tiles * c.steps / c.pieces;
-  c.most = (int)((c.steps + least - 2) / least + 1);
+  c.most = whole ? 1 : (int)((c.steps + least - 2) / least + 1);
+  c.whole = whole ? 1 : 0;
   return c;
 }
 
-template <int BN>
+template <int BN, typename T>
 cudaError_t launch(const LinearArgs& a, cudaStream_t s) {
   using C = Cfg<BN>;
-  auto kern = linear_split_kernel<BN>;
+  constexpr bool kWhole = !std::is_void<T>::value;
+  auto kern = linear_split_kernel<BN, T>;
   static std::atomic<int> cache[64] = {};
   int cap = 0;
   cudaError_t e = resident_grid(kern, kThreads, C::kSmem, cache, cap);  // opts in to the shared memory
@@ -294,7 +343,7 @@ cudaError_t launch(const LinearArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = make_codes_map(&xmap, a.qa, a.M, a.K / 2, kBK / 2, BN);
   if (e != cudaSuccess) return e;
-  const Cut cut = cut_of(a.M, a.N, a.K, BN);
+  const Cut cut = cut_of(a.M, a.N, a.K, BN, kWhole);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -306,7 +355,7 @@ cudaError_t launch(const LinearArgs& a, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kern, a, wmap, xmap, cut);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || kWhole) return e;
   const int tokens = (int)std::min<int64_t>(a.M, BN);
   const int ty = tokens >= 8 ? 8 : tokens;
   cfg.gridDim = dim3((unsigned)cut.tiles, (unsigned)((tokens + ty - 1) / ty));
@@ -316,19 +365,25 @@ cudaError_t launch(const LinearArgs& a, cudaStream_t s) {
                     : cudaLaunchKernelEx(&cfg, linear_join_kernel<float>, a, cut, BN);
 }
 
+template <int BN>
+cudaError_t launch_cut(const LinearArgs& a, bool whole, cudaStream_t s) {
+  if (!whole) return launch<BN, void>(a, s);
+  return a.out_bf16 ? launch<BN, bf16>(a, s) : launch<BN, float>(a, s);
+}
+
 }  // namespace
 
 int64_t split_workspace(int64_t M, int64_t N, int64_t K, int bn) {
-  const Cut c = cut_of(M, N, K, bn);
+  const Cut c = cut_of(M, N, K, bn, false);
   return c.tiles * c.most * bn * kLaneRows * 4;
 }
 
-cudaError_t launch_split(const LinearArgs& a, int bn, cudaStream_t s) {
+cudaError_t launch_split(const LinearArgs& a, int bn, bool whole, cudaStream_t s) {
   switch (bn) {
-    case 16: return launch<16>(a, s);
-    case 32: return launch<32>(a, s);
-    case 64: return launch<64>(a, s);
-    default: return launch<128>(a, s);
+    case 16: return launch_cut<16>(a, whole, s);
+    case 32: return launch_cut<32>(a, whole, s);
+    case 64: return launch_cut<64>(a, whole, s);
+    default: return launch<128, void>(a, s);
   }
 }
 
