@@ -47,6 +47,7 @@ constexpr int kSmem = kStages * kStageBytes + kStageOut + kBN * 4 /* bias */ + 5
 constexpr uint32_t kSfCols = 16 + 16 * kBands;
 constexpr uint32_t kTmemCols = 512;
 static_assert(kBN + kStages * kSfCols <= kTmemCols, "TMEM columns");
+static_assert(2 * kBox == 32 * 32 * 4, "a warp's staging buffers hold a square of 32 x 32 values");
 static_assert(kStageBytes % 1024 == 0 && 8 * (kBars + 2) <= 512 && kSmem <= 232448, "shared memory");
 
 // Named barrier of `threads` threads; true if `v` holds in all of them.
@@ -130,28 +131,52 @@ __device__ __forceinline__ void affine(float* v, const float* bias, float scale)
   }
 }
 
-// Outputs that cannot go through a tensor map (rows that are not 16-byte
-// aligned), or a z beside a residual: 32 consecutive features of one token.
+// Outputs that cannot go through a tensor map (rows that are not 16-byte aligned),
+// or a z beside a residual: 32 rows x 32 features of a warp.  `v` is this lane's
+// row of products; through `tile` (32 x 32 values, element (r, c) at column c ^ r, so
+// that neither its rows nor its columns meet in a bank) the lanes become columns
+// and each access to memory is a piece of one row.  (With a row per lane and
+// scalar accesses, 4096 x 20479 x 5120 took 798 us instead of 160.)
 template <typename T>
-__device__ __forceinline__ uint32_t put32(const LinearArgs& a, int64_t m, int64_t n, float* v, uint32_t top) {
-  const int cols = a.N - n < 32 ? (int)(a.N - n) : 32;
-  if (a.z) {
-    T* p = static_cast<T*>(a.z) + m * a.ldz + n;
+__device__ __forceinline__ uint32_t put_square(const LinearArgs& a, int64_t row0, int64_t n, const float* v, float* tile,
+                                               float bias, float scale, uint32_t top) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (i < cols) p[i] = from_f32<T>(v[i]);
-  }
-  act_all<32>(v, a.act);
-  const T* res = a.residual ? static_cast<const T*>(a.residual) + m * a.ldr + n : nullptr;
-  T* p = static_cast<T*>(a.d) + m * a.ldd + n;
+  for (int c = 0; c < 32; ++c) tile[lane * 32 + (c ^ lane)] = v[c];
+  __syncwarp();
+  const int rows = a.M - row0 < 32 ? (int)(a.M - row0) : 32;
+  if (n + lane < a.N) {
+    T* d = static_cast<T*>(a.d) + row0 * a.ldd + n + lane;
+    T* z = a.z ? static_cast<T*>(a.z) + row0 * a.ldz + n + lane : nullptr;
+    const T* res = a.residual ? static_cast<const T*>(a.residual) + row0 * a.ldr + n + lane : nullptr;
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += 8) {
+      float w[8];
+      T add[8];
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    if (i < cols) {
-      const T o = from_f32<T>(v[i] + (res ? to_f32(res[i]) : 0.0f));
-      p[i] = o;
-      top = max(top, abs_bits(to_f32(o)));
+      for (int i = 0; i < 8; ++i) {
+        add[i] = from_f32<T>(0.0f);
+        if (res && r0 + i < rows) add[i] = res[(r0 + i) * a.ldr];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = fmaf(tile[(r0 + i) * 32 + (lane ^ (r0 + i))], scale, bias);
+      if (z) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (r0 + i < rows) z[(r0 + i) * a.ldz] = from_f32<T>(w[i]);
+      }
+      act_all<8>(w, a.act);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (r0 + i < rows) {
+          const T o = from_f32<T>(w[i] + to_f32(add[i]));
+          d[(r0 + i) * a.ldd] = o;
+          top = max(top, abs_bits(to_f32(o)));
+        }
+      }
     }
   }
+  __syncwarp();
   return top;
 }
 
@@ -383,14 +408,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             top = max(top, most);
           }
         }
-      } else if (row < a.M) {
+      } else {
 #pragma unroll
-        for (int c = 0; c < kHalf; c += 32) {
-          if (col + c < a.N) {
-            affine<32>(r + c, bias + c, scale);
-            top = put32<T>(a, row, col + c, r + c, top);
-          }
-        }
+        for (int c = 0; c < kHalf; c += 32)
+          if (col + c < a.N) top = put_square<T>(a, row0, col + c, r + c, reinterpret_cast<float*>(buf), bias[c + lane], scale, top);
       }
     }
     if (lane == 0) stores_done();

@@ -281,37 +281,35 @@ __device__ __forceinline__ uint32_t put(const LinearArgs& a, int64_t m, int64_t 
   return abs_bits(to_f32(o));
 }
 
-// The pieces of output tile blockIdx.x added in order: a thread takes four features of a token.
+// The pieces of output tile blockIdx.x added in order: a thread takes four features
+// of a token, 32 apart, so that every access is a piece of one row whatever its
+// alignment.
 template <typename T>
 __global__ void __launch_bounds__(256) linear_join_kernel(const LinearArgs a, const Cut cut, int bn) {
   const int64_t tile = blockIdx.x, f = tile % cut.tiles_f, tok = tile / cut.tiles_f;
-  const int64_t m = tok * bn + (int64_t)blockIdx.y * blockDim.y + threadIdx.y, n = f * kLaneRows + 4 * threadIdx.x;
+  const int64_t m = tok * bn + (int64_t)blockIdx.y * blockDim.y + threadIdx.y, n = f * kLaneRows + threadIdx.x;
   const bool there = m < a.M && m < (tok + 1) * bn;
   float bias[4] = {};
   if (a.bias) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (n + i < a.N) bias[i] = load_as_f32(a.bias, n + i, a.bias_bf16);
+      if (n + 32 * i < a.N) bias[i] = load_as_f32(a.bias, n + 32 * i, a.bias_bf16);
   }
   const float scale = a.alpha_a[0] * a.alpha_b[0];
   const int parts = cut.piece_of((tile + 1) * cut.steps - 1) - cut.piece_of(tile * cut.steps) + 1;
-  const float* in = a.ws + (tile * cut.most * bn + (m - tok * bn)) * kLaneRows + 4 * threadIdx.x;
+  const float* in = a.ws + (tile * cut.most * bn + (m - tok * bn)) * kLaneRows + threadIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   uint32_t top = 0;
   if (there) {
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float v[4] = {};
 #pragma unroll 4
     for (int p = 0; p < parts; ++p) {
-      const float4 w = *reinterpret_cast<const float4*>(in + (int64_t)p * bn * kLaneRows);
-      v.x += w.x;
-      v.y += w.y;
-      v.z += w.z;
-      v.w += w.w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += in[(int64_t)p * bn * kLaneRows + 32 * i];
     }
-    const float s[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (n + i < a.N) top = max(top, put<T>(a, m, n + i, fmaf(s[i], scale, bias[i])));
+      if (n + 32 * i < a.N) top = max(top, put<T>(a, m, n + 32 * i, fmaf(v[i], scale, bias[i])));
   }
   if (a.amax) put_amax(a.amax, top);
 }
