@@ -92,17 +92,37 @@ __device__ __forceinline__ void to_pairs(const Raw<T, 8> (&raw)[NC], float2 (&f)
 // R neighbouring rows at a time, which share a barrier, the sums' exchanges and the
 // loop's overhead.  S times R rows of each group are in shared memory or on their
 // way there; dy and x are read from it again after the sums instead of being
-// kept in registers.  16-byte aligned rows.
-template <typename DT, typename XT, int NC, int R, int S, bool RES, int THREADS, int BLOCKS>
-__global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_kernel(const NormGradArgs a, int group_threads) {
+// kept in registers.  ODD: the rows are one of `period` classes, of class
+// blockIdx.x mod period; the values of the neighbouring rows in the row's first
+// and last chunk count as zeros.
+template <typename DT, typename XT, int NC, int R, int S, bool RES, int THREADS, int BLOCKS, bool ODD>
+__global__ void __launch_bounds__(THREADS, BLOCKS)
+    norm_grad_kernel(const NormGradArgs args, int group_threads, int row_classes) {
   constexpr int P = NC * 4, K = R == 3 ? 8 : 2 * R;  // sums of a round, a power of two
   extern __shared__ uint4 ring[];
   __shared__ float buf[2][THREADS / 32 * K];
-  const int N = (int)a.N;
+  const int period = ODD ? row_classes : 1;
+  const RowClass own(period, ODD ? (int)(blockIdx.x % period) : 0, args.ldx, args.M);
+  NormGradArgs moved;
+  const NormGradArgs& a = ODD ? moved : args;
+  if (ODD) {
+    moved = args;
+    moved.dy = static_cast<const DT*>(args.dy) + own.start(args.lddy);
+    moved.x = static_cast<const XT*>(args.x) + own.start(args.ldx);
+    if (RES) moved.dres = static_cast<const XT*>(args.dres) + own.start(args.lddres);
+    moved.dx = static_cast<XT*>(args.dx) + own.start(args.lddx);
+    moved.lddy *= period;
+    moved.ldx *= period;
+    moved.lddres *= period;
+    moved.lddx *= period;
+    moved.M = own.rows;
+  }
+  const int skip = ODD ? own.shift : 0, N = (int)a.N + skip;  // the row is columns skip .. N - 1
   const int warps = group_threads >> 5, group = (int)threadIdx.x / group_threads, ngroups = (int)blockDim.x / group_threads;
   const int t = (int)threadIdx.x - group * group_threads;
-  const int64_t step = (int64_t)gridDim.x * ngroups * R, first = ((int64_t)blockIdx.x * ngroups + group) * R;
-  const float inv = 1.0f / (float)N;
+  const int64_t step = (int64_t)(gridDim.x / period) * ngroups * R;
+  const int64_t first = ((int64_t)(blockIdx.x / period) * ngroups + group) * R;
+  const float inv = 1.0f / (float)a.N;
   // this thread's slots: per stage and row NC chunks of dy, of x and of dres, each blockDim.x apart
   constexpr uint32_t kDy = sizeof(Raw<DT, 8>), kX = sizeof(Raw<XT, 8>);
   const uint32_t threads = blockDim.x, at_x = NC * threads * kDy, at_res = at_x + NC * threads * kX;
@@ -123,10 +143,17 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_kernel(const NormGr
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
           const int off = 8 * i * group_threads;
-          const bool there = 8 * t + off < N;
-          copy_chunk<DT>(my_dy + at + i * threads * kDy, dy + q * a.lddy, off, there);
-          copy_chunk<XT>(my_x + at + i * threads * kX, x + q * a.ldx, off, there);
-          if constexpr (RES) copy_chunk<XT>(my_x + (at_res - at_x) + at + i * threads * kX, res + q * a.lddres, off, there);
+          if constexpr (ODD) {
+            const int there = N - 8 * t - off;
+            copy_part<DT>(my_dy + at + i * threads * kDy, dy + q * a.lddy, off, there);
+            copy_part<XT>(my_x + at + i * threads * kX, x + q * a.ldx, off, there);
+            if constexpr (RES) copy_part<XT>(my_x + (at_res - at_x) + at + i * threads * kX, res + q * a.lddres, off, there);
+          } else {
+            const bool there = 8 * t + off < N;
+            copy_chunk<DT>(my_dy + at + i * threads * kDy, dy + q * a.lddy, off, there);
+            copy_chunk<XT>(my_x + at + i * threads * kX, x + q * a.ldx, off, there);
+            if constexpr (RES) copy_chunk<XT>(my_x + (at_res - at_x) + at + i * threads * kX, res + q * a.lddres, off, there);
+          }
         }
       }
     }
@@ -138,7 +165,12 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_kernel(const NormGr
   };
   float2 gamma[P], dg[P], db[P];
 #pragma unroll
-  for (int i = 0; i < NC; ++i) load_weights2(a.gamma, a.w_bf16, 8 * (t + i * group_threads), N, 1.0f, gamma + 4 * i);
+  for (int i = 0; i < NC; ++i) {
+    if (ODD)
+      load_weights_part(a.gamma, a.w_bf16, 8 * (t + i * group_threads) - skip, (int)a.N, 1.0f, gamma + 4 * i);
+    else
+      load_weights2(a.gamma, a.w_bf16, 8 * (t + i * group_threads), N, 1.0f, gamma + 4 * i);
+  }
 #pragma unroll
   for (int p = 0; p < P; ++p) dg[p] = db[p] = splat(0.0f);
 #pragma unroll
@@ -147,8 +179,8 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_kernel(const NormGr
   auto load_stats = [&](int64_t r) {
 #pragma unroll
     for (int q = 0; q < R; ++q) {
-      mean[q] = r + q < a.M ? a.mean[r + q] : 0.0f;
-      rstd[q] = r + q < a.M ? a.rstd[r + q] : 0.0f;
+      mean[q] = r + q < a.M ? a.mean[(r + q) * period + own.j] : 0.0f;
+      rstd[q] = r + q < a.M ? a.rstd[(r + q) * period + own.j] : 0.0f;
     }
   };
   load_stats(first);
@@ -171,6 +203,13 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_kernel(const NormGr
     };
     copy_rows(stage == 0 ? (S - 1) * stage_bytes : stage - stage_bytes);  // the slots read in the previous round
     copies_wait<S - 1>();
+    if (ODD && t == 0) {
+#pragma unroll
+      for (int q = 0; q < R; ++q) {
+        clear_head<DT>(my_dy + stage + q * row_bytes, skip);
+        clear_head<XT>(my_x + stage + q * row_bytes, skip);
+      }
+    }
     float2 scale[R], shift[R];
     float sums[K];
 #pragma unroll
@@ -226,7 +265,12 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_kernel(const NormGr
         const int off = 8 * i * group_threads;
         if (8 * t + off < N) {
           XT* o = dx + q * a.lddx + off;
-          *reinterpret_cast<Raw<XT, 8>*>(o) = pack2(d[q] + 4 * i, Raw<XT, 8>());
+          const Raw<XT, 8> v = pack2(d[q] + 4 * i, Raw<XT, 8>());
+          const int lo = skip - 8 * t - off, hi = N - 8 * t - off;
+          if (!ODD || (lo <= 0 && hi >= 8))
+            *reinterpret_cast<Raw<XT, 8>*>(o) = v;
+          else
+            store_part(o, v, lo, hi);
         }
       }
     }
@@ -236,28 +280,30 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_kernel(const NormGr
   // one row of column sums per block; alone it is the result
   float* out_g = gridDim.x == 1 ? a.dgamma : a.ws + (int64_t)blockIdx.x * 2 * a.N;
   float* out_b = gridDim.x == 1 ? a.dbeta : a.ws + ((int64_t)blockIdx.x * 2 + 1) * a.N;
-  float* join = reinterpret_cast<float*>(ring);  // [2][N]: the groups' sums, added one group after the other
+  // the groups' sums side by side in shared memory, then added in order, a column per thread
+  float* sums = reinterpret_cast<float*>(ring);  // [group][2][width]
+  const int width = group_threads * NC * 8;
   copies_wait<0>();
-  for (int q = 0; q < ngroups; ++q) {
-    if (ngroups > 1) __syncthreads();
-    if (q != group) continue;
+  __syncthreads();
 #pragma unroll
-    for (int e = 0; e < NC * 8; ++e) {
-      const int c = 8 * (t + e / 8 * group_threads) + e % 8;
-      if (c >= N) continue;
-      float vg = e % 2 ? dg[e / 2].y : dg[e / 2].x, vb = e % 2 ? db[e / 2].y : db[e / 2].x;
-      if (q > 0) {
-        vg += join[c];
-        vb += join[N + c];
-      }
-      if (q < ngroups - 1) {
-        join[c] = vg;
-        join[N + c] = vb;
-      } else {
-        if (out_g) out_g[c] = vg;
-        if (out_b) out_b[c] = vb;
-      }
+  for (int i = 0; i < NC; ++i) {
+    float4* to = reinterpret_cast<float4*>(sums + group * 2 * width + 8 * (t + i * group_threads));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int p = 4 * i + 2 * h;
+      to[h] = make_float4(dg[p].x, dg[p].y, dg[p + 1].x, dg[p + 1].y);
+      to[h + width / 4] = make_float4(db[p].x, db[p].y, db[p + 1].x, db[p + 1].y);
     }
+  }
+  __syncthreads();
+  for (int c = (int)threadIdx.x; c < (int)a.N; c += (int)blockDim.x) {
+    float vg = 0.0f, vb = 0.0f;
+    for (int q = 0; q < ngroups; ++q) {
+      vg += sums[q * 2 * width + skip + c];
+      vb += sums[q * 2 * width + width + skip + c];
+    }
+    if (out_g) out_g[c] = vg;
+    if (out_b) out_b[c] = vb;
   }
 }
 
@@ -429,25 +475,28 @@ cudaError_t join(const NormGradArgs& a, int64_t parts, cudaStream_t s) {
   return colsum::launch_join<2>(a.ws, (int)parts, a.N, a.dgamma, a.dbeta, s);
 }
 
-template <typename DT, typename XT, int NC, int R, int S, int THREADS, int BLOCKS>
+template <typename DT, typename XT, int NC, int R, int S, int THREADS, int BLOCKS, bool ODD>
 cudaError_t run(const NormGradArgs& a, cudaStream_t s) {
-  auto kern = a.dres ? norm_grad_kernel<DT, XT, NC, R, S, true, THREADS, BLOCKS>
-                     : norm_grad_kernel<DT, XT, NC, R, S, false, THREADS, BLOCKS>;
+  auto kern = a.dres ? norm_grad_kernel<DT, XT, NC, R, S, true, THREADS, BLOCKS, ODD>
+                     : norm_grad_kernel<DT, XT, NC, R, S, false, THREADS, BLOCKS, ODD>;
   static BlocksPerSm cache[2];
-  const int group = round32((a.N + 8 * NC - 1) / (8 * NC));
+  const int period = ODD ? row_period(a.ldx) : 1;
+  const int group = round32((a.N + (ODD ? 7 : 0) + 8 * NC - 1) / (8 * NC));
   // groups of a block: as many as fit, fewer where that leaves SMs without a block
   const int64_t rows_of_all = (int64_t)152 * R;
   const int groups = (int)std::max<int64_t>(1, std::min<int64_t>(THREADS / group, (a.M + rows_of_all - 1) / rows_of_all));
   const int threads = group * groups;
   int smem = R * S * NC * threads * (int)(sizeof(Raw<DT, 8>) + sizeof(Raw<XT, 8>) * (a.dres ? 2 : 1));
-  if (groups > 1) smem = std::max(smem, (int)(8 * a.N));
+  smem = std::max(smem, threads * NC * 8 * 8);  // the column sums
   int sms = 0, per_sm = 0;
   const cudaError_t e = cache[a.dres ? 1 : 0].get(kern, threads, smem, sms, per_sm);
   if (e != cudaSuccess) return e;
-  const int64_t rows = (int64_t)groups * R;
-  const int64_t blocks = std::min<int64_t>(std::min<int64_t>((a.M + rows - 1) / rows, kMaxBlocks), (int64_t)sms * per_sm);
-  kern<<<(unsigned)blocks, threads, smem, s>>>(a, group);
-  return join(a, blocks, s);
+  const int64_t rows = (int64_t)groups * R, of_class = (a.M + period - 1) / period;
+  // blocks of a class (`period` divides kMaxBlocks)
+  const int64_t blocks = std::min<int64_t>((of_class + rows - 1) / rows,
+                                           std::max<int64_t>(1, std::min<int64_t>(kMaxBlocks, (int64_t)sms * per_sm) / period));
+  kern<<<(unsigned)(blocks * period), threads, smem, s>>>(a, group, period);
+  return join(a, blocks * period, s);
 }
 
 template <typename DT, typename XT, int NC, int THREADS, int BLOCKS>
@@ -477,26 +526,41 @@ cudaError_t run_long(const NormGradArgs& a, cudaStream_t s) {
   return join(a, grid.y, s);
 }
 
+// The kernel for rows of vectors, or cudaErrorNotSupported where they are too long for it.
+template <typename DT, typename XT, bool ODD>
+cudaError_t launch_rows(const NormGradArgs& a, cudaStream_t s) {
+  const int64_t N = a.N + (ODD ? 7 : 0);                           // columns that a row may touch
+  const int64_t bytes = sizeof(DT) + sizeof(XT) * (a.dres ? 2 : 1);  // of a value of the row
+  const int64_t group = round32((N + 15) / 16);
+  if (N <= 5120) {
+    const int64_t row = 320 / group * group * 16 * bytes;  // a row of each group of a block
+    // As many rows at a time as two sets of them fit shared memory: the loop's overhead is shared (16384 x 5120
+    // bf16 with residual: one row 160 us, two 117, three 108; without it, four rows 89 us, two 103).
+    // With few rows one at a time, so that they spread over the SMs.
+    const bool many = a.M >= 8 * 152;
+    if (many && group == 192 && 8 * row <= kRing) return run<DT, XT, 2, 2, 2, 192, 2, ODD>(a, s);
+    if (many && group == 192 && 6 * row <= kRing) return run<DT, XT, 2, 1, 3, 192, 2, ODD>(a, s);
+    if (many && 8 * row <= kRing) return run<DT, XT, 2, 4, 2, 320, 1, ODD>(a, s);
+    if (many && 6 * row <= kRing) return run<DT, XT, 2, 3, 2, 320, 1, ODD>(a, s);
+    if (many && 4 * row <= kRing) return run<DT, XT, 2, 2, 2, 320, 1, ODD>(a, s);
+    return run<DT, XT, 2, 1, 3, 320, 1, ODD>(a, s);
+  }
+  if (N <= 10240 && 2 * group * 16 * bytes <= kRing) return run<DT, XT, 2, 1, 2, 640, 1, ODD>(a, s);
+  return cudaErrorNotSupported;
+}
+
 template <typename DT, typename XT>
 cudaError_t launch(const NormGradArgs& a, cudaStream_t s) {
   const bool vec = a.N % 8 == 0 && rows16(a.dy, a.lddy, sizeof(DT)) && rows16(a.x, a.ldx, sizeof(XT)) &&
                    rows16(a.dx, a.lddx, sizeof(XT)) && rows16(a.dres, a.lddres, sizeof(XT)) && rows16(a.gamma, 0, 4);
   if (vec) {
-    const int64_t bytes = sizeof(DT) + sizeof(XT) * (a.dres ? 2 : 1);  // of a value of the row
-    const int64_t group = round32((a.N + 15) / 16);
-    if (a.N <= 5120) {
-      const int64_t row = 320 / group * group * 16 * bytes;  // a row of each group of a block
-      // As many rows at a time as two sets of them fit shared memory: the loop's overhead is shared (16384 x 5120
-      // bf16 with residual: one row 160 us, two 117, three 108; without it, four rows 89 us, two 103).
-      // With few rows one at a time, so that they spread over the SMs.
-      const bool many = a.M >= 8 * 152;
-      if (many && 8 * row <= kRing) return run<DT, XT, 2, 4, 2, 320, 1>(a, s);
-      if (many && 6 * row <= kRing) return run<DT, XT, 2, 3, 2, 320, 1>(a, s);
-      if (many && 4 * row <= kRing) return run<DT, XT, 2, 2, 2, 320, 1>(a, s);
-      return run<DT, XT, 2, 1, 3, 320, 1>(a, s);
-    }
-    if (a.N <= 10240 && 2 * group * 16 * bytes <= kRing) return run<DT, XT, 2, 1, 2, 640, 1>(a, s);
-    return run_long<DT, XT, 8>(a, s);
+    const cudaError_t e = launch_rows<DT, XT, false>(a, s);
+    return e == cudaErrorNotSupported ? run_long<DT, XT, 8>(a, s) : e;
+  }
+  if (rows_shift_as(a.dy, a.lddy, a.ldx) && rows_shift_as(a.x, a.ldx, a.ldx) && rows_shift_as(a.dx, a.lddx, a.ldx) &&
+      rows_shift_as(a.dres, a.lddres, a.ldx)) {
+    const cudaError_t e = launch_rows<DT, XT, true>(a, s);
+    if (e != cudaErrorNotSupported) return e;
   }
   // few rows: more threads to a row, the latency counts; many: fewer, the instructions do (16384 x 2731 fp32 89 us
   // with sixteen values per thread, 180 with eight; 515 x 1023 fp32 9.6 and 6.4 us)

@@ -311,7 +311,13 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const LinearArgs a, co
     for (int i = 0; i < 4; ++i)
       if (n + 32 * i < a.N) top = max(top, put<T>(a, m, n + 32 * i, fmaf(v[i], scale, bias[i])));
   }
-  if (a.amax) put_amax(a.amax, top);
+  if (a.amax) {  // one warp per block: an atomic per warp cost 8 us for 1000 x 1000 outputs
+    __shared__ uint32_t tops[8];
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    if (threadIdx.x == 0) tops[threadIdx.y] = top;
+    __syncthreads();
+    if (threadIdx.y == 0) put_amax(a.amax, threadIdx.x < blockDim.y ? tops[threadIdx.x] : 0u);
+  }
 }
 
 Cut cut_of(int64_t M, int64_t N, int64_t K, int bn, bool whole) {

@@ -116,6 +116,39 @@ __device__ __forceinline__ void copies_wait() {  // all but the LEFT latest grou
   asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
 }
 
+// The first `count` (any number) of a chunk's values, zeros after them.
+template <typename T>
+__device__ __forceinline__ void copy_part(uint32_t dst, const T* row, int c, int count) {
+  constexpr int kPer = 16 / (int)sizeof(T);
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+    const int n = min(max(count - i * kPer, 0), kPer);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 16u * (uint32_t)i),
+                 "l"(n > 0 ? row + c + i * kPer : row), "r"(n * (int)sizeof(T))
+                 : "memory");
+  }
+}
+// Zeros in place of the first `count` (below 8) values of a chunk that has arrived.
+template <typename T>
+__device__ __forceinline__ void clear_head(uint32_t at, int count) {
+#pragma unroll
+  for (int i = 0; i < 7; ++i) {
+    if (i < count) {
+      if (sizeof(T) == 2)
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + 2u * i), "h"((short)0) : "memory");
+      else
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 4u * i), "r"(0) : "memory");
+    }
+  }
+}
+// Values lo .. hi - 1 of a chunk, the others left as they are.
+template <typename T>
+__device__ __forceinline__ void store_part(T* to, const Raw<T, 8>& v, int lo, int hi) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i >= lo && i < hi) to[i] = reinterpret_cast<const T*>(&v)[i];
+}
+
 // 8 values as pairs for the packed fp32 instructions.
 __device__ __forceinline__ void unpack2(const Raw<bf16, 8>& r, float2* f) {
   f[0] = bf16x2_to_f32x2(r.v.x);
@@ -240,6 +273,36 @@ class BlocksPerSm {
 
 inline bool rows16(const void* p, int64_t ld, int size) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * size % 16 == 0;
+}
+
+// Weights at columns c .. c + 7 of a row that begins at column 0, where c may be below it.
+__device__ __forceinline__ void load_weights_part(const void* w, int is_bf16, int c, int N, float none, float2* f) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = w && c + i >= 0 && c + i < N ? load_as_f32(w, c + i, is_bf16) : none;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = make_float2(v[2 * i], v[2 * i + 1]);
+}
+
+// ---- rows whose length or stride is no multiple of 8 values: row r begins r * ld
+// mod 8 values after a boundary of 8 values, which is the same for
+// every `period`-th row.  A block that works on such a class of rows alone has
+// aligned vectors as any other: it counts columns from the boundary before the
+// row's first value, and only the row's first and last chunk are partly its own.
+struct RowClass {
+  int period, j, shift;  // rows j, j + period, ..; values between the boundary and a row's first value
+  int64_t rows;          // of the class
+  __device__ RowClass(int period, int j, int64_t ld, int64_t M)
+      : period(period), j(j), shift((int)(j * (ld & 7) & 7)), rows((M - j + period - 1) / period) {}
+  // start of the class, counted from a tensor's first value; its rows are period * ld apart
+  __device__ int64_t start(int64_t ld) const { return j * ld - shift; }
+};
+
+inline int row_period(int64_t ld) { return ld % 2 ? 8 : (ld % 4 ? 4 : (ld % 8 ? 2 : 1)); }
+
+// Whether a tensor (or none) has row 0 on a boundary and its rows' shifts are those of stride ld.
+inline bool rows_shift_as(const void* p, int64_t own_ld, int64_t ld) {
+  return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (own_ld - ld) % 8 == 0);
 }
 
 }  // namespace norm

@@ -127,6 +127,31 @@ def test_layernorm_many_rows(M, N, xt, yt):
     assert r.amax.tolist() == [float(r.y.float().abs().max())] * 2
 
 
+# rows of each shift against 16-byte boundaries: strides N + pad that are 0, 1, 2, 3 and 4 mod 8, more rows than fit one
+# block; N around a chunk's and a block's width
+ODD_ROWS = [(259, 7, 0), (300, 48, 1), (1030, 1001, 0), (1217, 1001, 7), (777, 84, 0), (2049, 130, 4), (641, 2731, 4),
+            (1300, 1022, 0), (1219, 1025, 1), (601, 4099, 0), (1250, 5113, 0), (1240, 5119, 4), (700, 8193, 0)]
+
+
+@pytest.mark.parametrize("xt,yt", TYPES)
+@pytest.mark.parametrize("M,N,pad", ODD_ROWS + [(1301, 8199, 0), (650, 12379, 0), (700, 20479, 1)])
+def test_layernorm_odd_rows(M, N, pad, xt, yt):
+    """Nothing beside the rows is written, and neighbouring rows' NaN reaches no other."""
+    x = rand((M, N), xt, M + 3 * N, 2.0, 0.5)
+    gamma, beta = rand((N,), F32, 1, 0.1, 1.0), rand((N,), F32, 2, 0.1)
+    xv = strided(x, pad, 0)[1]
+    base, out = strided(torch.zeros((M, N), dtype=yt, device="cuda"), pad, 0)
+    r = nv.nvfp4_layernorm(xv, gamma, beta, 1e-5, out=out, want_amax=True)
+    check_norm(x, gamma, beta, 1e-5, r, yt)
+    assert untouched(base, M, N, pad, 0)
+    assert r.amax.tolist() == [float(r.y.float().abs().max())] * 2
+    clean = r.y.clone()
+    xv[M // 2] = float("nan")
+    got = nv.nvfp4_layernorm(xv, gamma, beta, 1e-5, out=xv if xt == yt else out).y  # in place
+    rows = torch.arange(M, device="cuda") != M // 2
+    assert torch.equal(got[rows], clean[rows])
+
+
 @pytest.mark.parametrize("pad,offset", [(8, 0), (8, 8), (3, 1), (0, 1), (4, 2)])
 @pytest.mark.parametrize("xt,yt", TYPES)
 def test_layernorm_strides_and_alignment(xt, yt, pad, offset):
@@ -285,6 +310,28 @@ def test_layernorm_backward_strides_and_alignment(xt, dt, pad, offset):
         assert untouched(base, M, N, pad, offset)
 
 
+@pytest.mark.parametrize("xt,dt", TYPES)
+@pytest.mark.parametrize("M,N,pad", ODD_ROWS)
+def test_layernorm_backward_odd_rows(M, N, pad, xt, dt):
+    """Nothing beside the rows is written, and neighbouring rows' NaN reaches no other."""
+    x, dy, dres = rand((M, N), xt, M + N, 2.0, 0.3), rand((M, N), dt, M + N + 1, 1e-3), rand((M, N), xt, 14, 1e-3)
+    gamma = rand((N,), F32, 13, 0.2, 1.0)
+    mean, rstd = stats(x)
+    base, out = strided(torch.zeros_like(x), pad, 0)
+    xv, dyv, resv = strided(x, pad, 0)[1], strided(dy, pad, 0)[1], strided(dres, pad, 0)[1]
+    check_norm_grad(dy, x, mean, rstd, gamma, None, nv.nvfp4_layernorm_backward(dyv, xv, mean, rstd, gamma, out=out))
+    r = nv.nvfp4_layernorm_backward(dyv, xv, mean, rstd, gamma, resv, out=out)
+    check_norm_grad(dy, x, mean, rstd, gamma, dres, r)
+    assert untouched(base, M, N, pad, 0)
+    clean = r.dx.clone()
+    xv[M // 2] = float("nan")
+    dyv[M // 3] = float("inf")
+    got = nv.nvfp4_layernorm_backward(dyv, xv, mean, rstd, gamma, resv, out=resv).dx  # in place
+    rows = torch.arange(M, device="cuda")
+    rows = (rows != M // 2) & (rows != M // 3)
+    assert torch.equal(got[rows], clean[rows])
+
+
 def test_layernorm_backward_options():
     x, dy, gamma = rand((50, 640), BF, 18), rand((50, 640), BF, 19), rand((640,), BF, 20, 0.1, 1.0)
     mean, rstd = stats(x)
@@ -395,6 +442,24 @@ def test_act_backward_strides_and_alignment(dt, pad, offset):
         r = nv.nvfp4_act_backward(strided(dy, pad, offset)[1], strided(z, pad, offset)[1], nv.ACT_GELU, out=out)
         check_act_grad(dy, z, nv.ACT_GELU, r)
         assert untouched(base, M, N, pad, offset)
+
+
+@pytest.mark.parametrize("act", [nv.ACT_NONE, nv.ACT_RELU, nv.ACT_GELU_TANH])
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("M,N,pad", ODD_ROWS)
+def test_act_backward_odd_rows(M, N, pad, dt, act):
+    """Nothing beside the rows is written, and neighbouring rows' NaN reaches no other."""
+    dy, z = rand((M, N), dt, M + N, 1e-3), rand((M, N), dt, N, 2.0)
+    base, out = strided(torch.zeros_like(dy), pad, 0)
+    dyv, zv = strided(dy, pad, 0)[1], strided(z, pad, 0)[1]
+    r = nv.nvfp4_act_backward(dyv, zv, act, out=out)
+    check_act_grad(dy, z, act, r)
+    assert untouched(base, M, N, pad, 0)
+    clean = r.dz.clone()
+    dyv[M // 2] = float("nan")
+    got = nv.nvfp4_act_backward(dyv, zv, act, out=dyv).dz  # in place
+    rows = torch.arange(M, device="cuda") != M // 2
+    assert torch.equal(got[rows], clean[rows])
 
 
 def test_act_backward_options_and_in_place():
