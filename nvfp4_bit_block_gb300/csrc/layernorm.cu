@@ -119,18 +119,37 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a) {
   if (a.amax) put_amax(a, top, top_s);
 }
 
-// The same for 16-byte rows and many of them: S rows of each group on their way in
-// shared memory, packed fp32 arithmetic.  KEEP: gamma and beta stay in registers.
-template <typename XT, typename YT, int NC, int S, bool WARP, bool KEEP, int THREADS>
-__global__ void __launch_bounds__(THREADS) norm_stream_kernel(const NormArgs a) {
+enum { kInRegisters, kInShared, kInMemory };
+
+// The same for rows of vectors and many of them: S rows of each group on their way
+// in shared memory, packed fp32 arithmetic.  gamma and beta stay in registers, in
+// shared memory or, of the longest rows, where they are.  ODD: the rows begin at several
+// places against the boundaries of 16 bytes, and a block takes those of one class;
+// the values of the neighbouring rows in the row's first and last chunk count for
+// nothing.
+template <typename XT, typename YT, int NC, int S, bool WARP, int WEIGHTS, int THREADS, bool ODD>
+__global__ void __launch_bounds__(THREADS) norm_stream_kernel(const NormArgs args) {
   extern __shared__ uint4 ring[];
   __shared__ __align__(16) float buf[2][32];
   __shared__ uint32_t top_s[32];
-  const int N = (int)a.N;
+  const int period = ODD ? row_period(args.ldx) : 1;
+  const RowClass own(period, ODD ? (int)(blockIdx.x % period) : 0, args.ldx, args.M);
+  NormArgs moved;
+  const NormArgs& a = ODD ? moved : args;
+  if (ODD) {
+    moved = args;
+    moved.x = static_cast<const XT*>(args.x) + own.start(args.ldx);
+    moved.y = static_cast<YT*>(args.y) + own.start(args.ldy);
+    moved.ldx *= period;
+    moved.ldy *= period;
+    moved.M = own.rows;
+  }
+  const int skip = ODD ? own.shift : 0, N = (int)a.N + skip;  // the row is columns skip .. N - 1
   const int lane = WARP ? threadIdx.x & 31 : threadIdx.x, group = WARP ? 32 : blockDim.x;
-  const int64_t groups = WARP ? (int64_t)gridDim.x * (THREADS / 32) : gridDim.x;
-  const int64_t first = WARP ? (int64_t)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5) : blockIdx.x;
-  const float inv = 1.0f / (float)N;
+  const int64_t blocks = gridDim.x / period, block = blockIdx.x / period;  // of the class
+  const int64_t groups = WARP ? blocks * (THREADS / 32) : blocks;
+  const int64_t first = WARP ? block * (THREADS / 32) + (threadIdx.x >> 5) : block;
+  const float inv = 1.0f / (float)a.N;
   // this thread's slots: [stage][chunk], blockDim.x apart
   Raw<XT, 8>* mine = reinterpret_cast<Raw<XT, 8>*>(ring) + threadIdx.x;
   const uint32_t mine_s = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
@@ -140,26 +159,50 @@ __global__ void __launch_bounds__(THREADS) norm_stream_kernel(const NormArgs a) 
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         const int c = 8 * (lane + i * group);
-        copy_chunk<XT>(mine_s + (uint32_t)((stage * NC + i) * (int)blockDim.x * (int)sizeof(Raw<XT, 8>)), row, c, c < N);
+        const uint32_t at = mine_s + (uint32_t)((stage * NC + i) * (int)blockDim.x * (int)sizeof(Raw<XT, 8>));
+        if constexpr (ODD)
+          copy_part<XT>(at, row, c, N - c);
+        else
+          copy_chunk<XT>(at, row, c, c < N);
       }
     }
     copies_commit();
   };
-  float2 g[KEEP ? NC : 1][4], b[KEEP ? NC : 1][4];
-  if (KEEP) {
-#pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      load_weights2(a.gamma, a.w_bf16, 8 * (lane + i * group), N, 1.0f, g[i]);
-      load_weights2(a.beta, a.w_bf16, 8 * (lane + i * group), N, 0.0f, b[i]);
+  constexpr bool kKeep = WEIGHTS == kInRegisters;
+  float2 g[kKeep ? NC : 1][4], b[kKeep ? NC : 1][4];
+  auto load_weights = [&](int c, float2* to_g, float2* to_b) {
+    if (ODD) {
+      load_weights_part(a.gamma, a.w_bf16, c - skip, (int)a.N, 1.0f, to_g);
+      load_weights_part(a.beta, a.w_bf16, c - skip, (int)a.N, 0.0f, to_b);
+    } else {
+      load_weights2(a.gamma, a.w_bf16, c, N, 1.0f, to_g);
+      load_weights2(a.beta, a.w_bf16, c, N, 0.0f, to_b);
     }
-  }
+  };
+  // in shared memory: per chunk two quads of gamma and two of beta, at the thread's own chunks
+  float4* weights = reinterpret_cast<float4*>(reinterpret_cast<Raw<XT, 8>*>(ring) + S * NC * (int)blockDim.x) + threadIdx.x;
   uint32_t top = 0;
 #pragma unroll
   for (int s = 0; s < S - 1; ++s) copy_row(first + s * groups, s);
+  if constexpr (WEIGHTS != kInMemory) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = 8 * (lane + i * group), at = kKeep ? i : 0;
+      load_weights(c, g[at], b[at]);
+      if (!kKeep && c < N) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          weights[(4 * i + h) * (int)blockDim.x] = make_float4(g[0][2 * h].x, g[0][2 * h].y, g[0][2 * h + 1].x, g[0][2 * h + 1].y);
+          weights[(4 * i + 2 + h) * (int)blockDim.x] = make_float4(b[0][2 * h].x, b[0][2 * h].y, b[0][2 * h + 1].x, b[0][2 * h + 1].y);
+        }
+      }
+    }
+  }
   int stage = 0;
   for (int64_t r = first; r < a.M; r += groups) {
     copy_row(r + (S - 1) * groups, stage == 0 ? S - 1 : stage - 1);  // the slot read in the previous round
     copies_wait<S - 1>();
+    if (ODD && lane == 0) clear_head<XT>(mine_s + (uint32_t)(stage * NC * (int)blockDim.x * (int)sizeof(Raw<XT, 8>)), skip);
     float2 x[NC][4];
     float2 sum = splat(0.0f);
 #pragma unroll
@@ -178,18 +221,27 @@ __global__ void __launch_bounds__(THREADS) norm_stream_kernel(const NormArgs a) 
     for (int i = 0; i < NC; ++i) {
       if (8 * (lane + i * group) < N) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x[i][j] = add2(x[i][j], shift);
-          sum = fma2(x[i][j], x[i][j], sum);
+        for (int j = 0; j < 4; ++j) x[i][j] = add2(x[i][j], shift);
+        if (ODD) {
+          const int lo = skip - 8 * (lane + i * group), hi = N - 8 * (lane + i * group);
+          if (lo > 0 || hi < 8) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (2 * j < lo || 2 * j >= hi) x[i][j].x = 0.0f;
+              if (2 * j + 1 < lo || 2 * j + 1 >= hi) x[i][j].y = 0.0f;
+            }
+          }
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum = fma2(x[i][j], x[i][j], sum);
       }
     }
     float t[1] = {sum.x + sum.y};
     group_sums<WARP, 1>(t, buf[1]);
     const float rstd = 1.0f / sqrtf(t[0] * inv + a.eps);
     if (lane == 0) {
-      if (a.mean) a.mean[r] = mean;
-      if (a.rstd) a.rstd[r] = rstd;
+      if (a.mean) a.mean[r * period + own.j] = mean;
+      if (a.rstd) a.rstd[r * period + own.j] = rstd;
     }
     YT* y = static_cast<YT*>(a.y) + r * a.ldy;
     const float2 scale = splat(rstd);
@@ -197,14 +249,24 @@ __global__ void __launch_bounds__(THREADS) norm_stream_kernel(const NormArgs a) 
     for (int i = 0; i < NC; ++i) {
       const int c = 8 * (lane + i * group);
       if (c >= N) break;
-      if (!KEEP) {
-        load_weights2(a.gamma, a.w_bf16, c, N, 1.0f, g[0]);
-        load_weights2(a.beta, a.w_bf16, c, N, 0.0f, b[0]);
+      if constexpr (WEIGHTS == kInMemory) load_weights(c, g[0], b[0]);
+      if constexpr (WEIGHTS == kInShared) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float4 vg = weights[(4 * i + h) * (int)blockDim.x], vb = weights[(4 * i + 2 + h) * (int)blockDim.x];
+          g[0][2 * h] = make_float2(vg.x, vg.y);
+          g[0][2 * h + 1] = make_float2(vg.z, vg.w);
+          b[0][2 * h] = make_float2(vb.x, vb.y);
+          b[0][2 * h + 1] = make_float2(vb.z, vb.w);
+        }
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[i][j] = fma2(mul2(x[i][j], scale), g[KEEP ? i : 0][j], b[KEEP ? i : 0][j]);
+      for (int j = 0; j < 4; ++j) x[i][j] = fma2(mul2(x[i][j], scale), g[kKeep ? i : 0][j], b[kKeep ? i : 0][j]);
       const Raw<YT, 8> o = pack2(x[i], Raw<YT, 8>());
-      *reinterpret_cast<Raw<YT, 8>*>(y + c) = o;
+      if (!ODD || (skip <= c && c + 8 <= N))
+        *reinterpret_cast<Raw<YT, 8>*>(y + c) = o;
+      else
+        store_part(y + c, o, skip - c, N - c);
       if (a.amax) top = top_of(o, top);
     }
   }
@@ -310,15 +372,17 @@ __global__ void __launch_bounds__(kMaxThreads) norm_long_kernel(const NormArgs a
   if (a.amax) put_amax(a, top, top_s);
 }
 
-// `blocks` blocks of a kernel, or as many as the GPU holds at once; the amax pair
-// is zeroed unless one block alone writes it.
+// `blocks` blocks of a kernel, or as many as the GPU holds at once (of either for
+// each of `period` classes of rows); the amax pair is zeroed unless one block alone
+// writes it.
 template <auto KERN>
-cudaError_t run(const NormArgs& a, int64_t blocks, int threads, cudaStream_t s, int smem = 0) {
+cudaError_t run(const NormArgs& a, int64_t blocks, int threads, cudaStream_t s, int smem = 0, int period = 1) {
   static BlocksPerSm cache;
   int sms = 0, per_sm = 0;
   cudaError_t e = cache.get(KERN, threads, smem, sms, per_sm);
   if (e != cudaSuccess) return e;
-  blocks = blocks < (int64_t)sms * per_sm ? blocks : (int64_t)sms * per_sm;
+  const int64_t most = (int64_t)sms * per_sm / period;
+  blocks = (blocks < most ? blocks : (most > 0 ? most : 1)) * period;
   if (a.amax && blocks > 1) {
     e = cudaMemsetAsync(a.amax, 0, 2 * sizeof(float), s);
     if (e != cudaSuccess) return e;
@@ -329,24 +393,48 @@ cudaError_t run(const NormArgs& a, int64_t blocks, int threads, cudaStream_t s, 
 
 int round32(int64_t v) { return (int)((v + 31) / 32 * 32); }
 
+// Many rows of vectors; cudaErrorNotSupported where they are too long.
+template <typename XT, typename YT, bool ODD>
+cudaError_t launch_rows(const NormArgs& a, cudaStream_t s) {
+  // Four chunks of eight values per thread (five warps to a row of 5120 values, 58 us for 16384 x 5120 bf16; with
+  // two chunks 69 us, with one 100 us), three rows in flight; gamma and beta in registers as far as they fit (read
+  // again for each row: 92 us).
+  constexpr int kSlot = 8 * (int)sizeof(XT);  // bytes of a thread's chunk in flight
+  const int64_t chunks = (a.N + (ODD ? 14 : 0)) / 8;
+  const int period = ODD ? row_period(a.ldx) : 1;
+  const int64_t rows = (a.M + period - 1) / period;
+  if (chunks <= 32)
+    return run<norm_stream_kernel<XT, YT, 1, 4, true, kInRegisters, 256, ODD>>(a, (rows + 7) / 8, 256, s, 256 * 4 * kSlot, period);
+  if (chunks <= 128)
+    return run<norm_stream_kernel<XT, YT, 4, 3, true, kInRegisters, 256, ODD>>(a, (rows + 7) / 8, 256, s, 256 * 12 * kSlot, period);
+  const int t = round32((chunks + 3) / 4);
+  if (chunks <= 1024)
+    return run<norm_stream_kernel<XT, YT, 4, 3, false, kInRegisters, 256, ODD>>(a, rows, t, s, t * 12 * kSlot, period);
+  if (chunks > 4096) return cudaErrorNotSupported;
+  // bf16 rows leave space for the weights in shared memory (6000 x 9008: 45 us, from memory 54; fp32 101 and 97)
+  const int smem = t * 8 * kSlot, with_weights = smem + t * 16 * 16;
+  if constexpr (sizeof(XT) == 2) {
+    if (with_weights <= 224 * 1024)
+      return run<norm_stream_kernel<XT, YT, 4, 2, false, kInShared, 1024, ODD>>(a, rows, t, s, with_weights, period);
+  }
+  if (smem <= 224 * 1024)
+    return run<norm_stream_kernel<XT, YT, 4, 2, false, kInMemory, 1024, ODD>>(a, rows, t, s, smem, period);
+  return cudaErrorNotSupported;
+}
+
 template <typename XT, typename YT>
 cudaError_t launch(const NormArgs& a, cudaStream_t s) {
   const bool vec = a.N % 8 == 0 && rows16(a.x, a.ldx, sizeof(XT)) && rows16(a.y, a.ldy, sizeof(YT)) &&
                    rows16(a.gamma, 0, 4) && rows16(a.beta, 0, 4);
   const int64_t chunks = vec ? a.N / 8 : a.N;
   const int64_t per_warp_block = kWarpThreads / 32;
-  if (vec && a.M > 608) {
-    // Four chunks of eight values per thread (five warps to a row of 5120 values, 58 us for 16384 x 5120 bf16; with
-    // two chunks 69 us, with one 100 us), three rows in flight; gamma and beta in registers as far as they fit (read
-    // again for each row: 92 us).
-    const int slot = 8 * (int)sizeof(XT);  // bytes of a thread's chunk in flight
-    if (chunks <= 32) return run<norm_stream_kernel<XT, YT, 1, 4, true, true, 256>>(a, (a.M + 7) / 8, 256, s, 256 * 4 * slot);
-    if (chunks <= 128)
-      return run<norm_stream_kernel<XT, YT, 4, 3, true, true, 256>>(a, (a.M + 7) / 8, 256, s, 256 * 12 * slot);
-    const int t = round32((chunks + 3) / 4);
-    if (chunks <= 1024) return run<norm_stream_kernel<XT, YT, 4, 3, false, true, 256>>(a, a.M, t, s, t * 12 * slot);
-    if (chunks <= 4096 && t * 8 * slot <= 224 * 1024)
-      return run<norm_stream_kernel<XT, YT, 4, 2, false, false, 1024>>(a, a.M, t, s, t * 8 * slot);
+  // by classes of rows where that beats single values (16384 x 2731 bf16 41 us against 49, fp32 73 and 61; 16384 x 333
+  // bf16 17 and 12; 1010 x 12379 bf16 21 and 39, fp32 32 and 47)
+  const bool classes = a.N > (sizeof(XT) == 2 && sizeof(YT) == 2 ? 8 * 192 : 24 * 512) &&
+                       rows_shift_as(a.x, a.ldx, a.ldx) && rows_shift_as(a.y, a.ldy, a.ldx);
+  if (a.M > 608 && (vec || classes)) {
+    const cudaError_t e = vec ? launch_rows<XT, YT, false>(a, s) : launch_rows<XT, YT, true>(a, s);
+    if (e != cudaErrorNotSupported) return e;
   }
   if (vec) {
     if (chunks <= 128) {  // a warp holds the row
