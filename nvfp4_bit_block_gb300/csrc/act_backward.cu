@@ -95,6 +95,7 @@ __device__ __forceinline__ void band(const ActGradArgs& a, int64_t r0, int64_t r
 template <typename T, int V, int R, int TX, int TY, bool ODD>
 __global__ void __launch_bounds__(TX * TY, V == 1 ? (TY > 1 ? 768 : 1024) / (TX * TY) : 0)
     act_grad_kernel(const ActGradArgs args, int64_t rows, int period) {
+  after_previous();
   __shared__ float join[TY > 1 ? TY : 1][TY > 1 ? TX * V + 1 : 1];
   const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
   int64_t c = ((int64_t)blockIdx.x * TX + tx) * V, b = blockIdx.y, end = -1;
@@ -170,8 +171,7 @@ cudaError_t run(const ActGradArgs& a, int64_t bands, cudaStream_t s, int period 
   const int64_t of_class = (a.M + period - 1) / period, rows = (of_class + bands - 1) / bands;
   const int64_t width = a.N + (ODD ? 7 : 0);
   const dim3 grid((unsigned)((width + TX * V - 1) / (TX * V)), (unsigned)((of_class + rows - 1) / rows * period));
-  act_grad_kernel<T, V, R, TX, TY, ODD><<<grid, TX * TY, 0, s>>>(a, rows, period);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_early(act_grad_kernel<T, V, R, TX, TY, ODD>, grid, TX * TY, 0, s, a, rows, period);
   if (e != cudaSuccess || !a.dbias || grid.y == 1) return e;
   return colsum::launch_join<1>(a.ws, (int)grid.y, a.N, a.dbias, nullptr, s);
 }

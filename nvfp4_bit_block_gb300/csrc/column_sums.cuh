@@ -20,6 +20,7 @@ __global__ void __launch_bounds__(1024) join_kernel(const float* part, int parts
   const int64_t c = (int64_t)blockIdx.x * 32 + tx;
   float t[V] = {};
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (c < N) {
 #pragma unroll 8
     for (int p = ty; p < parts; p += 32)

@@ -40,6 +40,7 @@ __device__ __forceinline__ void put_amax(const NormArgs& a, uint32_t top, uint32
 // the barriers of the reductions.
 template <typename XT, typename YT, int V, int NC, int R, bool WARP, int THREADS>
 __global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a) {
+  after_previous();
   __shared__ __align__(16) float buf[2][R * 32];
   __shared__ uint32_t top_s[32];
   const int N = (int)a.N;
@@ -129,6 +130,7 @@ enum { kInRegisters, kInShared, kInMemory };
 // nothing.
 template <typename XT, typename YT, int NC, int S, bool WARP, int WEIGHTS, int THREADS, bool ODD>
 __global__ void __launch_bounds__(THREADS) norm_stream_kernel(const NormArgs args) {
+  after_previous();
   extern __shared__ uint4 ring[];
   __shared__ __align__(16) float buf[2][32];
   __shared__ uint32_t top_s[32];
@@ -279,6 +281,7 @@ __global__ void __launch_bounds__(THREADS) norm_stream_kernel(const NormArgs arg
 // instructions, and those per row and thread are shared.
 template <typename XT, typename YT, int NC, bool WARP, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS) norm_scalar_kernel(const NormArgs a) {
+  after_previous();
   __shared__ __align__(16) float buf[2][32];
   __shared__ uint32_t top_s[32];
   const int lane = WARP ? threadIdx.x & 31 : threadIdx.x, group = WARP ? 32 : blockDim.x;
@@ -340,6 +343,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_scalar_kernel(const Norm
 // Rows too long for the registers of a block: three passes over the row.
 template <typename XT, typename YT>
 __global__ void __launch_bounds__(kMaxThreads) norm_long_kernel(const NormArgs a) {
+  after_previous();
   __shared__ __align__(16) float buf[2][32];
   __shared__ uint32_t top_s[32];
   uint32_t top = 0;
@@ -387,8 +391,7 @@ cudaError_t run(const NormArgs& a, int64_t blocks, int threads, cudaStream_t s, 
     e = cudaMemsetAsync(a.amax, 0, 2 * sizeof(float), s);
     if (e != cudaSuccess) return e;
   }
-  KERN<<<(unsigned)blocks, threads, smem, s>>>(a);
-  return cudaGetLastError();
+  return launch_early(KERN, dim3((unsigned)blocks), threads, smem, s, a);
 }
 
 int round32(int64_t v) { return (int)((v + 31) / 32 * 32); }

@@ -100,6 +100,7 @@ __device__ __forceinline__ void to_pairs(const Raw<T, 8> (&raw)[NC], float2 (&f)
 template <typename DT, typename XT, int NC, int R, int S, bool RES, int THREADS, int BLOCKS, bool ODD>
 __global__ void __launch_bounds__(THREADS, BLOCKS)
     norm_grad_kernel(const NormGradArgs args, int group_threads, int row_classes) {
+  after_previous();
   constexpr int P = NC * 4, K = R == 3 ? 8 : 2 * R;  // sums of a round, a power of two
   extern __shared__ uint4 ring[];
   __shared__ float buf[2][THREADS / 32 * K];
@@ -314,6 +315,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
 // one is worked on.
 template <typename DT, typename XT, int NC, bool RES, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_scalar_kernel(const NormGradArgs a, int group_threads) {
+  after_previous();
   extern __shared__ uint4 ring[];
   __shared__ float buf[2][THREADS / 32 * 2];
   const int warps = group_threads >> 5, group = (int)threadIdx.x / group_threads, ngroups = (int)blockDim.x / group_threads;
@@ -411,6 +413,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_grad_scalar_kernel(const
 
 template <typename DT, typename XT>
 __global__ void __launch_bounds__(512) row_sums_kernel(const NormGradArgs a, float2* sums) {
+  after_previous();
   __shared__ __align__(16) float buf[2][2 * 32];
   int parity = 0;
   for (int64_t r = blockIdx.x; r < a.M; r += gridDim.x) {
@@ -433,6 +436,7 @@ __global__ void __launch_bounds__(512) row_sums_kernel(const NormGradArgs a, flo
 // A thread owns V columns of a band of rows.
 template <typename DT, typename XT, int V>
 __global__ void __launch_bounds__(128) columns_kernel(const NormGradArgs a, const float2* sums, int64_t rows) {
+  after_previous();
   const int64_t c = ((int64_t)blockIdx.x * 128 + threadIdx.x) * V;
   if (c >= a.N) return;
   const int64_t r0 = (int64_t)blockIdx.y * rows, r1 = min(r0 + rows, a.M);
@@ -471,8 +475,8 @@ int64_t bands_of(int64_t M, int64_t N, int V) {
 
 int round32(int64_t v) { return (int)((v + 31) / 32 * 32); }
 
-cudaError_t join(const NormGradArgs& a, int64_t parts, cudaStream_t s) {
-  const cudaError_t e = cudaGetLastError();
+// `e`: of the launch that leaves the parts.
+cudaError_t join(const NormGradArgs& a, int64_t parts, cudaError_t e, cudaStream_t s) {
   if (e != cudaSuccess || parts == 1 || (!a.dgamma && !a.dbeta)) return e;
   return colsum::launch_join<2>(a.ws, (int)parts, a.N, a.dgamma, a.dbeta, s);
 }
@@ -497,8 +501,7 @@ cudaError_t run(const NormGradArgs& a, cudaStream_t s) {
   // blocks of a class (`period` divides kMaxBlocks)
   const int64_t blocks = std::min<int64_t>((of_class + rows - 1) / rows,
                                            std::max<int64_t>(1, std::min<int64_t>(kMaxBlocks, (int64_t)sms * per_sm) / period));
-  kern<<<(unsigned)(blocks * period), threads, smem, s>>>(a, group, period);
-  return join(a, blocks * period, s);
+  return join(a, blocks * period, launch_early(kern, dim3((unsigned)(blocks * period)), threads, smem, s, a, group, period), s);
 }
 
 template <typename DT, typename XT, int NC, int THREADS, int BLOCKS>
@@ -514,8 +517,7 @@ cudaError_t run_scalar(const NormGradArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int64_t blocks =
       std::min<int64_t>(std::min<int64_t>((a.M + groups - 1) / groups, kMaxBlocks), (int64_t)sms * per_sm);
-  kern<<<(unsigned)blocks, threads, smem, s>>>(a, group);
-  return join(a, blocks, s);
+  return join(a, blocks, launch_early(kern, dim3((unsigned)blocks), threads, smem, s, a, group), s);
 }
 
 template <typename DT, typename XT, int V>
@@ -523,9 +525,10 @@ cudaError_t run_long(const NormGradArgs& a, cudaStream_t s) {
   const int64_t bands = bands_of(a.M, a.N, V), rows = (a.M + bands - 1) / bands;
   const dim3 grid((unsigned)((a.N + 128 * V - 1) / (128 * V)), (unsigned)((a.M + rows - 1) / rows));
   float2* sums = reinterpret_cast<float2*>(a.ws + kMaxBlocks * 2 * a.N);
-  row_sums_kernel<DT, XT><<<(unsigned)std::min<int64_t>(a.M, 152 * 4), 512, 0, s>>>(a, sums);
-  columns_kernel<DT, XT, V><<<grid, 128, 0, s>>>(a, sums, rows);
-  return join(a, grid.y, s);
+  const dim3 rows_grid((unsigned)std::min<int64_t>(a.M, 152 * 4));
+  cudaError_t e = launch_early(row_sums_kernel<DT, XT>, rows_grid, 512, 0, s, a, sums);
+  if (e == cudaSuccess) e = launch_early(columns_kernel<DT, XT, V>, grid, 128, 0, s, a, sums, rows);
+  return join(a, grid.y, e, s);
 }
 
 // The kernel for rows of vectors, or cudaErrorNotSupported where they are too long for it.

@@ -299,6 +299,7 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const LinearArgs a, co
   const int parts = cut.piece_of((tile + 1) * cut.steps - 1) - cut.piece_of(tile * cut.steps) + 1;
   const float* in = a.ws + (tile * cut.most * bn + (m - tok * bn)) * kLaneRows + threadIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   uint32_t top = 0;
   if (there) {
     float v[4] = {};
