@@ -388,7 +388,7 @@ cudaError_t run(const NormArgs& a, int64_t blocks, int threads, cudaStream_t s, 
   const int64_t most = (int64_t)sms * per_sm / period;
   blocks = (blocks < most ? blocks : (most > 0 ? most : 1)) * period;
   if (a.amax && blocks > 1) {
-    e = cudaMemsetAsync(a.amax, 0, 2 * sizeof(float), s);
+    e = zero_amax(a.amax, s);
     if (e != cudaSuccess) return e;
   }
   return launch_early(KERN, dim3((unsigned)blocks), threads, smem, s, a);

@@ -10,6 +10,7 @@
 #include <atomic>
 
 #include "layer_device.cuh"
+#include "launch_early.cuh"
 #include "nvfp4_device.cuh"
 
 namespace nvfp4 {
@@ -270,27 +271,6 @@ class BlocksPerSm {
  private:
   std::atomic<uint64_t> last_{0};
 };
-
-// A launch that may begin while the kernel before it ends (programmatic dependent
-// launch): its blocks call `after_previous` before they read or write memory.
-template <typename... P, typename... A>
-cudaError_t launch_early(void (*kern)(P...), dim3 grid, int threads, int smem, cudaStream_t s, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, P(args)...);
-}
-__device__ __forceinline__ void after_previous() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the next kernel may do the same
-}
 
 inline bool rows16(const void* p, int64_t ld, int size) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * size % 16 == 0;

@@ -581,6 +581,19 @@ def test_linear_every_epilogue(M, N, K, act):
                 check_linear(a, b, K, r, bias, act, res, dt)
 
 
+@pytest.mark.parametrize("M,N,K", [(2050, 5001, 96), (2050, 5000, 544), (300, 20001, 1056), (2560, 5120, 64)])
+def test_linear_several_tiles_per_pair(M, N, K):
+    """More tiles than pairs of SMs, outputs with and without rows of whole vectors, everything on."""
+    a, b = operand(M, K, M + K), operand(N, K, N + K)
+    bias = rand((N,), F32, 3)
+    for dt in (BF, F32):
+        res = rand((M, N), dt, 5)
+        for r, z in ((None, True), (res, False), (res, True)):
+            got = nv.nvfp4_linear(*a, *b, bias=bias, act=nv.ACT_SILU, residual=r, out_dtype=dt, want_z=z,
+                                  want_amax=dt is BF)
+            check_linear(a, b, K, got, bias, nv.ACT_SILU, r, dt)
+
+
 @pytest.mark.parametrize("pad,offset", [(8, 0), (8, 8), (3, 1), (0, 1), (2, 0)])
 @pytest.mark.parametrize("dt", [BF, F32])
 def test_linear_strides_and_alignment(dt, pad, offset):
