@@ -399,8 +399,8 @@ int round32(int64_t v) { return (int)((v + 31) / 32 * 32); }
 // Many rows of vectors; cudaErrorNotSupported where they are too long.
 template <typename XT, typename YT, bool ODD>
 cudaError_t launch_rows(const NormArgs& a, cudaStream_t s) {
-  // Four chunks of eight values per thread (five warps to a row of 5120 values, 58 us for 16384 x 5120 bf16; with
-  // two chunks 69 us, with one 100 us), three rows in flight; gamma and beta in registers as far as they fit (read
+  // Four chunks of eight values per thread (five warps to a row of 5120 values, 53 us for 16384 x 5120 bf16; when it was 58,
+  // with two chunks 69 us, with one 100 us), three rows in flight; gamma and beta in registers as far as they fit (read
   // again for each row: 92 us).
   constexpr int kSlot = 8 * (int)sizeof(XT);  // bytes of a thread's chunk in flight
   const int64_t chunks = (a.N + (ODD ? 14 : 0)) / 8;
