@@ -188,7 +188,8 @@ cudaError_t launch_t(const ActGradArgs& a, cudaStream_t s) {
     const int64_t bands = bands_of(a.M, a.N, 8, 1);
     return bands == 1 ? run<T, 8, R, 8, 32>(a, 1, s) : run<T, 8, R, kWide, 1>(a, bands, s);
   }
-  if (a.M > kFewRows1 && rows_shift_as(a.dy, a.lddy, a.lddy) && rows_shift_as(a.z, a.ldz, a.lddy) &&
+  // from eight values on a chunk that begins in a row ends before the end of the next
+  if (a.M > kFewRows1 && a.N >= 8 && rows_shift_as(a.dy, a.lddy, a.lddy) && rows_shift_as(a.z, a.ldz, a.lddy) &&
       rows_shift_as(a.dz, a.lddz, a.lddy))
     return run<T, 8, R, kWide, 1, true>(a, bands_of(a.M, a.N, 8, period), s, period);
   const int64_t bands = bands_of(a.M, a.N, 1, 1);

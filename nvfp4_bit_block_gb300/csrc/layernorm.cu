@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(THREADS) norm_stream_kernel(const NormArgs arg
     }
   };
   // in shared memory: per chunk two quads of gamma and two of beta, at the thread's own chunks
-  float4* weights = reinterpret_cast<float4*>(reinterpret_cast<Raw<XT, 8>*>(ring) + S * NC * (int)blockDim.x) + threadIdx.x;
+  float4* weights = reinterpret_cast<float4*>(mine - threadIdx.x + S * NC * (int)blockDim.x) + threadIdx.x;
   uint32_t top = 0;
 #pragma unroll
   for (int s = 0; s < S - 1; ++s) copy_row(first + s * groups, s);
@@ -194,8 +194,9 @@ __global__ void __launch_bounds__(THREADS) norm_stream_kernel(const NormArgs arg
       if (!kKeep && c < N) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          weights[(4 * i + h) * (int)blockDim.x] = make_float4(g[0][2 * h].x, g[0][2 * h].y, g[0][2 * h + 1].x, g[0][2 * h + 1].y);
-          weights[(4 * i + 2 + h) * (int)blockDim.x] = make_float4(b[0][2 * h].x, b[0][2 * h].y, b[0][2 * h + 1].x, b[0][2 * h + 1].y);
+          const float2 *pg = g[0] + 2 * h, *pb = b[0] + 2 * h;
+          weights[(4 * i + h) * (int)blockDim.x] = make_float4(pg[0].x, pg[0].y, pg[1].x, pg[1].y);
+          weights[(4 * i + 2 + h) * (int)blockDim.x] = make_float4(pb[0].x, pb[0].y, pb[1].x, pb[1].y);
         }
       }
     }
@@ -399,17 +400,19 @@ int round32(int64_t v) { return (int)((v + 31) / 32 * 32); }
 // Many rows of vectors; cudaErrorNotSupported where they are too long.
 template <typename XT, typename YT, bool ODD>
 cudaError_t launch_rows(const NormArgs& a, cudaStream_t s) {
-  // Four chunks of eight values per thread (five warps to a row of 5120 values, 53 us for 16384 x 5120 bf16; when it was 58,
-  // with two chunks 69 us, with one 100 us), three rows in flight; gamma and beta in registers as far as they fit (read
+  // Four chunks of eight values per thread (five warps to a row of 5120 values, 53 us for 16384 x 5120 bf16; when it
+  // took 58, two chunks took 69 us and one 100), three rows in flight; gamma and beta in registers as far as they fit (read
   // again for each row: 92 us).
   constexpr int kSlot = 8 * (int)sizeof(XT);  // bytes of a thread's chunk in flight
   const int64_t chunks = (a.N + (ODD ? 14 : 0)) / 8;
   const int period = ODD ? row_period(a.ldx) : 1;
   const int64_t rows = (a.M + period - 1) / period;
   if (chunks <= 32)
-    return run<norm_stream_kernel<XT, YT, 1, 4, true, kInRegisters, 256, ODD>>(a, (rows + 7) / 8, 256, s, 256 * 4 * kSlot, period);
+    return run<norm_stream_kernel<XT, YT, 1, 4, true, kInRegisters, 256, ODD>>(a, (rows + 7) / 8, 256, s,
+                                                                               256 * 4 * kSlot, period);
   if (chunks <= 128)
-    return run<norm_stream_kernel<XT, YT, 4, 3, true, kInRegisters, 256, ODD>>(a, (rows + 7) / 8, 256, s, 256 * 12 * kSlot, period);
+    return run<norm_stream_kernel<XT, YT, 4, 3, true, kInRegisters, 256, ODD>>(a, (rows + 7) / 8, 256, s,
+                                                                               256 * 12 * kSlot, period);
   const int t = round32((chunks + 3) / 4);
   if (chunks <= 1024)
     return run<norm_stream_kernel<XT, YT, 4, 3, false, kInRegisters, 256, ODD>>(a, rows, t, s, t * 12 * kSlot, period);

@@ -130,7 +130,8 @@ def test_layernorm_many_rows(M, N, xt, yt):
 # rows of each shift against 16-byte boundaries: strides N + pad that are 0, 1, 2, 3 and 4 mod 8, more rows than fit one
 # block; N around a chunk's and a block's width
 ODD_ROWS = [(259, 7, 0), (300, 48, 1), (1030, 1001, 0), (1217, 1001, 7), (777, 84, 0), (2049, 130, 4), (641, 2731, 4),
-            (1300, 1022, 0), (1219, 1025, 1), (601, 4099, 0), (1250, 5113, 0), (1240, 5119, 4), (700, 8193, 0)]
+            (1300, 1022, 0), (1219, 1025, 1), (601, 4099, 0), (1250, 5113, 0), (1240, 5119, 4), (700, 8193, 0),
+            (1001, 2, 0), (999, 3, 0), (1003, 8, 1), (1300, 9, 0)]
 
 
 @pytest.mark.parametrize("xt,yt", TYPES)
