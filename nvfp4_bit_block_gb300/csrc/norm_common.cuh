@@ -241,8 +241,10 @@ __device__ __forceinline__ void group_sums(float (&v)[K], float* buf) {
 }
 
 // Blocks of a kernel that an SM holds, asked for once per (device, threads, shared
-// memory) and kept while the same are asked for again; opts the kernel in to the
-// shared memory that it needs.
+// memory) and kept in a small table.  One kernel is launched with many amounts of
+// shared memory, by several host threads at once: it is opted in to all that a block
+// may have, whatever this call needs, so that no call lowers what another's launch
+// relies on.
 class BlocksPerSm {
  public:
   template <typename Kernel>
@@ -252,24 +254,30 @@ class BlocksPerSm {
     if (e != cudaSuccess) return e;
     // key: device (8 bits), threads / 32 (8), smem / 16 (16); value: SMs (16), blocks (16)
     const uint64_t key = (uint64_t)(dev & 255) << 24 | (uint64_t)(threads / 32) << 16 | (uint64_t)((smem + 15) / 16);
-    const uint64_t seen = last_.load(std::memory_order_relaxed);
+    std::atomic<uint64_t>& slot = seen_[(unsigned)(threads / 32) % kSlots];
+    const uint64_t seen = slot.load(std::memory_order_relaxed);
     if (seen >> 32 == key && seen != 0) {
       sms = (int)(seen >> 16 & 0xFFFF);
       per_sm = (int)(seen & 0xFFFF);
       return cudaSuccess;
     }
+    int most = 0;
+    cudaFuncAttributes attr;
     e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess && smem > 40 * 1024)
-      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&attr, kern);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most - (int)attr.sharedSizeBytes);
     if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
     if (e != cudaSuccess) return e;
     if (per_sm < 1) return cudaErrorInvalidConfiguration;
-    last_.store(key << 32 | (uint64_t)sms << 16 | (uint64_t)per_sm, std::memory_order_relaxed);
+    slot.store(key << 32 | (uint64_t)sms << 16 | (uint64_t)per_sm, std::memory_order_relaxed);
     return cudaSuccess;
   }
 
  private:
-  std::atomic<uint64_t> last_{0};
+  static constexpr unsigned kSlots = 32;
+  std::atomic<uint64_t> seen_[kSlots] = {};
 };
 
 inline bool rows16(const void* p, int64_t ld, int size) {

@@ -1,0 +1,72 @@
+"""The operators around the linear layer where they are easily wrong: host threads,
+streams, argument ranges, rows without spread, long sums, the tail of the
+Gaussian, scratch memory of exactly the size asked for.  Tolerances as in
+test_gpu_layer.py unless a test derives its own."""
+import ctypes
+import math
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+import nvfp4_bit_block_gb300 as nv
+from nvfp4_bit_block_gb300 import layer
+from test_gpu_layer import (BF, F32, U, act64, check_act_grad, check_linear, check_norm, check_norm_grad, operand, rand,
+                            slope64, stats, strided, untouched)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    nv.build()
+
+
+# ---------------------------------------------------------------- host threads
+
+
+def test_concurrent_host_threads_with_rows_of_different_widths():
+    """C callers launch from several threads at once.  Rows of different widths
+    run in the same kernel with different amounts of shared memory; no thread's
+    launch may depend on what another has just asked for."""
+    L = nv.layer_lib()
+    M, rounds, faults = 620, 400, []
+    jobs = []
+    for N in (1032, 5120, 8192, 5120, 8192):
+        x, y = rand((M, N), F32, N), torch.empty((M, N), device="cuda")
+        jobs.append((lambda s, x=x, y=y, N=N: L.nvfp4_layernorm(x.data_ptr(), M, N, N, 0, None, None, 0, 1e-5,
+                                                                y.data_ptr(), N, 0, None, None, None, s),
+                     y, nv.nvfp4_layernorm(x).y))
+    for N in (264, 5120, 2048):
+        x, dy, dx = rand((M, N), F32, N), rand((M, N), F32, N + 1), torch.empty((M, N), device="cuda")
+        mean, rstd = stats(x)
+        n = L.nvfp4_layernorm_backward_workspace(M, N)
+        ws, sums = torch.empty(n, dtype=torch.uint8, device="cuda"), torch.empty((2, N), device="cuda")
+        jobs.append((lambda s, x=x, dy=dy, dx=dx, mean=mean, rstd=rstd, ws=ws, sums=sums, n=n, N=N:
+                     L.nvfp4_layernorm_backward(dy.data_ptr(), N, 0, x.data_ptr(), N, 0, M, N, mean.data_ptr(),
+                                                rstd.data_ptr(), None, 0, dy.data_ptr(), N, dx.data_ptr(), N,
+                                                sums[0].data_ptr(), sums[1].data_ptr(), ws.data_ptr(), n, s),
+                     dx, nv.nvfp4_layernorm_backward(dy, x, mean, rstd, None, dy).dx))
+    torch.cuda.synchronize()
+    start = threading.Barrier(len(jobs))
+
+    def work(call):
+        s = torch.cuda.Stream()
+        start.wait()
+        for k in range(rounds):
+            status = call(s.cuda_stream)
+            if status:
+                faults.append((k, status))
+                return
+        s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(j[0],)) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not faults, faults
+    for _, got, want in jobs:
+        assert torch.equal(got, want)
