@@ -84,10 +84,13 @@ def _binding():
     return _ext
 
 
-def _entered(stream):
-    """Context in which `stream` (a torch stream or a raw cudaStream_t) is torch's current one."""
+def _entered(stream, x):
+    """Context in which `stream` (a torch stream or a raw cudaStream_t) is torch's current one, for a call on tensor x.
+    The raw handle 0 is the default stream (an ExternalStream of it would be a new stream of torch's pool)."""
     import torch
-    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 @dataclass
@@ -125,7 +128,7 @@ def nvfp4_layernorm(x, gamma=None, beta=None, eps: float = 1e-5, out=None, out_d
     with `want_amax` the amax that :func:`nvfp4_quantize` takes.  gamma and beta
     are bf16 or fp32 vectors of one type.  `out` may be x."""
     if stream is not None:
-        with _entered(stream):
+        with _entered(stream, x):
             return nvfp4_layernorm(x, gamma, beta, eps, out, out_dtype, want_stats, want_amax)
     return Normed(*(_ext or _binding()).layernorm(x, gamma, beta, eps, out, out_dtype, want_stats, want_amax))
 
@@ -136,7 +139,7 @@ def nvfp4_layernorm_backward(dy, x, mean, rstd, gamma=None, dres=None, out=None,
     x's type (plus `dres`, the residual branch's gradient) and the fp32 sums
     dgamma and dbeta.  `out` (dx) may be dy or dres."""
     if stream is not None:
-        with _entered(stream):
+        with _entered(stream, x):
             return nvfp4_layernorm_backward(dy, x, mean, rstd, gamma, dres, out, want_dgamma, want_dbeta)
     return NormGrads(*(_ext or _binding()).layernorm_backward(dy, x, mean, rstd, gamma, dres, out, want_dgamma,
                                                               want_dbeta))
@@ -152,7 +155,7 @@ def nvfp4_linear(qa, sfa, alpha_a, qb, sfb, alpha_b, bias=None, act: int = ACT_N
     `want_amax` the amax that :func:`nvfp4_quantize` takes.  `residual` has d's
     type and may be `out`.  `status`: int32[1] on the device, as nvfp4_gemm's."""
     if stream is not None:
-        with _entered(stream):
+        with _entered(stream, qa):
             return nvfp4_linear(qa, sfa, alpha_a, qb, sfb, alpha_b, bias, act, residual, out, out_dtype, want_z,
                                 want_amax, status)
     return LinearOut(*(_ext or _binding()).linear(qa, sfa, alpha_a, qb, sfb, alpha_b, bias, act, residual, out,
@@ -165,6 +168,6 @@ def nvfp4_act_backward(dy, z, act: int, out=None, want_dz: bool = True, want_dbi
     bias gradient, the column sums of dz.  z may be None with ACT_NONE, where
     `want_dz=False` leaves the bias gradient alone.  `out` may be dy or z."""
     if stream is not None:
-        with _entered(stream):
+        with _entered(stream, dy):
             return nvfp4_act_backward(dy, z, act, out, want_dz, want_dbias)
     return ActGrads(*(_ext or _binding()).act_backward(dy, z, act, out, want_dz, want_dbias))

@@ -70,3 +70,28 @@ def test_concurrent_host_threads_with_rows_of_different_widths():
     assert not faults, faults
     for _, got, want in jobs:
         assert torch.equal(got, want)
+
+
+# ---------------------------------------------------------------- streams
+
+
+def test_the_raw_handle_of_the_default_stream():
+    """torch.cuda.default_stream().cuda_stream is 0: given as a raw handle it is the
+    default stream, behind what was put there before."""
+    assert torch.cuda.default_stream().cuda_stream == 0
+    new = rand((700, 512), BF, 1)
+    want = nv.nvfp4_layernorm(new).y
+    x = torch.zeros_like(new)
+    big = torch.randn(8192, 8192, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(10):  # some 100 ms
+        big = big @ big * 1e-3
+    x.copy_(new)
+    got = nv.nvfp4_layernorm(x, stream=0).y
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):  # whatever stream is current
+        with layer._entered(0, x):
+            assert torch.cuda.current_stream() == torch.cuda.default_stream()
+        assert torch.cuda.current_stream() == side
