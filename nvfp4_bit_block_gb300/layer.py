@@ -12,7 +12,7 @@ wrong types raise TypeError, wrong shapes, strides or devices ValueError, and
 what the library refuses Nvfp4Error.
 
 Results are allocated on the stream that the call runs on (``stream``, a torch
-stream or a raw cudaStream_t, or torch's current one), as are workspaces, so
+stream or a raw cudaStream_t of the tensors' device, or torch's current one), as are workspaces, so
 torch's allocator hands their memory out again in that stream's order.  To use a
 result on another stream, make that stream wait and call ``record_stream`` on the
 tensor, as for any torch tensor.  The small fp32 results of one call (mean, rstd
@@ -20,6 +20,7 @@ and amax; dgamma and dbeta) share one allocation.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -85,11 +86,17 @@ def _binding():
 
 
 def _entered(stream, x):
-    """Context in which `stream` (a torch stream or a raw cudaStream_t) is torch's current one, for a call on tensor x.
-    The raw handle 0 is the default stream (an ExternalStream of it would be a new stream of torch's pool)."""
+    """Context in which `stream` (a torch stream or a raw cudaStream_t) is the current one of the device of x, the tensor
+    that the call is on.  The raw handle 0 is the default stream (an ExternalStream of it would be a new stream of torch's
+    pool)."""
     import torch
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    if not getattr(x, "is_cuda", False):
+        return contextlib.nullcontext()  # the call refuses it
+    if not hasattr(stream, "cuda_stream"):  # a handle has no device of its own: it is taken for one of x's
+        handle = int(stream)
+        stream = torch.cuda.ExternalStream(handle, device=x.device) if handle else torch.cuda.default_stream(x.device)
+    elif stream.device != x.device:
+        raise ValueError(f"stream must be on {x.device} (got {stream.device})")
     return torch.cuda.stream(stream)
 
 
