@@ -12,6 +12,7 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
+#include <climits>
 #include <string>
 
 #include "nvfp4_layer.h"
@@ -51,10 +52,13 @@ bool truth(PyObject* o) {
   if (r < 0) throw Refused{nullptr, ""};
   return r != 0;
 }
-long integer(PyObject* o) {
-  const long v = PyLong_AsLong(o);
+// An activation's code; a number that an int does not hold is none, and refused as the library would.
+int activation(PyObject* o, const char* where) {
+  int over = 0;
+  const long v = PyLong_AsLongAndOverflow(o, &over);
   if (v == -1 && PyErr_Occurred()) throw Refused{nullptr, ""};
-  return v;
+  if (over != 0 || v < INT_MIN || v > INT_MAX) throw Status{NVFP4_ERR_FLAGS, where};
+  return (int)v;
 }
 
 // 1 for bfloat16, 0 for float32.
@@ -254,7 +258,7 @@ PyObject* linear(PyObject* const* a) {
                    &qb = needed(a[3], "qb"), &sfb = needed(a[4], "sfb"), &ab = needed(a[5], "alpha_b");
   const at::Tensor *bias = tensor(a[6], "bias"), *res = tensor(a[8], "residual"), *out = tensor(a[9], "out"),
                    *status = tensor(a[13], "status");
-  const long act = integer(a[7]);
+  const int act = activation(a[7], "nvfp4_linear");
   const bool want_z = truth(a[11]), want_amax = truth(a[12]);
   if (qa.dim() != 2 || qb.dim() != 2) type_error("qa and qb must be 2-D tensors");
   const c10::Device dev = qa.device();
@@ -282,7 +286,7 @@ PyObject* linear(PyObject* const* a) {
   const Workspace ws(nvfp4_linear_workspace(M, N, K), "nvfp4_linear_workspace", dev);
   auto bytes = [](void* p) { return static_cast<const uint8_t*>(p); };
   check(nvfp4_linear(bytes(ap), bytes(sap), static_cast<float*>(aap), bytes(bp), bytes(sbp), static_cast<float*>(abp), M,
-                     N, K, biasp, biasb, (int)act, rm.p, rm.ld, want_z ? z.data_ptr() : nullptr, N, dm.p, dm.ld, ob,
+                     N, K, biasp, biasb, act, rm.p, rm.ld, want_z ? z.data_ptr() : nullptr, N, dm.p, dm.ld, ob,
                      want_amax ? amax.data_ptr<float>() : nullptr, ws.p, ws.n, static_cast<int*>(stp), stream_of(dev)),
         "nvfp4_linear");
   return tuple(out ? given(a[9]) : THPVariable_Wrap(std::move(made)), want_z ? THPVariable_Wrap(std::move(z)) : none(),
@@ -293,7 +297,7 @@ PyObject* linear(PyObject* const* a) {
 PyObject* act_backward(PyObject* const* a) {
   const at::Tensor& dy = needed(a[0], "dy");
   const at::Tensor *z = tensor(a[1], "z"), *out = tensor(a[3], "out");
-  const long act = integer(a[2]);
+  const int act = activation(a[2], "nvfp4_act_backward");
   const bool want_dz = truth(a[4]), want_dbias = truth(a[5]);
   const c10::Device dev = dy.device();
   const Matrix dm = matrix(dy, "dy", dev);
@@ -313,7 +317,7 @@ PyObject* act_backward(PyObject* const* a) {
     dbias = fresh({N}, at::kFloat, dev);
     ws = Workspace(nvfp4_act_backward_workspace(M, N), "nvfp4_act_backward_workspace", dev);
   }
-  check(nvfp4_act_backward(dm.p, dm.ld, zm.p, zm.ld, M, N, b, (int)act, om.p, om.ld,
+  check(nvfp4_act_backward(dm.p, dm.ld, zm.p, zm.ld, M, N, b, act, om.p, om.ld,
                            want_dbias ? dbias.data_ptr<float>() : nullptr, ws.p, ws.n, stream_of(dev)),
         "nvfp4_act_backward");
   return tuple(!want_dz ? none() : (out ? given(a[3]) : THPVariable_Wrap(std::move(made))),

@@ -95,3 +95,15 @@ def test_the_raw_handle_of_the_default_stream():
         with layer._entered(0, x):
             assert torch.cuda.current_stream() == torch.cuda.default_stream()
         assert torch.cuda.current_stream() == side
+
+
+# ---------------------------------------------------------------- arguments
+
+
+@pytest.mark.parametrize("act", [2 ** 32, 2 ** 32 + 2, -2 ** 32, 2 ** 63, -2 ** 200])
+def test_activations_beyond_32_bits_are_refused(act):
+    a, b, x = operand(16, 64, 1), operand(32, 64, 2), rand((4, 32), F32, 3)
+    for call in (lambda: nv.nvfp4_linear(*a, *b, act=act), lambda: nv.nvfp4_act_backward(x, x, act)):
+        with pytest.raises(nv.Nvfp4Error) as e:
+            call()
+        assert e.value.status == -4
