@@ -5,6 +5,7 @@
 // mean is summed first and the squares about it second (two reductions: no
 // cancellation however far the mean is from zero).
 #include <atomic>
+#include <cfloat>
 
 #include "layer_internal.h"
 #include "norm_common.cuh"
@@ -16,6 +17,16 @@ namespace {
 
 constexpr int kMaxThreads = 1024;
 constexpr int kWarpThreads = 256;  // block of the one-warp-per-row kernels
+
+// sum / N from the sum and the rounded 1 / N, refined by the remainder sum - N * mean,
+// which a fused multiply-add forms without rounding.  Of a row without spread, whose
+// sum is often exact, this is the row's value; sum * (1 / N) alone may be a unit off,
+// which rstd makes a visible y (-16320 in 408 columns: 0.3).  A division instead of the
+// refinement took 53.5 us for 16384 x 5120 bf16, this takes 53.0 to 53.3.
+__device__ __forceinline__ float mean_of(float sum, float n, float inv) {
+  const float mean = sum * inv, more = fmaf(fmaf(-n, mean, sum), inv, mean);
+  return fabsf(mean) <= FLT_MAX ? more : mean;  // Inf stays (its remainder is NaN)
+}
 
 // The block's largest magnitude into both amax entries: by one block alone
 // stored, by several joined (the pair is zeroed before the launch).
@@ -72,7 +83,7 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a) {
     group_sums<WARP, R>(mean, buf[0]);
 #pragma unroll
     for (int q = 0; q < R; ++q) {
-      mean[q] *= inv;
+      mean[q] = mean_of(mean[q], (float)N, inv);
       t[q] = 0.0f;
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
@@ -217,7 +228,7 @@ __global__ void __launch_bounds__(THREADS) norm_stream_kernel(const NormArgs arg
     stage = stage == S - 1 ? 0 : stage + 1;
     float m[1] = {sum.x + sum.y};
     group_sums<WARP, 1>(m, buf[0]);
-    const float mean = m[0] * inv;
+    const float mean = mean_of(m[0], (float)a.N, inv);
     const float2 shift = splat(-mean);
     sum = splat(0.0f);
 #pragma unroll
@@ -317,7 +328,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_scalar_kernel(const Norm
     }
     if (r + groups < a.M) load();
     group_sums<WARP, 1>(s, buf[0]);
-    const float mean = s[0] * inv;
+    const float mean = mean_of(s[0], (float)a.N, inv);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       x[i] -= mean;

@@ -107,3 +107,47 @@ def test_activations_beyond_32_bits_are_refused(act):
         with pytest.raises(nv.Nvfp4Error) as e:
             call()
         assert e.value.status == -4
+
+
+# ---------------------------------------------------------------- rows without spread
+
+
+def exact_constants(N):
+    """Whole numbers below 256 whose sum over N fp32 values is exact in any order, and
+    whose sum times the rounded 1 / N is not the number (where there are some)."""
+    inv = np.float32(1) / np.float32(N)
+    c = [k for k in range(1, 256) if np.float32(N * k) * inv != np.float32(k)]
+    return (c or [3])[:5] + [255]
+
+
+# every kernel: few rows and many, vectors, single values and rows by classes, up to the longest
+CONSTANT = [(5, 56), (5, 408), (5, 1128), (5, 9024), (5, 17704), (700, 56), (700, 408), (700, 1128), (700, 9024),
+            (700, 20504), (5, 307), (5, 647), (5, 2213), (5, 3081), (5, 6145), (5, 12289), (700, 1543), (700, 3081),
+            (5, 34263)]
+
+
+@pytest.mark.parametrize("xt", [BF, F32])
+@pytest.mark.parametrize("M,N", CONSTANT)
+def test_layernorm_of_constant_rows_is_beta(M, N, xt):
+    """A row of one value far from zero has that mean and no spread: where its sum is
+    exact, so are the mean and y = beta."""
+    c = torch.tensor(exact_constants(N), device="cuda", dtype=torch.float32)
+    c = c.repeat(-(-M // c.numel()))[:M] * -64.0
+    x = c[:, None].expand(M, N).to(xt).contiguous()
+    gamma, beta = rand((N,), F32, 1, 0.1, 1.0), rand((N,), F32, 2)
+    r = nv.nvfp4_layernorm(x, gamma, beta, 1e-5, out_dtype=F32)
+    assert torch.equal(r.mean, c)
+    assert torch.equal(r.y, beta.expand(M, N))
+    assert bool(((r.rstd.double() - 1e-5 ** -0.5).abs() <= 4 * U * 1e-5 ** -0.5).all())
+
+
+@pytest.mark.parametrize("M,N", [(8, 1), (8, 64), (8, 1023), (8, 5120), (8, 33000), (700, 264), (700, 5120), (700, 9008),
+                                 (700, 2731), (700, 12379)])
+def test_layernorm_of_a_row_with_an_infinity(M, N):
+    """Its mean is infinite, its y NaN throughout; no other row takes notice."""
+    x = rand((M, N), BF, 10)
+    x[5, N - 1], x[6, 0] = float("inf"), float("-inf")
+    r = nv.nvfp4_layernorm(x)
+    assert r.mean[5:7].tolist() == [float("inf"), float("-inf")] and bool(r.rstd[5:7].isnan().all())
+    bad = r.y.isnan().all(1)
+    assert bad.nonzero().flatten().tolist() == [5, 6] and bool(r.y[~bad].isfinite().all())
