@@ -276,11 +276,13 @@ __global__ void __launch_bounds__(THREADS) norm_stream_kernel(const NormArgs arg
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) x[i][j] = fma2(mul2(x[i][j], scale), g[kKeep ? i : 0][j], b[kKeep ? i : 0][j]);
-      const Raw<YT, 8> o = pack2(x[i], Raw<YT, 8>());
-      if (!ODD || (skip <= c && c + 8 <= N))
+      Raw<YT, 8> o = pack2(x[i], Raw<YT, 8>());
+      if (!ODD || (skip <= c && c + 8 <= N)) {
         *reinterpret_cast<Raw<YT, 8>*>(y + c) = o;
-      else
+      } else {
         store_part(y + c, o, skip - c, N - c);
+        if (rstd > FLT_MAX) keep_part<YT>(o, skip - c, N - c);  // columns beside the row: 0 * Inf is no output
+      }
       if (a.amax) top = top_of(o, top);
     }
   }

@@ -150,6 +150,14 @@ __device__ __forceinline__ void store_part(T* to, const Raw<T, 8>& v, int lo, in
     if (i >= lo && i < hi) to[i] = reinterpret_cast<const T*>(&v)[i];
 }
 
+// Zeros in place of a chunk's values other than lo .. hi - 1.
+template <typename T>
+__device__ __forceinline__ void keep_part(Raw<T, 8>& v, int lo, int hi) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < lo || i >= hi) reinterpret_cast<T*>(&v)[i] = from_f32<T>(0.0f);
+}
+
 // 8 values as pairs for the packed fp32 instructions.
 __device__ __forceinline__ void unpack2(const Raw<bf16, 8>& r, float2* f) {
   f[0] = bf16x2_to_f32x2(r.v.x);

@@ -151,3 +151,15 @@ def test_layernorm_of_a_row_with_an_infinity(M, N):
     assert r.mean[5:7].tolist() == [float("inf"), float("-inf")] and bool(r.rstd[5:7].isnan().all())
     bad = r.y.isnan().all(1)
     assert bad.nonzero().flatten().tolist() == [5, 6] and bool(r.y[~bad].isfinite().all())
+
+
+def test_layernorm_amax_of_rows_whose_squares_vanish():
+    """eps = 0 and values whose squares are zero in fp32: rstd is Inf and so is every y.
+    The amax is that of the outputs; the columns beside a row, which its vectors
+    take along, are none (0 * Inf would make it NaN)."""
+    for M, N, ld in ((700, 2000, 2000), (700, 2000, 2001), (700, 1538, 1539), (5, 2000, 2001), (700, 9008, 9009)):
+        x = torch.full((M, N), 1e-30, device="cuda")
+        x[:, ::2] *= -1
+        xv = strided(x.to(BF), ld - N, 0)[1]
+        r = nv.nvfp4_layernorm(xv, eps=0.0, out=strided(torch.zeros_like(xv), ld - N, 0)[1], want_amax=True)
+        assert bool(r.y.isinf().all()) and r.amax.tolist() == [float("inf")] * 2, (M, N, ld)
