@@ -63,7 +63,7 @@ typedef enum {
  *   amax_dev     float[2] or NULL: both set to max |y| over the rounded y, as
  *                nvfp4_amax(y) without an RHT flag gives (NaN in y gives NaN), so
  *                that nvfp4_quantize can follow without another pass over y
- * M = 0 or N = 0: no rows are written, amax (if given) is 0.
+ * M = 0 or N = 0: nothing is written but amax (0).
  * A NaN or Inf in a row makes that row NaN and touches no other.
  * Errors: SHAPE (negative sizes, ld < N), NULL, ALIGN, FLAGS, CUDA.
  */

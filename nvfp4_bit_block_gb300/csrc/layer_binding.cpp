@@ -13,6 +13,7 @@
 #include <c10/cuda/CUDAStream.h>
 
 #include <climits>
+#include <cmath>
 #include <string>
 
 #include "nvfp4_layer.h"
@@ -215,6 +216,10 @@ PyObject* layernorm(PyObject* const* a) {
                         stats ? f.ptr(am) : nullptr, stats ? f.ptr(ar) : nullptr, amax ? f.ptr(aa) : nullptr,
                         stream_of(dev)),
         "nvfp4_layernorm");
+  if (stats && N == 0) {  // the library writes none; the mean of no values is 0 / 0
+    f.view(am, M).fill_(NAN);
+    f.view(ar, M).fill_(NAN);
+  }
   return tuple(out ? given(a[4]) : THPVariable_Wrap(std::move(made)), stats ? THPVariable_Wrap(f.view(am, M)) : none(),
                stats ? THPVariable_Wrap(f.view(ar, M)) : none(), amax ? THPVariable_Wrap(f.view(aa, 2)) : none());
 }

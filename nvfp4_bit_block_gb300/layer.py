@@ -133,7 +133,8 @@ def nvfp4_layernorm(x, gamma=None, beta=None, eps: float = 1e-5, out=None, out_d
     """Layer norm of each row of x (M x N, bf16 or fp32): y of `out_dtype`
     (default: out's or x's), the rows' mean and rstd for the backward pass, and
     with `want_amax` the amax that :func:`nvfp4_quantize` takes.  gamma and beta
-    are bf16 or fp32 vectors of one type.  `out` may be x."""
+    are bf16 or fp32 vectors of one type.  `out` may be x.  Rows of no values have
+    mean and rstd NaN."""
     if stream is not None:
         with _entered(stream, x):
             return nvfp4_layernorm(x, gamma, beta, eps, out, out_dtype, want_stats, want_amax)

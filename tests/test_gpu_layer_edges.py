@@ -163,3 +163,13 @@ def test_layernorm_amax_of_rows_whose_squares_vanish():
         xv = strided(x.to(BF), ld - N, 0)[1]
         r = nv.nvfp4_layernorm(xv, eps=0.0, out=strided(torch.zeros_like(xv), ld - N, 0)[1], want_amax=True)
         assert bool(r.y.isinf().all()) and r.amax.tolist() == [float("inf")] * 2, (M, N, ld)
+
+
+def test_layernorm_statistics_of_empty_rows_are_nan():
+    """The mean of no values is 0 / 0."""
+    for M in (1, 3, 1000):
+        junk = [torch.zeros(2 * M + 8, device="cuda") for _ in range(4)]  # memory that the results may be given
+        del junk
+        r = nv.nvfp4_layernorm(torch.empty((M, 0), dtype=BF, device="cuda"), want_amax=True)
+        assert r.mean.shape == (M,) and bool(r.mean.isnan().all()) and bool(r.rstd.isnan().all())
+        assert r.amax.tolist() == [0.0, 0.0]
