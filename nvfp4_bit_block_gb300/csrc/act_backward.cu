@@ -30,7 +30,7 @@ __device__ __forceinline__ Raw<T, V> slope_chunk(const Raw<T, V>& dy, const Raw<
   if (act) {
     unpack(z, v);
 #pragma unroll
-    for (int i = 0; i < V; ++i) d[i] = __fmul_rn(d[i], act_slope(v[i], act));
+    for (int i = 0; i < V; ++i) d[i] = __fmul_rn(d[i], act_slope<T>(v[i], act));
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) sum[i] += d[i];

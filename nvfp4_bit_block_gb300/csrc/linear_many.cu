@@ -158,7 +158,7 @@ __device__ __forceinline__ uint32_t put_rows(const LinearArgs& a, T* d, T* z, co
       for (int i = 0; i < B; ++i, z += a.ldz)
         if (FULL || r0 + i < rows) *z = from_f32<T>(w[i]);
     }
-    act_all<B>(w, a.act);
+    act_all<B, T>(w, a.act);
     if (res) {
 #pragma unroll
       for (int i = 0; i < B; ++i) w[i] += to_f32(add[i]);
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             return buf + slot * kBox;
           };
           if (a.z) put(&zmap, next_buffer());
-          act_all<kCols>(v, a.act);
+          act_all<kCols, T>(v, a.act);
           if (a.residual) {
             uint8_t* b = buf + (c & 1) * kBox;
             const uint32_t bit = 1u << (c & 1);

@@ -72,7 +72,7 @@ __device__ __forceinline__ void put_tokens(const LinearArgs& a, int64_t m, int64
     for (int i = 0; i < 16; ++i)
       if (i < count) z[i * a.ldz] = from_f32<T>(v[i]);
   }
-  act_all<16>(v, a.act);
+  act_all<16, T>(v, a.act);
   if (a.residual) {
     const T* r = static_cast<const T*>(a.residual) + m * a.ldr + n;
 #pragma unroll
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <typename T>
 __device__ __forceinline__ uint32_t put(const LinearArgs& a, int64_t m, int64_t n, float z) {
   if (a.z) static_cast<T*>(a.z)[m * a.ldz + n] = from_f32<T>(z);
-  float d = act_value(z, a.act);
+  float d = act_value<T>(z, a.act);
   if (a.residual) d += to_f32(static_cast<const T*>(a.residual)[m * a.ldr + n]);
   const T o = from_f32<T>(d);
   static_cast<T*>(a.d)[m * a.ldd + n] = o;

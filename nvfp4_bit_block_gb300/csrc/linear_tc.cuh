@@ -254,7 +254,7 @@ __device__ __forceinline__ float2 gate2(float2 z, float2 neg) {  // z / (1 + 2^n
   const float2 e = add2(make_float2(ex2(neg.x), ex2(neg.y)), splat2(1.0f));
   return mul2(z, make_float2(rcp(e.x), rcp(e.y)));
 }
-template <int ACT>
+template <int ACT, typename T>
 __device__ __forceinline__ float2 act_pair(float2 z) {
   if constexpr (ACT == NVFP4_ACT_RELU) {
     asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(z.x) : "f"(z.x));
@@ -264,6 +264,16 @@ __device__ __forceinline__ float2 act_pair(float2 z) {
     return gate2(z, mul2(z, fma2(mul2(z, z), splat2(-kLog2e * kGeluC * kGeluA), splat2(-kLog2e * kGeluC))));
   } else if constexpr (ACT == NVFP4_ACT_SILU) {
     return gate2(z, mul2(z, splat2(-kLog2e)));
+  } else if constexpr (sizeof(T) == 4) {
+    const float2 d = fma2(splat2(kGaussV), make_float2(fabsf(z.x), fabsf(z.y)), splat2(1.0f));
+    const float2 y = mul2(mul2(z, z), splat2(-kHalfLog2e));
+    const float2 t = make_float2(rcp(d.x), rcp(d.y)), e = make_float2(ex2(y.x), ex2(y.y));
+    float2 q = splat2(gauss_v(8));
+#pragma unroll
+    for (int i = 7; i >= 0; --i) q = fma2(q, t, splat2(gauss_v(i)));
+    q = mul2(mul2(q, t), e);
+    const float2 r = sub2(splat2(1.0f), q);
+    return mul2(z, make_float2(z.x < 0.0f ? q.x : r.x, z.y < 0.0f ? q.y : r.y));
   } else {
     const float2 x = mul2(make_float2(fabsf(z.x), fabsf(z.y)), splat2(kRsqrt2));
     const float2 d = fma2(splat2(0.3275911f), x, splat2(1.0f)), y = mul2(mul2(splat2(-kLog2e), x), x);
@@ -277,23 +287,23 @@ __device__ __forceinline__ float2 act_pair(float2 z) {
     return mul2(z, make_float2(z.x < 0.0f ? q.x : r.x, z.y < 0.0f ? q.y : r.y));
   }
 }
-template <int NV, int ACT>
+template <int NV, int ACT, typename T>
 __device__ __forceinline__ void act_each(float* v) {
 #pragma unroll
   for (int i = 0; i < NV; i += 2) {
-    const float2 r = act_pair<ACT>(make_float2(v[i], v[i + 1]));
+    const float2 r = act_pair<ACT, T>(make_float2(v[i], v[i + 1]));
     v[i] = r.x;
     v[i + 1] = r.y;
   }
 }
-// act over a register array, the choice taken once.
-template <int NV>
+// act over a register array, for results of type T; the choice is taken once.
+template <int NV, typename T>
 __device__ __forceinline__ void act_all(float* v, int act) {
   switch (act) {
-    case NVFP4_ACT_RELU: act_each<NV, NVFP4_ACT_RELU>(v); break;
-    case NVFP4_ACT_GELU: act_each<NV, NVFP4_ACT_GELU>(v); break;
-    case NVFP4_ACT_GELU_TANH: act_each<NV, NVFP4_ACT_GELU_TANH>(v); break;
-    case NVFP4_ACT_SILU: act_each<NV, NVFP4_ACT_SILU>(v); break;
+    case NVFP4_ACT_RELU: act_each<NV, NVFP4_ACT_RELU, T>(v); break;
+    case NVFP4_ACT_GELU: act_each<NV, NVFP4_ACT_GELU, T>(v); break;
+    case NVFP4_ACT_GELU_TANH: act_each<NV, NVFP4_ACT_GELU_TANH, T>(v); break;
+    case NVFP4_ACT_SILU: act_each<NV, NVFP4_ACT_SILU, T>(v); break;
     default: break;
   }
 }

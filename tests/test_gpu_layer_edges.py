@@ -173,3 +173,81 @@ def test_layernorm_statistics_of_empty_rows_are_nan():
         r = nv.nvfp4_layernorm(torch.empty((M, 0), dtype=BF, device="cuda"), want_amax=True)
         assert r.mean.shape == (M,) and bool(r.mean.isnan().all()) and bool(r.rstd.isnan().all())
         assert r.amax.tolist() == [0.0, 0.0]
+
+
+# ---------------------------------------------------------------- erf GELU in fp32
+
+
+def far(got, want):
+    return float((got.double() - want).norm() / want.norm())
+
+
+def linear_of(z, tokens):
+    """nvfp4_linear's erf GELU of z: zero operands, z as the bias, the same in every token's row."""
+    b = operand(z.numel(), 64, 3)
+    a = (torch.zeros((tokens, 32), dtype=torch.uint8, device="cuda"),
+         torch.zeros((-(-tokens // 128) * 128, 4), dtype=torch.uint8, device="cuda"), torch.ones(1, device="cuda"))
+    d = nv.nvfp4_linear(*a, *b, bias=z, act=nv.ACT_GELU, out_dtype=F32).d
+    assert torch.equal(d[0].expand_as(d), d)
+    return d[0]
+
+
+# one and several tokens: joined pieces, whole tiles, pairs of SMs with vectors and with single values
+GELU_PATHS = [(1, 20480), (40, 20480), (200, 640), (1100, 4096), (1100, 4097)]
+
+
+@pytest.mark.parametrize("tokens,N", GELU_PATHS)
+def test_gelu_in_fp32_is_as_close_as_the_plain_formula(tokens, N):
+    """No farther from the 64-bit formula than z / 2 * (1 + erf(z / sqrt 2)) in
+    elementary fp32 operations, by more than a quarter."""
+    z = rand((N,), F32, 1, 1.5)
+    plain = 0.5 * z * (1.0 + torch.erf(z * math.sqrt(0.5)))
+    want = act64(z.double(), nv.ACT_GELU)
+    assert far(linear_of(z, tokens), want) <= 1.25 * far(plain, want)
+
+
+@pytest.mark.parametrize("M,N", [(64, 4096), (64, 4097), (1000, 1024), (1000, 1001)])
+def test_gelu_gradient_in_fp32_is_as_close_as_the_plain_formula(M, N):
+    z = rand((M, N), F32, 2, 1.5)
+    plain = 0.5 * (1.0 + torch.erf(z * math.sqrt(0.5))) + z * torch.exp(-0.5 * z * z) / math.sqrt(2 * math.pi)
+    want = slope64(z.double(), nv.ACT_GELU)
+    got = nv.nvfp4_act_backward(torch.ones_like(z), z, nv.ACT_GELU).dz
+    assert far(got, want) <= 1.25 * far(plain, want)
+
+
+def test_gelu_in_fp32_keeps_the_tail():
+    """For z in [-5, -2] value and derivative are tiny and still have their leading
+    digits.  erfc(-z / sqrt 2) changes by z^2 <= 25 times its argument's relative
+    error, of two roundings: 50 u; erfc itself is within 4 units (8 u).  The
+    density's exponent z^2 / 2 <= 12.5 has one rounding, the exponential is within 2
+    units: 17 u.  Products add a few u.  In the derivative Phi + z phi the first
+    term is at most a quarter of the second there, so that errors grow by at most
+    1.25 / 0.75: all below 2^7 u."""
+    z = torch.linspace(-5.0, -2.0, 20000, device="cuda")
+    for got, want in ((linear_of(z, 1), act64(z.double(), nv.ACT_GELU)),
+                      (linear_of(z, 1100), act64(z.double(), nv.ACT_GELU)),
+                      (nv.nvfp4_act_backward(torch.ones_like(z)[None], z[None], nv.ACT_GELU).dz[0],
+                       slope64(z.double(), nv.ACT_GELU))):
+        assert float(((got.double() - want) / want).abs().max()) <= 2.0 ** 7 * U
+
+
+@pytest.mark.parametrize("act", range(1, 5))
+@pytest.mark.parametrize("tokens", [1, 40, 1100])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_linear_activations_of_extreme_values(act, tokens, dt):
+    """Large and tiny z have the limits of the activation, Inf stays, NaN stays; -Inf
+    is 0 for ReLU and, as the formulas have it (-Inf * 0), NaN for the others."""
+    z = torch.zeros(2600, device="cuda")
+    z[:11] = torch.tensor([0.0, 1e-30, 1e30, -1e30, 1e4, -1e4, 30.0, -30.0, float("inf"), float("nan"), float("-inf")])
+    b = operand(z.numel(), 64, 3)
+    a = (torch.zeros((tokens, 32), dtype=torch.uint8, device="cuda"),
+         torch.zeros((-(-tokens // 128) * 128, 4), dtype=torch.uint8, device="cuda"), torch.ones(1, device="cuda"))
+    r = nv.nvfp4_linear(*a, *b, bias=z, act=act, out_dtype=dt, want_z=True)
+    assert torch.equal(r.z[0, :9], z[:9].to(dt))
+    d = r.d[-1, :11].float()
+    big = torch.tensor([1e30, 1e4, 30.0], device="cuda").to(dt).float()
+    assert d[0] == 0 and 0 <= d[1] <= z[1].to(dt)
+    assert torch.equal(d[[2, 4, 6]], big) and bool((d[[3, 5, 7]].abs() <= 1e-10).all())
+    assert d[8] == float("inf") and bool(d[9].isnan())
+    assert d[10] == 0 if act == nv.ACT_RELU else bool(d[10].isnan())
+    assert bool((r.d[:, 11:] == 0).all())
