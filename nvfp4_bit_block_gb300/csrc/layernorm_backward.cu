@@ -24,7 +24,7 @@ namespace nvfp4 {
 namespace norm {
 namespace {
 
-constexpr int kMaxBlocks = 608;          // rows of partial sums in the workspace
+constexpr int kMaxBlocks = 608;          // blocks or bands that leave a row of partial sums each
 constexpr int64_t kRing = 220 * 1024;    // shared memory for rows on their way
 
 // Barrier of a row's group (its threads are whole warps of one block).
@@ -475,6 +475,10 @@ int64_t bands_of(int64_t M, int64_t N, int V) {
 
 int round32(int64_t v) { return (int)((v + 31) / 32 * 32); }
 
+// Rows of partial sums in the workspace.  Every block or band has a row of the matrix of its own, so that there are
+// no more of them than rows (100 MB for one row of 20480 values otherwise); by classes go only more rows than kMaxBlocks.
+int64_t most_parts(int64_t M) { return std::min<int64_t>(M, kMaxBlocks); }
+
 // `e`: of the launch that leaves the parts.
 cudaError_t join(const NormGradArgs& a, int64_t parts, cudaError_t e, cudaStream_t s) {
   if (e != cudaSuccess || parts == 1 || (!a.dgamma && !a.dbeta)) return e;
@@ -524,7 +528,7 @@ template <typename DT, typename XT, int V>
 cudaError_t run_long(const NormGradArgs& a, cudaStream_t s) {
   const int64_t bands = bands_of(a.M, a.N, V), rows = (a.M + bands - 1) / bands;
   const dim3 grid((unsigned)((a.N + 128 * V - 1) / (128 * V)), (unsigned)((a.M + rows - 1) / rows));
-  float2* sums = reinterpret_cast<float2*>(a.ws + kMaxBlocks * 2 * a.N);
+  float2* sums = reinterpret_cast<float2*>(a.ws + most_parts(a.M) * 2 * a.N);
   const dim3 rows_grid((unsigned)std::min<int64_t>(a.M, 152 * 4));
   cudaError_t e = launch_early(row_sums_kernel<DT, XT>, rows_grid, 512, 0, s, a, sums);
   if (e == cudaSuccess) e = launch_early(columns_kernel<DT, XT, V>, grid, 128, 0, s, a, sums, rows);
@@ -584,7 +588,7 @@ cudaError_t launch(const NormGradArgs& a, cudaStream_t s) {
 
 int64_t norm_grad_workspace(int64_t M, int64_t N) {
   // partial column sums of every block or band, and two sums per row
-  return norm::kMaxBlocks * 2 * N * 4 + (M + 1) / 2 * 2 * 8;
+  return norm::most_parts(M) * 2 * N * 4 + (M + 1) / 2 * 2 * 8;
 }
 
 cudaError_t launch_norm_grad(const NormGradArgs& a, cudaStream_t s) {

@@ -251,3 +251,60 @@ def test_linear_activations_of_extreme_values(act, tokens, dt):
     assert d[8] == float("inf") and bool(d[9].isnan())
     assert d[10] == 0 if act == nv.ACT_RELU else bool(d[10].isnan())
     assert bool((r.d[:, 11:] == 0).all())
+
+
+# ---------------------------------------------------------------- scratch memory
+
+
+GUARD = 4096
+
+
+def guarded(n):
+    """n bytes between guard bytes: (buffer, the n bytes)."""
+    base = torch.full((n + 2 * GUARD,), 0xA5, dtype=torch.uint8, device="cuda")
+    return base, base[GUARD:GUARD + n]
+
+
+def guards_hold(base):
+    return bool((base[:GUARD] == 0xA5).all() and (base[-GUARD:] == 0xA5).all())
+
+
+@pytest.mark.parametrize("M,N,pad", [(1, 1, 0), (1, 5120, 0), (1, 20480, 0), (2, 133, 0), (3, 5128, 0), (7, 33001, 0),
+                                     (100, 2731, 0), (700, 5120, 0), (1217, 1001, 0), (1300, 4096, 0), (2000, 8192, 0),
+                                     (900, 12288, 0), (16384, 264, 0), (3000, 333, 1)])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_layernorm_backward_in_the_workspace_asked_for(M, N, pad, dt):
+    """With exactly the bytes asked for: nothing beside them is written."""
+    L = nv.layer_lib()
+    x, dy, dres = rand((M, N), dt, M + N, 2.0, 0.3), rand((M, N), dt, M + N + 1, 1e-3), rand((M, N), dt, 14, 1e-3)
+    mean, rstd = stats(x)
+    n = L.nvfp4_layernorm_backward_workspace(M, N)
+    for res in (None, dres):
+        base, ws = guarded(n)
+        xv, dyv = strided(x, pad, 0)[1], strided(dy, pad, 0)[1]
+        dx, sums = strided(torch.zeros_like(x), pad, 0)[1], torch.empty((2, N), device="cuda")
+        rv = strided(res, pad, 0)[1] if res is not None else None
+        b = int(dt is BF)
+        assert L.nvfp4_layernorm_backward(dyv.data_ptr(), N + pad, b, xv.data_ptr(), N + pad, b, M, N, mean.data_ptr(),
+                                          rstd.data_ptr(), None, 0, rv.data_ptr() if rv is not None else None, N + pad,
+                                          dx.data_ptr(), N + pad, sums[0].data_ptr(), sums[1].data_ptr(),
+                                          ws.data_ptr(), n, torch.cuda.current_stream().cuda_stream) == 0
+        check_norm_grad(dy, x, mean, rstd, None, res, nv.NormGrads(dx, sums[0], sums[1]))
+        assert guards_hold(base)
+
+
+@pytest.mark.parametrize("M,N,pad", [(1, 33, 0), (300, 33, 0), (700, 20480, 0), (513, 2048, 0), (4000, 1001, 0),
+                                     (4001, 1002, 0), (4000, 1004, 0), (16384, 72, 1), (5000, 9, 0)])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_act_backward_in_the_workspace_asked_for(M, N, pad, dt):
+    L = nv.layer_lib()
+    dy, z = rand((M, N), dt, M + N, 1e-3), rand((M, N), dt, N, 2.0)
+    n = L.nvfp4_act_backward_workspace(M, N)
+    base, ws = guarded(n)
+    dyv, zv, dz = strided(dy, pad, 0)[1], strided(z, pad, 0)[1], strided(torch.zeros_like(z), pad, 0)[1]
+    dbias = torch.empty(N, device="cuda")
+    assert L.nvfp4_act_backward(dyv.data_ptr(), N + pad, zv.data_ptr(), N + pad, M, N, int(dt is BF), nv.ACT_SILU,
+                                dz.data_ptr(), N + pad, dbias.data_ptr(), ws.data_ptr(), n,
+                                torch.cuda.current_stream().cuda_stream) == 0
+    check_act_grad(dy, z, nv.ACT_SILU, nv.ActGrads(dz, dbias))
+    assert guards_hold(base)
