@@ -158,12 +158,18 @@ __global__ void __launch_bounds__(TX * TY, V == 1 ? (TY > 1 ? 768 : 1024) / (TX 
 constexpr int64_t kFewRows8 = 512, kFewRows1 = 256;
 constexpr int kWide = 128;
 
+// Rows that a thread adds one after another in fp32, at most: a sum of n values is off by up to n roundings.
+// (The join adds the bands 32 apart; beyond 2^25 rows the grid's limit makes the bands longer.)
+constexpr int64_t kMostRows = 512;
+
 // Bands of rows of each of `period` classes.
 int64_t bands_of(int64_t M, int64_t N, int V, int period) {
   if (M <= (V == 8 && period == 1 ? kFewRows8 : kFewRows1)) return 1;
-  const int64_t strips = (N + (period > 1 ? 7 : 0) + kWide * V - 1) / (kWide * V);
+  const int64_t strips = (N + (period > 1 ? 7 : 0) + kWide * V - 1) / (kWide * V), of_class = (M + period - 1) / period;
   const int64_t want = std::max<int64_t>(1, 152 * 8 / strips / period);
-  return std::max<int64_t>(1, std::min(want, (M / period + kMinRows - 1) / kMinRows));
+  const int64_t once = std::max<int64_t>(1, std::min(want, (M / period + kMinRows - 1) / kMinRows));
+  // more in multiples of that, so that the blocks still come in whole rounds
+  return std::min(once * ((of_class + once * kMostRows - 1) / (once * kMostRows)), (int64_t)65535 / period);
 }
 
 template <typename T, int V, int R, int TX, int TY, bool ODD = false>

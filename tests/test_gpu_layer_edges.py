@@ -308,3 +308,27 @@ def test_act_backward_in_the_workspace_asked_for(M, N, pad, dt):
                                 torch.cuda.current_stream().cuda_stream) == 0
     check_act_grad(dy, z, nv.ACT_SILU, nv.ActGrads(dz, dbias))
     assert guards_hold(base)
+
+
+# ---------------------------------------------------------------- long sums over rows
+
+
+# A sum's first value is 2^24 and all others are 1, so that every one added to it alone is lost (2^24 + 1 is a tie,
+# which goes to the even 2^24).  With chains of at most 512 values at most 511 are lost; what the join adds are multiples
+# of 2 or lost too, one rounding of at most 1 for each of its additions.
+MOST_LOST = 511 + 64
+
+
+def first_dwarfs_the_rest(M, N, offset):
+    base = torch.ones(offset + M * N, dtype=BF, device="cuda")
+    t = base[offset:].view(M, N)
+    t[0] = 2.0 ** 24
+    return t
+
+
+@pytest.mark.parametrize("M,N,offset", [(16384, 81920, 0), (16384, 40001, 0), (8192, 20481, 1), (1000000, 64, 0),
+                                        (1000000, 33, 1)])
+def test_bias_gradient_of_many_rows_loses_no_more_than_a_chain(M, N, offset):
+    dy = first_dwarfs_the_rest(M, N, offset)
+    got = nv.nvfp4_act_backward(dy, None, nv.ACT_NONE, want_dz=False).dbias
+    assert float((got.double() - (2.0 ** 24 + M - 1)).abs().max()) <= MOST_LOST

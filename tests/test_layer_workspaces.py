@@ -20,3 +20,11 @@ def test_the_norm_gradients_workspace_follows_the_rows(L, M, N):
 
 def test_the_norm_gradients_workspace_of_many_rows_stays_bounded(L):
     assert L.nvfp4_layernorm_backward_workspace(16384, 5120) <= 30e6
+
+
+@pytest.mark.parametrize("M,N", [(1, 1), (257, 33), (16384, 20480), (16384, 131072), (1000000, 64), (2 ** 31 - 1, 8),
+                                 (2 ** 31 - 1, 9)])
+def test_the_epilogue_gradients_workspace_stays_within_a_grid(L, M, N):
+    """Partial sums of at most 65535 bands (the most blocks of a grid's second dimension)."""
+    n = L.nvfp4_act_backward_workspace(M, N)
+    assert 0 <= n <= 65535 * N * 4
