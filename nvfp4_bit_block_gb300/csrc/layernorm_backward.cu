@@ -24,7 +24,10 @@ namespace nvfp4 {
 namespace norm {
 namespace {
 
-constexpr int kMaxBlocks = 608;          // blocks or bands that leave a row of partial sums each
+constexpr int kMaxBlocks = 608;          // blocks or bands that leave a row of partial sums each; more only for kMostRows
+// Rows that a thread adds one after another in fp32, at most: a sum of n values is off by up to n roundings.  (The
+// join adds the blocks' sums 32 apart; beyond 2^25 rows of over 5120 values the grid's limit makes bands longer.)
+constexpr int64_t kMostRows = 512;
 constexpr int64_t kRing = 220 * 1024;    // shared memory for rows on their way
 
 // Barrier of a row's group (its threads are whole warps of one block).
@@ -468,16 +471,25 @@ __global__ void __launch_bounds__(128) columns_kernel(const NormGradArgs a, cons
   }
 }
 
+// `once` blocks or bands of `groups` groups, which take R rows at a time of `rows`: as many times more that no group
+// adds more than kMostRows (a multiple of R: 510 or 512), so that the GPU's rounds of blocks stay whole.
+int64_t enough(int64_t once, int64_t rows, int groups, int R) {
+  const int64_t most = once * groups * (kMostRows / R * R);
+  return once * ((rows + most - 1) / most);
+}
+
 int64_t bands_of(int64_t M, int64_t N, int V) {
   const int64_t strips = (N + 128 * V - 1) / (128 * V);
-  return std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(152 * 8 / strips + 1, kMaxBlocks), (M + 15) / 16));
+  const int64_t once = std::min<int64_t>(std::min<int64_t>(152 * 8 / strips + 1, kMaxBlocks), (M + 15) / 16);
+  return std::min<int64_t>(enough(std::max<int64_t>(1, once), M, 1, 1), 65535);  // the grid's limit
 }
 
 int round32(int64_t v) { return (int)((v + 31) / 32 * 32); }
 
 // Rows of partial sums in the workspace.  Every block or band has a row of the matrix of its own, so that there are
 // no more of them than rows (100 MB for one row of 20480 values otherwise); by classes go only more rows than kMaxBlocks.
-int64_t most_parts(int64_t M) { return std::min<int64_t>(M, kMaxBlocks); }
+// `enough` makes fewer than `once` more than the rows need, over all classes kMaxBlocks + (M + 7) / 510.
+int64_t most_parts(int64_t M) { return std::min<int64_t>(M, kMaxBlocks + 1 + (M + 7) / 510); }
 
 // `e`: of the launch that leaves the parts.
 cudaError_t join(const NormGradArgs& a, int64_t parts, cudaError_t e, cudaStream_t s) {
@@ -503,8 +515,8 @@ cudaError_t run(const NormGradArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)groups * R, of_class = (a.M + period - 1) / period;
   // blocks of a class (`period` divides kMaxBlocks)
-  const int64_t blocks = std::min<int64_t>((of_class + rows - 1) / rows,
-                                           std::max<int64_t>(1, std::min<int64_t>(kMaxBlocks, (int64_t)sms * per_sm) / period));
+  const int64_t once = std::max<int64_t>(1, std::min<int64_t>(kMaxBlocks, (int64_t)sms * per_sm) / period);
+  const int64_t blocks = std::min<int64_t>((of_class + rows - 1) / rows, enough(once, of_class, groups, R));
   return join(a, blocks * period, launch_early(kern, dim3((unsigned)(blocks * period)), threads, smem, s, a, group, period), s);
 }
 
@@ -519,8 +531,8 @@ cudaError_t run_scalar(const NormGradArgs& a, cudaStream_t s) {
   int sms = 0, per_sm = 0;
   const cudaError_t e = cache[a.dres ? 1 : 0].get(kern, threads, smem, sms, per_sm);
   if (e != cudaSuccess) return e;
-  const int64_t blocks =
-      std::min<int64_t>(std::min<int64_t>((a.M + groups - 1) / groups, kMaxBlocks), (int64_t)sms * per_sm);
+  const int64_t once = std::min<int64_t>(kMaxBlocks, (int64_t)sms * per_sm);
+  const int64_t blocks = std::min<int64_t>((a.M + groups - 1) / groups, enough(once, a.M, groups, 1));
   return join(a, blocks, launch_early(kern, dim3((unsigned)blocks), threads, smem, s, a, group), s);
 }
 

@@ -332,3 +332,12 @@ def test_bias_gradient_of_many_rows_loses_no_more_than_a_chain(M, N, offset):
     dy = first_dwarfs_the_rest(M, N, offset)
     got = nv.nvfp4_act_backward(dy, None, nv.ACT_NONE, want_dz=False).dbias
     assert float((got.double() - (2.0 ** 24 + M - 1)).abs().max()) <= MOST_LOST
+
+
+@pytest.mark.parametrize("M,N,offset", [(1600000, 264, 0), (170000, 5120, 0), (170000, 5001, 1), (170000, 4999, 0),
+                                        (400000, 1001, 1), (8192, 20481, 1), (16384, 81920, 0)])
+def test_beta_gradient_of_many_rows_loses_no_more_than_a_chain(M, N, offset):
+    dy = first_dwarfs_the_rest(M, N, offset)
+    mean, rstd = torch.ones(M, device="cuda"), torch.ones(M, device="cuda")
+    r = nv.nvfp4_layernorm_backward(dy, dy, mean, rstd)
+    assert float((r.dbeta.double() - (2.0 ** 24 + M - 1)).abs().max()) <= MOST_LOST

@@ -28,3 +28,9 @@ def test_the_epilogue_gradients_workspace_stays_within_a_grid(L, M, N):
     """Partial sums of at most 65535 bands (the most blocks of a grid's second dimension)."""
     n = L.nvfp4_act_backward_workspace(M, N)
     assert 0 <= n <= 65535 * N * 4
+
+
+@pytest.mark.parametrize("M", [608, 5000, 16384, 10 ** 6, 2 ** 31 - 1])
+def test_the_norm_gradients_workspace_grows_with_a_part_for_every_510_rows(L, M):
+    n = L.nvfp4_layernorm_backward_workspace(M, 64)
+    assert 0 <= n <= (608 + 2 + M / 510) * 2 * 64 * 4 + (M + 1) * 8
