@@ -96,6 +96,25 @@ def _build_lib(sources, build_dir, lib, force, verbose, flags=NVCC_FLAGS):
     return lib
 
 
+EXT_STAMP = os.path.join(LAYER_BUILD, "layer_binding.txt")
+
+
+def _ext_tag() -> str:
+    """What the binding's object and its library paths depend on beside the sources."""
+    import sys
+
+    import torch
+    return f"python {sys.version}\ntorch {torch.__version__} {torch.__file__}\n"
+
+
+def _ext_stale() -> bool:
+    """Whether the binding was built against another Python or torch (or never)."""
+    if not os.path.exists(EXT_STAMP):
+        return True
+    with open(EXT_STAMP) as f:
+        return f.read() != _ext_tag()
+
+
 def _build_ext(force: bool, verbose: bool) -> tuple:
     """Compile the layer's binding; returns (object, whether it is new)."""
     import sysconfig
@@ -103,7 +122,7 @@ def _build_ext(force: bool, verbose: bool) -> tuple:
     from torch.utils.cpp_extension import include_paths
     os.makedirs(LAYER_BUILD, exist_ok=True)
     src, o = os.path.join(CSRC, "layer_binding.cpp"), os.path.join(LAYER_BUILD, "layer_binding.o")
-    stale = force or _stale(o, [src] + [h for h in _headers() if h.startswith(INCLUDE)])
+    stale = force or _ext_stale() or _stale(o, [src] + [h for h in _headers() if h.startswith(INCLUDE)])
     if stale:
         cuda = os.path.dirname(os.path.dirname(_nvcc()))
         inc = [*include_paths(), sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
@@ -118,10 +137,13 @@ def _link_ext(o: str, force: bool, verbose: bool) -> None:
         return
     libs = library_paths()
     tmp = LAYER_EXT + f".tmp{os.getpid()}"
-    _run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, o, LAYER_LIB, *[f"-L{p}" for p in libs],
-          *[f"-Wl,-rpath,{p}" for p in ["$ORIGIN", *libs]], "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"],
-         verbose)
+    # the library by its name, not its path: the binding loads the one beside it ($ORIGIN), wherever the tree is
+    _run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, o, *[f"-L{p}" for p in [BUILD, *libs]],
+          "-l:" + os.path.basename(LAYER_LIB), *[f"-Wl,-rpath,{p}" for p in ["$ORIGIN", *libs]], "-lc10", "-lc10_cuda",
+          "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"], verbose)
     os.replace(tmp, LAYER_EXT)
+    with open(EXT_STAMP, "w") as f:
+        f.write(_ext_tag())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
