@@ -179,18 +179,6 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Sum over the block, the same bits in every thread; `buf` holds 32 floats and
-// is free again after the call's last barrier.
-__device__ __forceinline__ float block_sum(float v, float* buf) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = (blockDim.x + 31) >> 5;
-  v = warp_sum(v);
-  if (lane == 0) buf[warp] = v;
-  __syncthreads();
-  v = warp_sum(lane < warps ? buf[lane] : 0.0f);
-  __syncthreads();
-  return v;
-}
-
 // The magnitude of v as an ordered integer: larger magnitudes are larger, NaN the largest.
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 

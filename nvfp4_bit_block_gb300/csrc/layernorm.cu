@@ -420,12 +420,14 @@ cudaError_t launch_rows(const NormArgs& a, cudaStream_t s) {
   const int64_t chunks = (a.N + (ODD ? 14 : 0)) / 8;
   const int period = ODD ? row_period(a.ldx) : 1;
   const int64_t rows = (a.M + period - 1) / period;
-  if (chunks <= 32)
-    return run<norm_stream_kernel<XT, YT, 1, 4, true, kInRegisters, 256, ODD>>(a, (rows + 7) / 8, 256, s,
-                                                                               256 * 4 * kSlot, period);
-  if (chunks <= 128)
-    return run<norm_stream_kernel<XT, YT, 4, 3, true, kInRegisters, 256, ODD>>(a, (rows + 7) / 8, 256, s,
-                                                                               256 * 12 * kSlot, period);
+  if constexpr (!ODD) {  // classes begin at longer rows
+    if (chunks <= 32)
+      return run<norm_stream_kernel<XT, YT, 1, 4, true, kInRegisters, 256, false>>(a, (rows + 7) / 8, 256, s,
+                                                                                   256 * 4 * kSlot);
+    if (chunks <= 128)
+      return run<norm_stream_kernel<XT, YT, 4, 3, true, kInRegisters, 256, false>>(a, (rows + 7) / 8, 256, s,
+                                                                                   256 * 12 * kSlot);
+  }
   const int t = round32((chunks + 3) / 4);
   if (chunks <= 1024)
     return run<norm_stream_kernel<XT, YT, 4, 3, false, kInRegisters, 256, ODD>>(a, rows, t, s, t * 12 * kSlot, period);
