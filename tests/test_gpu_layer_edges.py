@@ -341,3 +341,36 @@ def test_beta_gradient_of_many_rows_loses_no_more_than_a_chain(M, N, offset):
     mean, rstd = torch.ones(M, device="cuda"), torch.ones(M, device="cuda")
     r = nv.nvfp4_layernorm_backward(dy, dy, mean, rstd)
     assert float((r.dbeta.double() - (2.0 ** 24 + M - 1)).abs().max()) <= MOST_LOST
+
+
+# ---------------------------------------------------------------- shapes and outputs that nothing else reaches
+
+
+@pytest.mark.parametrize("xt,dt", [(BF, BF), (F32, BF), (F32, F32), (BF, F32)])
+@pytest.mark.parametrize("M,N,pad", [(1300, 1, 0), (1301, 2, 0), (1300, 3, 0), (1217, 4, 1), (1300, 5, 0), (1299, 6, 0),
+                                     (2001, 7, 0), (1300, 7, 2), (1300, 3, 6)])
+def test_layernorm_backward_of_many_narrow_rows(M, N, pad, xt, dt):
+    """A vector holds several rows: nothing beside a row is written, neighbours' NaN reaches no other."""
+    x, dy, dres = rand((M, N), xt, M + N, 2.0, 0.3), rand((M, N), dt, M + N + 1, 1e-3), rand((M, N), xt, 14, 1e-3)
+    gamma = rand((N,), F32, 13, 0.2, 1.0)
+    mean, rstd = stats(x)
+    base, out = strided(torch.zeros_like(x), pad, 0)
+    xv, dyv, resv = strided(x, pad, 0)[1], strided(dy, pad, 0)[1], strided(dres, pad, 0)[1]
+    r = nv.nvfp4_layernorm_backward(dyv, xv, mean, rstd, gamma, resv, out=out)
+    check_norm_grad(dy, x, mean, rstd, gamma, dres, r)
+    assert untouched(base, M, N, pad, 0)
+    clean = r.dx.clone()
+    xv[M // 2] = float("nan")
+    got = nv.nvfp4_layernorm_backward(dyv, xv, mean, rstd, gamma, resv, out=resv).dx  # in place
+    rows = torch.arange(M, device="cuda") != M // 2
+    assert torch.equal(got[rows], clean[rows])
+
+
+@pytest.mark.parametrize("M,N,K", [(2050, 5001, 96), (2050, 5000, 544), (2560, 5120, 64), (40, 640, 512)])
+def test_linear_amax_beside_a_residual(M, N, K):
+    a, b, res = operand(M, K, M + K), operand(N, K, N + K), rand((M, N), BF, 5)
+    for act in (nv.ACT_NONE, nv.ACT_SILU):
+        for z in (False, True):
+            r = nv.nvfp4_linear(*a, *b, act=act, residual=res, want_z=z, want_amax=True)
+            check_linear(a, b, K, r, None, act, res)
+            assert r.amax.tolist() == [float(r.d.float().abs().max())] * 2
