@@ -29,8 +29,19 @@ __device__ __forceinline__ Raw<T, V> slope_chunk(const Raw<T, V>& dy, const Raw<
   unpack(dy, d);
   if (act) {
     unpack(z, v);
+    if (sizeof(T) == 4 && V > 1 && act == NVFP4_ACT_GELU) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) d[i] = __fmul_rn(d[i], act_slope<T>(v[i], act));
+      for (int i = 0; i < V; i += 2) {
+        const float2 p = gelu_slope2(make_float2(v[i], v[V > 1 ? i + 1 : i]));
+        v[i] = p.x;
+        v[V > 1 ? i + 1 : i] = p.y;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = act_slope<T>(v[i], act);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) d[i] = __fmul_rn(d[i], v[i]);
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) sum[i] += d[i];

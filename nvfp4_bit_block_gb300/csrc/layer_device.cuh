@@ -6,6 +6,7 @@
 
 #include <cstdint>
 
+#include "nvfp4_device.cuh"
 #include "nvfp4_layer.h"
 
 namespace nvfp4 {
@@ -96,18 +97,36 @@ __device__ __forceinline__ constexpr float gauss_a(int i) {
                           0.107330345f, -0.188380703f, 0.0688984767f};
   return c[i];
 }
-__device__ __forceinline__ void gauss(float z, float& cdf, float& density, float) {
-  const float x = fabsf(z), w = z * z;
-  const float t = rcp(fmaf(0.4f, x, 1.0f));
-  density = ex2(-kHalfLog2e * w);
-  float b = gauss_b(5), q = gauss_a(6);
-#pragma unroll
-  for (int i = 4; i >= 0; --i) b = fmaf(b, w, gauss_b(i));
-#pragma unroll
-  for (int i = 5; i >= 0; --i) q = fmaf(q, t, gauss_a(i));
-  q = q * t * density;
-  cdf = x < 1.25f ? fmaf(z, b, 0.5f) : (z < 0.0f ? q : 1.0f - q);
+// One value or, with the packed instructions, two (778 x 84 in fp32, where the arithmetic's
+// latency counts: 10.1 instead of 10.8 us).
+__device__ __forceinline__ float mul_of(float a, float b) { return a * b; }
+__device__ __forceinline__ float2 mul_of(float2 a, float2 b) { return mul2(a, b); }
+__device__ __forceinline__ float fma_of(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float2 fma_of(float2 a, float2 b, float2 c) { return fma2(a, b, c); }
+__device__ __forceinline__ float each(float v, float) { return v; }
+__device__ __forceinline__ float2 each(float v, float2) { return make_float2(v, v); }
+__device__ __forceinline__ float gauss_t(float z) { return rcp(fmaf(0.4f, fabsf(z), 1.0f)); }
+__device__ __forceinline__ float2 gauss_t(float2 z) { return make_float2(gauss_t(z.x), gauss_t(z.y)); }
+__device__ __forceinline__ float ex2_of(float v) { return ex2(v); }
+__device__ __forceinline__ float2 ex2_of(float2 v) { return make_float2(ex2(v.x), ex2(v.y)); }
+__device__ __forceinline__ float gauss_part(float z, float mid, float tail) {
+  return fabsf(z) < 1.25f ? mid : (z < 0.0f ? tail : 1.0f - tail);
 }
+__device__ __forceinline__ float2 gauss_part(float2 z, float2 mid, float2 tail) {
+  return make_float2(gauss_part(z.x, mid.x, tail.x), gauss_part(z.y, mid.y, tail.y));
+}
+template <typename V>
+__device__ __forceinline__ void gauss_long(V z, V& cdf, V& density) {
+  const V w = mul_of(z, z), t = gauss_t(z);
+  density = ex2_of(mul_of(w, each(-kHalfLog2e, z)));
+  V b = each(gauss_b(5), z), q = each(gauss_a(6), z);
+#pragma unroll
+  for (int i = 4; i >= 0; --i) b = fma_of(b, w, each(gauss_b(i), z));
+#pragma unroll
+  for (int i = 5; i >= 0; --i) q = fma_of(q, t, each(gauss_a(i), z));
+  cdf = gauss_part(z, fma_of(z, b, each(0.5f, z)), mul_of(mul_of(q, t), density));
+}
+__device__ __forceinline__ void gauss(float z, float& cdf, float& density, float) { gauss_long(z, cdf, density); }
 // Phi alone, in one piece: t V(t) exp(-z^2 / 2) with t = 1 / (1 + 0.35 |z|), a minimax fit as
 // above (3.2e-8).  About zero t's rounding shows in Phi, but z Phi is small there:
 // relative error of the value 3.7e-8, of the formula with erff 3.6e-8, of the short
@@ -170,6 +189,13 @@ __device__ __forceinline__ float act_slope(float z, int act) {
     }
     default: return 1.0f;
   }
+}
+
+// erf GELU's derivative of two values for fp32 results.
+__device__ __forceinline__ float2 gelu_slope2(float2 z) {
+  float2 p, e;
+  gauss_long(z, p, e);
+  return fma2(mul2(make_float2(limit(z.x, 16.0f), limit(z.y, 16.0f)), make_float2(kRsqrt2Pi, kRsqrt2Pi)), e, p);
 }
 
 // ---------------------------------------------------------------- reductions
