@@ -95,7 +95,8 @@ __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity) {
   return false;
 }
 
-// ---- stores of staged tiles by TMA, tracked in bulk groups of the issuing thread.
+// ---- stores of staged tiles by TMA, tracked in bulk groups of the issuing thread.  A
+// row of the tensor is written in whole pieces of 16 bytes: it has to end at one.
 __device__ __forceinline__ void store_2d(const CUtensorMap* map, int x, int y, uint32_t src) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n" ::"l"(
                    reinterpret_cast<uint64_t>(map)),

@@ -374,3 +374,30 @@ def test_linear_amax_beside_a_residual(M, N, K):
             r = nv.nvfp4_linear(*a, *b, act=act, residual=res, want_z=z, want_amax=True)
             check_linear(a, b, K, r, None, act, res)
             assert r.amax.tolist() == [float(r.d.float().abs().max())] * 2
+
+
+@pytest.mark.parametrize("M,N,K", [(2327, 1246, 96), (700, 2601, 288), (2050, 5006, 64), (1100, 2607, 160), (300, 260, 512),
+                                   (1, 333, 64), (40, 333, 64), (200, 333, 64)])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_linear_rows_that_end_inside_16_bytes(M, N, K, dt):
+    """Rows that begin at 16 bytes and do not end there: what lies behind a row's last
+    value is another tensor's, for d and for z."""
+    L = nv.layer_lib()
+    per = 16 // dt.itemsize
+    pad = -N % per + per * (M % 2)
+    a, b = operand(-(-M // 16) * 16, K, M), operand(-(-N // 16) * 16, K, N + K, 0.05)
+    a, b = (a[0][:M].contiguous(), a[1], a[2]), (b[0][:N].contiguous(), b[1], b[2])
+    bias, res = rand((N,), F32, 3), rand((M, N), dt, 5)
+    s = torch.cuda.current_stream().cuda_stream
+    ws = torch.empty(max(16, L.nvfp4_linear_workspace(M, N, K)), dtype=torch.uint8, device="cuda")
+    for r, keep in ((None, False), (None, True), (res, False), (res, True)):
+        d_base, d = strided(r if r is not None else torch.zeros((M, N), dtype=dt, device="cuda"), pad, 0)
+        z_base, z = strided(torch.zeros((M, N), dtype=dt, device="cuda"), pad, 0)
+        amax = torch.empty(2, device="cuda")
+        assert L.nvfp4_linear(*[t.data_ptr() for t in (*a, *b)], M, N, K, bias.data_ptr(), 0, nv.ACT_SILU,
+                              d.data_ptr() if r is not None else None, N + pad, z.data_ptr() if keep else None, N + pad,
+                              d.data_ptr(), N + pad, int(dt is BF), amax.data_ptr(), ws.data_ptr(), ws.numel(), None,
+                              s) == 0
+        check_linear(a, b, K, nv.LinearOut(d, z if keep else None, amax), bias, nv.ACT_SILU, r, dt)
+        assert untouched(d_base, M, N, pad, 0) and untouched(z_base, M, N, pad, 0)
+        assert amax.tolist() == [float(d.float().abs().max())] * 2
