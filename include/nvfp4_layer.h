@@ -13,12 +13,13 @@
  *   nvfp4_linear or nvfp4_gemm (dgrad, wgrad) -> nvfp4_layernorm_backward.
  *
  * Conventions, as in nvfp4.h: pointers named *_dev are device pointers owned by
- * the caller; the library allocates nothing and keeps no state; every call is
- * asynchronous on `stream` (a cudaStream_t as void*, NULL = legacy default
- * stream); argument errors are returned at once, before anything is enqueued.
- * Matrices are row-major with a row stride in elements (ld >= columns); any
- * stride and any base address aligned to the element is accepted, 16-byte
- * aligned rows are faster.  An "is_bf16" argument is 1 for bf16 elements and 0
+ * the caller; the library allocates nothing and keeps nothing between calls but
+ * what its kernels' launches need on a device; several host threads may call it at
+ * once; every call is asynchronous on `stream` (a cudaStream_t as void*, NULL =
+ * legacy default stream); argument errors are returned at once, before anything is
+ * enqueued.  Matrices are row-major with a row stride in elements (ld >= columns);
+ * any stride and any base address aligned to the element is accepted, rows that
+ * begin and end at 16 bytes are faster; nothing between the rows is written.  An "is_bf16" argument is 1 for bf16 elements and 0
  * for fp32.  Arithmetic is fp32; a bf16 result is rounded once, to nearest even.
  * The results do not depend on the order in which blocks run: the same call
  * on the same device gives the same bits.

@@ -27,7 +27,9 @@ int whole_columns(int64_t M) { return M <= 64 ? columns(M) : 64; }
 // tiles 0.5 per step, at least 4.6 (512 x 10240: 14.2, 17.2, 36.0); split with a
 // join 8.5 + 0.4 per step of an SM + 0.035 per tile (512 x 5120: K 2048 17.7, 8192
 // 26.5; 512 x 2560: 13.2, 18.3); whole tiles 3.5 + 2 per round + 0.26 per step
-// (512 x 2560, 5120, 10240, K 512: 8.5, 11.0, 16.2).
+// (512 x 2560, 5120, 10240, K 512: 8.5, 11.0, 16.2).  Whether an amax is wanted is not
+// asked here (the workspace's size does not depend on it), although a call with one
+// does not take whole tiles.
 bool many(int64_t M, int64_t N, int64_t K) {
   if (M <= 128) return false;
   const int64_t steps = ceil_div(K, 256), f = ceil_div(N, 128), t = f * ceil_div(M, 128);

@@ -136,7 +136,7 @@ __device__ __forceinline__ void affine(float* v, const float* bias, float scale)
 // row of products; through `tile` (32 x 32 values, element (r, c) at column c ^ r, so
 // that neither its rows nor its columns meet in a bank) the lanes become columns
 // and each access to memory is a piece of one row, 16 rows at a time (4096 x 20479
-// x 5120: 204 us; with a row per lane and scalar accesses 798 us).
+// x 5120: 202 us; with a row per lane and scalar accesses 798 us).
 template <typename T, bool FULL>
 __device__ __forceinline__ uint32_t put_rows(const LinearArgs& a, T* d, T* z, const T* res, const float* tile, int rows,
                                              float bias, float scale, uint32_t top) {
