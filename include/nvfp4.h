@@ -71,9 +71,11 @@ typedef enum {
   NVFP4_ERR_NONFINITE = -6, /* device status: amax is Inf or NaN                      */
   NVFP4_ERR_RANGE = -7,     /* device status: 0 < amax < 2^-100 (the per-block
                                reciprocal could overflow FP32)                        */
-  NVFP4_ERR_PIPELINE = -8   /* device status: a tile copy into shared memory did not
+  NVFP4_ERR_PIPELINE = -8,  /* device status: a tile copy into shared memory did not
                                complete within about a second; the kernel stopped
                                and the outputs are incomplete                         */
+  NVFP4_ERR_INDEX = -9      /* device status: a batch's start, length or page number is
+                               out of range (nvfp4_attention.h)                       */
 } nvfp4_status;
 
 enum {

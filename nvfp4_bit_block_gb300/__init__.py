@@ -16,6 +16,10 @@ The functions keep the C names:
 The operators around the linear layer (include/nvfp4_layer.h) are in
 :mod:`.layer` and exported here too: :func:`nvfp4_layernorm`,
 :func:`nvfp4_layernorm_backward`, :func:`nvfp4_linear`, :func:`nvfp4_act_backward`.
+The attention operators on an NVFP4 cache (include/nvfp4_attention.h) are in
+:mod:`.attention` and exported here too: :func:`nvfp4_qk_rope`,
+:func:`nvfp4_qk_rope_backward`, :func:`nvfp4_kv_cache`, :func:`nvfp4_cache_write`,
+:func:`nvfp4_cache_read`, :func:`nvfp4_cache_attention`.
 """
 from __future__ import annotations
 
@@ -24,6 +28,8 @@ import os
 from dataclasses import dataclass
 from typing import Optional
 
+from .attention import (AttentionOut, CacheTokens, KVCache, QKRope, QKRopeGrads, attention_lib, nvfp4_cache_attention,
+                        nvfp4_cache_read, nvfp4_cache_write, nvfp4_kv_cache, nvfp4_qk_rope, nvfp4_qk_rope_backward)
 from .build import LIB as _LIB_PATH
 from .build import build
 from .layer import (ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU, ActGrads, LinearOut, Normed, NormGrads,
@@ -35,6 +41,8 @@ __all__ = [
     "nvfp4_amax", "nvfp4_quantize", "nvfp4_dequantize", "nvfp4_gemm", "nvfp4_strerror", "output_shapes",
     "ACT_NONE", "ACT_RELU", "ACT_GELU", "ACT_GELU_TANH", "ACT_SILU", "Normed", "NormGrads", "LinearOut", "ActGrads",
     "layer_lib", "nvfp4_layernorm", "nvfp4_layernorm_backward", "nvfp4_linear", "nvfp4_act_backward",
+    "KVCache", "QKRope", "QKRopeGrads", "CacheTokens", "AttentionOut", "attention_lib", "nvfp4_qk_rope",
+    "nvfp4_qk_rope_backward", "nvfp4_kv_cache", "nvfp4_cache_write", "nvfp4_cache_read", "nvfp4_cache_attention",
 ]
 
 ROWWISE, COLWISE, TWO_D, RHT_ROW, RHT_COL, SR, FOUR_SIX, SF_SWIZZLED = 1, 2, 4, 8, 16, 32, 64, 128

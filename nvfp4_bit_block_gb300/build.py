@@ -7,6 +7,9 @@
   of its own because the quantizer's arithmetic is compiled without fused
   multiply-adds and theirs with them; _build/_nvfp4_layer.so is its Python
   binding (a CPython extension against torch's C++ interface);
+* nvfp4_bit_block_gb300/_build/libnvfp4_attention.so and _nvfp4_attention.so --
+  the attention operators (the C ABI of include/nvfp4_attention.h) and their
+  binding, likewise;
 * tests/selftest/_build/libnvfp4_selftest.so and libnvfp4_layer_selftest.so --
   device self-checks used only by the tests (build_selftest,
   build_layer_selftest); they hold no product entry point.
@@ -27,6 +30,9 @@ LIB = os.path.join(BUILD, "libnvfp4.so")
 LAYER_BUILD = os.path.join(BUILD, "layer")
 LAYER_LIB = os.path.join(BUILD, "libnvfp4_layer.so")
 LAYER_EXT = os.path.join(BUILD, "_nvfp4_layer.so")
+ATTENTION_BUILD = os.path.join(BUILD, "attention")
+ATTENTION_LIB = os.path.join(BUILD, "libnvfp4_attention.so")
+ATTENTION_EXT = os.path.join(BUILD, "_nvfp4_attention.so")
 INCLUDE = os.path.join(ROOT, "include")
 SELFTEST_DIR = os.path.join(ROOT, "tests", "selftest")
 SELFTEST_BUILD = os.path.join(SELFTEST_DIR, "_build")
@@ -37,6 +43,7 @@ SOURCES = ["api.cu", "tmap.cu", "amax.cu", "quant1d.cu", "quant1d_sr.cu", "quant
            "quant2d.cu", "dequant.cu", "analysis.cu", "gemm.cu"]
 LAYER_SOURCES = ["layer_api.cu", "layernorm.cu", "layernorm_backward.cu", "act_backward.cu", "linear.cu", "linear_split.cu", "linear_many.cu", "out_tmap.cu",
                  "tmap.cu"]
+ATTENTION_SOURCES = ["attention_api.cu", "rope.cu", "rope_backward.cu", "cache.cu", "attend.cu"]
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
     "-O3", "-lineinfo", "-std=c++17",
@@ -62,7 +69,7 @@ def _stale(target: str, deps) -> bool:
 
 def _headers():
     hs = [os.path.join(CSRC, h) for h in os.listdir(CSRC) if h.endswith((".cuh", ".h"))]
-    hs += [os.path.join(INCLUDE, h) for h in ("nvfp4.h", "nvfp4_layer.h")]
+    hs += [os.path.join(INCLUDE, h) for h in ("nvfp4.h", "nvfp4_layer.h", "nvfp4_attention.h")]
     return hs
 
 
@@ -96,67 +103,77 @@ def _build_lib(sources, build_dir, lib, force, verbose, flags=NVCC_FLAGS):
     return lib
 
 
+# What a binding was built against is kept beside its object.
 EXT_STAMP = os.path.join(LAYER_BUILD, "layer_binding.txt")
+ATTENTION_STAMP = os.path.join(ATTENTION_BUILD, "attention_binding.txt")
 
 
 def _ext_tag() -> str:
-    """What the binding's object and its library paths depend on beside the sources."""
+    """What a binding's object and its library paths depend on beside the sources."""
     import sys
 
     import torch
     return f"python {sys.version}\ntorch {torch.__version__} {torch.__file__}\n"
 
 
-def _ext_stale() -> bool:
+def _ext_stale(stamp: str = EXT_STAMP) -> bool:
     """Whether the binding was built against another Python or torch (or never)."""
-    if not os.path.exists(EXT_STAMP):
+    if not os.path.exists(stamp):
         return True
-    with open(EXT_STAMP) as f:
+    with open(stamp) as f:
         return f.read() != _ext_tag()
 
 
-def _build_ext(force: bool, verbose: bool) -> tuple:
-    """Compile the layer's binding; returns (object, whether it is new)."""
+def _build_ext(source: str, build_dir: str, stamp: str, force: bool, verbose: bool) -> tuple:
+    """Compile a binding; returns (object, whether it is new)."""
     import sysconfig
 
     from torch.utils.cpp_extension import include_paths
-    os.makedirs(LAYER_BUILD, exist_ok=True)
-    src, o = os.path.join(CSRC, "layer_binding.cpp"), os.path.join(LAYER_BUILD, "layer_binding.o")
-    stale = force or _ext_stale() or _stale(o, [src] + [h for h in _headers() if h.startswith(INCLUDE)])
+    os.makedirs(build_dir, exist_ok=True)
+    src, o = os.path.join(CSRC, source), os.path.join(build_dir, source.replace(".cpp", ".o"))
+    deps = [src, os.path.join(CSRC, "binding.h")] + [h for h in _headers() if h.startswith(INCLUDE)]
+    stale = force or _ext_stale(stamp) or _stale(o, deps)
     if stale:
         cuda = os.path.dirname(os.path.dirname(_nvcc()))
-        inc = [*include_paths(), sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
+        inc = [*include_paths(), sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE, CSRC]
         _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-w",
               *[x for i in inc for x in ("-I", i)], "-c", src, "-o", o], verbose)
     return o, stale
 
 
-def _link_ext(o: str, force: bool, verbose: bool) -> None:
+def _link_ext(o: str, ext: str, lib: str, stamp: str, force: bool, verbose: bool) -> None:
     from torch.utils.cpp_extension import library_paths
-    if not force and not _stale(LAYER_EXT, [o]):
+    if not force and not _stale(ext, [o]):
         return
     libs = library_paths()
-    tmp = LAYER_EXT + f".tmp{os.getpid()}"
+    tmp = ext + f".tmp{os.getpid()}"
     # the library by its name, not its path: the binding loads the one beside it ($ORIGIN), wherever the tree is
     _run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, o, *[f"-L{p}" for p in [BUILD, *libs]],
-          "-l:" + os.path.basename(LAYER_LIB), *[f"-Wl,-rpath,{p}" for p in ["$ORIGIN", *libs]], "-lc10", "-lc10_cuda",
+          "-l:" + os.path.basename(lib), *[f"-Wl,-rpath,{p}" for p in ["$ORIGIN", *libs]], "-lc10", "-lc10_cuda",
           "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"], verbose)
-    os.replace(tmp, LAYER_EXT)
-    with open(EXT_STAMP, "w") as f:
+    os.replace(tmp, ext)
+    with open(stamp, "w") as f:
         f.write(_ext_tag())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """The product libraries and the layer's binding, side by side; returns the path of libnvfp4.so."""
-    with ThreadPoolExecutor(max_workers=3) as ex:
-        ext = ex.submit(_build_ext, force, verbose)
-        main = ex.submit(_build_lib, [os.path.join(CSRC, s) for s in SOURCES], BUILD, LIB, force, verbose)
-        layer = ex.submit(_build_lib, [os.path.join(CSRC, s) for s in LAYER_SOURCES], LAYER_BUILD, LAYER_LIB, force,
-                          verbose, LAYER_NVCC_FLAGS)
-        layer.result()
-        o, fresh = ext.result()
-        _link_ext(o, fresh, verbose)
-        return main.result()
+    """The product libraries and their bindings, side by side; returns the path of libnvfp4.so."""
+    with ThreadPoolExecutor(max_workers=5) as ex:
+        exts = [(ex.submit(_build_ext, source, where, stamp, force, verbose), ext, lib, stamp)
+                for source, where, stamp, ext, lib in (
+                    ("layer_binding.cpp", LAYER_BUILD, EXT_STAMP, LAYER_EXT, LAYER_LIB),
+                    ("attention_binding.cpp", ATTENTION_BUILD, ATTENTION_STAMP, ATTENTION_EXT, ATTENTION_LIB))]
+        libs = [ex.submit(_build_lib, [os.path.join(CSRC, s) for s in sources], where, lib, force, verbose, flags)
+                for sources, where, lib, flags in ((SOURCES, BUILD, LIB, NVCC_FLAGS),
+                                                   (LAYER_SOURCES, LAYER_BUILD, LAYER_LIB, LAYER_NVCC_FLAGS),
+                                                   (ATTENTION_SOURCES, ATTENTION_BUILD, ATTENTION_LIB,
+                                                    LAYER_NVCC_FLAGS))]
+        for lib in libs:
+            lib.result()
+        for made, ext, lib, stamp in exts:
+            o, fresh = made.result()
+            _link_ext(o, ext, lib, stamp, fresh, verbose)
+        return libs[0].result()
 
 
 def build_layer_selftest(force: bool = False, verbose: bool = False) -> str:

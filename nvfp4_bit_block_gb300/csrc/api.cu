@@ -195,6 +195,7 @@ const char* nvfp4_strerror(int status) {
     case NVFP4_ERR_NONFINITE: return "amax is Inf or NaN";
     case NVFP4_ERR_RANGE: return "amax below 2^-100";
     case NVFP4_ERR_PIPELINE: return "a tile copy did not arrive within the wait limit";
+    case NVFP4_ERR_INDEX: return "a start, length or page number is out of range";
     default: return "unknown status";
   }
 }

@@ -1,0 +1,196 @@
+// rope_common.cuh -- what the norm and rotation of queries and keys shares with its
+// gradient: a head's values in the registers of a few lanes, and the angles.
+//
+// A head is cut into slots of 2 V values, two vectors of V: a slot of the rotated part
+// holds V whole pairs (both halves of (i, i + rotated), or 2 V neighbours), so that the
+// turn needs no other lane; the rest passes in slots of its own.  Lane l of the L lanes
+// that share a head has slots l, l + L, ..  V is the largest number of values that a load
+// can take at this alignment.
+#pragma once
+
+#include "attention_internal.h"
+#include "launch_early.cuh"
+#include "layer_device.cuh"
+
+namespace nvfp4 {
+namespace rope {
+
+using bf16 = __nv_bfloat16;
+using layer::after_previous;
+using layer::launch_early;
+
+constexpr int kThreads = 256;
+
+// V values of type T as fp32, and back.
+template <int V, typename T>
+__device__ __forceinline__ void load_vec(const T* p, float* x) {
+  if constexpr (sizeof(T) * V == 16) {
+    const uint4 w = *reinterpret_cast<const uint4*>(p);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = bf16_lo(u[i]);
+        x[2 * i + 1] = bf16_hi(u[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(u[i]);
+    }
+  } else if constexpr (sizeof(T) * V == 8) {
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
+    if constexpr (sizeof(T) == 2) {
+      x[0] = bf16_lo(w.x);
+      x[1] = bf16_hi(w.x);
+      x[2] = bf16_lo(w.y);
+      x[3] = bf16_hi(w.y);
+    } else {
+      x[0] = __uint_as_float(w.x);
+      x[1] = __uint_as_float(w.y);
+    }
+  } else if constexpr (sizeof(T) == 2 && V == 2) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+    x[0] = bf16_lo(w);
+    x[1] = bf16_hi(w);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = layer::to_f32(p[i]);
+  }
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <int V, typename T>
+__device__ __forceinline__ void store_vec(T* p, const float* x) {
+  if constexpr (sizeof(T) == 2 && V == 8) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                                              pack_bf16(x[6], x[7]));
+  } else if constexpr (sizeof(T) == 2 && V == 4) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+  } else if constexpr (sizeof(T) == 2 && V == 2) {
+    *reinterpret_cast<uint32_t*>(p) = pack_bf16(x[0], x[1]);
+  } else if constexpr (sizeof(T) == 4 && V == 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  } else if constexpr (sizeof(T) == 4 && V == 2) {
+    *reinterpret_cast<float2*>(p) = make_float2(x[0], x[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) p[i] = layer::from_f32<T>(x[i]);
+  }
+}
+
+// Where a lane's slots lie in a head.
+template <int V, int SLOTS, bool INTER>
+struct Slots {
+  int first[SLOTS], second[SLOTS];  // offsets of the slot's two vectors; -1: none
+  int pair[SLOTS];                  // first pair of the slot; -1: it passes
+
+  __device__ __forceinline__ Slots(int lane, int lanes, int D, int rotated) {
+    const int turned = rotated / V, all = turned + ((D - 2 * rotated) / V + 1) / 2;
+#pragma unroll
+    for (int i = 0; i < SLOTS; ++i) {
+      const int u = lane + i * lanes;
+      first[i] = second[i] = pair[i] = -1;
+      if (u < turned) {
+        first[i] = INTER ? 2 * V * u : V * u;
+        second[i] = INTER ? first[i] + V : rotated + V * u;
+        pair[i] = V * u;
+      } else if (u < all) {
+        first[i] = 2 * rotated + 2 * V * (u - turned);
+        second[i] = first[i] + V < D ? first[i] + V : -1;
+      }
+    }
+  }
+};
+
+// Each slot's 2 V values of a head, zeros where there are none.
+template <int V, int SLOTS, bool INTER, typename T>
+__device__ __forceinline__ void load_head(const Slots<V, SLOTS, INTER>& s, const T* p, float x[SLOTS][2 * V]) {
+#pragma unroll
+  for (int i = 0; i < SLOTS; ++i) {
+#pragma unroll
+    for (int e = 0; e < 2 * V; ++e) x[i][e] = 0.0f;
+    if (s.first[i] >= 0) load_vec<V>(p + s.first[i], x[i]);
+    if (s.second[i] >= 0) load_vec<V>(p + s.second[i], x[i] + V);
+  }
+}
+template <int V, int SLOTS, bool INTER, typename T>
+__device__ __forceinline__ void store_head(const Slots<V, SLOTS, INTER>& s, T* p, const float x[SLOTS][2 * V]) {
+#pragma unroll
+  for (int i = 0; i < SLOTS; ++i) {
+    if (s.first[i] >= 0) store_vec<V>(p + s.first[i], x[i]);
+    if (s.second[i] >= 0) store_vec<V>(p + s.second[i], x[i] + V);
+  }
+}
+// The same of a head's weights (ones for NULL), whose type is known at run time only.
+template <int V, int SLOTS, bool INTER>
+__device__ __forceinline__ void load_gamma(const Slots<V, SLOTS, INTER>& s, const void* g, int is_bf16,
+                                           float x[SLOTS][2 * V]) {
+#pragma unroll
+  for (int i = 0; i < SLOTS; ++i)
+#pragma unroll
+    for (int e = 0; e < 2 * V; ++e) {
+      const int at = e < V ? s.first[i] : s.second[i];
+      x[i][e] = at < 0 ? 0.0f : (g ? layer::load_as_f32(g, at + e % V, is_bf16) : 1.0f);
+    }
+}
+
+// Sum over the L lanes (a power of two) that share a head.
+__device__ __forceinline__ float lanes_sum(float v, int L) {
+  for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+// cos and sin of position * frequency.  The product and its remainder of a whole turn are
+// formed in 64 bits, where they cost nothing beside a token's heads: in fp32 an angle of
+// 10^6 would be off by 0.03.  sincospif takes half turns.
+__device__ __forceinline__ float2 angle(int position, float freq, float turn) {
+  const double t = (double)position * (double)freq * 0.15915494309189533577;
+  float s, c;
+  sincospif((float)(2.0 * (t - rint(t))), &s, &c);
+  return make_float2(c, s * turn);
+}
+
+// The slots' pairs turned by the angles in cs.
+template <int V, int SLOTS, bool INTER>
+__device__ __forceinline__ void turn_pairs(const Slots<V, SLOTS, INTER>& s, const float2* cs, float x[SLOTS][2 * V]) {
+#pragma unroll
+  for (int i = 0; i < SLOTS; ++i) {
+    if (s.pair[i] < 0) continue;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const int ia = INTER ? 2 * e : e, ib = INTER ? 2 * e + 1 : V + e;
+      const float2 t = cs[s.pair[i] + e];
+      const float a = x[i][ia], b = x[i][ib];
+      x[i][ia] = a * t.x - b * t.y;
+      x[i][ib] = b * t.x + a * t.y;
+    }
+  }
+}
+
+// Values per vector at these sizes and this alignment: every vector of a slot begins at a
+// multiple of its size, so rotated and what passes are multiples of V.  `widest` is 16
+// bytes of the wider type.
+inline int vector_values(int widest, int D, int rotated, const Tokens* const* t, const int* bytes, int n) {
+  for (int V = widest; V > 1; V /= 2) {
+    bool ok = rotated % V == 0 && (D - 2 * rotated) % V == 0;
+    for (int i = 0; i < n && ok; ++i)
+      ok = reinterpret_cast<uintptr_t>(t[i]->p) % (V * bytes[i]) == 0 && t[i]->ts % V == 0 && t[i]->hs % V == 0;
+    if (ok) return V;
+  }
+  return 1;
+}
+
+// Lanes that share a head: a power of two that covers its slots, at most a warp.
+inline int lanes_of(int V, int D, int rotated) {
+  const int slots = rotated / V + ((D - 2 * rotated) / V + 1) / 2;
+  int L = 1;
+  while (L < slots && L < 32) L *= 2;
+  return L;
+}
+// Slots that a lane of a whole warp may have (D <= 512).
+constexpr int slots_of(int V) { return V == 8 ? 1 : 8 / V; }
+
+}  // namespace rope
+}  // namespace nvfp4
