@@ -1,20 +1,15 @@
-// attend.cu -- attention of a batch's queries to the NVFP4 cache.
+// attend.cu -- attention of a batch's queries to the NVFP4 cache: sequences with few rows go
+// to attend_few.cu, the others are taken here.
 //
 // For each row (token and query head), with the running maximum m and sum l of a softmax
 // over the visible keys j: o = sum exp(s_j - m) v_j / l, lse = m + log l.  One block per
 // row; its warps take every fourth key, a lane some of a key's values.
 #include <cmath>
 
-#include "attention_device.cuh"
-#include "launch_early.cuh"
-#include "layer_device.cuh"
+#include "attend.cuh"
 
 namespace nvfp4 {
 namespace attention {
-
-using layer::after_previous;
-using layer::launch_early;
-using bf16 = __nv_bfloat16;
 
 constexpr int kThreads = 128;
 
@@ -29,11 +24,10 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a) {
   __shared__ float ms[4], ls[4], os[4][256];
   const CacheView& c = a.c;
   after_previous();
-  if (blockIdx.x == 0 && blockIdx.y == 0) check_batch(c);
   const int t = blockIdx.x, h = blockIdx.y, D = c.dim;
   if (threadIdx.x == 0) {
     at = find_sequence(c, t);
-    if (at < 0 || !load_sequence(c, at, seq) || t >= seq.first + seq.rows) at = -1;
+    if (at < 0 || !load_sequence(c, at, seq) || t >= seq.first + seq.rows || is_few(a, seq)) at = -1;
   }
   __syncthreads();
   if (at < 0) return;
@@ -96,10 +90,14 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(AttendArgs a) {
 
 }  // namespace attention
 
-int64_t attend_workspace(int64_t, int, int, int, int64_t) { return 0; }
+int64_t attend_workspace(int64_t, int, int, int dim, int64_t) {
+  return attention::few_floats(attention::few_width(dim)) * (int64_t)sizeof(float);
+}
 
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t s) {
   using namespace attention;
+  const cudaError_t e = launch_attend_few(a, s);
+  if (e != cudaSuccess || a.c.T <= 1 || (int64_t)a.c.T * a.group <= kFewRows) return e;
   return launch_early(attend_kernel, dim3((unsigned)a.c.T, (unsigned)a.Hq), kThreads, 0, s, a);
 }
 
