@@ -43,7 +43,7 @@ SOURCES = ["api.cu", "tmap.cu", "amax.cu", "quant1d.cu", "quant1d_sr.cu", "quant
            "quant2d.cu", "dequant.cu", "analysis.cu", "gemm.cu"]
 LAYER_SOURCES = ["layer_api.cu", "layernorm.cu", "layernorm_backward.cu", "act_backward.cu", "linear.cu", "linear_split.cu", "linear_many.cu", "out_tmap.cu",
                  "tmap.cu"]
-ATTENTION_SOURCES = ["attention_api.cu", "rope.cu", "rope_backward.cu", "cache.cu", "attend.cu", "attend_few.cu"]
+ATTENTION_SOURCES = ["attention_api.cu", "rope.cu", "rope_backward.cu", "cache.cu", "attend.cu", "attend_few.cu", "attend_many.cu"]
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
     "-O3", "-lineinfo", "-std=c++17",

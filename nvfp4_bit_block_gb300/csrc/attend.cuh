@@ -28,53 +28,109 @@ __device__ __forceinline__ bool visible(const AttendArgs& a, const Sequence& s, 
   return j <= p && (a.window == 0 || p - j < a.window || j < a.sinks);
 }
 
-// The keys that any of a tile of rows sees, in chunks of 16: the first `sinks` chunks, then
+// The keys that any of a tile of rows sees, in chunks of CH: the first `sinks` chunks, then
 // those from `first` on.
+template <int CH>
 struct Keys {
   int sinks, first, count;  // count: of both
   int all_from, all_to;     // keys that every row sees lie within these (sinks aside)
   int all_sinks;            // .. or below this
   __device__ __forceinline__ int chunk(int i) const { return i < sinks ? i : first + (i - sinks); }
-  // steps of 64 keys; a tile that sees nothing has one all the same, which writes its zeros
+  // steps of four chunks; a tile that sees nothing has one all the same, which writes its zeros
   __device__ __forceinline__ int steps() const { return count <= 4 ? 1 : (count + 3) / 4; }
+  // whether every row sees the whole chunk that begins at `key`
   __device__ __forceinline__ bool all_visible(int key) const {
-    return key + 15 < all_to && (key >= all_from || key + 15 < all_sinks);
+    return key < all_to - (CH - 1) && (key >= all_from || key < all_sinks - (CH - 1));
   }
 };
 
 // Rows first_row .. first_row + n - 1 of a sequence's rows of one key head.
-__device__ __forceinline__ Keys rows_keys(const AttendArgs& a, const Sequence& s, int first_row, int n) {
-  Keys k = {0, 0, 0, 0, s.length, 0};
+template <int CH>
+__device__ __forceinline__ Keys<CH> rows_keys(const AttendArgs& a, const Sequence& s, int64_t first_row, int n) {
+  Keys<CH> k = {0, 0, 0, 0, s.length, 0};
   int end = s.length;
   if (a.causal) {
     const int before = s.length - s.rows;  // position of the first new token, >= -2^31 + 1
-    const int p0 = before + first_row / a.group, p1 = before + (first_row + n - 1) / a.group;
+    const int p0 = before + (int)(first_row / a.group), p1 = before + (int)((first_row + n - 1) / a.group);
     end = min(end, p1 + 1);
     k.all_to = min(s.length, p0 + 1);
     if (a.window) {
       const int low = (int)max((int64_t)0, (int64_t)p0 - a.window + 1);
       k.all_from = (int)max((int64_t)0, (int64_t)p1 - a.window + 1);
       k.all_sinks = a.sinks;
-      k.sinks = (max(0, min(min(a.sinks, low), end)) + 15) / 16;
-      k.first = max(low / 16, k.sinks);
+      k.sinks = (max(0, min(min(a.sinks, low), end)) + (CH - 1)) / CH;
+      k.first = max(low / CH, k.sinks);
     }
   }
-  k.count = k.sinks + max(0, (max(end, 0) + 15) / 16 - k.first);
+  k.count = k.sinks + max(0, (int)(((int64_t)max(end, 0) + (CH - 1)) / CH) - k.first);
   return k;
 }
-__device__ __forceinline__ Keys tile_keys(const AttendArgs& a, const Sequence& s, int tile) {
-  return rows_keys(a, s, 16 * tile, min(16, s.rows * a.group - 16 * tile));
+__device__ __forceinline__ Keys<16> tile_keys(const AttendArgs& a, const Sequence& s, int tile) {
+  return rows_keys<16>(a, s, 16 * tile, min(16, s.rows * a.group - 16 * tile));
 }
 
-// o and lse of one row from its sums (unnormalised, to base 2).
+// lse of one row from its maximum and sum to base 2, both -Inf and 0 where it sees nothing.
+__device__ __forceinline__ float row_lse(float top, float l) {
+  if (l == 0.0f) return -INFINITY;
+  return top == -INFINITY ? l : (top + log2f(l)) * 0.6931471805599453f;  // NaN leaves the maximum alone
+}
+// One value of o and, with the first, lse of one row from its sums (unnormalised).
 __device__ __forceinline__ void finish(const AttendArgs& a, const Sequence& s, int head, int row, int d, float sum,
                                        float top, float l, float alpha_v) {
   const int64_t t = (int64_t)s.first + row / a.group;
   const int h = head * a.group + row % a.group;
   const float share = l != 0.0f ? alpha_v / l : 0.0f;  // nothing seen: zeros
   static_cast<bf16*>(a.o.p)[t * a.o.ts + (int64_t)h * a.o.hs + d] = layer::from_f32<bf16>(sum * share);
-  if (d == 0 && a.lse)
-    a.lse[t * a.Hq + h] = l != 0.0f ? (top == -INFINITY ? l : (top + log2f(l)) * 0.6931471805599453f) : -INFINITY;
+  if (d == 0 && a.lse) a.lse[t * a.Hq + h] = row_lse(top, l);
+}
+
+// ---- fp16 products --------------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// The eight codes of a word as four f16x2 (byte j: its low nibble, then its high one).
+__device__ __forceinline__ void codes8(uint32_t w, uint32_t* h) {
+  asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t scales2(uint32_t two) {  // two scale bytes as f16x2
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
+  return r;
+}
+// Queries go to fp16 scaled by a power of two per row.  From the bits of the row's largest
+// magnitude (they order as the numbers do, NaN above all): what brings it below 4, and what
+// undoes that.
+__device__ __forceinline__ float query_down(uint32_t top) {
+  const int e = min(max((int)(top >> 23), 1), 253);
+  return __int_as_float((254 - e) << 23);
+}
+__device__ __forceinline__ float query_up(uint32_t top) {
+  return __int_as_float(min(max((int)(top >> 23), 1), 253) << 23);
+}
+__device__ __forceinline__ uint32_t larger_magnitude(uint32_t top, uint32_t two_bf16) {
+  return max(top, max(two_bf16 << 16 & 0x7FFF0000u, two_bf16 & 0x7FFF0000u));
+}
+// Eight queries as they lie in memory; vec: the address is a multiple of 16.
+__device__ __forceinline__ uint4 load_query8(const bf16* p, bool vec) {
+  if (vec) return *reinterpret_cast<const uint4*>(p);
+  const uint16_t* e = reinterpret_cast<const uint16_t*>(p);
+  return make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16, e[4] | (uint32_t)e[5] << 16,
+                    e[6] | (uint32_t)e[7] << 16);
+}
+__device__ __forceinline__ bool rows_at_16(const Tokens& t) {
+  return reinterpret_cast<uintptr_t>(t.p) % 16 == 0 && t.ts % 8 == 0 && t.hs % 8 == 0;
 }
 
 // ---- the line of work -----------------------------------------------------------------------
@@ -106,26 +162,23 @@ struct Pieces {
   }
 };
 
-// Where the pieces begin: every block adds up the sequences' steps, THREADS of them at a time,
-// and finds the sequence that its piece begins in.
+// A line of work along the sequences, `weight(sequence)` units for each: its length, and the
+// sequence that unit `mine(length)` of it is in.  Every block adds them up for itself, a
+// consecutive part of them in each thread.
 struct Line {
   int64_t total;
   int64_t base;  // where `sequence` begins
   int sequence;
   int64_t sums[32];
 };
-template <int THREADS>
-__device__ __forceinline__ void find_line(const AttendArgs& a, Line& line) {
+template <int THREADS, typename Weight, typename Mine>
+__device__ __forceinline__ void find_line(const CacheView& c, Line& line, Weight weight, Mine mine_of) {
   constexpr int WARPS = THREADS / 32;
   const int t = threadIdx.x, lane = t % 32, warp = t / 32;
-  const int64_t each = ((int64_t)a.c.sequences + THREADS - 1) / THREADS;
-  const int64_t from = min((int64_t)a.c.sequences, t * each), to = min((int64_t)a.c.sequences, from + each);
+  const int64_t each = ((int64_t)c.sequences + THREADS - 1) / THREADS;
+  const int64_t from = min((int64_t)c.sequences, t * each), to = min((int64_t)c.sequences, from + each);
   int64_t sum = 0;
-  for (int64_t b = from; b < to; ++b) {
-    Sequence s;
-    load_few(a, (int)b, s);
-    sum += sequence_steps(a, s) * a.c.heads;
-  }
+  for (int64_t b = from; b < to; ++b) sum += weight((int)b);
   int64_t up = sum;  // with all before
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -142,12 +195,10 @@ __device__ __forceinline__ void find_line(const AttendArgs& a, Line& line) {
   }
   int64_t base = before + up - sum;
   if (t == 0) line.total = total;
-  const int64_t mine = Pieces(total, gridDim.x).begin(blockIdx.x);
+  const int64_t mine = mine_of(total);
   if (mine >= base && mine < base + sum) {
     for (int64_t b = from; b < to; ++b) {
-      Sequence s;
-      load_few(a, (int)b, s);
-      const int64_t n = sequence_steps(a, s) * a.c.heads;
+      const int64_t n = weight((int)b);
       if (mine < base + n) {
         line.base = base;
         line.sequence = (int)b;
@@ -171,5 +222,6 @@ constexpr int64_t few_floats(int DP) { return few_head_floats(DP) + 2 * few_bloc
 }  // namespace attention
 
 cudaError_t launch_attend_few(const AttendArgs& a, cudaStream_t s);
+cudaError_t launch_attend_many(const AttendArgs& a, cudaStream_t s);
 
 }  // namespace nvfp4

@@ -49,29 +49,6 @@ struct Raw {
   uint32_t ks[2], vs[4];  // scale bytes, first lowest
 };
 
-__device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-// The eight codes of a word as four f16x2 (byte j: its low nibble, then its high one).
-__device__ __forceinline__ void codes8(uint32_t w, uint32_t* h) {
-  asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n"
-      " cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n"
-      " cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-      : "r"(w));
-}
-__device__ __forceinline__ uint32_t scales2(uint32_t two) {  // two scale bytes as f16x2
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
-  return r;
-}
 __device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -135,7 +112,7 @@ __device__ __forceinline__ void load_chunk(const CacheView& c, int h, int page, 
   }
 }
 
-// A row's queries, scaled by a power of two to below 4 and rounded to fp16; what undoes it.
+// A lane's part of a row's queries in fp16; returns what undoes their scaling.
 template <int DP>
 __device__ __forceinline__ float load_query(const AttendArgs& a, bool vec, bool on, int64_t token, int head, uint32_t* h) {
   constexpr int N = DP / 4;  // this lane's values
@@ -143,31 +120,21 @@ __device__ __forceinline__ float load_query(const AttendArgs& a, bool vec, bool 
   const bf16* p = static_cast<const bf16*>(a.q.p) + token * a.q.ts + (int64_t)head * a.q.hs + q * N;
 #pragma unroll
   for (int i = 0; i < N / 8; ++i) {
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (on && q * N + 8 * i < D) {
-      if (vec) {
-        w = *reinterpret_cast<const uint4*>(p + 8 * i);
-      } else {
-        const uint16_t* e = reinterpret_cast<const uint16_t*>(p + 8 * i);
-        w = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16, e[4] | (uint32_t)e[5] << 16,
-                       e[6] | (uint32_t)e[7] << 16);
-      }
-    }
+    const uint4 w = on && q * N + 8 * i < D ? load_query8(p + 8 * i, vec) : make_uint4(0, 0, 0, 0);
     h[4 * i] = w.x;
     h[4 * i + 1] = w.y;
     h[4 * i + 2] = w.z;
     h[4 * i + 3] = w.w;
   }
-  uint32_t top = 0;  // the largest magnitude's bits: they order as the numbers do, NaN above all
+  uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < N / 2; ++i) top = max(top, max(h[i] << 16 & 0x7FFF0000u, h[i] & 0x7FFF0000u));
+  for (int i = 0; i < N / 2; ++i) top = larger_magnitude(top, h[i]);
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-  const int e = min(max((int)(top >> 23), 1), 253);
-  const float down = __int_as_float((254 - e) << 23);
+  const float down = query_down(top);
 #pragma unroll
   for (int i = 0; i < N / 2; ++i) h[i] = pack_h2(bf16_lo(h[i]) * down, bf16_hi(h[i]) * down);
-  return __int_as_float(e << 23);
+  return query_up(top);
 }
 
 template <int DP>
@@ -184,7 +151,13 @@ __global__ void __launch_bounds__(kThreadsFew, few_per_sm(DP)) few_kernel(Attend
   float* ls = ms + kWarps * 16;                  // [warps][16]
   uint4* qs = reinterpret_cast<uint4*>(ls + kWarps * 16);  // [STEPS][32], DP = 256 only
 
-  find_line<kThreadsFew>(a, line);
+  find_line<kThreadsFew>(
+      c, line, [&](int b) {
+        Sequence s;
+        load_few(a, b, s);
+        return sequence_steps(a, s) * c.heads;
+      },
+      [&](int64_t total) { return Pieces(total, gridDim.x).begin(blockIdx.x); });
   const Pieces pieces(line.total, gridDim.x);
   int64_t w = pieces.begin(blockIdx.x);
   const int64_t w_end = pieces.begin(blockIdx.x + 1);
@@ -198,7 +171,7 @@ __global__ void __launch_bounds__(kThreadsFew, few_per_sm(DP)) few_kernel(Attend
   int64_t base = line.base;  // where sequence b begins on the line
   const float alpha_v = c.alpha[1], scale = a.scale * c.alpha[0] * layer::kLog2e;
 
-  const bool vec = reinterpret_cast<uintptr_t>(a.q.p) % 16 == 0 && a.q.ts % 8 == 0 && a.q.hs % 8 == 0;
+  const bool vec = rows_at_16(a.q);
 
   while (w < w_end) {
     // the unit that w is in
@@ -211,7 +184,7 @@ __global__ void __launch_bounds__(kThreadsFew, few_per_sm(DP)) few_kernel(Attend
     const int h = (int)((w - base) / per_head);
     int64_t u0 = base + h * per_head;
     int r = 0;
-    Keys keys = tile_keys(a, seq, 0);
+    Keys<16> keys = tile_keys(a, seq, 0);
     while (w >= u0 + keys.steps()) {
       u0 += keys.steps();
       keys = tile_keys(a, seq, ++r);

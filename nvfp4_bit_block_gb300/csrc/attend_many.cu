@@ -1,0 +1,474 @@
+// attend_many.cu -- attention of sequences with many new rows (tokens times the query heads
+// that share a key head) to the NVFP4 cache: prompts, or their parts.
+//
+// 4 D operations per row and visible key bound it: the tensor cores' rate.  A block takes 256
+// rows of one key head as two tiles of 128 (one tile of 128 for D > 128, where TMEM holds no
+// more) and walks over the visible keys, 128 (64) at a time:
+//   warps 8-11  bring codes and scales of a block of keys and values and leave them as fp16
+//               in shared memory, in the layout that the tensor core reads (a code times its
+//               scale is exact in fp16); done once for both tiles;
+//   warp 12     issues S = Q K^T (shared memory to TMEM) and O += P V (P from TMEM);
+//   warps 0-7   a thread for each row: S from TMEM, exponentials, P back to TMEM as fp16 in
+//               the columns that S had.
+// While the tensor core works for one tile, the other's rows are at their exponentials; with
+// one tile two S buffers alternate.  The running maximum moves only where a score passes it by
+// more than 2^8, so that O in TMEM is rarely touched between products.
+#include <cmath>
+
+#include "attend.cuh"
+#include "tcgen05.cuh"
+#include "tma.cuh"
+
+namespace nvfp4 {
+namespace attention {
+
+namespace many {
+
+constexpr int kRowWarps = 8, kFillWarps = 4;
+constexpr int kThreads = 32 * (kRowWarps + kFillWarps + 1);
+
+template <int DP>
+struct Shape {
+  static constexpr int TILES = DP <= 128 ? 2 : 1;
+  static constexpr int BN = DP <= 128 ? 128 : 64;  // keys of a block
+  static constexpr int CHUNKS = DP / 64;           // 128-byte columns of fp16
+  static constexpr int Q_TILE = 128 * DP * 2;
+  static constexpr int STAGE = BN * DP * 2;
+  static constexpr int KS = 0;                     // two stages of keys, two of values, then the queries
+  static constexpr int VS = 2 * STAGE;
+  static constexpr int QS = 4 * STAGE;
+  static constexpr int BARS = QS + TILES * Q_TILE;
+  static constexpr int SMEM = BARS + 256 + 1024;   // 1024: what alignment may take
+  static constexpr int FILL = DP * BN / 128;       // values of a filling thread: a part of a row
+  static constexpr int O_COL = 256;                // TMEM: S at 0 and 128, then O
+};
+
+// mbarriers, eight bytes each
+enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPFull = 10, kOFull = 12, kPvDone = 14, kDrain = 15 };
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// A warp's wait and its look at whether the block has given up: the same answer in every lane.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xFFFFFFFFu, tma::wait(bar, parity));
+}
+__device__ __forceinline__ bool stopped(const volatile int& stop) { return __any_sync(0xFFFFFFFFu, stop != 0); }
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// fp16 operands, fp32 sums: A (128 rows) and B with K contiguous, or B with its rows contiguous.
+constexpr uint32_t idesc_f16(int N, bool b_rows) {
+  return (1u << 4) | ((b_rows ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+__device__ __forceinline__ void st_x16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void st_x32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,"
+      "%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+// One thread's part of a key or value row: FILL values as codes and scales.
+template <int DP>
+struct Raw {
+  uint4 codes[Shape<DP>::FILL / 32];
+  uint32_t scales[Shape<DP>::FILL / 32];  // two bytes of each
+};
+
+template <int DP>
+__device__ __forceinline__ void load_raw(const uint8_t* codes, const uint8_t* scales, bool on, int first, int D, Raw<DP>& r) {
+#pragma unroll
+  for (int i = 0; i < Shape<DP>::FILL / 32; ++i) {
+    const bool in = on && first + 32 * i < D;
+    r.codes[i] = in ? *reinterpret_cast<const uint4*>(codes + 16 * i) : make_uint4(0, 0, 0, 0);
+    r.scales[i] = in ? *reinterpret_cast<const uint16_t*>(scales + 2 * i) : 0;
+  }
+}
+
+// .. and as fp16 in shared memory: row `row` of columns of 64 values, 16-byte pieces in the
+// 128-byte swizzle.
+template <int DP>
+__device__ __forceinline__ void store_raw(uint8_t* stage, int row, int first, int D, const Raw<DP>& r) {
+#pragma unroll
+  for (int i = 0; i < Shape<DP>::FILL / 32; ++i) {
+    if (first + 32 * i >= D) continue;
+    const uint32_t w[4] = {r.codes[i].x, r.codes[i].y, r.codes[i].z, r.codes[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t byte = r.scales[i] >> (8 * (k / 2)) & 0xFFu;
+      const uint32_t f = scales2(byte | byte << 8);
+      uint32_t h[4];
+      codes8(w[k], h);
+      const int piece = (first + 32 * i) / 8 + k;
+      *reinterpret_cast<uint4*>(stage + piece / 8 * (Shape<DP>::BN * 128) + row * 128 + ((piece % 8) ^ (row & 7)) * 16) =
+          make_uint4(h2_mul(h[0], f), h2_mul(h[1], f), h2_mul(h[2], f), h2_mul(h[3], f));
+    }
+  }
+}
+
+__device__ __forceinline__ int64_t tiles_of(const AttendArgs& a, int rows_per_block, int b, Sequence& s) {
+  load_sequence(a.c, b, s);
+  if (is_few(a, s)) return 0;
+  return ((int64_t)s.rows * a.group + rows_per_block - 1) / rows_per_block;
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
+  using S = Shape<DP>;
+  constexpr int ROWS = 128 * S::TILES, BN = S::BN;
+  extern __shared__ uint8_t dyn[];
+  __shared__ Line line;
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int stop;
+  __shared__ int bad_page;
+  const CacheView& c = a.c;
+  after_previous();
+  find_line<kThreads>(
+      c, line, [&](int b) {
+        Sequence s;
+        return tiles_of(a, ROWS, b, s) * c.heads;
+      },
+      [&](int64_t) { return (int64_t)blockIdx.x; });
+  if ((int64_t)blockIdx.x >= line.total) return;
+
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, b = line.sequence, D = c.dim;
+  uint8_t* sm = dyn + (1024 - smem_u32(dyn) % 1024) % 1024;
+  const uint32_t base = smem_u32(sm), bars = base + S::BARS;
+  auto bar = [&](int i) { return bars + 8 * i; };
+  Sequence seq;
+  const int64_t tiles = tiles_of(a, ROWS, b, seq);
+  const int64_t unit = blockIdx.x - line.base;
+  const int head = (int)(unit % c.heads);
+  const int64_t row0 = (tiles - 1 - unit / c.heads) * ROWS;  // the tiles with the most keys first
+  const int rows = (int)min((int64_t)ROWS, (int64_t)seq.rows * a.group - row0);
+  const int nt = rows > 128 ? 2 : 1;
+  const Keys<BN> keys = rows_keys<BN>(a, seq, row0, rows);
+  const int nb = keys.count, jobs = nt * nb;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      tma::mbar_init(bar(kKFull + i), 32 * kFillWarps);
+      tma::mbar_init(bar(kVFull + i), 32 * kFillWarps);
+      tma::mbar_init(bar(kKEmpty + i), 1);
+      tma::mbar_init(bar(kVEmpty + i), 1);
+      tma::mbar_init(bar(kSFull + i), 1);
+      tma::mbar_init(bar(kPFull + i), 128);
+      tma::mbar_init(bar(kOFull + i), 1);
+    }
+    tma::mbar_init(bar(kPvDone), 1);
+    tma::mbar_init(bar(kDrain), 1);
+    tma::fence_barrier_init();
+    stop = 0;
+    bad_page = 0;
+  }
+  if (warp == kRowWarps + kFillWarps) {
+    tc5::alloc(smem_u32(&tmem_slot), 512);
+    tc5::relinquish_alloc_permit();
+  }
+
+  // queries: a thread for each row
+  const int tile = warp / 4, row_in = tile * 128 + tid % 128;
+  const bool is_row = warp < 4 * nt, on = is_row && row_in < rows;
+  const int64_t row = row0 + row_in;
+  const int64_t token = on ? seq.first + row / a.group : 0;
+  const int qh = on ? head * a.group + (int)(row % a.group) : 0;
+  const int p = seq.length - seq.rows + (int)(row / a.group);  // position
+  float f = 0.0f;
+  if (is_row) {
+    const bf16* q = static_cast<const bf16*>(a.q.p) + token * a.q.ts + (int64_t)qh * a.q.hs;
+    const bool vec = rows_at_16(a.q);
+    uint32_t top = 0;
+    if (on) {
+#pragma unroll 4
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 w = load_query8(q + 8 * i, vec);
+        top = larger_magnitude(larger_magnitude(larger_magnitude(larger_magnitude(top, w.x), w.y), w.z), w.w);
+      }
+    }
+    // scores to base 2 are f * S with f > 0: the scale's sign goes into the queries, and where it
+    // vanishes f is the smallest number, so that -Inf stays -Inf
+    f = a.scale * c.alpha[0] * layer::kLog2e * query_up(top);
+    const float down = f < 0.0f ? -query_down(top) : query_down(top);
+    f = fmaxf(fabsf(f), 0x1p-126f);
+    uint8_t* qs = sm + S::QS + tile * S::Q_TILE;
+    const int r = tid % 128;
+#pragma unroll 4
+    for (int i = 0; i < D / 8; ++i) {
+      const uint4 w = on ? load_query8(q + 8 * i, vec) : make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(qs + i / 8 * (128 * 128) + r * 128 + ((i % 8) ^ (r & 7)) * 16) =
+          make_uint4(pack_h2(bf16_lo(w.x) * down, bf16_hi(w.x) * down), pack_h2(bf16_lo(w.y) * down, bf16_hi(w.y) * down),
+                     pack_h2(bf16_lo(w.z) * down, bf16_hi(w.z) * down), pack_h2(bf16_lo(w.w) * down, bf16_hi(w.w) * down));
+    }
+    fence_async_smem();
+  }
+  tc5::fence_before_thread_sync();
+  __syncthreads();
+  tc5::fence_after_thread_sync();
+  // pages out of range, all of them before any key is used: their keys are hidden
+  {
+    bool bad = false;
+    for (int i = tid; i < nb; i += kThreads) {
+      const int64_t key = (int64_t)keys.chunk(i) * BN, end = min(key + BN, (int64_t)seq.length);
+      for (int64_t j = key; j < end; j = (j / c.page_size + 1) * c.page_size) bad |= page_of(c, b, (int)j) < 0;
+    }
+    if (bad) {
+      bad_page = 1;
+      set_status(c.status, NVFP4_ERR_INDEX);
+    }
+  }
+  __syncthreads();
+  const uint32_t tmem = tmem_slot;
+  const bool holes = bad_page != 0;
+
+  if (warp < kRowWarps) {
+    if (is_row) {
+      const uint32_t at = tmem + ((uint32_t)(warp % 4 * 32) << 16), o_at = at + S::O_COL + tile * D;
+      float m = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+      const int hi = a.causal ? min(p, seq.length - 1) : seq.length - 1;  // the last key that this row sees
+      const int64_t lo = a.causal && a.window ? (int64_t)p - a.window : -1;  // keys up to this one lie before the window
+      int n = nt == 2 ? tile : 0;
+      for (int i = 0; i < nb && !stopped(stop); ++i, n += nt) {
+        const int buf = n & 1;
+        if (!warp_wait(bar(kSFull + buf), (n >> 1) & 1)) {
+          stop = 1;
+          break;
+        }
+        tc5::fence_after_thread_sync();
+        const uint32_t s_at = at + 128 * buf;
+        const int key = keys.chunk(i) * BN;
+        const bool part = holes || !keys.all_visible(key);
+        // columns up to last, of them those behind before and those below first
+        const int last = hi - key, before = (int)max(lo - key, (int64_t)-1), first = a.sinks - key;
+        auto scores = [&](int x, float* s) {
+          tc5::ld_32x32b_x32(s_at + x, reinterpret_cast<uint32_t*>(s));
+          tc5::wait_ld();
+          if (part) {
+#pragma unroll
+            for (int y = 0; y < 32; ++y)
+              if (!(x + y <= last && (x + y > before || x + y < first))) s[y] = -INFINITY;
+            if (holes) {
+#pragma unroll
+              for (int y = 0; y < 32; ++y)
+                if (x + y <= last && page_of(c, b, key + x + y) < 0) s[y] = -INFINITY;
+            }
+          }
+        };
+        float high = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < BN; x += 32) {
+          float s[32];
+          scores(x, s);
+#pragma unroll
+          for (int y = 0; y < 32; y += 2) high = fmaxf(high, fmaxf(s[y], s[y + 1]));
+        }
+        high *= f;
+        const bool up = high > m + 8.0f;
+        if (__any_sync(0xFFFFFFFFu, up)) {
+          const float d = up ? layer::ex2(m - high) : 1.0f;
+          if (up) m = high;
+          l0 *= d;
+          l1 *= d;
+          if (i > 0) {  // what O holds of the blocks before; with two tiles S comes after that product
+            if (nt == 1 && !warp_wait(bar(kPvDone), (i - 1) & 1)) {
+              stop = 1;
+              break;
+            }
+            tc5::fence_after_thread_sync();
+            for (int x = 0; x < D; x += 32) {
+              uint32_t o[32];
+              tc5::ld_32x32b_x32(o_at + x, o);
+              tc5::wait_ld();
+#pragma unroll
+              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * d);
+              st_x32(o_at + x, o);
+            }
+          }
+        }
+        const float z = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int x = 0; x < BN; x += 32) {
+          float s[32];
+          scores(x, s);
+          uint32_t h[16];
+#pragma unroll
+          for (int y = 0; y < 16; ++y) {
+            const float2 t = fma2(make_float2(s[2 * y], s[2 * y + 1]), make_float2(f, f), make_float2(-z, -z));
+            const float e0 = layer::ex2(t.x), e1 = layer::ex2(t.y);
+            l0 += e0;
+            l1 += e1;
+            h[y] = pack_h2(e0, e1);
+          }
+          st_x16(s_at + x / 2, h);  // columns that have been read
+        }
+        tc5::wait_st();
+        tc5::fence_before_thread_sync();
+        arrive(bar(kPFull + buf));
+      }
+      // the result
+      const float l = l0 + l1;
+      const float share = l != 0.0f ? c.alpha[1] / l : 0.0f;
+      if (on && a.lse) a.lse[token * a.Hq + qh] = row_lse(m, l);
+      bool got = nb > 0 && !stopped(stop);
+      if (got && !warp_wait(bar(kOFull + tile), 0)) {
+        stop = 1;
+        got = false;
+      }
+      tc5::fence_after_thread_sync();
+      bf16* out = static_cast<bf16*>(a.o.p) + token * a.o.ts + (int64_t)qh * a.o.hs;
+      const bool vec = rows_at_16(a.o);
+      for (int x = 0; x < D; x += 32) {
+        uint32_t o[32];
+        if (got) {
+          tc5::ld_32x32b_x32(o_at + x, o);
+          tc5::wait_ld();
+        } else {
+#pragma unroll
+          for (int y = 0; y < 32; ++y) o[y] = 0;
+        }
+        if (!on) continue;
+        uint32_t h[16];
+#pragma unroll
+        for (int y = 0; y < 16; ++y) {
+          const __nv_bfloat162 v =
+              __floats2bfloat162_rn(__uint_as_float(o[2 * y]) * share, __uint_as_float(o[2 * y + 1]) * share);
+          h[y] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+        if (vec) {
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            reinterpret_cast<uint4*>(out + x)[y] = make_uint4(h[4 * y], h[4 * y + 1], h[4 * y + 2], h[4 * y + 3]);
+        } else {
+          uint16_t* e = reinterpret_cast<uint16_t*>(out + x);
+#pragma unroll
+          for (int y = 0; y < 16; ++y) {
+            e[2 * y] = (uint16_t)h[y];
+            e[2 * y + 1] = (uint16_t)(h[y] >> 16);
+          }
+        }
+      }
+    }
+  } else if (warp < kRowWarps + kFillWarps) {
+    constexpr int PARTS = 128 / BN;  // threads of a row
+    const int t = tid - 32 * kRowWarps, r = t / PARTS, first = t % PARTS * S::FILL;
+    const int64_t hc = (int64_t)head * c.ch + first / 2, hs = (int64_t)head * c.sh + first / 16;
+    Raw<DP> k, v;
+    auto load = [&](int i) {
+      const int64_t key = (int64_t)keys.chunk(i) * BN + r;
+      const int page = key < seq.length ? page_of(c, b, (int)key) : -1;
+      const int64_t in = page >= 0 ? key % c.page_size : 0, pg = page >= 0 ? page : 0;
+      const int64_t co = pg * c.cp + in * c.cr + hc, so = pg * c.sp + in * c.sr + hs;
+      load_raw<DP>(c.kc + co, c.ks + so, page >= 0, first, D, k);
+      load_raw<DP>(c.vc + co, c.vs + so, page >= 0, first, D, v);
+    };
+    if (nb > 0) load(0);
+    for (int i = 0; i < nb && !stopped(stop); ++i) {
+      const int st = i & 1;
+      if (i >= 2 && !warp_wait(bar(kKEmpty + st), ((i >> 1) - 1) & 1)) {
+        stop = 1;
+        break;
+      }
+      store_raw<DP>(sm + S::KS + st * S::STAGE, r, first, D, k);
+      fence_async_smem();
+      arrive(bar(kKFull + st));
+      if (i >= 2 && !warp_wait(bar(kVEmpty + st), ((i >> 1) - 1) & 1)) {
+        stop = 1;
+        break;
+      }
+      store_raw<DP>(sm + S::VS + st * S::STAGE, r, first, D, v);
+      fence_async_smem();
+      arrive(bar(kVFull + st));
+      if (i + 1 < nb) load(i + 1);
+    }
+  } else if (lane == 0 && jobs > 0) {
+    const uint32_t qk = idesc_f16(BN, false), pv = idesc_f16(D, true);
+    auto product_qk = [&](int n) {
+      const int i = nt == 2 ? n >> 1 : n, t = nt == 2 ? n & 1 : 0, st = i & 1;
+      if (t == 0 && !tma::wait(bar(kKFull + st), (i >> 1) & 1)) return false;
+      tc5::fence_after_thread_sync();
+      for (int x = 0; x < D / 16; ++x) {
+        const uint32_t in = x / 4, of = x % 4 * 32;
+        mma_ss(tmem + 128 * (n & 1), tc5::smem_desc(base + S::QS + t * S::Q_TILE + in * (128 * 128) + of, 16, 1024, tc5::kLayoutSwizzle128B),
+               tc5::smem_desc(base + S::KS + st * S::STAGE + in * (BN * 128) + of, 16, 1024, tc5::kLayoutSwizzle128B), qk, x > 0);
+      }
+      tc5::commit(bar(kSFull + (n & 1)));
+      if (t == nt - 1) tc5::commit(bar(kKEmpty + st));
+      return true;
+    };
+    auto product_pv = [&](int n) {
+      const int i = nt == 2 ? n >> 1 : n, t = nt == 2 ? n & 1 : 0, st = i & 1;
+      if (t == 0 && !tma::wait(bar(kVFull + st), (i >> 1) & 1)) return false;
+      if (!tma::wait(bar(kPFull + (n & 1)), (n >> 1) & 1)) return false;
+      tc5::fence_after_thread_sync();
+      for (int x = 0; x < BN / 16; ++x)
+        mma_ts(tmem + S::O_COL + t * D, tmem + 128 * (n & 1) + 8 * x,
+               tc5::smem_desc(base + S::VS + st * S::STAGE + x * 2048, BN * 128, 1024, tc5::kLayoutSwizzle128B), pv,
+               i > 0 || x > 0);
+      if (t == nt - 1) tc5::commit(bar(kVEmpty + st));
+      if (nt == 1) tc5::commit(bar(kPvDone));
+      if (i == nb - 1) tc5::commit(bar(kOFull + t));
+      return true;
+    };
+    bool ok = product_qk(0);
+    for (int n = 1; ok && n < jobs && !stop; ++n) ok = product_qk(n) && product_pv(n - 1);
+    if (ok && !stop) ok = product_pv(jobs - 1);
+    tc5::commit(bar(kDrain));
+    if (!tma::wait(bar(kDrain), 0) || !ok) stop = 1;
+  }
+  __syncwarp();
+  tc5::fence_before_thread_sync();
+  __syncthreads();
+  tc5::fence_after_thread_sync();
+  if (warp == kRowWarps + kFillWarps) tc5::dealloc(tmem, 512);
+  if (tid == 0 && stop) set_status(c.status, NVFP4_ERR_PIPELINE);
+}
+
+template <int DP>
+cudaError_t launch(const AttendArgs& a, cudaStream_t s) {
+  using S = Shape<DP>;
+  const cudaError_t e = cudaFuncSetAttribute(many_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+  if (e != cudaSuccess) return e;
+  // as many blocks as the batch can have tiles: one more for each sequence of more than kFewRows rows
+  const int64_t rows = (int64_t)a.c.T * a.group, sequences = rows / (kFewRows + 1);
+  const int64_t tiles = rows / (128 * S::TILES) + (sequences < a.c.sequences ? sequences : a.c.sequences);
+  const int64_t blocks = tiles * a.c.heads;
+  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  return launch_early(many_kernel<DP>, dim3((unsigned)blocks), kThreads, S::SMEM, s, a);
+}
+
+}  // namespace many
+}  // namespace attention
+
+cudaError_t launch_attend_many(const AttendArgs& a, cudaStream_t s) {
+  using namespace attention;
+  if (a.c.dim <= 64) return many::launch<64>(a, s);
+  if (a.c.dim <= 128) return many::launch<128>(a, s);
+  return many::launch<256>(a, s);
+}
+
+}  // namespace nvfp4
