@@ -1,8 +1,9 @@
 // rope.cu -- norm of each head's queries and keys and their rotation, in one pass.
 //
 // For each token and head y = turn(x * rsqrt(mean(x^2) + eps) * gamma): read once and
-// written once, HBM bounds it.  A block takes a few tokens: their angles go to shared
-// memory once, for all heads.
+// written once, HBM bounds it.  A block walks over groups of a few tokens: their angles go to
+// shared memory once for all heads, and a thread keeps those of its pairs for all heads of its
+// token.  The next heads' loads are on their way while these are turned, the next group's too.
 #include <cmath>
 
 #include "rope_common.cuh"
@@ -11,63 +12,91 @@ namespace nvfp4 {
 namespace rope {
 
 template <int V, bool INTER, typename TI, typename TO>
-__global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, int lanes, int tokens) {
+__global__ void __launch_bounds__(kThreads, 2) rope_kernel(RopeArgs a, int lanes, int tokens, bool gamma_vec) {
   constexpr int SLOTS = slots_of(V);
-  extern __shared__ float2 cs[];  // tokens x rotated
+  constexpr int U = sizeof(TI) == 2 && V > 1 ? 2 : 1;  // heads at a time
+  extern __shared__ unsigned long long turns[];  // rotated; then the angles of two groups
+  float2* const angles = reinterpret_cast<float2*>(turns + a.rotated);
+  float2* cs = angles;
   after_previous();
-  const int64_t t0 = (int64_t)blockIdx.x * tokens;
-  const int here = (int)(a.T - t0 < tokens ? a.T - t0 : tokens);
-  for (int i = threadIdx.x; i < here * a.rotated; i += kThreads)
-    cs[i] = angle(a.positions[t0 + i / a.rotated], a.inv_freq[i % a.rotated], a.turn);
-  __syncthreads();
-  const int lane = threadIdx.x % lanes, sub = threadIdx.x / lanes, subs = kThreads / lanes;
-  const Slots<V, SLOTS, INTER> s(lane, lanes, a.D, a.rotated);
+  const Deal at(lanes, tokens);
+  const Slots<V, SLOTS, INTER> s(at.lane, lanes, a.D, a.rotated);
   const float share = 1.0f / (float)a.D;
+  const int H = a.Hq + a.Hk;
+  RawHead<V, SLOTS, TI> raw[U];
+  auto fetch = [&](int64_t t, int h0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = h0 + u * at.per;
+      const TI* p = h < a.Hq ? static_cast<const TI*>(a.q.p) + t * a.q.ts + (int64_t)h * a.q.hs
+                             : static_cast<const TI*>(a.k.p) + t * a.k.ts + (int64_t)(h - a.Hq) * a.k.hs;
+      raw[u].load(s, t < a.T && h < H, p);
+    }
+  };
+  const int64_t step = (int64_t)gridDim.x * tokens;
+  fetch((int64_t)blockIdx.x * tokens + at.token, at.head);
+  for (int i = threadIdx.x; i < a.rotated; i += kThreads) turns[i] = turns_of(a.inv_freq[i]);
+  __syncthreads();
+  float gamma[SLOTS][2 * V];
+  int of = -1;  // whose weights these are: queries' (0) or keys' (1)
+  for (int64_t t0 = (int64_t)blockIdx.x * tokens; t0 < a.T; t0 += step) {
+    const int here = (int)(a.T - t0 < tokens ? a.T - t0 : tokens);
+    for (int i = threadIdx.x; i < here * a.rotated; i += kThreads)
+      cs[i] = angle(a.positions[t0 + i / a.rotated], turns[i % a.rotated], a.turn);
+    __syncthreads();
+    const int64_t tt = t0 + at.token;
+    const bool there = tt < a.T;
+    float2 t[SLOTS][V];
+    load_angles(s, cs + (there ? at.token * a.rotated : 0), t);
+    cs = cs == angles ? cs + tokens * a.rotated : angles;
 #pragma unroll 1
-  for (int keys = 0; keys < 2; ++keys) {
-    const int H = keys ? a.Hk : a.Hq;
-    const Tokens in = keys ? a.k : a.q, out = keys ? a.ok : a.oq;
-    float gamma[SLOTS][2 * V];
-    load_gamma(s, keys ? a.gamma_k : a.gamma_q, a.w_bf16, gamma);
-    const int rows = here * H;
-#pragma unroll 1
-    for (int r0 = 0; r0 < rows; r0 += subs) {  // the whole warp stays: lanes of one row share sums
-      const int r = r0 + sub;
-      const bool on = r < rows;
-      const int t = on ? r / H : 0, h = on ? r % H : 0;
-      float x[SLOTS][2 * V];
-      if (on) {
-        load_head(s, static_cast<const TI*>(in.p) + (t0 + t) * in.ts + (int64_t)h * in.hs, x);
-      } else {
+    for (int h0 = at.head; h0 - at.head < H; h0 += U * at.per) {  // whole warps: lanes of a head share sums
+      RawHead<V, SLOTS, TI> now[U];
 #pragma unroll
-        for (int i = 0; i < SLOTS; ++i)
+      for (int u = 0; u < U; ++u) now[u] = raw[u];
+      const int next = h0 + U * at.per;
+      if (next - at.head < H)
+        fetch(tt, next);
+      else
+        fetch(tt + step, at.head);
 #pragma unroll
-          for (int e = 0; e < 2 * V; ++e) x[i][e] = 0.0f;
+      for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * at.per;
+        float x[SLOTS][2 * V];
+        now[u].widen(x);
+        if (a.norm) {
+          if (of != (h < a.Hq ? 0 : 1)) {
+            of = h < a.Hq ? 0 : 1;
+            load_gamma(s, of ? a.gamma_k : a.gamma_q, a.w_bf16, gamma_vec, gamma);
+          }
+          float r = 0.0f;
+#pragma unroll
+          for (int i = 0; i < SLOTS; ++i)
+#pragma unroll
+            for (int e = 0; e < 2 * V; ++e) r = fmaf(x[i][e], x[i][e], r);
+          r = rsqrtf(fmaf(lanes_sum(r, lanes), share, a.eps));
+#pragma unroll
+          for (int i = 0; i < SLOTS; ++i)
+#pragma unroll
+            for (int e = 0; e < 2 * V; ++e) x[i][e] *= r * gamma[i][e];
+        }
+        turn_pairs(s, t, x);
+        if (there && h < H)
+          store_head(s, h < a.Hq ? static_cast<TO*>(a.oq.p) + tt * a.oq.ts + (int64_t)h * a.oq.hs
+                                 : static_cast<TO*>(a.ok.p) + tt * a.ok.ts + (int64_t)(h - a.Hq) * a.ok.hs,
+                     x);
       }
-      if (a.norm) {
-        float q = 0.0f;
-#pragma unroll
-        for (int i = 0; i < SLOTS; ++i)
-#pragma unroll
-          for (int e = 0; e < 2 * V; ++e) q = fmaf(x[i][e], x[i][e], q);
-        const float rstd = rsqrtf(fmaf(lanes_sum(q, lanes), share, a.eps));
-#pragma unroll
-        for (int i = 0; i < SLOTS; ++i)
-#pragma unroll
-          for (int e = 0; e < 2 * V; ++e) x[i][e] *= rstd * gamma[i][e];
-      }
-      turn_pairs(s, cs + t * a.rotated, x);
-      if (on) store_head(s, static_cast<TO*>(out.p) + (t0 + t) * out.ts + (int64_t)h * out.hs, x);
     }
   }
 }
 
 template <int V, bool INTER, typename TI, typename TO>
 cudaError_t launch(const RopeArgs& a, cudaStream_t s) {
-  const int tokens = a.T >= 2048 ? 4 : 1;
-  const dim3 grid((unsigned)((a.T + tokens - 1) / tokens));
-  return launch_early(rope_kernel<V, INTER, TI, TO>, grid, kThreads, tokens * a.rotated * (int)sizeof(float2), s, a,
-                      lanes_of(V, a.D, a.rotated), tokens);
+  const int lanes = lanes_of(V, a.D, a.rotated), tokens = tokens_of(a.T);
+  const int64_t groups = (a.T + tokens - 1) / tokens;
+  const int smem = a.rotated * (8 + 2 * tokens * (int)sizeof(float2));
+  return launch_early(rope_kernel<V, INTER, TI, TO>, dim3((unsigned)(groups < kBlocks ? groups : kBlocks)), kThreads, smem,
+                      s, a, lanes, tokens, gamma_vectors(a, V));
 }
 
 template <typename TI, typename TO>

@@ -15,43 +15,60 @@ namespace nvfp4 {
 namespace rope {
 
 template <int V, bool INTER, typename TG, typename TX>
-__global__ void __launch_bounds__(kThreads) rope_grad_kernel(RopeGradArgs b, int lanes, int tokens, int sums) {
+__global__ void __launch_bounds__(kThreads, 2) rope_grad_kernel(RopeGradArgs b, int lanes, int tokens, bool gamma_vec,
+                                                                int sums) {
   constexpr int SLOTS = slots_of(V);
-  extern __shared__ float2 cs[];  // tokens x rotated, then the sums of eight warps
+  // whether the next head's loads are on their way while one is worked on: in bf16 the registers hold both
+  constexpr bool AHEAD = sizeof(TG) + sizeof(TX) == 4 && V > 1;
+  extern __shared__ unsigned long long turns[];  // rotated; then the angles of two groups, or the sums of eight warps
   const RopeArgs& a = b.r;
+  float2* const angles = reinterpret_cast<float2*>(turns + a.rotated);
   after_previous();
-  const int lane = threadIdx.x % lanes, sub = threadIdx.x / lanes, subs = kThreads / lanes;
-  const Slots<V, SLOTS, INTER> s(lane, lanes, a.D, a.rotated);
+  for (int i = threadIdx.x; i < a.rotated; i += kThreads) turns[i] = turns_of(a.inv_freq[i]);
+  const Deal at(lanes, tokens);
+  const Slots<V, SLOTS, INTER> s(at.lane, lanes, a.D, a.rotated);
   const float share = 1.0f / (float)a.D;
-  float dg[2][SLOTS][2 * V] = {};
-  for (int64_t t0 = (int64_t)blockIdx.x * tokens; t0 < a.T; t0 += (int64_t)gridDim.x * tokens) {
-    const int here = (int)(a.T - t0 < tokens ? a.T - t0 : tokens);
-    for (int i = threadIdx.x; i < here * a.rotated; i += kThreads)
-      cs[i] = angle(a.positions[t0 + i / a.rotated], a.inv_freq[i % a.rotated], a.turn);
-    __syncthreads();
-#pragma unroll
-    for (int keys = 0; keys < 2; ++keys) {
-      const int H = keys ? a.Hk : a.Hq;
-      const Tokens in = keys ? a.k : a.q, out = keys ? a.ok : a.oq, xin = keys ? b.xk : b.xq;
-      float gamma[SLOTS][2 * V];
-      load_gamma(s, keys ? a.gamma_k : a.gamma_q, a.w_bf16, gamma);
-      const int rows = here * H;
+  // queries, then keys: one set of weights and sums at a time
 #pragma unroll 1
-      for (int r0 = 0; r0 < rows; r0 += subs) {
-        const int r = r0 + sub;
-        const bool on = r < rows;
-        const int t = on ? r / H : 0, h = on ? r % H : 0;
+  for (int keys = 0; keys < 2; ++keys) {
+    const int H = keys ? a.Hk : a.Hq;
+    const Tokens in = keys ? a.k : a.q, out = keys ? a.ok : a.oq, xin = keys ? b.xk : b.xq;
+    float gamma[SLOTS][2 * V], dg[SLOTS][2 * V] = {};
+    load_gamma(s, keys ? a.gamma_k : a.gamma_q, a.w_bf16, gamma_vec, gamma);
+    float2* cs = angles;
+    __syncthreads();
+    RawHead<V, SLOTS, TG> raw_g;
+    RawHead<V, SLOTS, TX> raw_x;
+    auto fetch = [&](int64_t t, int h) {
+      const bool on = t < a.T && h < H;
+      raw_g.load(s, on, static_cast<const TG*>(in.p) + t * in.ts + (int64_t)h * in.hs);
+      raw_x.load(s, on, static_cast<const TX*>(xin.p) + t * xin.ts + (int64_t)h * xin.hs);
+    };
+    const int64_t step = (int64_t)gridDim.x * tokens;
+    if (AHEAD && H > 0) fetch((int64_t)blockIdx.x * tokens + at.token, at.head);
+    for (int64_t t0 = (int64_t)blockIdx.x * tokens; H > 0 && t0 < a.T; t0 += step) {
+      const int here = (int)(a.T - t0 < tokens ? a.T - t0 : tokens);
+      for (int i = threadIdx.x; i < here * a.rotated; i += kThreads)
+        cs[i] = angle(a.positions[t0 + i / a.rotated], turns[i % a.rotated], a.turn);
+      __syncthreads();
+      const int64_t tt = t0 + at.token;
+      const bool there = tt < a.T;
+      float2 t[SLOTS][V];
+      load_angles(s, cs + (there ? at.token * a.rotated : 0), t);
+      cs = cs == angles ? cs + tokens * a.rotated : angles;
+#pragma unroll 1
+      for (int h = at.head; h - at.head < H; h += at.per) {  // whole warps: lanes of a head share sums
         float g[SLOTS][2 * V], x[SLOTS][2 * V];
-        if (on) {
-          load_head(s, static_cast<const TG*>(in.p) + (t0 + t) * in.ts + (int64_t)h * in.hs, g);
-          load_head(s, static_cast<const TX*>(xin.p) + (t0 + t) * xin.ts + (int64_t)h * xin.hs, x);
-        } else {
-#pragma unroll
-          for (int i = 0; i < SLOTS; ++i)
-#pragma unroll
-            for (int e = 0; e < 2 * V; ++e) g[i][e] = x[i][e] = 0.0f;
+        if (!AHEAD) fetch(tt, h);
+        raw_g.widen(g);
+        raw_x.widen(x);
+        if (AHEAD) {
+          if (h + at.per - at.head < H)
+            fetch(tt, h + at.per);
+          else
+            fetch(tt + step, at.head);
         }
-        turn_pairs(s, cs + t * a.rotated, g);
+        turn_pairs(s, t, g);
         float q = 0.0f, p = 0.0f;
 #pragma unroll
         for (int i = 0; i < SLOTS; ++i)
@@ -64,64 +81,57 @@ __global__ void __launch_bounds__(kThreads) rope_grad_kernel(RopeGradArgs b, int
         p = lanes_sum(p, lanes);
         const float rstd = rsqrtf(fmaf(q, share, a.eps));
         const float along = p * share * rstd * rstd;
-        if (on) {
+        if (there && h < H) {
 #pragma unroll
           for (int i = 0; i < SLOTS; ++i)
 #pragma unroll
             for (int e = 0; e < 2 * V; ++e) {
-              dg[keys][i][e] = fmaf(g[i][e], x[i][e] * rstd, dg[keys][i][e]);
+              dg[i][e] = fmaf(g[i][e], x[i][e] * rstd, dg[i][e]);
               x[i][e] = rstd * (g[i][e] * gamma[i][e] - x[i][e] * along);
             }
-          store_head(s, static_cast<TX*>(out.p) + (t0 + t) * out.ts + (int64_t)h * out.hs, x);
+          store_head(s, static_cast<TX*>(out.p) + tt * out.ts + (int64_t)h * out.hs, x);
         }
       }
     }
+    if (!sums) continue;
+    // the lanes of a warp that hold the same values, then the warps one after another
     __syncthreads();
-  }
-  if (!sums) return;
-  // the lanes of a warp that hold the same values, then the warps one after another
-  float* part = reinterpret_cast<float*>(cs);  // [8][2][D]
-  const int warp = threadIdx.x / 32;
-#pragma unroll
-  for (int keys = 0; keys < 2; ++keys)
+    float* part = reinterpret_cast<float*>(angles);  // [8][D]
 #pragma unroll
     for (int i = 0; i < SLOTS; ++i)
 #pragma unroll
       for (int e = 0; e < 2 * V; ++e) {
-        float v = dg[keys][i][e];
+        float v = dg[i][e];
         for (int o = 16; o >= lanes; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-        const int at = e < V ? s.first[i] : s.second[i];
-        if (at >= 0 && threadIdx.x % 32 < lanes) part[(warp * 2 + keys) * a.D + at + e % V] = v;
+        const int d = e < V ? s.first[i] : s.second[i];
+        if (d >= 0 && threadIdx.x % 32 < lanes) part[threadIdx.x / 32 * a.D + d + e % V] = v;
       }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 2 * a.D; i += kThreads) {
-    float v = 0.0f;
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.D; i += kThreads) {
+      float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) v += part[w * 2 * a.D + i];
-    b.ws[(int64_t)blockIdx.x * 2 * a.D + i] = v;
+      for (int w = 0; w < kThreads / 32; ++w) v += part[w * a.D + i];
+      b.ws[((int64_t)blockIdx.x * 2 + keys) * a.D + i] = v;
+    }
   }
 }
 
-// Tokens that a block takes at a time, and blocks: enough to fill the GPU, and so many that
-// a thread adds at most 512 heads one after another.
-constexpr int kTokens = 4;
-constexpr int kBlocks = 152 * 4;
+// Blocks: enough to fill the GPU, and so many that a thread adds at most 512 heads one after
+// another.
 static int64_t blocks_of(int64_t T, int H) {
-  const int64_t groups = (T + kTokens - 1) / kTokens;
-  // a group's heads are spread over at least 8 rows of lanes
-  const int64_t per_group = ((int64_t)kTokens * H + 7) / 8;
-  const int64_t few = (groups * per_group + 511) / 512;
-  return std::min(groups, std::max<int64_t>(kBlocks, few));
+  const int tokens = tokens_of(T);
+  const int64_t groups = (T + tokens - 1) / tokens, per_group = H;
+  return std::min(groups, std::max<int64_t>(kBlocks, (groups * per_group + 511) / 512));
 }
 
 template <int V, bool INTER, typename TG, typename TX>
 cudaError_t launch(const RopeGradArgs& b, cudaStream_t s) {
   const RopeArgs& a = b.r;
-  const int sums = b.dgamma_q || b.dgamma_k;
+  const int sums = b.dgamma_q || b.dgamma_k, tokens = tokens_of(a.T);
   const int64_t blocks = blocks_of(a.T, std::max(a.Hq, a.Hk));
-  const int smem = std::max(kTokens * a.rotated * (int)sizeof(float2), 8 * 2 * a.D * (int)sizeof(float));
+  const int smem = a.rotated * 8 + std::max(2 * tokens * a.rotated * (int)sizeof(float2), 8 * a.D * (int)sizeof(float));
   const cudaError_t e = launch_early(rope_grad_kernel<V, INTER, TG, TX>, dim3((unsigned)blocks), kThreads, smem, s, b,
-                                     lanes_of(V, a.D, a.rotated), kTokens, sums);
+                                     lanes_of(V, a.D, a.rotated), tokens, gamma_vectors(a, V), sums);
   if (e != cudaSuccess || !sums) return e;
   return colsum::launch_join<2>(b.ws, (int)blocks, a.D, b.dgamma_q, b.dgamma_k, s);
 }

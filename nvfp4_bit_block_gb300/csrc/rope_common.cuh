@@ -104,17 +104,55 @@ struct Slots {
   }
 };
 
-// Each slot's 2 V values of a head, zeros where there are none.
-template <int V, int SLOTS, bool INTER, typename T>
-__device__ __forceinline__ void load_head(const Slots<V, SLOTS, INTER>& s, const T* p, float x[SLOTS][2 * V]) {
+// Each slot's 2 V values of a head as they lie in memory, zeros where there are none: loaded
+// early, widened when their turn comes.
+template <int V, int SLOTS, typename T>
+struct RawHead {
+  static constexpr int N = V * (int)sizeof(T) >= 4 ? V * (int)sizeof(T) / 4 : 1;  // words of a vector
+  uint32_t w[SLOTS][2][N];
+
+  template <bool INTER>
+  __device__ __forceinline__ void load(const Slots<V, SLOTS, INTER>& s, bool on, const T* p) {
 #pragma unroll
-  for (int i = 0; i < SLOTS; ++i) {
+    for (int i = 0; i < SLOTS; ++i)
 #pragma unroll
-    for (int e = 0; e < 2 * V; ++e) x[i][e] = 0.0f;
-    if (s.first[i] >= 0) load_vec<V>(p + s.first[i], x[i]);
-    if (s.second[i] >= 0) load_vec<V>(p + s.second[i], x[i] + V);
+      for (int half = 0; half < 2; ++half) {
+        const int at = half ? s.second[i] : s.first[i];
+        uint32_t* to = w[i][half];
+#pragma unroll
+        for (int e = 0; e < N; ++e) to[e] = 0;
+        if (!on || at < 0) continue;
+        if constexpr (N == 4) {
+          const uint4 v = *reinterpret_cast<const uint4*>(p + at);
+          to[0] = v.x;
+          to[1] = v.y;
+          to[2] = v.z;
+          to[3] = v.w;
+        } else if constexpr (N == 2) {
+          const uint2 v = *reinterpret_cast<const uint2*>(p + at);
+          to[0] = v.x;
+          to[1] = v.y;
+        } else if constexpr (V * sizeof(T) == 4) {
+          to[0] = *reinterpret_cast<const uint32_t*>(p + at);
+        } else {
+          to[0] = *reinterpret_cast<const uint16_t*>(p + at);
+        }
+      }
   }
-}
+  __device__ __forceinline__ void widen(float x[SLOTS][2 * V]) const {
+#pragma unroll
+    for (int i = 0; i < SLOTS; ++i)
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          if constexpr (sizeof(T) == 4)
+            x[i][half * V + e] = __uint_as_float(w[i][half][e]);
+          else
+            x[i][half * V + e] = e & 1 ? bf16_hi(w[i][half][e / 2]) : bf16_lo(w[i][half][e / 2]);
+        }
+  }
+};
 template <int V, int SLOTS, bool INTER, typename T>
 __device__ __forceinline__ void store_head(const Slots<V, SLOTS, INTER>& s, T* p, const float x[SLOTS][2 * V]) {
 #pragma unroll
@@ -123,16 +161,31 @@ __device__ __forceinline__ void store_head(const Slots<V, SLOTS, INTER>& s, T* p
     if (s.second[i] >= 0) store_vec<V>(p + s.second[i], x[i] + V);
   }
 }
-// The same of a head's weights (ones for NULL), whose type is known at run time only.
+// The same of a head's weights (ones for NULL), whose type is known at run time only; vec: every
+// vector of V begins at a multiple of 16 bytes, or of its size.
 template <int V, int SLOTS, bool INTER>
-__device__ __forceinline__ void load_gamma(const Slots<V, SLOTS, INTER>& s, const void* g, int is_bf16,
+__device__ __forceinline__ void load_gamma(const Slots<V, SLOTS, INTER>& s, const void* g, int is_bf16, bool vec,
                                            float x[SLOTS][2 * V]) {
 #pragma unroll
   for (int i = 0; i < SLOTS; ++i)
 #pragma unroll
-    for (int e = 0; e < 2 * V; ++e) {
-      const int at = e < V ? s.first[i] : s.second[i];
-      x[i][e] = at < 0 ? 0.0f : (g ? layer::load_as_f32(g, at + e % V, is_bf16) : 1.0f);
+    for (int half = 0; half < 2; ++half) {
+      const int at = half ? s.second[i] : s.first[i];
+      float* to = x[i] + half * V;
+#pragma unroll
+      for (int e = 0; e < V; ++e) to[e] = at < 0 ? 0.0f : 1.0f;
+      if (at < 0 || !g) continue;
+      if (vec && V >= 4) {
+        if (is_bf16) {
+          load_vec<V>(static_cast<const bf16*>(g) + at, to);
+        } else {
+#pragma unroll
+          for (int e = 0; e < V; e += 4) load_vec<V < 4 ? V : 4>(static_cast<const float*>(g) + at + e, to + e);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) to[e] = layer::load_as_f32(g, at + e, is_bf16);
+      }
     }
 }
 
@@ -142,29 +195,55 @@ __device__ __forceinline__ float lanes_sum(float v, int L) {
   return v;
 }
 
-// cos and sin of position * frequency.  The product and its remainder of a whole turn are
-// formed in 64 bits, where they cost nothing beside a token's heads: in fp32 an angle of
-// 10^6 would be off by 0.03.  sincospif takes half turns.
-__device__ __forceinline__ float2 angle(int position, float freq, float turn) {
-  const double t = (double)position * (double)freq * 0.15915494309189533577;
+// Angles.  With u = frequency / 2 pi in whole turns, position * u modulo 1 depends on u modulo 1
+// alone, so u is kept as a 64-bit fraction and the remainder is the product's low 64 bits, for any
+// position, negative ones too: exact but for u's own rounding (2^-54, so an angle at position
+// 2^31 is off by 2^-21).  In fp32 an angle of 10^6 would be off by 0.03, and a product in fp64 for each
+// token and pair took a quarter of the kernel's time (16384 tokens).
+__device__ __forceinline__ unsigned long long turns_of(float freq) {
+  const double u = (double)freq * 0.15915494309189533577;
+  return __double2ull_rz((u - floor(u)) * 18446744073709551616.0);
+}
+__device__ __forceinline__ float2 angle(int position, unsigned long long u, float turn) {
+  const long long r = (long long)((unsigned long long)(long long)position * u);
   float s, c;
-  sincospif((float)(2.0 * (t - rint(t))), &s, &c);
+  sincospif((float)(int)(r >> 32) * 0x1p-31f, &s, &c);  // half turns
   return make_float2(c, s * turn);
 }
 
-// The slots' pairs turned by the angles in cs.
+// A block's place: which token of its group and which of that token's heads a thread begins
+// with.  The lanes of a head lie side by side; a token's heads are dealt out to `per` of them.
+struct Deal {
+  int lane, token, head, per;
+  __device__ __forceinline__ Deal(int lanes, int tokens) {
+    const int sub = threadIdx.x / lanes;
+    per = kThreads / lanes / tokens;
+    lane = threadIdx.x % lanes;
+    token = sub / per;
+    head = sub % per;
+  }
+};
+
+// The cosines and sines of a lane's pairs: V of each slot.
 template <int V, int SLOTS, bool INTER>
-__device__ __forceinline__ void turn_pairs(const Slots<V, SLOTS, INTER>& s, const float2* cs, float x[SLOTS][2 * V]) {
+__device__ __forceinline__ void load_angles(const Slots<V, SLOTS, INTER>& s, const float2* cs, float2 t[SLOTS][V]) {
+#pragma unroll
+  for (int i = 0; i < SLOTS; ++i)
+#pragma unroll
+    for (int e = 0; e < V; ++e) t[i][e] = s.pair[i] >= 0 ? cs[s.pair[i] + e] : make_float2(1.0f, 0.0f);
+}
+template <int V, int SLOTS, bool INTER>
+__device__ __forceinline__ void turn_pairs(const Slots<V, SLOTS, INTER>& s, const float2 t[SLOTS][V],
+                                           float x[SLOTS][2 * V]) {
 #pragma unroll
   for (int i = 0; i < SLOTS; ++i) {
     if (s.pair[i] < 0) continue;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       const int ia = INTER ? 2 * e : e, ib = INTER ? 2 * e + 1 : V + e;
-      const float2 t = cs[s.pair[i] + e];
       const float a = x[i][ia], b = x[i][ib];
-      x[i][ia] = a * t.x - b * t.y;
-      x[i][ib] = b * t.x + a * t.y;
+      x[i][ia] = a * t[i][e].x - b * t[i][e].y;
+      x[i][ib] = b * t[i][e].x + a * t[i][e].y;
     }
   }
 }
@@ -188,6 +267,18 @@ inline int lanes_of(int V, int D, int rotated) {
   int L = 1;
   while (L < slots && L < 32) L *= 2;
   return L;
+}
+// Tokens that a block takes at a time: eight, so that a thread of 8 lanes has every fourth head
+// and several on their way; few tokens are spread out.
+constexpr int kBlocks = 152 * 2;
+inline int tokens_of(int64_t T) {
+  int n = 8;
+  while (n > 1 && T < (int64_t)n * kBlocks) n /= 2;
+  return n;
+}
+inline bool gamma_vectors(const RopeArgs& a, int V) {
+  const uintptr_t n = a.w_bf16 ? 2 * V : 16;
+  return reinterpret_cast<uintptr_t>(a.gamma_q) % n == 0 && reinterpret_cast<uintptr_t>(a.gamma_k) % n == 0;
 }
 // Slots that a lane of a whole warp may have (D <= 512).
 constexpr int slots_of(int V) { return V == 8 ? 1 : 8 / V; }
