@@ -60,7 +60,8 @@ typedef struct {
  *   pages      0..2^31 - 1;  heads 1..65535
  *   codes and their strides: multiples of 16 bytes; scales and theirs: of 2 bytes;
  *   no stride may be less than what it steps over makes necessary for rows not to
- *   overlap: any order of page, head and row is accepted.
+ *   overlap: any order of page, head and row is accepted; strides of pages and rows are
+ *   below 2^32.
  */
 typedef struct {
   uint8_t *k_codes, *k_scales, *v_codes, *v_scales;

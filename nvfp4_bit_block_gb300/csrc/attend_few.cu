@@ -7,8 +7,10 @@
 // long sequence and many short ones fill the GPU alike.  Pieces that are part of a unit leave
 // (m, l, o) in the workspace and a second kernel joins them in order.
 //
-// Within a step each of a block's four warps takes 16 keys, all the way from the cache's bytes
-// to the output in registers: S = Q K^T and O += P V as m16n8k16 products in fp16 with fp32
+// Within a step each of a block's four warps takes 16 keys, whose bytes come by asynchronous
+// copies into the warp's own ring in shared memory, a few chunks ahead (with the next chunk on
+// its way in registers instead, each SM had 20 KB in flight where the latency wants 45).  From
+// there to the output they stay in registers: S = Q K^T and O += P V as m16n8k16 products in fp16 with fp32
 // sums.  A code times its scale has at most 6 significant bits within 2^-10..2688, so it is
 // exact in fp16; queries are scaled by a power of two per row.  Which of a product's k's (and of
 // the output's columns) a value counts as is free, as long as both operands agree: each lane
@@ -38,15 +40,28 @@ struct Few {
   static constexpr int VS = VN >= 32 ? 2 : 1;
   // A row of o in shared memory: value n * VN + i at 9 i + n; rows 8 banks apart.
   static constexpr int ROW = DP == 64 ? 72 : DP == 128 ? 168 : 296;
-  static constexpr int QBYTES = DP == 256 ? STEPS * 32 * 16 : 0;
-  static constexpr int SMEM = kWarps * 16 * ROW * 4 + 2 * kWarps * 16 * 4 + QBYTES;
+  // A chunk in a warp's ring: rows of codes (16 bytes apart in their banks), then scales as the
+  // cache has them; of keys, then of values.
+  static constexpr int CODE_ROW = DP / 2 + 16;
+  static constexpr int CODES = 16 * CODE_ROW, SCALES = 16 * (DP / 16);
+  static constexpr int STAGE = 2 * (CODES + SCALES);
+  static constexpr int STAGES = 4;
+  static constexpr int COPIES = DP / 64;  // 16-byte pieces of a lane in 16 rows of codes
+  // shared memory: the rings, and in the end o of the four warps in their place; m and l; queries
+  static constexpr int RING = kWarps * STAGES * STAGE, O = kWarps * 16 * ROW * 4;
+  static constexpr int ML = RING > O ? RING : O;
+  static constexpr int QS = ML + 2 * kWarps * 16 * 4;
+  static constexpr int SMEM = QS + (DP == 256 ? STEPS * 32 * 16 : 0);
 };
 
-// One lane's bytes of 16 keys and values.
+// One lane's bytes of 16 keys, and of 16 values; scale bytes, first lowest.
 template <int DP>
-struct Raw {
-  uint32_t k[2][Few<DP>::KW], v[4][Few<DP>::VW];
-  uint32_t ks[2], vs[4];  // scale bytes, first lowest
+struct RawKeys {
+  uint32_t w[2][Few<DP>::KW], s[2];
+};
+template <int DP>
+struct RawValues {
+  uint32_t w[4][Few<DP>::VW], s[4];
 };
 
 __device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -55,62 +70,143 @@ __device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, ui
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Bytes of the chunk at `page`, row `row` (a multiple of 16); parts beyond D are zeros.
-template <int DP>
-__device__ __forceinline__ void load_chunk(const CacheView& c, int h, int page, int row, Raw<DP>& r) {
+// What lane (g, q) needs of a chunk in the ring; FULL: D is DP, else parts beyond D are zeros.
+template <int DP, bool FULL>
+__device__ __forceinline__ void take_keys(const uint8_t* stage, int D, int g, int q, RawKeys<DP>& r) {
   using F = Few<DP>;
-  const int lane = threadIdx.x % 32, g = lane / 4, q = lane % 4;
-  const int64_t co = (int64_t)page * c.cp + (int64_t)h * c.ch, so = (int64_t)page * c.sp + (int64_t)h * c.sh;
+  const int row = FULL ? DP / 16 : D / 16;
+  const uint8_t* p = stage + g * F::CODE_ROW + q * (DP / 8);
+  const uint8_t* s = stage + 2 * F::CODES + g * row + q * F::KS;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const int64_t at = row + 8 * t + g;
-    const uint8_t* p = c.kc + co + at * c.cr + q * (DP / 8);
-    const uint8_t* s = c.ks + so + at * c.sr + q * F::KS;
+    r.s[t] = 0;
     if constexpr (DP == 64) {
-      const bool on = q * 16 < c.dim;
-      const uint2 w = on ? *reinterpret_cast<const uint2*>(p) : make_uint2(0, 0);
-      r.k[t][0] = w.x;
-      r.k[t][1] = w.y;
-      r.ks[t] = on ? *s : 0;
+      if (FULL || q * 16 < D) {
+        const uint2 w = *reinterpret_cast<const uint2*>(p + 8 * t * F::CODE_ROW);
+        r.w[t][0] = w.x;
+        r.w[t][1] = w.y;
+        r.s[t] = s[8 * t * row];
+      } else {
+        r.w[t][0] = r.w[t][1] = 0;
+      }
     } else {
-      r.ks[t] = 0;
 #pragma unroll
       for (int i = 0; i < F::KW / 4; ++i) {
-        const bool on = q * (DP / 4) + 32 * i < c.dim;
-        const uint4 w = on ? *reinterpret_cast<const uint4*>(p + 16 * i) : make_uint4(0, 0, 0, 0);
-        r.k[t][4 * i] = w.x;
-        r.k[t][4 * i + 1] = w.y;
-        r.k[t][4 * i + 2] = w.z;
-        r.k[t][4 * i + 3] = w.w;
-        if (on) r.ks[t] |= (uint32_t)*reinterpret_cast<const uint16_t*>(s + 2 * i) << (16 * i);
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (FULL || q * (DP / 4) + 32 * i < D) {
+          w = *reinterpret_cast<const uint4*>(p + 8 * t * F::CODE_ROW + 16 * i);
+          r.s[t] |= (uint32_t)*reinterpret_cast<const uint16_t*>(s + 8 * t * row + 2 * i) << (16 * i);
+        }
+        r.w[t][4 * i] = w.x;
+        r.w[t][4 * i + 1] = w.y;
+        r.w[t][4 * i + 2] = w.z;
+        r.w[t][4 * i + 3] = w.w;
       }
     }
   }
-  const bool on = g * F::VN < c.dim;
+}
+template <int DP, bool FULL>
+__device__ __forceinline__ void take_values(const uint8_t* stage, int D, int g, int q, RawValues<DP>& r) {
+  using F = Few<DP>;
+  const int row = FULL ? DP / 16 : D / 16;
+  const uint8_t* p = stage + F::CODES + 2 * q * F::CODE_ROW + g * (DP / 16);
+  const uint8_t* s = stage + 2 * F::CODES + F::SCALES + 2 * q * row + g * F::VN / 16;
+  const bool on = FULL || g * F::VN < D;
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
-    const int64_t at = row + 8 * (t / 2) + 2 * q + t % 2;
-    const uint8_t* p = c.vc + co + at * c.cr + g * (DP / 16);
-    const uint8_t* s = c.vs + so + at * c.sr + g * F::VN / 16;
-    r.vs[t] = 0;
+    const int at = 8 * (t / 2) + t % 2;
+    r.s[t] = 0;
+#pragma unroll
+    for (int i = 0; i < F::VW; ++i) r.w[t][i] = 0;
+    if (!on) continue;
+    const uint8_t* w = p + at * F::CODE_ROW;
     if constexpr (DP == 64) {
-      r.v[t][0] = on ? *reinterpret_cast<const uint32_t*>(p) : 0;
-      if (on) r.vs[t] = *s;
+      r.w[t][0] = *reinterpret_cast<const uint32_t*>(w);
+      r.s[t] = s[at * row];
     } else if constexpr (DP == 128) {
-      const uint2 w = on ? *reinterpret_cast<const uint2*>(p) : make_uint2(0, 0);
-      r.v[t][0] = w.x;
-      r.v[t][1] = w.y;
-      if (on) r.vs[t] = *s;
+      const uint2 v = *reinterpret_cast<const uint2*>(w);
+      r.w[t][0] = v.x;
+      r.w[t][1] = v.y;
+      r.s[t] = s[at * row];
     } else {
-      const uint4 w = on ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
-      r.v[t][0] = w.x;
-      r.v[t][1] = w.y;
-      r.v[t][2] = w.z;
-      r.v[t][3] = w.w;
-      if (on) r.vs[t] = *reinterpret_cast<const uint16_t*>(s);
+      const uint4 v = *reinterpret_cast<const uint4*>(w);
+      r.w[t][0] = v.x;
+      r.w[t][1] = v.y;
+      r.w[t][2] = v.z;
+      r.w[t][3] = v.w;
+      r.s[t] = *reinterpret_cast<const uint16_t*>(s + at * row);
     }
   }
 }
+
+__device__ __forceinline__ void copy16(uint32_t to, const uint8_t* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A lane's share of the copies of one chunk.
+template <int DP, bool FULL>
+struct Copies {
+  using F = Few<DP>;
+  uint64_t from[F::COPIES];  // offsets from the chunk's first row of codes
+  uint32_t to[F::COPIES];    // .. and in a stage of the ring
+  int lane;
+  __device__ __forceinline__ Copies(const CacheView& c, int lane_) : lane(lane_) {
+    const int pieces = FULL ? DP / 32 : c.dim / 32;  // of a row
+#pragma unroll
+    for (int i = 0; i < F::COPIES; ++i) {
+      const int x = lane + 32 * i, row = x / pieces, piece = x % pieces;
+      from[i] = (uint64_t)row * c.cr + 16 * piece;
+      to[i] = row < 16 ? row * F::CODE_ROW + 16 * piece : ~0u;
+    }
+  }
+  // kc .. vs: where the chunk begins; dense: its 16 rows of scales lie side by side, at 16 bytes
+  __device__ __forceinline__ void issue(const CacheView& c, const uint8_t* kc, const uint8_t* ks, const uint8_t* vc,
+                                        const uint8_t* vs, uint32_t stage, bool dense) const {
+#pragma unroll
+    for (int i = 0; i < F::COPIES; ++i) {
+      if (!FULL && to[i] == ~0u) continue;
+      copy16(stage + to[i], kc + from[i]);
+      copy16(stage + F::CODES + to[i], vc + from[i]);
+    }
+    const int half = lane / 16, x = lane % 16, row = FULL ? DP / 16 : c.dim / 16;
+    const uint8_t* s = half ? vs : ks;
+    const uint32_t at = stage + 2 * F::CODES + half * F::SCALES;
+    if (dense) {
+      if (x < row) copy16(at + 16 * x, s + 16 * x);
+    } else {
+      const uint8_t* p = s + (uint64_t)x * c.sr;
+      for (int i = 0; i < row; i += 2)
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + x * row + i), "h"(*reinterpret_cast<const uint16_t*>(p + i)) : "memory");
+    }
+  }
+};
+
+// A warp's way along its chunks, four apart: which page holds the chunk, and where in it.
+struct Walk {
+  int chunk, slot, in;  // in: chunks of the page before it
+  __device__ __forceinline__ void begin(int c, int per_page) {
+    chunk = c;
+    slot = c / per_page;
+    in = c - slot * per_page;
+  }
+  __device__ __forceinline__ void go(int c, int per_page) {
+    if (c != chunk + kWarps) {  // from the first keys to the window
+      begin(c, per_page);
+      return;
+    }
+    chunk = c;
+    in += kWarps;
+    while (in >= per_page) {
+      in -= per_page;
+      ++slot;
+    }
+  }
+};
 
 // A lane's part of a row's queries in fp16; returns what undoes their scaling.
 template <int DP>
@@ -137,19 +233,21 @@ __device__ __forceinline__ float load_query(const AttendArgs& a, bool vec, bool 
   return query_up(top);
 }
 
-template <int DP>
+template <int DP, bool FULL>
 __global__ void __launch_bounds__(kThreadsFew, few_per_sm(DP)) few_kernel(AttendArgs a) {
   using F = Few<DP>;
-  extern __shared__ __align__(16) float sm[];
+  extern __shared__ __align__(16) uint8_t sm[];
   __shared__ Line line;
   const CacheView& c = a.c;
   after_previous();
   if (blockIdx.x == 0) check_batch(c);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, q = lane % 4;
-  float* os = sm;                                // [warps][16][ROW]
-  float* ms = sm + kWarps * 16 * F::ROW;         // [warps][16]
-  float* ls = ms + kWarps * 16;                  // [warps][16]
-  uint4* qs = reinterpret_cast<uint4*>(ls + kWarps * 16);  // [STEPS][32], DP = 256 only
+  float* os = reinterpret_cast<float*>(sm);          // [warps][16][ROW]
+  float* ms = reinterpret_cast<float*>(sm + F::ML);  // [warps][16]
+  float* ls = ms + kWarps * 16;                      // [warps][16]
+  uint4* qs = reinterpret_cast<uint4*>(sm + F::QS);  // [STEPS][32], DP = 256 only
+  uint8_t* ring = sm + warp * F::STAGES * F::STAGE;
+  const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
 
   find_line<kThreadsFew>(
       c, line, [&](int b) {
@@ -172,6 +270,9 @@ __global__ void __launch_bounds__(kThreadsFew, few_per_sm(DP)) few_kernel(Attend
   const float alpha_v = c.alpha[1], scale = a.scale * c.alpha[0] * layer::kLog2e;
 
   const bool vec = rows_at_16(a.q);
+  const bool dense = c.sr == c.dim / 16 &&
+                     (reinterpret_cast<uintptr_t>(c.ks) | reinterpret_cast<uintptr_t>(c.vs) | c.sp | c.sh) % 16 == 0;
+  const Copies<DP, FULL> copies(c, lane);
 
   while (w < w_end) {
     // the unit that w is in
@@ -214,8 +315,8 @@ __global__ void __launch_bounds__(kThreadsFew, few_per_sm(DP)) few_kernel(Attend
         qf[j][3] = x[2 * j + 1];
       }
     }
+    __syncthreads();  // the part before is read
     if constexpr (DP == 256) {
-      __syncthreads();
       if (warp == 0)
 #pragma unroll
         for (int j = 0; j < F::STEPS; ++j) qs[j * 32 + lane] = make_uint4(qf[j][0], qf[j][1], qf[j][2], qf[j][3]);
@@ -225,121 +326,150 @@ __global__ void __launch_bounds__(kThreadsFew, few_per_sm(DP)) few_kernel(Attend
 
     float o[F::VN][4] = {};
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
-    Raw<DP> next;
-    int next_chunk = -1, next_page = -1;
-    auto fetch = [&](int s) {
-      const int i = 4 * s + warp;
-      next_page = -1;
-      next_chunk = -1;
-      if (s >= s_end || i >= keys.count) return;
-      next_chunk = keys.chunk(i);
-      next_page = page_of(c, b, 16 * next_chunk);
-      if (next_page >= 0)
-        load_chunk<DP>(c, h, next_page, 16 * next_chunk % c.page_size, next);
-      else
-        set_status(c.status, NVFP4_ERR_INDEX);
+    // This warp's chunks are those of i, i + 4, ..; the copies are STAGES - 1 of them ahead, the
+    // page of the next to be copied one more.
+    const int per_page = c.page_size / 16, i_end = min(keys.count, 4 * s_end);
+    const int32_t* table = c.table + (int64_t)b * c.table_stride;
+    const uint8_t *kc = c.kc + h * c.ch, *vc = c.vc + h * c.ch, *ks = c.ks + h * c.sh, *vs = c.vs + h * c.sh;
+    Walk at;
+    int ahead = 4 * s_begin + warp, page = -1, put = 0;
+    uint32_t there = 0;  // by stage: whether the chunk's page is in range
+    if (ahead < i_end) {
+      at.begin(keys.chunk(ahead), per_page);
+      page = __ldg(table + at.slot);
+    }
+    auto copy = [&]() {
+      if (ahead < i_end) {
+        there &= ~(1u << put);
+        if ((uint32_t)page < (uint32_t)c.pages) {
+          const uint32_t pg = page, row = 16 * at.in;
+          const uint64_t codes = (uint64_t)pg * c.cp + (uint64_t)row * c.cr, scales = (uint64_t)pg * c.sp + (uint64_t)row * c.sr;
+          copies.issue(c, kc + codes, ks + scales, vc + codes, vs + scales, ring_at + put * F::STAGE, dense);
+          there |= 1u << put;
+        } else {
+          set_status(c.status, NVFP4_ERR_INDEX);
+        }
+        put = (put + 1) % F::STAGES;
+        ahead += kWarps;
+        if (ahead < i_end) {
+          at.go(keys.chunk(ahead), per_page);
+          page = __ldg(table + at.slot);
+        }
+      }
+      copies_end();
     };
-    fetch(s_begin);
-    for (int s = s_begin; s < s_end; ++s) {
-      Raw<DP> raw = next;
-      const int first = 16 * next_chunk, page = next_page;
-      const bool there = next_chunk >= 0 && page >= 0;
-      fetch(s + 1);
-      if (!there) continue;
-      // scores
+#pragma unroll
+    for (int x = 0; x < F::STAGES - 1; ++x) copy();
+    int get = 0;
+    for (int i = 4 * s_begin + warp; i < i_end; i += kWarps) {
+      const int first = 16 * keys.chunk(i);
+      const bool now = there >> get & 1u;
+      const uint8_t* stage = ring + get * F::STAGE;
+      get = (get + 1) % F::STAGES;
+      copies_wait<F::STAGES - 2>();
+      __syncwarp();  // every lane's copies are there, and the stage before is read
+      copy();
+      RawKeys<DP> rk;
+      RawValues<DP> rv;
+      take_keys<DP, FULL>(stage, c.dim, g, q, rk);
       float sc[2][4] = {};
+      if (now) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
+        for (int x = 0; x < F::KW; ++x) {
 #pragma unroll
-        for (int i = 0; i < F::KW; ++i) {
-          uint32_t x[4];
-          codes8(raw.k[t][i], x);
-          const uint32_t byte = raw.ks[t] >> (8 * (i / 2)) & 0xFFu;
-          const uint32_t f = scales2(byte | byte << 8);
+          for (int t = 0; t < 2; ++t) {
+            uint32_t y[4];
+            codes8(rk.w[t][x], y);
+            const uint32_t byte = rk.s[t] >> (8 * (x / 2)) & 0xFFu;
+            const uint32_t f = scales2(byte * 0x101u);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int j = 2 * i + e;
-            if constexpr (DP == 256) {
-              const uint4 y = qs[j * 32 + lane];
-              const uint32_t qa[4] = {y.x, y.y, y.z, y.w};
-              mma(sc[t], qa, h2_mul(x[2 * e], f), h2_mul(x[2 * e + 1], f));
-            } else {
-              mma(sc[t], qf[j], h2_mul(x[2 * e], f), h2_mul(x[2 * e + 1], f));
+            for (int e = 0; e < 2; ++e) {
+              const int j = 2 * x + e;
+              if constexpr (DP == 256) {
+                const uint4 z = qs[j * 32 + lane];
+                const uint32_t qa[4] = {z.x, z.y, z.z, z.w};
+                mma(sc[t], qa, h2_mul(y[2 * e], f), h2_mul(y[2 * e + 1], f));
+              } else {
+                mma(sc[t], qf[j], h2_mul(y[2 * e], f), h2_mul(y[2 * e + 1], f));
+              }
             }
           }
         }
       }
+      take_values<DP, FULL>(stage, c.dim, g, q, rv);
+      if (now) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        sc[t][0] *= f0;
-        sc[t][1] *= f0;
-        sc[t][2] *= f1;
-        sc[t][3] *= f1;
-      }
-      if (!keys.all_visible(first)) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int j = first + 8 * t + 2 * q + e;
-            if (!visible(a, seq, p0, j)) sc[t][e] = -INFINITY;
-            if (!visible(a, seq, p1, j)) sc[t][2 + e] = -INFINITY;
-          }
-        // what lies behind the end is no number: its weight is 0, and so is its scale
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-          if (first + 8 * (t / 2) + 2 * q + t % 2 >= seq.length) raw.vs[t] = 0;
-      }
-      const float x0 = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
-      const float x1 = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
-      if (__any_sync(0xFFFFFFFFu, x0 > m0 + 8.0f || x1 > m1 + 8.0f)) {
-        float n0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, 1)), n1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, 1));
-        n0 = fmaxf(m0, fmaxf(n0, __shfl_xor_sync(0xFFFFFFFFu, n0, 2)));
-        n1 = fmaxf(m1, fmaxf(n1, __shfl_xor_sync(0xFFFFFFFFu, n1, 2)));
-        const float d0 = n0 == m0 ? 1.0f : layer::ex2(m0 - n0), d1 = n1 == m1 ? 1.0f : layer::ex2(m1 - n1);
-        m0 = n0;
-        m1 = n1;
-        l0 *= d0;
-        l1 *= d1;
-#pragma unroll
-        for (int i = 0; i < F::VN; ++i) {
-          o[i][0] *= d0;
-          o[i][1] *= d0;
-          o[i][2] *= d1;
-          o[i][3] *= d1;
+        for (int t = 0; t < 2; ++t) {
+          sc[t][0] *= f0;
+          sc[t][1] *= f0;
+          sc[t][2] *= f1;
+          sc[t][3] *= f1;
         }
-      }
-      const float z0 = m0 == -INFINITY ? 0.0f : m0, z1 = m1 == -INFINITY ? 0.0f : m1;
+        if (!keys.all_visible(first)) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        sc[t][0] = layer::ex2(sc[t][0] - z0);
-        sc[t][1] = layer::ex2(sc[t][1] - z0);
-        sc[t][2] = layer::ex2(sc[t][2] - z1);
-        sc[t][3] = layer::ex2(sc[t][3] - z1);
-      }
-      l0 += (sc[0][0] + sc[0][1]) + (sc[1][0] + sc[1][1]);
-      l1 += (sc[0][2] + sc[0][3]) + (sc[1][2] + sc[1][3]);
-      const uint32_t pf[4] = {pack_h2(sc[0][0], sc[0][1]), pack_h2(sc[0][2], sc[0][3]), pack_h2(sc[1][0], sc[1][1]),
-                              pack_h2(sc[1][2], sc[1][3])};
-      // values: the codes of two keys side by side in each byte
+          for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int i = 0; i < F::VW; ++i) {
-        const int sh = 8 * (i / 2);
-        const uint32_t fa = scales2((raw.vs[0] >> sh & 0xFFu) | (raw.vs[1] >> sh & 0xFFu) << 8);
-        const uint32_t fb = scales2((raw.vs[2] >> sh & 0xFFu) | (raw.vs[3] >> sh & 0xFFu) << 8);
-        const uint32_t a0 = raw.v[0][i], a1 = raw.v[1][i], b0 = raw.v[2][i], b1 = raw.v[3][i];
-        uint32_t even_a[4], odd_a[4], even_b[4], odd_b[4];
-        codes8((a0 & 0x0F0F0F0Fu) | (a1 << 4 & 0xF0F0F0F0u), even_a);
-        codes8((a0 >> 4 & 0x0F0F0F0Fu) | (a1 & 0xF0F0F0F0u), odd_a);
-        codes8((b0 & 0x0F0F0F0Fu) | (b1 << 4 & 0xF0F0F0F0u), even_b);
-        codes8((b0 >> 4 & 0x0F0F0F0Fu) | (b1 & 0xF0F0F0F0u), odd_b);
+            for (int e = 0; e < 2; ++e) {
+              const int j = first + 8 * t + 2 * q + e;
+              if (!visible(a, seq, p0, j)) sc[t][e] = -INFINITY;
+              if (!visible(a, seq, p1, j)) sc[t][2 + e] = -INFINITY;
+            }
+          // what lies behind the end is no number: its weight is 0, and so is its scale
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          mma(o[8 * i + 2 * e], pf, h2_mul(even_a[e], fa), h2_mul(even_b[e], fb));
-          mma(o[8 * i + 2 * e + 1], pf, h2_mul(odd_a[e], fa), h2_mul(odd_b[e], fb));
+          for (int t = 0; t < 4; ++t)
+            if (first + 8 * (t / 2) + 2 * q + t % 2 >= seq.length) rv.s[t] = 0;
+        }
+        const float x0 = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
+        const float x1 = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
+        if (__any_sync(0xFFFFFFFFu, x0 > m0 + 8.0f || x1 > m1 + 8.0f)) {
+          float n0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, 1)), n1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, 1));
+          n0 = fmaxf(m0, fmaxf(n0, __shfl_xor_sync(0xFFFFFFFFu, n0, 2)));
+          n1 = fmaxf(m1, fmaxf(n1, __shfl_xor_sync(0xFFFFFFFFu, n1, 2)));
+          const float d0 = n0 == m0 ? 1.0f : layer::ex2(m0 - n0), d1 = n1 == m1 ? 1.0f : layer::ex2(m1 - n1);
+          m0 = n0;
+          m1 = n1;
+          l0 *= d0;
+          l1 *= d1;
+#pragma unroll
+          for (int x = 0; x < F::VN; ++x) {
+            o[x][0] *= d0;
+            o[x][1] *= d0;
+            o[x][2] *= d1;
+            o[x][3] *= d1;
+          }
+        }
+        const float z0 = m0 == -INFINITY ? 0.0f : m0, z1 = m1 == -INFINITY ? 0.0f : m1;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          sc[t][0] = layer::ex2(sc[t][0] - z0);
+          sc[t][1] = layer::ex2(sc[t][1] - z0);
+          sc[t][2] = layer::ex2(sc[t][2] - z1);
+          sc[t][3] = layer::ex2(sc[t][3] - z1);
+        }
+        l0 += (sc[0][0] + sc[0][1]) + (sc[1][0] + sc[1][1]);
+        l1 += (sc[0][2] + sc[0][3]) + (sc[1][2] + sc[1][3]);
+        const uint32_t pf[4] = {pack_h2(sc[0][0], sc[0][1]), pack_h2(sc[0][2], sc[0][3]), pack_h2(sc[1][0], sc[1][1]),
+                                pack_h2(sc[1][2], sc[1][3])};
+        // values: the codes of two keys side by side in each byte
+#pragma unroll
+        for (int x = 0; x < F::VW; ++x) {
+          const int sh = 8 * (x / 2);
+          const uint32_t fa = scales2((rv.s[0] >> sh & 0xFFu) | (rv.s[1] >> sh & 0xFFu) << 8);
+          const uint32_t fb = scales2((rv.s[2] >> sh & 0xFFu) | (rv.s[3] >> sh & 0xFFu) << 8);
+          const uint32_t a0 = rv.w[0][x], a1 = rv.w[1][x], b0 = rv.w[2][x], b1 = rv.w[3][x];
+          uint32_t even_a[4], odd_a[4], even_b[4], odd_b[4];
+          codes8((a0 & 0x0F0F0F0Fu) | (a1 << 4 & 0xF0F0F0F0u), even_a);
+          codes8((b0 & 0x0F0F0F0Fu) | (b1 << 4 & 0xF0F0F0F0u), even_b);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mma(o[8 * x + 2 * e], pf, h2_mul(even_a[e], fa), h2_mul(even_b[e], fb));
+          codes8((a0 >> 4 & 0x0F0F0F0Fu) | (a1 & 0xF0F0F0F0u), odd_a);
+          codes8((b0 >> 4 & 0x0F0F0F0Fu) | (b1 & 0xF0F0F0F0u), odd_b);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mma(o[8 * x + 2 * e + 1], pf, h2_mul(odd_a[e], fa), h2_mul(odd_b[e], fb));
         }
       }
     }
+    copies_wait<0>();
 
     // the four warps' parts
 #pragma unroll
@@ -347,7 +477,7 @@ __global__ void __launch_bounds__(kThreadsFew, few_per_sm(DP)) few_kernel(Attend
       l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, x);
       l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, x);
     }
-    __syncthreads();  // the part before is read
+    __syncthreads();  // the rings are read
     if (q == 0) {
       ms[warp * 16 + g] = m0;
       ms[warp * 16 + 8 + g] = m1;
@@ -420,25 +550,29 @@ __global__ void __launch_bounds__(DP) few_join_kernel(AttendArgs a) {
   }
 }
 
-template <int DP>
+template <int DP, bool FULL>
 cudaError_t launch(const AttendArgs& a, cudaStream_t s) {
   using F = Few<DP>;
-  cudaError_t e = cudaFuncSetAttribute(few_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM);
+  cudaError_t e = cudaFuncSetAttribute(few_kernel<DP, FULL>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM);
   if (e != cudaSuccess) return e;
   constexpr int G = few_blocks(DP);
-  e = launch_early(few_kernel<DP>, dim3((unsigned)G), kThreadsFew, F::SMEM, s, a);
+  e = launch_early(few_kernel<DP, FULL>, dim3((unsigned)G), kThreadsFew, F::SMEM, s, a);
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)a.c.T * a.group;
   return launch_early(few_join_kernel<DP>, dim3((unsigned)G, (unsigned)(rows < 4 ? rows : 4)), DP, 0, s, a);
+}
+template <int DP>
+cudaError_t by_dim(const AttendArgs& a, cudaStream_t s) {
+  return a.c.dim == DP ? launch<DP, true>(a, s) : launch<DP, false>(a, s);
 }
 
 }  // namespace attention
 
 cudaError_t launch_attend_few(const AttendArgs& a, cudaStream_t s) {
   using namespace attention;
-  if (a.c.dim <= 64) return launch<64>(a, s);
-  if (a.c.dim <= 128) return launch<128>(a, s);
-  return launch<256>(a, s);
+  if (a.c.dim <= 64) return by_dim<64>(a, s);
+  if (a.c.dim <= 128) return by_dim<128>(a, s);
+  return by_dim<256>(a, s);
 }
 
 }  // namespace nvfp4

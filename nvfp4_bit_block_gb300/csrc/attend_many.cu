@@ -381,8 +381,9 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
     auto load = [&](int i) {
       const int64_t key = (int64_t)keys.chunk(i) * BN + r;
       const int page = key < seq.length ? page_of(c, b, (int)key) : -1;
-      const int64_t in = page >= 0 ? key % c.page_size : 0, pg = page >= 0 ? page : 0;
-      const int64_t co = pg * c.cp + in * c.cr + hc, so = pg * c.sp + in * c.sr + hs;
+      const uint32_t in = page >= 0 ? (uint32_t)key % (uint32_t)c.page_size : 0, pg = page >= 0 ? page : 0;
+      const int64_t co = hc + (int64_t)((uint64_t)pg * c.cp + (uint64_t)in * c.cr);
+      const int64_t so = hs + (int64_t)((uint64_t)pg * c.sp + (uint64_t)in * c.sr);
       load_raw<DP>(c.kc + co, c.ks + so, page >= 0, first, D, k);
       load_raw<DP>(c.vc + co, c.vs + so, page >= 0, first, D, v);
     };

@@ -70,8 +70,8 @@ int check_cache(const nvfp4_kv_cache* c, const nvfp4_batch* b, int64_t T, const 
   const int64_t strides[2][3] = {{c->code_page, c->code_head, c->code_row}, {c->scale_page, c->scale_head, c->scale_row}};
   for (int k = 0; k < 2; ++k) {
     int o[3] = {0, 1, 2};  // by stride, smallest first; axes of one entry are not stepped over
-    for (int i = 0; i < 3; ++i)
-      if (strides[k][i] < 0 || strides[k][i] > kMaxStride) return NVFP4_ERR_SHAPE;
+    for (int i = 0; i < 3; ++i)  // pages and rows are stepped over in the kernels' loops
+      if (strides[k][i] < 0 || strides[k][i] > (i == 1 ? kMaxStride : (int64_t)UINT32_MAX)) return NVFP4_ERR_SHAPE;
     for (int i = 0; i < 2; ++i)
       for (int j = 0; j < 2 - i; ++j)
         if (strides[k][o[j]] > strides[k][o[j + 1]]) {
@@ -114,12 +114,12 @@ nvfp4::CacheView view(const nvfp4_kv_cache* c, const nvfp4_batch* b, int64_t T, 
   v.vc = c->v_codes;
   v.vs = c->v_scales;
   v.alpha = c->alpha_dev;
-  v.cp = c->code_page;
   v.ch = c->code_head;
-  v.cr = c->code_row;
-  v.sp = c->scale_page;
   v.sh = c->scale_head;
-  v.sr = c->scale_row;
+  v.cp = (uint32_t)c->code_page;
+  v.cr = (uint32_t)c->code_row;
+  v.sp = (uint32_t)c->scale_page;
+  v.sr = (uint32_t)c->scale_row;
   v.table_width = b->table_width;
   v.table_stride = b->table_stride;
   v.starts = b->starts;

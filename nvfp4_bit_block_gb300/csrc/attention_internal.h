@@ -41,7 +41,8 @@ struct RopeGradArgs {
 struct CacheView {
   uint8_t *kc, *ks, *vc, *vs;
   const float* alpha;
-  int64_t cp, ch, cr, sp, sh, sr;  // strides of codes and scales in bytes: page, head, row
+  int64_t ch, sh;           // strides of codes and scales in bytes: head,
+  uint32_t cp, cr, sp, sr;  // page and row
   int64_t table_width, table_stride;
   const int32_t *starts, *lengths, *table;
   int sequences, pages, heads, page_size, dim;

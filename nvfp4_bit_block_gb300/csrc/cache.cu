@@ -41,8 +41,8 @@ __device__ __forceinline__ Place place_of(const CacheView& c, int t) {
   const int page = j >= 0 ? page_of(c, b, (int)j) : -1;
   if (page >= 0) {
     const int row = (int)j % c.page_size;
-    p.codes = (int64_t)page * c.cp + (int64_t)row * c.cr;
-    p.scales = (int64_t)page * c.sp + (int64_t)row * c.sr;
+    p.codes = (int64_t)((uint64_t)page * c.cp + (uint64_t)row * c.cr);
+    p.scales = (int64_t)((uint64_t)page * c.sp + (uint64_t)row * c.sr);
     p.there = true;
   } else {
     set_status(c.status, NVFP4_ERR_INDEX);
