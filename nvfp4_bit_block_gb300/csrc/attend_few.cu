@@ -51,7 +51,8 @@ struct Few {
   static constexpr int RING = kWarps * STAGES * STAGE, O = kWarps * 16 * ROW * 4;
   static constexpr int ML = RING > O ? RING : O;
   static constexpr int QS = ML + 2 * kWarps * 16 * 4;
-  static constexpr int SMEM = QS + (DP == 256 ? STEPS * 32 * 16 : 0);
+  static constexpr bool Q_SHARED = DP >= 128;
+  static constexpr int SMEM = QS + (Q_SHARED ? STEPS * 32 * 16 : 0);
 };
 
 // One lane's bytes of 16 keys, and of 16 values; scale bytes, first lowest.
@@ -245,7 +246,7 @@ __global__ void __launch_bounds__(kThreadsFew, few_per_sm(DP)) few_kernel(Attend
   float* os = reinterpret_cast<float*>(sm);          // [warps][16][ROW]
   float* ms = reinterpret_cast<float*>(sm + F::ML);  // [warps][16]
   float* ls = ms + kWarps * 16;                      // [warps][16]
-  uint4* qs = reinterpret_cast<uint4*>(sm + F::QS);  // [STEPS][32], DP = 256 only
+  uint4* qs = reinterpret_cast<uint4*>(sm + F::QS);  // [STEPS][32], Q_SHARED
   uint8_t* ring = sm + warp * F::STAGES * F::STAGE;
   const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
 
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(kThreadsFew, few_per_sm(DP)) few_kernel(Attend
       }
     }
     __syncthreads();  // the part before is read
-    if constexpr (DP == 256) {
+    if constexpr (F::Q_SHARED) {
       if (warp == 0)
 #pragma unroll
         for (int j = 0; j < F::STEPS; ++j) qs[j * 32 + lane] = make_uint4(qf[j][0], qf[j][1], qf[j][2], qf[j][3]);
@@ -385,7 +386,7 @@ __global__ void __launch_bounds__(kThreadsFew, few_per_sm(DP)) few_kernel(Attend
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int j = 2 * x + e;
-              if constexpr (DP == 256) {
+              if constexpr (F::Q_SHARED) {
                 const uint4 z = qs[j * 32 + lane];
                 const uint32_t qa[4] = {z.x, z.y, z.z, z.w};
                 mma(sc[t], qa, h2_mul(y[2 * e], f), h2_mul(y[2 * e + 1], f));
