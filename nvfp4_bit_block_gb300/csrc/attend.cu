@@ -9,8 +9,8 @@
 
 namespace nvfp4 {
 
-int64_t attend_workspace(int64_t, int, int, int dim, int64_t) {
-  return attention::few_floats(attention::few_width(dim)) * (int64_t)sizeof(float);
+int64_t attend_workspace(int64_t T, int Hq, int heads, int dim, int64_t sequences) {
+  return attend_few_workspace(T, Hq / heads, dim, sequences);
 }
 
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t s) {

@@ -65,10 +65,6 @@ __device__ __forceinline__ Keys<CH> rows_keys(const AttendArgs& a, const Sequenc
   k.count = k.sinks + max(0, (int)(((int64_t)max(end, 0) + (CH - 1)) / CH) - k.first);
   return k;
 }
-__device__ __forceinline__ Keys<16> tile_keys(const AttendArgs& a, const Sequence& s, int tile) {
-  return rows_keys<16>(a, s, 16 * tile, min(16, s.rows * a.group - 16 * tile));
-}
-
 // lse of one row from its maximum and sum to base 2, both -Inf and 0 where it sees nothing.
 __device__ __forceinline__ float row_lse(float top, float l) {
   if (l == 0.0f) return -INFINITY;
@@ -138,18 +134,8 @@ __device__ __forceinline__ bool rows_at_16(const Tokens& t) {
 // What a block leaves of the unit that it begins and does not end (last < 0: none).
 struct FewHead {
   int last;  // the block that ends it
-  int first, head, tile, rows;
+  int first, head, row, rows;  // the sequence's first row of the call, the key head, the unit's first row and how many
 };
-__device__ __forceinline__ void load_few(const AttendArgs& a, int b, Sequence& s) {
-  load_sequence(a.c, b, s);
-  if (!is_few(a, s)) s.rows = 0;
-}
-// Steps of a sequence's tiles of one key head.
-__device__ __forceinline__ int64_t sequence_steps(const AttendArgs& a, const Sequence& s) {
-  int64_t n = 0;
-  for (int r = 0; 16 * r < s.rows * a.group; ++r) n += tile_keys(a, s, r).steps();
-  return n;
-}
 
 // The line cut into G pieces, the first total % G of them a step longer.
 struct Pieces {
@@ -210,17 +196,9 @@ __device__ __forceinline__ void find_line(const CacheView& c, Line& line, Weight
   __syncthreads();
 }
 
-// Blocks of attend_few.cu's kernel: as many as an SM holds of them, on every SM.
-constexpr int few_per_sm(int DP) { return DP == 64 ? 4 : DP == 128 ? 3 : 2; }
-constexpr int few_blocks(int DP) { return 152 * few_per_sm(DP); }
-constexpr int few_width(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
-// The workspace: a FewHead for each block, then two slots (o, m and l of 16 rows) for each.
-constexpr int64_t few_slot_floats(int DP) { return 16 * DP + 32; }
-constexpr int64_t few_head_floats(int DP) { return (few_blocks(DP) * (int64_t)sizeof(FewHead) / 4 + 3) / 4 * 4; }
-constexpr int64_t few_floats(int DP) { return few_head_floats(DP) + 2 * few_blocks(DP) * few_slot_floats(DP); }
-
 }  // namespace attention
 
+int64_t attend_few_workspace(int64_t T, int group, int dim, int64_t sequences);
 cudaError_t launch_attend_few(const AttendArgs& a, cudaStream_t s);
 cudaError_t launch_attend_many(const AttendArgs& a, cudaStream_t s);
 

@@ -2,21 +2,24 @@
 // that share a key head) to the NVFP4 cache: the next token, or a few drafted ones.
 //
 // The cache's bytes are the floor: 9/16 byte per value, read once for all heads of a group.
-// A unit of work is 16 rows of one key head; its visible keys are cut into steps of 64 and the
-// steps of all units form one line that is cut into equal pieces, one per block, so that one
-// long sequence and many short ones fill the GPU alike.  Pieces that are part of a unit leave
-// (m, l, o) in the workspace and a second kernel joins them in order.
+// A unit of work is a tile of 8, 16 or 32 rows of one key head; its visible keys are cut into
+// steps of 64 and the steps of all units form one line that is cut into equal pieces, one per
+// block, so that one long sequence and many short ones fill the GPU alike.  Pieces that are part
+// of a unit leave (m, l, o) in the workspace and a second kernel joins them in order.
 //
 // Within a step each of a block's four warps takes 16 keys, whose bytes come by asynchronous
 // copies into the warp's own ring in shared memory, a few chunks ahead (with the next chunk on
 // its way in registers instead, each SM had 20 KB in flight where the latency wants 45).  From
-// there to the output they stay in registers: S = Q K^T and O += P V as m16n8k16 products in fp16 with fp32
-// sums.  A code times its scale has at most 6 significant bits within 2^-10..2688, so it is
-// exact in fp16; queries are scaled by a power of two per row.  Which of a product's k's (and of
-// the output's columns) a value counts as is free, as long as both operands agree: each lane
-// loads bytes that lie side by side and uses them where they are.  Lane (g, c) = (lane / 4,
-// lane % 4) has for key rows g and 8 + g the c-th quarter of the values, and for the value rows
-// 2c, 2c + 1, 8 + 2c, 9 + 2c the g-th eighth.
+// there to the output they stay in registers, as the first operand of m16n8k16 products in fp16
+// with fp32 sums: S^T = K Q^T for 16 keys and 8 rows, O^T += V^T P^T for 16 values and 8 rows.  (With
+// the rows first, a tile has 16 of them and most are empty: twice the products and registers for o.)
+// A code times its scale has at most 6 significant bits within 2^-10..2688, so it is exact in
+// fp16; queries are scaled by a power of two per row.  Which of a product's k's (and of its 16
+// values) a value counts as is free, as long as both operands agree: each lane loads bytes that
+// lie side by side and uses them where they are.  Lane (g, q) = (lane / 4, lane % 4) has for key
+// rows g and 8 + g the q-th quarter of the values, and for the value rows 2q, 2q + 1, 8 + 2q,
+// 9 + 2q the g-th eighth.  P leaves its product with keys along g and rows along q and enters the
+// next one the other way round: movmatrix turns it.
 //
 // The running maximum moves only where a score passes it by more than 2^8: weights stay below
 // 256, where fp16 holds them as well as below 1, and most steps leave o alone.
@@ -30,51 +33,63 @@ namespace attention {
 constexpr int kWarps = 4;
 constexpr int kThreadsFew = 32 * kWarps;
 
-template <int DP>
+template <int DP, int NT>
 struct Few {
+  static constexpr int ROWS = 8 * NT;   // of a tile
   static constexpr int KW = DP / 32;    // words of a lane's part of a key (DP / 4 values)
   static constexpr int KS = DP / 64;    // its scales
-  static constexpr int STEPS = DP / 16; // products over a key
   static constexpr int VN = DP / 8;     // values of a lane's part of a value row
   static constexpr int VW = VN / 8;     // words of it
-  static constexpr int VS = VN >= 32 ? 2 : 1;
-  // A row of o in shared memory: value n * VN + i at 9 i + n; rows 8 banks apart.
-  static constexpr int ROW = DP == 64 ? 72 : DP == 128 ? 168 : 296;
   // A chunk in a warp's ring: rows of codes (16 bytes apart in their banks), then scales as the
   // cache has them; of keys, then of values.
   static constexpr int CODE_ROW = DP / 2 + 16;
   static constexpr int CODES = 16 * CODE_ROW, SCALES = 16 * (DP / 16);
   static constexpr int STAGE = 2 * (CODES + SCALES);
-  static constexpr int STAGES = 4;
+  static constexpr int STAGES = DP == 256 ? 3 : 4;
   static constexpr int COPIES = DP / 64;  // 16-byte pieces of a lane in 16 rows of codes
+  // Queries stay in registers where they are few.
+  static constexpr bool Q_SHARED = DP * NT > 128;
   // shared memory: the rings, and in the end o of the four warps in their place; m and l; queries
-  static constexpr int RING = kWarps * STAGES * STAGE, O = kWarps * 16 * ROW * 4;
+  static constexpr int O_ROW = DP + 2;
+  static constexpr int RING = kWarps * STAGES * STAGE, O = kWarps * ROWS * O_ROW * 4;
   static constexpr int ML = RING > O ? RING : O;
-  static constexpr int QS = ML + 2 * kWarps * 16 * 4;
-  static constexpr bool Q_SHARED = DP >= 128;
-  static constexpr int SMEM = QS + (Q_SHARED ? STEPS * 32 * 16 : 0);
+  static constexpr int QS = ML + 2 * kWarps * ROWS * 4;
+  static constexpr int SMEM = QS + (Q_SHARED ? DP / 32 * NT * 32 * 16 : 0);
+  // Blocks: as many as an SM holds of them by registers, on every SM.
+  static constexpr int PER_SM = DP == 64 ? (NT == 1 ? 5 : NT == 2 ? 4 : 3) : DP == 128 ? (NT == 1 ? 4 : NT == 2 ? 3 : 2) : NT == 1 ? 3 : 2;
+  static constexpr int BLOCKS = 152 * PER_SM;
+  // The workspace: a FewHead for each block, then two slots (o, m and l of a tile) for each.
+  static constexpr int64_t SLOT = ROWS * DP + 2 * ROWS;
+  static constexpr int64_t HEADS = (BLOCKS * (int64_t)sizeof(FewHead) / 4 + 3) / 4 * 4;
+  static constexpr int64_t FLOATS = HEADS + 2 * BLOCKS * SLOT;
 };
 
 // One lane's bytes of 16 keys, and of 16 values; scale bytes, first lowest.
 template <int DP>
 struct RawKeys {
-  uint32_t w[2][Few<DP>::KW], s[2];
+  uint32_t w[2][DP / 32], s[2];
 };
 template <int DP>
 struct RawValues {
-  uint32_t w[4][Few<DP>::VW], s[4];
+  uint32_t w[4][DP / 64], s[4];
 };
 
-__device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// An 8 x 8 matrix of fp16, two of row lane / 4 in each lane, to its transpose.
+__device__ __forceinline__ uint32_t turned(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 
 // What lane (g, q) needs of a chunk in the ring; FULL: D is DP, else parts beyond D are zeros.
 template <int DP, bool FULL>
 __device__ __forceinline__ void take_keys(const uint8_t* stage, int D, int g, int q, RawKeys<DP>& r) {
-  using F = Few<DP>;
+  using F = Few<DP, 1>;
   const int row = FULL ? DP / 16 : D / 16;
   const uint8_t* p = stage + g * F::CODE_ROW + q * (DP / 8);
   const uint8_t* s = stage + 2 * F::CODES + g * row + q * F::KS;
@@ -108,7 +123,7 @@ __device__ __forceinline__ void take_keys(const uint8_t* stage, int D, int g, in
 }
 template <int DP, bool FULL>
 __device__ __forceinline__ void take_values(const uint8_t* stage, int D, int g, int q, RawValues<DP>& r) {
-  using F = Few<DP>;
+  using F = Few<DP, 1>;
   const int row = FULL ? DP / 16 : D / 16;
   const uint8_t* p = stage + F::CODES + 2 * q * F::CODE_ROW + g * (DP / 16);
   const uint8_t* s = stage + 2 * F::CODES + F::SCALES + 2 * q * row + g * F::VN / 16;
@@ -152,7 +167,7 @@ __device__ __forceinline__ void copies_wait() {
 // A lane's share of the copies of one chunk.
 template <int DP, bool FULL>
 struct Copies {
-  using F = Few<DP>;
+  using F = Few<DP, 1>;
   uint64_t from[F::COPIES];  // offsets from the chunk's first row of codes
   uint32_t to[F::COPIES];    // .. and in a stage of the ring
   int lane;
@@ -234,19 +249,37 @@ __device__ __forceinline__ float load_query(const AttendArgs& a, bool vec, bool 
   return query_up(top);
 }
 
-template <int DP, bool FULL>
-__global__ void __launch_bounds__(kThreadsFew, few_per_sm(DP)) few_kernel(AttendArgs a) {
-  using F = Few<DP>;
+// The keys of a tile of a sequence's rows, in chunks of 16, and the steps of 64 that all its
+// tiles make for one key head.
+template <int ROWS>
+__device__ __forceinline__ Keys<16> tile_keys(const AttendArgs& a, const Sequence& s, int tile) {
+  return rows_keys<16>(a, s, ROWS * tile, min(ROWS, s.rows * a.group - ROWS * tile));
+}
+template <int ROWS>
+__device__ __forceinline__ int64_t sequence_steps(const AttendArgs& a, const Sequence& s) {
+  int64_t n = 0;
+  for (int r = 0; ROWS * r < s.rows * a.group; ++r) n += tile_keys<ROWS>(a, s, r).steps();
+  return n;
+}
+__device__ __forceinline__ void load_few(const AttendArgs& a, int b, Sequence& s) {
+  load_sequence(a.c, b, s);
+  if (!is_few(a, s)) s.rows = 0;
+}
+
+template <int DP, int NT, bool FULL>
+__global__ void __launch_bounds__(kThreadsFew, Few<DP, NT>::PER_SM) few_kernel(AttendArgs a) {
+  using F = Few<DP, NT>;
+  constexpr int ROWS = F::ROWS;
   extern __shared__ __align__(16) uint8_t sm[];
   __shared__ Line line;
   const CacheView& c = a.c;
   after_previous();
   if (blockIdx.x == 0) check_batch(c);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, q = lane % 4;
-  float* os = reinterpret_cast<float*>(sm);          // [warps][16][ROW]
-  float* ms = reinterpret_cast<float*>(sm + F::ML);  // [warps][16]
-  float* ls = ms + kWarps * 16;                      // [warps][16]
-  uint4* qs = reinterpret_cast<uint4*>(sm + F::QS);  // [STEPS][32], Q_SHARED
+  float* os = reinterpret_cast<float*>(sm);          // [warps][ROWS][O_ROW]
+  float* ms = reinterpret_cast<float*>(sm + F::ML);  // [warps][ROWS]
+  float* ls = ms + kWarps * ROWS;                    // [warps][ROWS]
+  uint4* qs = reinterpret_cast<uint4*>(sm + F::QS);  // [KW][NT][32], Q_SHARED
   uint8_t* ring = sm + warp * F::STAGES * F::STAGE;
   const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
 
@@ -254,7 +287,7 @@ __global__ void __launch_bounds__(kThreadsFew, few_per_sm(DP)) few_kernel(Attend
       c, line, [&](int b) {
         Sequence s;
         load_few(a, b, s);
-        return sequence_steps(a, s) * c.heads;
+        return sequence_steps<ROWS>(a, s) * c.heads;
       },
       [&](int64_t total) { return Pieces(total, gridDim.x).begin(blockIdx.x); });
   const Pieces pieces(line.total, gridDim.x);
@@ -269,7 +302,6 @@ __global__ void __launch_bounds__(kThreadsFew, few_per_sm(DP)) few_kernel(Attend
   load_few(a, b, seq);
   int64_t base = line.base;  // where sequence b begins on the line
   const float alpha_v = c.alpha[1], scale = a.scale * c.alpha[0] * layer::kLog2e;
-
   const bool vec = rows_at_16(a.q);
   const bool dense = c.sr == c.dim / 16 &&
                      (reinterpret_cast<uintptr_t>(c.ks) | reinterpret_cast<uintptr_t>(c.vs) | c.sp | c.sh) % 16 == 0;
@@ -277,56 +309,59 @@ __global__ void __launch_bounds__(kThreadsFew, few_per_sm(DP)) few_kernel(Attend
 
   while (w < w_end) {
     // the unit that w is in
-    int64_t per_head = sequence_steps(a, seq);
+    int64_t per_head = sequence_steps<ROWS>(a, seq);
     while (w >= base + per_head * c.heads) {
       base += per_head * c.heads;
       load_few(a, ++b, seq);
-      per_head = sequence_steps(a, seq);
+      per_head = sequence_steps<ROWS>(a, seq);
     }
     const int h = (int)((w - base) / per_head);
     int64_t u0 = base + h * per_head;
     int r = 0;
-    Keys<16> keys = tile_keys(a, seq, 0);
+    Keys<16> keys = tile_keys<ROWS>(a, seq, 0);
     while (w >= u0 + keys.steps()) {
       u0 += keys.steps();
-      keys = tile_keys(a, seq, ++r);
+      keys = tile_keys<ROWS>(a, seq, ++r);
     }
     const int64_t u1 = u0 + keys.steps();
     const int s_begin = (int)(w - u0), s_end = (int)((w_end < u1 ? w_end : u1) - u0);
-    const int rows = min(16, seq.rows * a.group - 16 * r);
+    const int rows = min(ROWS, seq.rows * a.group - ROWS * r);
 
-    // queries
-    const int row0 = 16 * r + g, row1 = row0 + 8;
-    const bool on0 = g < rows, on1 = g + 8 < rows;
-    const int t0 = on0 ? row0 / a.group : 0, t1 = on1 ? row1 / a.group : 0;
-    uint32_t qf[F::STEPS][4];
-    float f0, f1;
-    {
-      uint32_t x[F::STEPS * 2];
-      f0 = scale * load_query<DP>(a, vec, on0, (int64_t)seq.first + t0, h * a.group + (on0 ? row0 % a.group : 0), x);
+    // queries: rows g of each eight; scores and o: rows 2q and 2q + 1
+    uint32_t qf[NT][F::KW * 4];
+    float f[NT][2];
+    int p[NT][2];
 #pragma unroll
-      for (int j = 0; j < F::STEPS; ++j) {
-        qf[j][0] = x[2 * j];
-        qf[j][2] = x[2 * j + 1];
-      }
-      f1 = scale * load_query<DP>(a, vec, on1, (int64_t)seq.first + t1, h * a.group + (on1 ? row1 % a.group : 0), x);
+    for (int n = 0; n < NT; ++n) {
+      const int row = ROWS * r + 8 * n + g;
+      const bool on = 8 * n + g < rows;
+      const float up = load_query<DP>(a, vec, on, (int64_t)seq.first + (on ? row / a.group : 0),
+                                      h * a.group + (on ? row % a.group : 0), qf[n]);
 #pragma unroll
-      for (int j = 0; j < F::STEPS; ++j) {
-        qf[j][1] = x[2 * j];
-        qf[j][3] = x[2 * j + 1];
+      for (int e = 0; e < 2; ++e) {
+        f[n][e] = scale * __shfl_sync(0xFFFFFFFFu, up, 8 * q + 4 * e);
+        const int x = 8 * n + 2 * q + e;
+        p[n][e] = seq.length - seq.rows + (x < rows ? (ROWS * r + x) / a.group : 0);
       }
     }
     __syncthreads();  // the part before is read
     if constexpr (F::Q_SHARED) {
       if (warp == 0)
 #pragma unroll
-        for (int j = 0; j < F::STEPS; ++j) qs[j * 32 + lane] = make_uint4(qf[j][0], qf[j][1], qf[j][2], qf[j][3]);
+        for (int x = 0; x < F::KW; ++x)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            qs[(x * NT + n) * 32 + lane] = make_uint4(qf[n][4 * x], qf[n][4 * x + 1], qf[n][4 * x + 2], qf[n][4 * x + 3]);
       __syncthreads();
     }
-    const int p0 = seq.length - seq.rows + t0, p1 = seq.length - seq.rows + t1;
 
-    float o[F::VN][4] = {};
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+    float o[F::VN / 2][NT][4] = {};
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.0f;
+    }
     // This warp's chunks are those of i, i + 4, ..; the copies are STAGES - 1 of them ahead, the
     // page of the next to be copied one more.
     const int per_page = c.page_size / 16, i_end = min(keys.count, 4 * s_end);
@@ -370,210 +405,229 @@ __global__ void __launch_bounds__(kThreadsFew, few_per_sm(DP)) few_kernel(Attend
       copies_wait<F::STAGES - 2>();
       __syncwarp();  // every lane's copies are there, and the stage before is read
       copy();
+      if (!now) continue;
       RawKeys<DP> rk;
       RawValues<DP> rv;
       take_keys<DP, FULL>(stage, c.dim, g, q, rk);
-      float sc[2][4] = {};
-      if (now) {
+      float sc[NT][4] = {};
 #pragma unroll
-        for (int x = 0; x < F::KW; ++x) {
+      for (int x = 0; x < F::KW; ++x) {
+        uint32_t y[2][4];
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            uint32_t y[4];
-            codes8(rk.w[t][x], y);
-            const uint32_t byte = rk.s[t] >> (8 * (x / 2)) & 0xFFu;
-            const uint32_t f = scales2(byte * 0x101u);
+        for (int t = 0; t < 2; ++t) {
+          codes8(rk.w[t][x], y[t]);
+          const uint32_t byte = rk.s[t] >> (8 * (x / 2)) & 0xFFu;
+          const uint32_t z = scales2(byte * 0x101u);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int j = 2 * x + e;
-              if constexpr (F::Q_SHARED) {
-                const uint4 z = qs[j * 32 + lane];
-                const uint32_t qa[4] = {z.x, z.y, z.z, z.w};
-                mma(sc[t], qa, h2_mul(y[2 * e], f), h2_mul(y[2 * e + 1], f));
-              } else {
-                mma(sc[t], qf[j], h2_mul(y[2 * e], f), h2_mul(y[2 * e + 1], f));
-              }
-            }
-          }
+          for (int e = 0; e < 4; ++e) y[t][e] = h2_mul(y[t][e], z);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          uint4 z;
+          if constexpr (F::Q_SHARED)
+            z = qs[(x * NT + n) * 32 + lane];
+          else
+            z = make_uint4(qf[n][4 * x], qf[n][4 * x + 1], qf[n][4 * x + 2], qf[n][4 * x + 3]);
+          mma(sc[n], y[0][0], y[1][0], y[0][1], y[1][1], z.x, z.y);
+          mma(sc[n], y[0][2], y[1][2], y[0][3], y[1][3], z.z, z.w);
         }
       }
       take_values<DP, FULL>(stage, c.dim, g, q, rv);
-      if (now) {
+      const bool part = !keys.all_visible(first);
+      bool up = false;
+      float x[NT][2];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          sc[t][0] *= f0;
-          sc[t][1] *= f0;
-          sc[t][2] *= f1;
-          sc[t][3] *= f1;
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sc[n][e] *= f[n][e & 1];
+          if (part && !visible(a, seq, p[n][e & 1], first + g + 8 * (e / 2))) sc[n][e] = -INFINITY;
         }
-        if (!keys.all_visible(first)) {
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int j = first + 8 * t + 2 * q + e;
-              if (!visible(a, seq, p0, j)) sc[t][e] = -INFINITY;
-              if (!visible(a, seq, p1, j)) sc[t][2 + e] = -INFINITY;
-            }
-          // what lies behind the end is no number: its weight is 0, and so is its scale
-#pragma unroll
-          for (int t = 0; t < 4; ++t)
-            if (first + 8 * (t / 2) + 2 * q + t % 2 >= seq.length) rv.s[t] = 0;
+        for (int e = 0; e < 2; ++e) {
+          x[n][e] = fmaxf(sc[n][e], sc[n][2 + e]);
+          up |= x[n][e] > m[n][e] + 8.0f;
         }
-        const float x0 = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
-        const float x1 = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
-        if (__any_sync(0xFFFFFFFFu, x0 > m0 + 8.0f || x1 > m1 + 8.0f)) {
-          float n0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, 1)), n1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, 1));
-          n0 = fmaxf(m0, fmaxf(n0, __shfl_xor_sync(0xFFFFFFFFu, n0, 2)));
-          n1 = fmaxf(m1, fmaxf(n1, __shfl_xor_sync(0xFFFFFFFFu, n1, 2)));
-          const float d0 = n0 == m0 ? 1.0f : layer::ex2(m0 - n0), d1 = n1 == m1 ? 1.0f : layer::ex2(m1 - n1);
-          m0 = n0;
-          m1 = n1;
-          l0 *= d0;
-          l1 *= d1;
+      }
+      if (part) {  // what lies behind the end is no number: its weight is 0, and so is its scale
 #pragma unroll
-          for (int x = 0; x < F::VN; ++x) {
-            o[x][0] *= d0;
-            o[x][1] *= d0;
-            o[x][2] *= d1;
-            o[x][3] *= d1;
+        for (int t = 0; t < 4; ++t)
+          if (first + 8 * (t / 2) + 2 * q + t % 2 >= seq.length) rv.s[t] = 0;
+      }
+      if (__any_sync(0xFFFFFFFFu, up)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float d[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float top = x[n][e];
+#pragma unroll
+            for (int s = 4; s < 32; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, s));
+            top = fmaxf(top, m[n][e]);
+            d[e] = top == m[n][e] ? 1.0f : layer::ex2(m[n][e] - top);
+            m[n][e] = top;
+            l[n][e] *= d[e];
           }
+#pragma unroll
+          for (int y = 0; y < F::VN / 2; ++y)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[y][n][e] *= d[e & 1];
         }
-        const float z0 = m0 == -INFINITY ? 0.0f : m0, z1 = m1 == -INFINITY ? 0.0f : m1;
+      }
+      uint32_t pf[NT][2];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          sc[t][0] = layer::ex2(sc[t][0] - z0);
-          sc[t][1] = layer::ex2(sc[t][1] - z0);
-          sc[t][2] = layer::ex2(sc[t][2] - z1);
-          sc[t][3] = layer::ex2(sc[t][3] - z1);
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sc[n][e] = layer::ex2(sc[n][e] - (m[n][e & 1] == -INFINITY ? 0.0f : m[n][e & 1]));
+          l[n][e & 1] += sc[n][e];
         }
-        l0 += (sc[0][0] + sc[0][1]) + (sc[1][0] + sc[1][1]);
-        l1 += (sc[0][2] + sc[0][3]) + (sc[1][2] + sc[1][3]);
-        const uint32_t pf[4] = {pack_h2(sc[0][0], sc[0][1]), pack_h2(sc[0][2], sc[0][3]), pack_h2(sc[1][0], sc[1][1]),
-                                pack_h2(sc[1][2], sc[1][3])};
-        // values: the codes of two keys side by side in each byte
+        pf[n][0] = turned(pack_h2(sc[n][0], sc[n][1]));
+        pf[n][1] = turned(pack_h2(sc[n][2], sc[n][3]));
+      }
+      // values: the codes of two keys side by side in each byte
 #pragma unroll
-        for (int x = 0; x < F::VW; ++x) {
-          const int sh = 8 * (x / 2);
-          const uint32_t fa = scales2((rv.s[0] >> sh & 0xFFu) | (rv.s[1] >> sh & 0xFFu) << 8);
-          const uint32_t fb = scales2((rv.s[2] >> sh & 0xFFu) | (rv.s[3] >> sh & 0xFFu) << 8);
-          const uint32_t a0 = rv.w[0][x], a1 = rv.w[1][x], b0 = rv.w[2][x], b1 = rv.w[3][x];
-          uint32_t even_a[4], odd_a[4], even_b[4], odd_b[4];
-          codes8((a0 & 0x0F0F0F0Fu) | (a1 << 4 & 0xF0F0F0F0u), even_a);
-          codes8((b0 & 0x0F0F0F0Fu) | (b1 << 4 & 0xF0F0F0F0u), even_b);
+      for (int y = 0; y < F::VW; ++y) {
+        const int sh = 8 * (y / 2);
+        const uint32_t fa = scales2((rv.s[0] >> sh & 0xFFu) | (rv.s[1] >> sh & 0xFFu) << 8);
+        const uint32_t fb = scales2((rv.s[2] >> sh & 0xFFu) | (rv.s[3] >> sh & 0xFFu) << 8);
+        const uint32_t a0 = rv.w[0][y], a1 = rv.w[1][y], b0 = rv.w[2][y], b1 = rv.w[3][y];
+        uint32_t even_a[4], odd_a[4], even_b[4], odd_b[4];
+        codes8((a0 & 0x0F0F0F0Fu) | (a1 << 4 & 0xF0F0F0F0u), even_a);
+        codes8((a0 >> 4 & 0x0F0F0F0Fu) | (a1 & 0xF0F0F0F0u), odd_a);
+        codes8((b0 & 0x0F0F0F0Fu) | (b1 << 4 & 0xF0F0F0F0u), even_b);
+        codes8((b0 >> 4 & 0x0F0F0F0Fu) | (b1 & 0xF0F0F0F0u), odd_b);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mma(o[8 * x + 2 * e], pf, h2_mul(even_a[e], fa), h2_mul(even_b[e], fb));
-          codes8((a0 >> 4 & 0x0F0F0F0Fu) | (a1 & 0xF0F0F0F0u), odd_a);
-          codes8((b0 >> 4 & 0x0F0F0F0Fu) | (b1 & 0xF0F0F0F0u), odd_b);
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t v0 = h2_mul(even_a[e], fa), v1 = h2_mul(odd_a[e], fa), v2 = h2_mul(even_b[e], fb),
+                         v3 = h2_mul(odd_b[e], fb);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mma(o[8 * x + 2 * e + 1], pf, h2_mul(odd_a[e], fa), h2_mul(odd_b[e], fb));
+          for (int n = 0; n < NT; ++n) mma(o[4 * y + e][n], v0, v1, v2, v3, pf[n][0], pf[n][1]);
         }
       }
     }
     copies_wait<0>();
 
     // the four warps' parts
-#pragma unroll
-    for (int x = 1; x < 4; x <<= 1) {
-      l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, x);
-      l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, x);
-    }
     __syncthreads();  // the rings are read
-    if (q == 0) {
-      ms[warp * 16 + g] = m0;
-      ms[warp * 16 + 8 + g] = m1;
-      ls[warp * 16 + g] = l0;
-      ls[warp * 16 + 8 + g] = l1;
-    }
-    float* mine = os + warp * 16 * F::ROW;
+    float* mine = os + warp * ROWS * F::O_ROW;
 #pragma unroll
-    for (int i = 0; i < F::VN; ++i)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) mine[(g + 8 * (e / 2)) * F::ROW + 9 * i + 2 * q + e % 2] = o[i][e];
+      for (int e = 0; e < 2; ++e) {
+        float sum = l[n][e];
+#pragma unroll
+        for (int s = 4; s < 32; s <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
+        const int row = 8 * n + 2 * q + e;
+        if (g == 0) {
+          ms[warp * ROWS + row] = m[n][e];
+          ls[warp * ROWS + row] = sum;
+        }
+#pragma unroll
+        for (int y = 0; y < F::VN / 2; ++y)
+          *reinterpret_cast<float2*>(mine + row * F::O_ROW + g * F::VN + 2 * y) = make_float2(o[y][n][e], o[y][n][2 + e]);
+      }
     __syncthreads();
     const bool whole = s_begin == 0 && s_end == keys.steps();
     const int slot = 2 * blockIdx.x + (s_begin == 0 ? 1 : 0);  // begun here, or begun before
-    float* part = a.ws + few_head_floats(DP) + (int64_t)slot * few_slot_floats(DP);
+    float* part = a.ws + F::HEADS + (int64_t)slot * F::SLOT;
     for (int x = threadIdx.x; x < rows * c.dim; x += kThreadsFew) {
-      const int row = x / c.dim, d = x % c.dim, at = row * F::ROW + 9 * (d % F::VN) + d / F::VN;
+      const int row = x / c.dim, d = x % c.dim;
       float top = ms[row];
 #pragma unroll
-      for (int i = 1; i < kWarps; ++i) top = fmaxf(top, ms[i * 16 + row]);
-      float sum = 0.0f, l = 0.0f;
+      for (int i = 1; i < kWarps; ++i) top = fmaxf(top, ms[i * ROWS + row]);
+      float sum = 0.0f, total = 0.0f;
 #pragma unroll
       for (int i = 0; i < kWarps; ++i) {
-        const float mi = ms[i * 16 + row], f = mi == top ? 1.0f : layer::ex2(mi - top);
-        sum = fmaf(os[i * 16 * F::ROW + at], f, sum);
-        l = fmaf(ls[i * 16 + row], f, l);
+        const float mi = ms[i * ROWS + row], y = mi == top ? 1.0f : layer::ex2(mi - top);
+        sum = fmaf(os[(i * ROWS + row) * F::O_ROW + d], y, sum);
+        total = fmaf(ls[i * ROWS + row], y, total);
       }
       if (whole) {
-        finish(a, seq, h, 16 * r + row, d, sum, top, l, alpha_v);
+        finish(a, seq, h, ROWS * r + row, d, sum, top, total, alpha_v);
       } else {
         part[row * DP + d] = sum;
         if (d == 0) {
-          part[16 * DP + row] = top;
-          part[16 * DP + 16 + row] = l;
+          part[ROWS * DP + row] = top;
+          part[ROWS * DP + ROWS + row] = total;
         }
       }
     }
     if (!whole && s_begin == 0 && threadIdx.x == 0)
-      heads[blockIdx.x] = {pieces.holds(u1 - 1), seq.first, h, r, rows};
+      heads[blockIdx.x] = {pieces.holds(u1 - 1), seq.first, h, ROWS * r, rows};
     w = u0 + s_end;
   }
 }
 
 // The pieces of each unit that is cut, added in order: block (i, y) takes the unit that begins in
 // piece i and does not end there, rows y, y + gridDim.y, ..
-template <int DP>
+template <int DP, int NT>
 __global__ void __launch_bounds__(DP) few_join_kernel(AttendArgs a) {
+  using F = Few<DP, NT>;
   after_previous();
   const FewHead head = reinterpret_cast<const FewHead*>(a.ws)[blockIdx.x];
   if (head.last < 0) return;
-  const float* slots = a.ws + few_head_floats(DP);
-  const int64_t n = few_slot_floats(DP);
+  const float* slots = a.ws + F::HEADS;
   Sequence seq = {head.first, 0, 0};
   const float alpha_v = a.c.alpha[1];
   const int d = threadIdx.x;
   for (int row = blockIdx.y; row < head.rows; row += gridDim.y) {
-    const float* p = slots + (2 * (int64_t)blockIdx.x + 1) * n;
-    float top = p[16 * DP + row], l = p[16 * DP + 16 + row], sum = d < a.c.dim ? p[row * DP + d] : 0.0f;
+    const float* p = slots + (2 * (int64_t)blockIdx.x + 1) * F::SLOT;
+    float top = p[F::ROWS * DP + row], l = p[F::ROWS * DP + F::ROWS + row], sum = d < a.c.dim ? p[row * DP + d] : 0.0f;
 #pragma unroll 4
     for (int j = blockIdx.x + 1; j <= head.last; ++j) {
-      const float* x = slots + 2 * (int64_t)j * n;
-      const float mj = x[16 * DP + row], lj = x[16 * DP + 16 + row], oj = d < a.c.dim ? x[row * DP + d] : 0.0f;
+      const float* x = slots + 2 * (int64_t)j * F::SLOT;
+      const float mj = x[F::ROWS * DP + row], lj = x[F::ROWS * DP + F::ROWS + row], oj = d < a.c.dim ? x[row * DP + d] : 0.0f;
       const float next = fmaxf(top, mj);
       const float f = top == next ? 1.0f : layer::ex2(top - next), fj = mj == next ? 1.0f : layer::ex2(mj - next);
       sum = fmaf(oj, fj, sum * f);
       l = fmaf(lj, fj, l * f);
       top = next;
     }
-    if (d < a.c.dim) finish(a, seq, head.head, 16 * head.tile + row, d, sum, top, l, alpha_v);
+    if (d < a.c.dim) finish(a, seq, head.head, head.row + row, d, sum, top, l, alpha_v);
   }
 }
 
-template <int DP, bool FULL>
+template <int DP, int NT, bool FULL>
 cudaError_t launch(const AttendArgs& a, cudaStream_t s) {
-  using F = Few<DP>;
-  cudaError_t e = cudaFuncSetAttribute(few_kernel<DP, FULL>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM);
+  using F = Few<DP, NT>;
+  cudaError_t e = cudaFuncSetAttribute(few_kernel<DP, NT, FULL>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM);
   if (e != cudaSuccess) return e;
-  constexpr int G = few_blocks(DP);
-  e = launch_early(few_kernel<DP, FULL>, dim3((unsigned)G), kThreadsFew, F::SMEM, s, a);
+  e = launch_early(few_kernel<DP, NT, FULL>, dim3((unsigned)F::BLOCKS), kThreadsFew, F::SMEM, s, a);
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)a.c.T * a.group;
-  return launch_early(few_join_kernel<DP>, dim3((unsigned)G, (unsigned)(rows < 4 ? rows : 4)), DP, 0, s, a);
+  return launch_early(few_join_kernel<DP, NT>, dim3((unsigned)F::BLOCKS, (unsigned)(rows < 4 ? rows : 4)), DP, 0, s, a);
 }
-template <int DP>
+template <int DP, int NT>
 cudaError_t by_dim(const AttendArgs& a, cudaStream_t s) {
-  return a.c.dim == DP ? launch<DP, true>(a, s) : launch<DP, false>(a, s);
+  return a.c.dim == DP ? launch<DP, NT, true>(a, s) : launch<DP, NT, false>(a, s);
+}
+
+// Tiles of 8, 16 or 32 rows (for D > 128 not 32: o would not fit the registers): the fewest that
+// hold an average sequence's, so that a key is unpacked once for all of them.  Sequences with more
+// take several tiles.
+static int tiles_of(int64_t T, int group, int dim, int64_t sequences) {
+  const int64_t rows = (T + sequences - 1) / sequences * group;
+  return rows <= 8 ? 1 : rows <= 16 || dim > 128 ? 2 : 4;
 }
 
 }  // namespace attention
 
+int64_t attend_few_workspace(int64_t T, int group, int dim, int64_t sequences) {
+  using namespace attention;
+  const int n = tiles_of(T, group, dim, sequences);
+  const int64_t floats = dim <= 64    ? (n == 1 ? Few<64, 1>::FLOATS : n == 2 ? Few<64, 2>::FLOATS : Few<64, 4>::FLOATS)
+                         : dim <= 128 ? (n == 1 ? Few<128, 1>::FLOATS : n == 2 ? Few<128, 2>::FLOATS : Few<128, 4>::FLOATS)
+                                      : (n == 1 ? Few<256, 1>::FLOATS : Few<256, 2>::FLOATS);
+  return floats * (int64_t)sizeof(float);
+}
+
 cudaError_t launch_attend_few(const AttendArgs& a, cudaStream_t s) {
   using namespace attention;
-  if (a.c.dim <= 64) return by_dim<64>(a, s);
-  if (a.c.dim <= 128) return by_dim<128>(a, s);
-  return by_dim<256>(a, s);
+  const int n = tiles_of(a.c.T, a.group, a.c.dim, a.c.sequences);
+  if (a.c.dim <= 64) return n == 1 ? by_dim<64, 1>(a, s) : n == 2 ? by_dim<64, 2>(a, s) : by_dim<64, 4>(a, s);
+  if (a.c.dim <= 128) return n == 1 ? by_dim<128, 1>(a, s) : n == 2 ? by_dim<128, 2>(a, s) : by_dim<128, 4>(a, s);
+  return n == 1 ? by_dim<256, 1>(a, s) : by_dim<256, 2>(a, s);
 }
 
 }  // namespace nvfp4
