@@ -23,9 +23,8 @@ __device__ __forceinline__ bool is_few(const AttendArgs& a, const Sequence& s) {
 
 // Whether the query at position p sees key j (0 <= j).
 __device__ __forceinline__ bool visible(const AttendArgs& a, const Sequence& s, int p, int j) {
-  if (j >= s.length) return false;
-  if (!a.causal) return true;
-  return j <= p && (a.window == 0 || p - j < a.window || j < a.sinks);
+  const bool near = (a.window == 0) | (p - j < a.window) | (j < a.sinks);  // without branches
+  return (j < s.length) & (!a.causal | ((j <= p) & near));
 }
 
 // The keys that any of a tile of rows sees, in chunks of CH: the first `sinks` chunks, then

@@ -164,40 +164,43 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A lane's share of the copies of one chunk.
+// A lane's share of the copies of one chunk: what it adds to where the chunk begins.
 template <int DP, bool FULL>
 struct Copies {
   using F = Few<DP, 1>;
-  uint64_t from[F::COPIES];  // offsets from the chunk's first row of codes
-  uint32_t to[F::COPIES];    // .. and in a stage of the ring
-  int lane;
-  __device__ __forceinline__ Copies(const CacheView& c, int lane_) : lane(lane_) {
+  const uint8_t* codes[F::COPIES];  // keys'
+  int64_t to_values;                // .. and values' from there
+  const uint8_t* scales;            // keys' in lanes 0-15, values' in the others
+  uint32_t code_at[F::COPIES], scale_at;  // in a stage of the ring; ~0: none
+  __device__ __forceinline__ Copies(const CacheView& c, int lane, int h, bool dense) {
     const int pieces = FULL ? DP / 32 : c.dim / 32;  // of a row
 #pragma unroll
     for (int i = 0; i < F::COPIES; ++i) {
       const int x = lane + 32 * i, row = x / pieces, piece = x % pieces;
-      from[i] = (uint64_t)row * c.cr + 16 * piece;
-      to[i] = row < 16 ? row * F::CODE_ROW + 16 * piece : ~0u;
+      codes[i] = c.kc + h * c.ch + (uint64_t)row * c.cr + 16 * piece;
+      code_at[i] = row < 16 ? row * F::CODE_ROW + 16 * piece : ~0u;
     }
+    to_values = c.vc - c.kc;
+    const int half = lane / 16, x = lane % 16, bytes = FULL ? DP / 16 : c.dim / 16;
+    scales = (half ? c.vs : c.ks) + h * c.sh + (dense ? (uint64_t)(16 * x) : (uint64_t)x * c.sr);
+    scale_at = 2 * F::CODES + half * F::SCALES + (dense ? 16 * x : x * bytes);
+    if (dense && x >= bytes) scale_at = ~0u;
   }
-  // kc .. vs: where the chunk begins; dense: its 16 rows of scales lie side by side, at 16 bytes
-  __device__ __forceinline__ void issue(const CacheView& c, const uint8_t* kc, const uint8_t* ks, const uint8_t* vc,
-                                        const uint8_t* vs, uint32_t stage, bool dense) const {
+  // code, scale: the chunk's offsets; dense: its 16 rows of scales lie side by side, at 16 bytes
+  __device__ __forceinline__ void issue(const CacheView& c, uint64_t code, uint64_t scale, uint32_t stage, bool dense) const {
 #pragma unroll
     for (int i = 0; i < F::COPIES; ++i) {
-      if (!FULL && to[i] == ~0u) continue;
-      copy16(stage + to[i], kc + from[i]);
-      copy16(stage + F::CODES + to[i], vc + from[i]);
+      if (!FULL && code_at[i] == ~0u) continue;
+      const uint8_t* p = codes[i] + code;
+      copy16(stage + code_at[i], p);
+      copy16(stage + F::CODES + code_at[i], p + to_values);
     }
-    const int half = lane / 16, x = lane % 16, row = FULL ? DP / 16 : c.dim / 16;
-    const uint8_t* s = half ? vs : ks;
-    const uint32_t at = stage + 2 * F::CODES + half * F::SCALES;
     if (dense) {
-      if (x < row) copy16(at + 16 * x, s + 16 * x);
+      if ((FULL && DP == 256) || scale_at != ~0u) copy16(stage + scale_at, scales + scale);
     } else {
-      const uint8_t* p = s + (uint64_t)x * c.sr;
-      for (int i = 0; i < row; i += 2)
-        asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + x * row + i), "h"(*reinterpret_cast<const uint16_t*>(p + i)) : "memory");
+      const uint8_t* p = scales + scale;
+      for (int i = 0; i < (FULL ? DP / 16 : c.dim / 16); i += 2)
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(stage + scale_at + i), "h"(*reinterpret_cast<const uint16_t*>(p + i)) : "memory");
     }
   }
 };
@@ -224,9 +227,11 @@ struct Walk {
   }
 };
 
-// A lane's part of a row's queries in fp16; returns what undoes their scaling.
+// A lane's part of a row's queries in fp16, their sign turned if `minus`; returns what undoes their
+// scaling.
 template <int DP>
-__device__ __forceinline__ float load_query(const AttendArgs& a, bool vec, bool on, int64_t token, int head, uint32_t* h) {
+__device__ __forceinline__ float load_query(const AttendArgs& a, bool vec, bool on, int64_t token, int head, bool minus,
+                                            uint32_t* h) {
   constexpr int N = DP / 4;  // this lane's values
   const int q = threadIdx.x % 4, D = a.c.dim;
   const bf16* p = static_cast<const bf16*>(a.q.p) + token * a.q.ts + (int64_t)head * a.q.hs + q * N;
@@ -243,7 +248,7 @@ __device__ __forceinline__ float load_query(const AttendArgs& a, bool vec, bool 
   for (int i = 0; i < N / 2; ++i) top = larger_magnitude(top, h[i]);
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-  const float down = query_down(top);
+  const float down = minus ? -query_down(top) : query_down(top);
 #pragma unroll
   for (int i = 0; i < N / 2; ++i) h[i] = pack_h2(bf16_lo(h[i]) * down, bf16_hi(h[i]) * down);
   return query_up(top);
@@ -305,7 +310,6 @@ __global__ void __launch_bounds__(kThreadsFew, Few<DP, NT>::PER_SM) few_kernel(A
   const bool vec = rows_at_16(a.q);
   const bool dense = c.sr == c.dim / 16 &&
                      (reinterpret_cast<uintptr_t>(c.ks) | reinterpret_cast<uintptr_t>(c.vs) | c.sp | c.sh) % 16 == 0;
-  const Copies<DP, FULL> copies(c, lane);
 
   while (w < w_end) {
     // the unit that w is in
@@ -336,10 +340,12 @@ __global__ void __launch_bounds__(kThreadsFew, Few<DP, NT>::PER_SM) few_kernel(A
       const int row = ROWS * r + 8 * n + g;
       const bool on = 8 * n + g < rows;
       const float up = load_query<DP>(a, vec, on, (int64_t)seq.first + (on ? row / a.group : 0),
-                                      h * a.group + (on ? row % a.group : 0), qf[n]);
+                                      h * a.group + (on ? row % a.group : 0), scale < 0.0f, qf[n]);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        f[n][e] = scale * __shfl_sync(0xFFFFFFFFu, up, 8 * q + 4 * e);
+        // scores to base 2 are f * S with f > 0: the scale's sign is in the queries, and where it vanishes
+        // f is the smallest number, so that -Inf stays -Inf
+        f[n][e] = fmaxf(fabsf(scale) * __shfl_sync(0xFFFFFFFFu, up, 8 * q + 4 * e), 0x1p-126f);
         const int x = 8 * n + 2 * q + e;
         p[n][e] = seq.length - seq.rows + (x < rows ? (ROWS * r + x) / a.group : 0);
       }
@@ -356,17 +362,17 @@ __global__ void __launch_bounds__(kThreadsFew, Few<DP, NT>::PER_SM) few_kernel(A
     }
 
     float o[F::VN / 2][NT][4] = {};
-    float m[NT][2], l[NT][2];
+    float m[NT][2], z[NT][2], l[NT][2];  // z: -m, 0 while nothing is seen
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       m[n][0] = m[n][1] = -INFINITY;
-      l[n][0] = l[n][1] = 0.0f;
+      z[n][0] = z[n][1] = l[n][0] = l[n][1] = 0.0f;
     }
     // This warp's chunks are those of i, i + 4, ..; the copies are STAGES - 1 of them ahead, the
     // page of the next to be copied one more.
     const int per_page = c.page_size / 16, i_end = min(keys.count, 4 * s_end);
     const int32_t* table = c.table + (int64_t)b * c.table_stride;
-    const uint8_t *kc = c.kc + h * c.ch, *vc = c.vc + h * c.ch, *ks = c.ks + h * c.sh, *vs = c.vs + h * c.sh;
+    const Copies<DP, FULL> copies(c, lane, h, dense);
     Walk at;
     int ahead = 4 * s_begin + warp, page = -1, put = 0;
     uint32_t there = 0;  // by stage: whether the chunk's page is in range
@@ -380,7 +386,7 @@ __global__ void __launch_bounds__(kThreadsFew, Few<DP, NT>::PER_SM) few_kernel(A
         if ((uint32_t)page < (uint32_t)c.pages) {
           const uint32_t pg = page, row = 16 * at.in;
           const uint64_t codes = (uint64_t)pg * c.cp + (uint64_t)row * c.cr, scales = (uint64_t)pg * c.sp + (uint64_t)row * c.sr;
-          copies.issue(c, kc + codes, ks + scales, vc + codes, vs + scales, ring_at + put * F::STAGE, dense);
+          copies.issue(c, codes, scales, ring_at + put * F::STAGE, dense);
           there |= 1u << put;
         } else {
           set_status(c.status, NVFP4_ERR_INDEX);
@@ -433,27 +439,25 @@ __global__ void __launch_bounds__(kThreadsFew, Few<DP, NT>::PER_SM) few_kernel(A
         }
       }
       take_values<DP, FULL>(stage, c.dim, g, q, rv);
-      const bool part = !keys.all_visible(first);
+      if (!keys.all_visible(first)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            sc[n][e] = visible(a, seq, p[n][e & 1], first + g + 8 * (e / 2)) ? sc[n][e] : -INFINITY;
+        // what lies behind the end is no number: its weight is 0, and so is its scale
+#pragma unroll
+        for (int t = 0; t < 4; ++t) rv.s[t] = first + 8 * (t / 2) + 2 * q + t % 2 < seq.length ? rv.s[t] : 0;
+      }
       bool up = false;
       float x[NT][2];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          sc[n][e] *= f[n][e & 1];
-          if (part && !visible(a, seq, p[n][e & 1], first + g + 8 * (e / 2))) sc[n][e] = -INFINITY;
-        }
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          x[n][e] = fmaxf(sc[n][e], sc[n][2 + e]);
+          x[n][e] = fmaxf(sc[n][e], sc[n][2 + e]) * f[n][e];
           up |= x[n][e] > m[n][e] + 8.0f;
         }
-      }
-      if (part) {  // what lies behind the end is no number: its weight is 0, and so is its scale
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-          if (first + 8 * (t / 2) + 2 * q + t % 2 >= seq.length) rv.s[t] = 0;
-      }
       if (__any_sync(0xFFFFFFFFu, up)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -466,6 +470,7 @@ __global__ void __launch_bounds__(kThreadsFew, Few<DP, NT>::PER_SM) few_kernel(A
             top = fmaxf(top, m[n][e]);
             d[e] = top == m[n][e] ? 1.0f : layer::ex2(m[n][e] - top);
             m[n][e] = top;
+            z[n][e] = top == -INFINITY ? 0.0f : -top;
             l[n][e] *= d[e];
           }
 #pragma unroll
@@ -478,10 +483,9 @@ __global__ void __launch_bounds__(kThreadsFew, Few<DP, NT>::PER_SM) few_kernel(A
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          sc[n][e] = layer::ex2(sc[n][e] - (m[n][e & 1] == -INFINITY ? 0.0f : m[n][e & 1]));
-          l[n][e & 1] += sc[n][e];
-        }
+        for (int e = 0; e < 4; ++e) sc[n][e] = layer::ex2(fmaf(sc[n][e], f[n][e & 1], z[n][e & 1]));
+        l[n][0] += sc[n][0] + sc[n][2];
+        l[n][1] += sc[n][1] + sc[n][3];
         pf[n][0] = turned(pack_h2(sc[n][0], sc[n][1]));
         pf[n][1] = turned(pack_h2(sc[n][2], sc[n][3]));
       }
@@ -560,32 +564,31 @@ __global__ void __launch_bounds__(kThreadsFew, Few<DP, NT>::PER_SM) few_kernel(A
 }
 
 // The pieces of each unit that is cut, added in order: block (i, y) takes the unit that begins in
-// piece i and does not end there, rows y, y + gridDim.y, ..
+// piece i and does not end there, and of that row y.
 template <int DP, int NT>
 __global__ void __launch_bounds__(DP) few_join_kernel(AttendArgs a) {
   using F = Few<DP, NT>;
   after_previous();
   const FewHead head = reinterpret_cast<const FewHead*>(a.ws)[blockIdx.x];
-  if (head.last < 0) return;
+  const int row = blockIdx.y;
+  if (head.last < 0 || row >= head.rows) return;
   const float* slots = a.ws + F::HEADS;
   Sequence seq = {head.first, 0, 0};
   const float alpha_v = a.c.alpha[1];
   const int d = threadIdx.x;
-  for (int row = blockIdx.y; row < head.rows; row += gridDim.y) {
-    const float* p = slots + (2 * (int64_t)blockIdx.x + 1) * F::SLOT;
-    float top = p[F::ROWS * DP + row], l = p[F::ROWS * DP + F::ROWS + row], sum = d < a.c.dim ? p[row * DP + d] : 0.0f;
+  const float* p = slots + (2 * (int64_t)blockIdx.x + 1) * F::SLOT;
+  float top = p[F::ROWS * DP + row], l = p[F::ROWS * DP + F::ROWS + row], sum = d < a.c.dim ? p[row * DP + d] : 0.0f;
 #pragma unroll 4
-    for (int j = blockIdx.x + 1; j <= head.last; ++j) {
-      const float* x = slots + 2 * (int64_t)j * F::SLOT;
-      const float mj = x[F::ROWS * DP + row], lj = x[F::ROWS * DP + F::ROWS + row], oj = d < a.c.dim ? x[row * DP + d] : 0.0f;
-      const float next = fmaxf(top, mj);
-      const float f = top == next ? 1.0f : layer::ex2(top - next), fj = mj == next ? 1.0f : layer::ex2(mj - next);
-      sum = fmaf(oj, fj, sum * f);
-      l = fmaf(lj, fj, l * f);
-      top = next;
-    }
-    if (d < a.c.dim) finish(a, seq, head.head, head.row + row, d, sum, top, l, alpha_v);
+  for (int j = blockIdx.x + 1; j <= head.last; ++j) {
+    const float* x = slots + 2 * (int64_t)j * F::SLOT;
+    const float mj = x[F::ROWS * DP + row], lj = x[F::ROWS * DP + F::ROWS + row], oj = d < a.c.dim ? x[row * DP + d] : 0.0f;
+    const float next = fmaxf(top, mj);
+    const float f = top == next ? 1.0f : layer::ex2(top - next), fj = mj == next ? 1.0f : layer::ex2(mj - next);
+    sum = fmaf(oj, fj, sum * f);
+    l = fmaf(lj, fj, l * f);
+    top = next;
   }
+  if (d < a.c.dim) finish(a, seq, head.head, head.row + row, d, sum, top, l, alpha_v);
 }
 
 template <int DP, int NT, bool FULL>
@@ -596,7 +599,7 @@ cudaError_t launch(const AttendArgs& a, cudaStream_t s) {
   e = launch_early(few_kernel<DP, NT, FULL>, dim3((unsigned)F::BLOCKS), kThreadsFew, F::SMEM, s, a);
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)a.c.T * a.group;
-  return launch_early(few_join_kernel<DP, NT>, dim3((unsigned)F::BLOCKS, (unsigned)(rows < 4 ? rows : 4)), DP, 0, s, a);
+  return launch_early(few_join_kernel<DP, NT>, dim3((unsigned)F::BLOCKS, (unsigned)(rows < F::ROWS ? rows : F::ROWS)), DP, 0, s, a);
 }
 template <int DP, int NT>
 cudaError_t by_dim(const AttendArgs& a, cudaStream_t s) {
