@@ -44,13 +44,13 @@ struct Keys {
 };
 
 // Rows first_row .. first_row + n - 1 of a sequence's rows of one key head.
-template <int CH>
-__device__ __forceinline__ Keys<CH> rows_keys(const AttendArgs& a, const Sequence& s, int64_t first_row, int n) {
+template <int CH, typename Index>
+__device__ __forceinline__ Keys<CH> rows_keys(const AttendArgs& a, const Sequence& s, Index first_row, int n) {
   Keys<CH> k = {0, 0, 0, 0, s.length, 0};
   int end = s.length;
   if (a.causal) {
     const int before = s.length - s.rows;  // position of the first new token, >= -2^31 + 1
-    const int p0 = before + (int)(first_row / a.group), p1 = before + (int)((first_row + n - 1) / a.group);
+    const int p0 = before + (int)(first_row / (Index)a.group), p1 = before + (int)((first_row + (Index)(n - 1)) / (Index)a.group);
     end = min(end, p1 + 1);
     k.all_to = min(s.length, p0 + 1);
     if (a.window) {
@@ -61,7 +61,7 @@ __device__ __forceinline__ Keys<CH> rows_keys(const AttendArgs& a, const Sequenc
       k.first = max(low / CH, k.sinks);
     }
   }
-  k.count = k.sinks + max(0, (int)(((int64_t)max(end, 0) + (CH - 1)) / CH) - k.first);
+  k.count = k.sinks + max(0, (int)(((uint32_t)max(end, 0) + (CH - 1)) / CH) - k.first);
   return k;
 }
 // lse of one row from its maximum and sum to base 2, both -Inf and 0 where it sees nothing.
@@ -69,16 +69,6 @@ __device__ __forceinline__ float row_lse(float top, float l) {
   if (l == 0.0f) return -INFINITY;
   return top == -INFINITY ? l : (top + log2f(l)) * 0.6931471805599453f;  // NaN leaves the maximum alone
 }
-// One value of o and, with the first, lse of one row from its sums (unnormalised).
-__device__ __forceinline__ void finish(const AttendArgs& a, const Sequence& s, int head, int row, int d, float sum,
-                                       float top, float l, float alpha_v) {
-  const int64_t t = (int64_t)s.first + row / a.group;
-  const int h = head * a.group + row % a.group;
-  const float share = l != 0.0f ? alpha_v / l : 0.0f;  // nothing seen: zeros
-  static_cast<bf16*>(a.o.p)[t * a.o.ts + (int64_t)h * a.o.hs + d] = layer::from_f32<bf16>(sum * share);
-  if (d == 0 && a.lse) a.lse[t * a.Hq + h] = row_lse(top, l);
-}
-
 // ---- fp16 products --------------------------------------------------------------------------
 
 __device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
@@ -139,7 +129,15 @@ struct FewHead {
 // The line cut into G pieces, the first total % G of them a step longer.
 struct Pieces {
   int64_t each, longer;
-  __device__ __forceinline__ Pieces(int64_t total, int64_t G) : each(total / G), longer(total % G) {}
+  __device__ __forceinline__ Pieces(int64_t total, int G) {
+    if (total <= UINT32_MAX) {  // a division of 64 bits takes about a hundred instructions
+      each = (uint32_t)total / (uint32_t)G;
+      longer = (uint32_t)total % (uint32_t)G;
+    } else {
+      each = total / G;
+      longer = total % G;
+    }
+  }
   __device__ __forceinline__ int64_t begin(int64_t i) const { return i * each + (i < longer ? i : longer); }
   __device__ __forceinline__ int holds(int64_t step) const {
     const int64_t cut = longer * (each + 1);

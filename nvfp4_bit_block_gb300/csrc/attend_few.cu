@@ -2,7 +2,7 @@
 // that share a key head) to the NVFP4 cache: the next token, or a few drafted ones.
 //
 // The cache's bytes are the floor: 9/16 byte per value, read once for all heads of a group.
-// A unit of work is a tile of 8, 16 or 32 rows of one key head; its visible keys are cut into
+// A unit of work is a tile of 8 or 16 rows of one key head; its visible keys are cut into
 // steps of 64 and the steps of all units form one line that is cut into equal pieces, one per
 // block, so that one long sequence and many short ones fill the GPU alike.  Pieces that are part
 // of a unit leave (m, l, o) in the workspace and a second kernel joins them in order.
@@ -56,7 +56,7 @@ struct Few {
   static constexpr int QS = ML + 2 * kWarps * ROWS * 4;
   static constexpr int SMEM = QS + (Q_SHARED ? DP / 32 * NT * 32 * 16 : 0);
   // Blocks: as many as an SM holds of them by registers, on every SM.
-  static constexpr int PER_SM = DP == 64 ? (NT == 1 ? 5 : NT == 2 ? 4 : 3) : DP == 128 ? (NT == 1 ? 4 : NT == 2 ? 3 : 2) : NT == 1 ? 3 : 2;
+  static constexpr int PER_SM = DP == 64 ? (NT == 1 ? 5 : 4) : DP == 128 ? (NT == 1 ? 4 : 3) : NT == 1 ? 3 : 2;
   static constexpr int BLOCKS = 152 * PER_SM;
   // The workspace: a FewHead for each block, then two slots (o, m and l of a tile) for each.
   static constexpr int64_t SLOT = ROWS * DP + 2 * ROWS;
@@ -258,7 +258,7 @@ __device__ __forceinline__ float load_query(const AttendArgs& a, bool vec, bool 
 // tiles make for one key head.
 template <int ROWS>
 __device__ __forceinline__ Keys<16> tile_keys(const AttendArgs& a, const Sequence& s, int tile) {
-  return rows_keys<16>(a, s, ROWS * tile, min(ROWS, s.rows * a.group - ROWS * tile));
+  return rows_keys<16, uint32_t>(a, s, ROWS * tile, min(ROWS, s.rows * a.group - ROWS * tile));
 }
 template <int ROWS>
 __device__ __forceinline__ int64_t sequence_steps(const AttendArgs& a, const Sequence& s) {
@@ -308,6 +308,7 @@ __global__ void __launch_bounds__(kThreadsFew, Few<DP, NT>::PER_SM) few_kernel(A
   int64_t base = line.base;  // where sequence b begins on the line
   const float alpha_v = c.alpha[1], scale = a.scale * c.alpha[0] * layer::kLog2e;
   const bool vec = rows_at_16(a.q);
+  const bool o_pairs = reinterpret_cast<uintptr_t>(a.o.p) % 4 == 0 && a.o.ts % 2 == 0 && a.o.hs % 2 == 0;
   const bool dense = c.sr == c.dim / 16 &&
                      (reinterpret_cast<uintptr_t>(c.ks) | reinterpret_cast<uintptr_t>(c.vs) | c.sp | c.sh) % 16 == 0;
 
@@ -319,7 +320,8 @@ __global__ void __launch_bounds__(kThreadsFew, Few<DP, NT>::PER_SM) few_kernel(A
       load_few(a, ++b, seq);
       per_head = sequence_steps<ROWS>(a, seq);
     }
-    const int h = (int)((w - base) / per_head);
+    const int64_t in = w - base;  // of the sequence
+    const int h = (in | per_head) <= UINT32_MAX ? (int)((uint32_t)in / (uint32_t)per_head) : (int)(in / per_head);
     int64_t u0 = base + h * per_head;
     int r = 0;
     Keys<16> keys = tile_keys<ROWS>(a, seq, 0);
@@ -535,26 +537,52 @@ __global__ void __launch_bounds__(kThreadsFew, Few<DP, NT>::PER_SM) few_kernel(A
     const bool whole = s_begin == 0 && s_end == keys.steps();
     const int slot = 2 * blockIdx.x + (s_begin == 0 ? 1 : 0);  // begun here, or begun before
     float* part = a.ws + F::HEADS + (int64_t)slot * F::SLOT;
-    for (int x = threadIdx.x; x < rows * c.dim; x += kThreadsFew) {
-      const int row = x / c.dim, d = x % c.dim;
-      float top = ms[row];
+    // a thread for each row: what its warps' parts count
+    if (threadIdx.x < rows) {
+      const int row = threadIdx.x;
+      float mi[kWarps], top = -INFINITY, total = 0.0f;
 #pragma unroll
-      for (int i = 1; i < kWarps; ++i) top = fmaxf(top, ms[i * ROWS + row]);
-      float sum = 0.0f, total = 0.0f;
+      for (int i = 0; i < kWarps; ++i) top = fmaxf(top, mi[i] = ms[i * ROWS + row]);
 #pragma unroll
       for (int i = 0; i < kWarps; ++i) {
-        const float mi = ms[i * ROWS + row], y = mi == top ? 1.0f : layer::ex2(mi - top);
-        sum = fmaf(os[(i * ROWS + row) * F::O_ROW + d], y, sum);
-        total = fmaf(ls[i * ROWS + row], y, total);
+        mi[i] = mi[i] == top ? 1.0f : layer::ex2(mi[i] - top);
+        total = fmaf(ls[i * ROWS + row], mi[i], total);
+      }
+      float share = 1.0f;
+      if (whole) {
+        const int64_t t = (int64_t)seq.first + (ROWS * r + row) / a.group;
+        if (a.lse) a.lse[t * a.Hq + h * a.group + (ROWS * r + row) % a.group] = row_lse(top, total);
+        share = total != 0.0f ? alpha_v / total : 0.0f;  // nothing seen: zeros
+      } else {
+        part[ROWS * DP + row] = top;
+        part[ROWS * DP + ROWS + row] = total;
+      }
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) ms[i * ROWS + row] = mi[i] * share;
+    }
+    __syncthreads();
+    // two values at a time
+    for (int x = threadIdx.x; x < rows * (c.dim / 2); x += kThreadsFew) {
+      const int row = x / (c.dim / 2), d = 2 * (x - row * (c.dim / 2));
+      float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) {
+        const float2 y = *reinterpret_cast<const float2*>(os + (i * ROWS + row) * F::O_ROW + d);
+        const float z = ms[i * ROWS + row];
+        sum.x = fmaf(y.x, z, sum.x);
+        sum.y = fmaf(y.y, z, sum.y);
       }
       if (whole) {
-        finish(a, seq, h, ROWS * r + row, d, sum, top, total, alpha_v);
-      } else {
-        part[row * DP + d] = sum;
-        if (d == 0) {
-          part[ROWS * DP + row] = top;
-          part[ROWS * DP + ROWS + row] = total;
+        const int at = ROWS * r + row, t = at / a.group;
+        bf16* out = static_cast<bf16*>(a.o.p) + ((int64_t)seq.first + t) * a.o.ts + (int64_t)(h * a.group + at - t * a.group) * a.o.hs + d;
+        if (o_pairs) {
+          *reinterpret_cast<__nv_bfloat162*>(out) = __floats2bfloat162_rn(sum.x, sum.y);
+        } else {
+          out[0] = layer::from_f32<bf16>(sum.x);
+          out[1] = layer::from_f32<bf16>(sum.y);
         }
+      } else {
+        *reinterpret_cast<float2*>(part + row * DP + d) = sum;
       }
     }
     if (!whole && s_begin == 0 && threadIdx.x == 0)
@@ -563,32 +591,41 @@ __global__ void __launch_bounds__(kThreadsFew, Few<DP, NT>::PER_SM) few_kernel(A
   }
 }
 
-// The pieces of each unit that is cut, added in order: block (i, y) takes the unit that begins in
-// piece i and does not end there, and of that row y.
+// The pieces of each unit that is cut, added in order: block i takes the unit that begins in
+// piece i and does not end there, a thread four values of one of its rows.
 template <int DP, int NT>
-__global__ void __launch_bounds__(DP) few_join_kernel(AttendArgs a) {
+__global__ void __launch_bounds__(DP / 4 * 8 * NT) few_join_kernel(AttendArgs a) {
   using F = Few<DP, NT>;
   after_previous();
   const FewHead head = reinterpret_cast<const FewHead*>(a.ws)[blockIdx.x];
-  const int row = blockIdx.y;
-  if (head.last < 0 || row >= head.rows) return;
-  const float* slots = a.ws + F::HEADS;
-  Sequence seq = {head.first, 0, 0};
-  const float alpha_v = a.c.alpha[1];
-  const int d = threadIdx.x;
-  const float* p = slots + (2 * (int64_t)blockIdx.x + 1) * F::SLOT;
-  float top = p[F::ROWS * DP + row], l = p[F::ROWS * DP + F::ROWS + row], sum = d < a.c.dim ? p[row * DP + d] : 0.0f;
+  const int row = threadIdx.x / (DP / 4), d = threadIdx.x % (DP / 4) * 4;
+  if (head.last < 0 || row >= head.rows || d >= a.c.dim) return;
+  const float* p = a.ws + F::HEADS + (2 * (int64_t)blockIdx.x + 1) * F::SLOT;
+  float top = p[F::ROWS * DP + row], l = p[F::ROWS * DP + F::ROWS + row];
+  float4 sum = *reinterpret_cast<const float4*>(p + row * DP + d);
 #pragma unroll 4
   for (int j = blockIdx.x + 1; j <= head.last; ++j) {
-    const float* x = slots + 2 * (int64_t)j * F::SLOT;
-    const float mj = x[F::ROWS * DP + row], lj = x[F::ROWS * DP + F::ROWS + row], oj = d < a.c.dim ? x[row * DP + d] : 0.0f;
+    const float* x = a.ws + F::HEADS + 2 * (int64_t)j * F::SLOT;
+    const float mj = x[F::ROWS * DP + row], lj = x[F::ROWS * DP + F::ROWS + row];
+    const float4 oj = *reinterpret_cast<const float4*>(x + row * DP + d);
     const float next = fmaxf(top, mj);
     const float f = top == next ? 1.0f : layer::ex2(top - next), fj = mj == next ? 1.0f : layer::ex2(mj - next);
-    sum = fmaf(oj, fj, sum * f);
+    sum.x = fmaf(oj.x, fj, sum.x * f);
+    sum.y = fmaf(oj.y, fj, sum.y * f);
+    sum.z = fmaf(oj.z, fj, sum.z * f);
+    sum.w = fmaf(oj.w, fj, sum.w * f);
     l = fmaf(lj, fj, l * f);
     top = next;
   }
-  if (d < a.c.dim) finish(a, seq, head.head, head.row + row, d, sum, top, l, alpha_v);
+  const int at = head.row + row;
+  const int64_t t = (int64_t)head.first + at / a.group;
+  const int h = head.head * a.group + at % a.group;
+  const float share = l != 0.0f ? a.c.alpha[1] / l : 0.0f;  // nothing seen: zeros
+  bf16* out = static_cast<bf16*>(a.o.p) + t * a.o.ts + (int64_t)h * a.o.hs + d;
+  const float v[4] = {sum.x * share, sum.y * share, sum.z * share, sum.w * share};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) out[e] = layer::from_f32<bf16>(v[e]);
+  if (d == 0 && a.lse) a.lse[t * a.Hq + h] = row_lse(top, l);
 }
 
 template <int DP, int NT, bool FULL>
@@ -598,38 +635,36 @@ cudaError_t launch(const AttendArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = launch_early(few_kernel<DP, NT, FULL>, dim3((unsigned)F::BLOCKS), kThreadsFew, F::SMEM, s, a);
   if (e != cudaSuccess) return e;
-  const int64_t rows = (int64_t)a.c.T * a.group;
-  return launch_early(few_join_kernel<DP, NT>, dim3((unsigned)F::BLOCKS, (unsigned)(rows < F::ROWS ? rows : F::ROWS)), DP, 0, s, a);
+  return launch_early(few_join_kernel<DP, NT>, dim3((unsigned)F::BLOCKS), DP / 4 * F::ROWS, 0, s, a);
 }
 template <int DP, int NT>
 cudaError_t by_dim(const AttendArgs& a, cudaStream_t s) {
   return a.c.dim == DP ? launch<DP, NT, true>(a, s) : launch<DP, NT, false>(a, s);
 }
 
-// Tiles of 8, 16 or 32 rows (for D > 128 not 32: o would not fit the registers): the fewest that
-// hold an average sequence's, so that a key is unpacked once for all of them.  Sequences with more
-// take several tiles.
-static int tiles_of(int64_t T, int group, int dim, int64_t sequences) {
-  const int64_t rows = (T + sequences - 1) / sequences * group;
-  return rows <= 8 ? 1 : rows <= 16 || dim > 128 ? 2 : 4;
+// Tiles of 8 rows if an average sequence's fit one, else of 16.  (Sixteen sequences of 20 rows in a
+// window of 2048: one tile of 24 rows, which takes so many registers that an SM holds 8 warps, 52 us;
+// two of 16 45.)
+static int tiles_of(int64_t T, int group, int64_t sequences) {
+  return (T + sequences - 1) / sequences * group <= 8 ? 1 : 2;
 }
 
 }  // namespace attention
 
 int64_t attend_few_workspace(int64_t T, int group, int dim, int64_t sequences) {
   using namespace attention;
-  const int n = tiles_of(T, group, dim, sequences);
-  const int64_t floats = dim <= 64    ? (n == 1 ? Few<64, 1>::FLOATS : n == 2 ? Few<64, 2>::FLOATS : Few<64, 4>::FLOATS)
-                         : dim <= 128 ? (n == 1 ? Few<128, 1>::FLOATS : n == 2 ? Few<128, 2>::FLOATS : Few<128, 4>::FLOATS)
+  const int n = tiles_of(T, group, sequences);
+  const int64_t floats = dim <= 64    ? (n == 1 ? Few<64, 1>::FLOATS : Few<64, 2>::FLOATS)
+                         : dim <= 128 ? (n == 1 ? Few<128, 1>::FLOATS : Few<128, 2>::FLOATS)
                                       : (n == 1 ? Few<256, 1>::FLOATS : Few<256, 2>::FLOATS);
   return floats * (int64_t)sizeof(float);
 }
 
 cudaError_t launch_attend_few(const AttendArgs& a, cudaStream_t s) {
   using namespace attention;
-  const int n = tiles_of(a.c.T, a.group, a.c.dim, a.c.sequences);
-  if (a.c.dim <= 64) return n == 1 ? by_dim<64, 1>(a, s) : n == 2 ? by_dim<64, 2>(a, s) : by_dim<64, 4>(a, s);
-  if (a.c.dim <= 128) return n == 1 ? by_dim<128, 1>(a, s) : n == 2 ? by_dim<128, 2>(a, s) : by_dim<128, 4>(a, s);
+  const int n = tiles_of(a.c.T, a.group, a.c.sequences);
+  if (a.c.dim <= 64) return n == 1 ? by_dim<64, 1>(a, s) : by_dim<64, 2>(a, s);
+  if (a.c.dim <= 128) return n == 1 ? by_dim<128, 1>(a, s) : by_dim<128, 2>(a, s);
   return n == 1 ? by_dim<256, 1>(a, s) : by_dim<256, 2>(a, s);
 }
 

@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
   const int64_t row0 = (tiles - 1 - unit / c.heads) * ROWS;  // the tiles with the most keys first
   const int rows = (int)min((int64_t)ROWS, (int64_t)seq.rows * a.group - row0);
   const int nt = rows > 128 ? 2 : 1;
-  const Keys<BN> keys = rows_keys<BN>(a, seq, row0, rows);
+  const Keys<BN> keys = rows_keys<BN, uint64_t>(a, seq, (uint64_t)row0, rows);
   const int nb = keys.count, jobs = nt * nb;
 
   if (tid == 0) {
