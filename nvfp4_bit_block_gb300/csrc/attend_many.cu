@@ -8,8 +8,8 @@
 //               in shared memory, in the layout that the tensor core reads (a code times its
 //               scale is exact in fp16); done once for both tiles;
 //   warp 12     issues S = Q K^T (shared memory to TMEM) and O += P V (P from TMEM);
-//   warps 0-7   a thread for each row: S from TMEM, exponentials, P back to TMEM as fp16 in
-//               the columns that S had.
+//   warps 0-7   a thread for each row: S from TMEM into registers that the other warps hand
+//               over (setmaxnreg), exponentials, P back to TMEM as fp16 in the columns that S had.
 // While the tensor core works for one tile, the other's rows are at their exponentials; with
 // one tile two S buffers alternate.  The running maximum moves only where a score passes it by
 // more than 2^8, so that O in TMEM is rarely touched between products.
@@ -25,7 +25,11 @@ namespace attention {
 namespace many {
 
 constexpr int kRowWarps = 8, kFillWarps = 4;
-constexpr int kThreads = 32 * (kRowWarps + kFillWarps + 1);
+constexpr int kMmaWarp = kRowWarps + kFillWarps;
+constexpr int kThreads = 32 * (kMmaWarp + 4);  // three warps do nothing: registers move by four warps
+// What each four warps have of the registers that the block is launched with, 128 a thread.
+constexpr int kRowRegs = 192, kFillRegs = 88, kMmaRegs = 40;
+static_assert(2 * kRowRegs + kFillRegs + kMmaRegs == 4 * 128, "register split");
 
 template <int DP>
 struct Shape {
@@ -52,9 +56,25 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
 __device__ __forceinline__ void arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// The wait of tma.cuh, asleep between its looks: eight warps that poll take issue slots from those
+// that compute.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = tma::globaltimer();
+  for (uint32_t i = 0; i < tma::kWaitLimitPolls; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(20000u)  // ns
+        : "memory");
+    if (ok) return true;
+    if (tma::globaltimer() - t0 > tma::kWaitLimitNs) return false;
+  }
+  return false;
+}
 // A warp's wait and its look at whether the block has given up: the same answer in every lane.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
-  return __all_sync(0xFFFFFFFFu, tma::wait(bar, parity));
+  return __all_sync(0xFFFFFFFFu, wait(bar, parity));
 }
 __device__ __forceinline__ bool stopped(const volatile int& stop) { return __any_sync(0xFFFFFFFFu, stop != 0); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -63,17 +83,34 @@ __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.a
 constexpr uint32_t idesc_f16(int N, bool b_rows) {
   return (1u << 4) | ((b_rows ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+// A whole warp comes to these and its leader issues: without a branch around them the descriptors
+// stay in uniform registers.  (Issued from inside `if (lane == 0)`, with descriptors formed for each
+// product, one took 88 clocks where the tensor core takes 64: prompts 755 us instead of 560.)
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(leader)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(leader)
       : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t leader, uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.u32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
+      "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t elected() {  // 1 in one lane of the warp
+  uint32_t r;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(r));
+  return r;
 }
 __device__ __forceinline__ void st_x16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
@@ -138,7 +175,7 @@ __device__ __forceinline__ int64_t tiles_of(const AttendArgs& a, int rows_per_bl
   return ((int64_t)s.rows * a.group + rows_per_block - 1) / rows_per_block;
 }
 
-template <int DP>
+template <int DP, bool FULL>
 __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
   using S = Shape<DP>;
   constexpr int ROWS = 128 * S::TILES, BN = S::BN;
@@ -157,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
       [&](int64_t) { return (int64_t)blockIdx.x; });
   if ((int64_t)blockIdx.x >= line.total) return;
 
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, b = line.sequence, D = c.dim;
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, b = line.sequence, D = FULL ? DP : c.dim;
   uint8_t* sm = dyn + (1024 - smem_u32(dyn) % 1024) % 1024;
   const uint32_t base = smem_u32(sm), bars = base + S::BARS;
   auto bar = [&](int i) { return bars + 8 * i; };
@@ -187,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
     stop = 0;
     bad_page = 0;
   }
-  if (warp == kRowWarps + kFillWarps) {
+  if (warp == kMmaWarp) {
     tc5::alloc(smem_u32(&tmem_slot), 512);
     tc5::relinquish_alloc_permit();
   }
@@ -247,9 +284,11 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
   const bool holes = bad_page != 0;
 
   if (warp < kRowWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
     if (is_row) {
       const uint32_t at = tmem + ((uint32_t)(warp % 4 * 32) << 16), o_at = at + S::O_COL + tile * D;
-      float m = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+      float m = -INFINITY;
+      float2 l0 = make_float2(0.0f, 0.0f), l1 = l0;
       const int hi = a.causal ? min(p, seq.length - 1) : seq.length - 1;  // the last key that this row sees
       const int64_t lo = a.causal && a.window ? (int64_t)p - a.window : -1;  // keys up to this one lie before the window
       int n = nt == 2 ? tile : 0;
@@ -262,38 +301,40 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
         tc5::fence_after_thread_sync();
         const uint32_t s_at = at + 128 * buf;
         const int key = keys.chunk(i) * BN;
-        const bool part = holes || !keys.all_visible(key);
+        const bool part = !keys.all_visible(key);
         // columns up to last, of them those behind before and those below first
         const int last = hi - key, before = (int)max(lo - key, (int64_t)-1), first = a.sinks - key;
-        auto scores = [&](int x, float* s) {
-          tc5::ld_32x32b_x32(s_at + x, reinterpret_cast<uint32_t*>(s));
-          tc5::wait_ld();
-          if (part) {
+        if (holes) {  // pages hold 16 keys at least, and are out of range for every row
+          for (int x = 0; x < BN; x += 16) {
+            if (key + x >= seq.length || page_of(c, b, key + x) >= 0) continue;
+            uint32_t none[16];
 #pragma unroll
-            for (int y = 0; y < 32; ++y)
-              if (!(x + y <= last && (x + y > before || x + y < first))) s[y] = -INFINITY;
-            if (holes) {
-#pragma unroll
-              for (int y = 0; y < 32; ++y)
-                if (x + y <= last && page_of(c, b, key + x + y) < 0) s[y] = -INFINITY;
-            }
+            for (int y = 0; y < 16; ++y) none[y] = 0xFF800000u;
+            st_x16(s_at + x, none);
           }
-        };
-        float high = -INFINITY;
-#pragma unroll
-        for (int x = 0; x < BN; x += 32) {
-          float s[32];
-          scores(x, s);
-#pragma unroll
-          for (int y = 0; y < 32; y += 2) high = fmaxf(high, fmaxf(s[y], s[y + 1]));
+          tc5::wait_st();
         }
+        float s[BN];
+#pragma unroll
+        for (int x = 0; x < BN; x += 32) tc5::ld_32x32b_x32(s_at + x, reinterpret_cast<uint32_t*>(s + x));
+        tc5::wait_ld();
+        if (part) {
+#pragma unroll
+          for (int x = 0; x < BN; ++x) s[x] = (x <= last) & ((x > before) | (x < first)) ? s[x] : -INFINITY;
+        }
+        float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int x = 4; x < BN; x += 8)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) top[y] = x + y + 4 < BN ? fmaxf(top[y], fmaxf(s[x + y], s[x + y + 4])) : fmaxf(top[y], s[x + y]);
+        float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         high *= f;
         const bool up = high > m + 8.0f;
         if (__any_sync(0xFFFFFFFFu, up)) {
           const float d = up ? layer::ex2(m - high) : 1.0f;
           if (up) m = high;
-          l0 *= d;
-          l1 *= d;
+          l0 = mul2(l0, make_float2(d, d));
+          l1 = mul2(l1, make_float2(d, d));
           if (i > 0) {  // what O holds of the blocks before; with two tiles S comes after that product
             if (nt == 1 && !warp_wait(bar(kPvDone), (i - 1) & 1)) {
               stop = 1;
@@ -310,28 +351,29 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
             }
           }
         }
-        const float z = m == -INFINITY ? 0.0f : m;
+        const float z = m == -INFINITY ? 0.0f : -m;
+        const float2 f2 = make_float2(f, f), z2 = make_float2(z, z);
 #pragma unroll
         for (int x = 0; x < BN; x += 32) {
-          float s[32];
-          scores(x, s);
           uint32_t h[16];
 #pragma unroll
           for (int y = 0; y < 16; ++y) {
-            const float2 t = fma2(make_float2(s[2 * y], s[2 * y + 1]), make_float2(f, f), make_float2(-z, -z));
-            const float e0 = layer::ex2(t.x), e1 = layer::ex2(t.y);
-            l0 += e0;
-            l1 += e1;
-            h[y] = pack_h2(e0, e1);
+            const float2 t = fma2(make_float2(s[x + 2 * y], s[x + 2 * y + 1]), f2, z2);
+            const float2 e = make_float2(layer::ex2(t.x), layer::ex2(t.y));
+            if (y & 1)
+              l1 = add2(l1, e);
+            else
+              l0 = add2(l0, e);
+            h[y] = pack_h2(e.x, e.y);
           }
-          st_x16(s_at + x / 2, h);  // columns that have been read
+          st_x16(s_at + x / 2, h);
         }
         tc5::wait_st();
         tc5::fence_before_thread_sync();
         arrive(bar(kPFull + buf));
       }
       // the result
-      const float l = l0 + l1;
+      const float l = (l0.x + l0.y) + (l1.x + l1.y);
       const float share = l != 0.0f ? c.alpha[1] / l : 0.0f;
       if (on && a.lse) a.lse[token * a.Hq + qh] = row_lse(m, l);
       bool got = nb > 0 && !stopped(stop);
@@ -373,21 +415,36 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
         }
       }
     }
-  } else if (warp < kRowWarps + kFillWarps) {
+  } else if (warp < kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFillRegs));
     constexpr int PARTS = 128 / BN;  // threads of a row
     const int t = tid - 32 * kRowWarps, r = t / PARTS, first = t % PARTS * S::FILL;
     const int64_t hc = (int64_t)head * c.ch + first / 2, hs = (int64_t)head * c.sh + first / 16;
+    // Keys of the next block are on their way while this block's values are unpacked, then its values;
+    // its page is looked up a block before.
     Raw<DP> k, v;
-    auto load = [&](int i) {
+    int64_t co = 0, so = 0;  // where this thread's row lies
+    int page = -1;
+    uint32_t in = 0;
+    auto look = [&](int i) {
       const int64_t key = (int64_t)keys.chunk(i) * BN + r;
-      const int page = key < seq.length ? page_of(c, b, (int)key) : -1;
-      const uint32_t in = page >= 0 ? (uint32_t)key % (uint32_t)c.page_size : 0, pg = page >= 0 ? page : 0;
-      const int64_t co = hc + (int64_t)((uint64_t)pg * c.cp + (uint64_t)in * c.cr);
-      const int64_t so = hs + (int64_t)((uint64_t)pg * c.sp + (uint64_t)in * c.sr);
-      load_raw<DP>(c.kc + co, c.ks + so, page >= 0, first, D, k);
-      load_raw<DP>(c.vc + co, c.vs + so, page >= 0, first, D, v);
+      page = key < seq.length ? c.table[(int64_t)b * c.table_stride + (uint32_t)key / (uint32_t)c.page_size] : -1;
+      in = (uint32_t)key % (uint32_t)c.page_size;
     };
-    if (nb > 0) load(0);
+    auto place = [&]() {
+      const bool on = (uint32_t)page < (uint32_t)c.pages;
+      co = hc + (int64_t)((uint64_t)(on ? page : 0) * c.cp + (uint64_t)in * c.cr);
+      so = hs + (int64_t)((uint64_t)(on ? page : 0) * c.sp + (uint64_t)in * c.sr);
+      return on;
+    };
+    bool on = false;
+    if (nb > 0) {
+      look(0);
+      on = place();
+      load_raw<DP>(c.kc + co, c.ks + so, on, first, D, k);
+      load_raw<DP>(c.vc + co, c.vs + so, on, first, D, v);
+      if (nb > 1) look(1);
+    }
     for (int i = 0; i < nb && !stopped(stop); ++i) {
       const int st = i & 1;
       if (i >= 2 && !warp_wait(bar(kKEmpty + st), ((i >> 1) - 1) & 1)) {
@@ -397,6 +454,10 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
       store_raw<DP>(sm + S::KS + st * S::STAGE, r, first, D, k);
       fence_async_smem();
       arrive(bar(kKFull + st));
+      if (i + 1 < nb) {
+        on = place();
+        load_raw<DP>(c.kc + co, c.ks + so, on, first, D, k);
+      }
       if (i >= 2 && !warp_wait(bar(kVEmpty + st), ((i >> 1) - 1) & 1)) {
         stop = 1;
         break;
@@ -404,62 +465,80 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
       store_raw<DP>(sm + S::VS + st * S::STAGE, r, first, D, v);
       fence_async_smem();
       arrive(bar(kVFull + st));
-      if (i + 1 < nb) load(i + 1);
-    }
-  } else if (lane == 0 && jobs > 0) {
-    const uint32_t qk = idesc_f16(BN, false), pv = idesc_f16(D, true);
-    auto product_qk = [&](int n) {
-      const int i = nt == 2 ? n >> 1 : n, t = nt == 2 ? n & 1 : 0, st = i & 1;
-      if (t == 0 && !tma::wait(bar(kKFull + st), (i >> 1) & 1)) return false;
-      tc5::fence_after_thread_sync();
-      for (int x = 0; x < D / 16; ++x) {
-        const uint32_t in = x / 4, of = x % 4 * 32;
-        mma_ss(tmem + 128 * (n & 1), tc5::smem_desc(base + S::QS + t * S::Q_TILE + in * (128 * 128) + of, 16, 1024, tc5::kLayoutSwizzle128B),
-               tc5::smem_desc(base + S::KS + st * S::STAGE + in * (BN * 128) + of, 16, 1024, tc5::kLayoutSwizzle128B), qk, x > 0);
+      if (i + 1 < nb) {
+        load_raw<DP>(c.vc + co, c.vs + so, on, first, D, v);
+        if (i + 2 < nb) look(i + 2);
       }
-      tc5::commit(bar(kSFull + (n & 1)));
-      if (t == nt - 1) tc5::commit(bar(kKEmpty + st));
-      return true;
-    };
-    auto product_pv = [&](int n) {
-      const int i = nt == 2 ? n >> 1 : n, t = nt == 2 ? n & 1 : 0, st = i & 1;
-      if (t == 0 && !tma::wait(bar(kVFull + st), (i >> 1) & 1)) return false;
-      if (!tma::wait(bar(kPFull + (n & 1)), (n >> 1) & 1)) return false;
-      tc5::fence_after_thread_sync();
-      for (int x = 0; x < BN / 16; ++x)
-        mma_ts(tmem + S::O_COL + t * D, tmem + 128 * (n & 1) + 8 * x,
-               tc5::smem_desc(base + S::VS + st * S::STAGE + x * 2048, BN * 128, 1024, tc5::kLayoutSwizzle128B), pv,
-               i > 0 || x > 0);
-      if (t == nt - 1) tc5::commit(bar(kVEmpty + st));
-      if (nt == 1) tc5::commit(bar(kPvDone));
-      if (i == nb - 1) tc5::commit(bar(kOFull + t));
-      return true;
-    };
-    bool ok = product_qk(0);
-    for (int n = 1; ok && n < jobs && !stop; ++n) ok = product_qk(n) && product_pv(n - 1);
-    if (ok && !stop) ok = product_pv(jobs - 1);
-    tc5::commit(bar(kDrain));
-    if (!tma::wait(bar(kDrain), 0) || !ok) stop = 1;
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
+    if (warp == kMmaWarp && jobs > 0) {
+      const uint32_t leader = elected();
+      constexpr uint32_t qk = idesc_f16(BN, false);
+      const uint32_t pv = FULL ? idesc_f16(DP, true) : idesc_f16(D, true);
+      const int steps = FULL ? DP / 16 : D / 16;
+      // descriptors count addresses in 16 bytes: what a tile, a stage and a step of K add to them
+      const uint64_t q0 = tc5::smem_desc(base + S::QS, 16, 1024, tc5::kLayoutSwizzle128B);
+      const uint64_t k0 = tc5::smem_desc(base + S::KS, 16, 1024, tc5::kLayoutSwizzle128B);
+      const uint64_t v0 = tc5::smem_desc(base + S::VS, BN * 128, 1024, tc5::kLayoutSwizzle128B);
+      auto product_qk = [&](int n) {
+        const int i = nt == 2 ? n >> 1 : n, t = nt == 2 ? n & 1 : 0, st = i & 1;
+        if (t == 0 && !warp_wait(bar(kKFull + st), (i >> 1) & 1)) return false;
+        tc5::fence_after_thread_sync();
+        const uint64_t qd = q0 + t * (S::Q_TILE / 16), kd = k0 + st * (S::STAGE / 16);
+        const uint32_t to = tmem + 128 * (n & 1);
+#pragma unroll
+        for (int x = 0; x < DP / 16; ++x)
+          if (FULL || x < steps)
+            mma_ss(leader, to, qd + (x / 4 * (128 * 128) + x % 4 * 32) / 16, kd + (x / 4 * (BN * 128) + x % 4 * 32) / 16, qk, x > 0);
+        commit(leader, bar(kSFull + (n & 1)));
+        if (t == nt - 1) commit(leader, bar(kKEmpty + st));
+        return true;
+      };
+      auto product_pv = [&](int n) {
+        const int i = nt == 2 ? n >> 1 : n, t = nt == 2 ? n & 1 : 0, st = i & 1;
+        if (t == 0 && !warp_wait(bar(kVFull + st), (i >> 1) & 1)) return false;
+        if (!warp_wait(bar(kPFull + (n & 1)), (n >> 1) & 1)) return false;
+        tc5::fence_after_thread_sync();
+        const uint64_t vd = v0 + st * (S::STAGE / 16);
+        const uint32_t to = tmem + S::O_COL + t * D, from = tmem + 128 * (n & 1);
+#pragma unroll
+        for (int x = 0; x < BN / 16; ++x) mma_ts(leader, to, from + 8 * x, vd + x * (2048 / 16), pv, i > 0 || x > 0);
+        if (t == nt - 1) commit(leader, bar(kVEmpty + st));
+        if (nt == 1) commit(leader, bar(kPvDone));
+        if (i == nb - 1) commit(leader, bar(kOFull + t));
+        return true;
+      };
+      bool ok = product_qk(0);
+      for (int n = 1; ok && n < jobs && !stopped(stop); ++n) ok = product_qk(n) && product_pv(n - 1);
+      if (ok && !stopped(stop)) ok = product_pv(jobs - 1);
+      commit(leader, bar(kDrain));
+      if (!warp_wait(bar(kDrain), 0) || !ok) stop = 1;
+    }
   }
   __syncwarp();
   tc5::fence_before_thread_sync();
   __syncthreads();
   tc5::fence_after_thread_sync();
-  if (warp == kRowWarps + kFillWarps) tc5::dealloc(tmem, 512);
+  if (warp == kMmaWarp) tc5::dealloc(tmem, 512);
   if (tid == 0 && stop) set_status(c.status, NVFP4_ERR_PIPELINE);
 }
 
-template <int DP>
+template <int DP, bool FULL>
 cudaError_t launch(const AttendArgs& a, cudaStream_t s) {
   using S = Shape<DP>;
-  const cudaError_t e = cudaFuncSetAttribute(many_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+  cudaError_t e = cudaFuncSetAttribute(many_kernel<DP, FULL>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
   if (e != cudaSuccess) return e;
+  // the register split draws on what the block is launched with: less than that would wait forever
+  cudaFuncAttributes attr;
+  if ((e = cudaFuncGetAttributes(&attr, many_kernel<DP, FULL>)) != cudaSuccess) return e;
+  if (attr.numRegs != 128) return cudaErrorInvalidConfiguration;
   // as many blocks as the batch can have tiles: one more for each sequence of more than kFewRows rows
   const int64_t rows = (int64_t)a.c.T * a.group, sequences = rows / (kFewRows + 1);
   const int64_t tiles = rows / (128 * S::TILES) + (sequences < a.c.sequences ? sequences : a.c.sequences);
   const int64_t blocks = tiles * a.c.heads;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-  return launch_early(many_kernel<DP>, dim3((unsigned)blocks), kThreads, S::SMEM, s, a);
+  return launch_early(many_kernel<DP, FULL>, dim3((unsigned)blocks), kThreads, S::SMEM, s, a);
 }
 
 }  // namespace many
@@ -467,9 +546,9 @@ cudaError_t launch(const AttendArgs& a, cudaStream_t s) {
 
 cudaError_t launch_attend_many(const AttendArgs& a, cudaStream_t s) {
   using namespace attention;
-  if (a.c.dim <= 64) return many::launch<64>(a, s);
-  if (a.c.dim <= 128) return many::launch<128>(a, s);
-  return many::launch<256>(a, s);
+  if (a.c.dim <= 64) return a.c.dim == 64 ? many::launch<64, true>(a, s) : many::launch<64, false>(a, s);
+  if (a.c.dim <= 128) return a.c.dim == 128 ? many::launch<128, true>(a, s) : many::launch<128, false>(a, s);
+  return a.c.dim == 256 ? many::launch<256, true>(a, s) : many::launch<256, false>(a, s);
 }
 
 }  // namespace nvfp4
