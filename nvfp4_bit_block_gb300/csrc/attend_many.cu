@@ -3,16 +3,18 @@
 //
 // 4 D operations per row and visible key bound it: the tensor cores' rate.  A block takes 256
 // rows of one key head as two tiles of 128 (one tile of 128 for D > 128, where TMEM holds no
-// more) and walks over the visible keys, 128 (64) at a time:
+// more) and walks over the visible keys, 64 at a time:
 //   warps 8-11  bring codes and scales of a block of keys and values and leave them as fp16
 //               in shared memory, in the layout that the tensor core reads (a code times its
 //               scale is exact in fp16); done once for both tiles;
 //   warp 12     issues S = Q K^T (shared memory to TMEM) and O += P V (P from TMEM);
-//   warps 0-7   a thread for each row: S from TMEM into registers that the other warps hand
-//               over (setmaxnreg), exponentials, P back to TMEM as fp16 in the columns that S had.
-// While the tensor core works for one tile, the other's rows are at their exponentials; with
-// one tile two S buffers alternate.  The running maximum moves only where a score passes it by
-// more than 2^8, so that O in TMEM is rarely touched between products.
+//   warps 0-7   a thread for each row: S from TMEM, exponentials, P back to TMEM as fp16 in
+//               the columns that S had.
+// Each tile has two buffers of S: the next block's scores are formed while this one's rows are at
+// their exponentials, so that these never wait for a product.  (128 keys at a time leave TMEM for one
+// buffer; a row's next scores then had to wait for both products, 1800 of 4200 clocks.)  The running
+// maximum moves only where a score passes it by more than 2^8, so that O in TMEM is rarely touched
+// between products.
 #include <cmath>
 
 #include "attend.cuh"
@@ -26,29 +28,26 @@ namespace many {
 
 constexpr int kRowWarps = 8, kFillWarps = 4;
 constexpr int kMmaWarp = kRowWarps + kFillWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 4);  // three warps do nothing: registers move by four warps
-// What each four warps have of the registers that the block is launched with, 128 a thread.
-constexpr int kRowRegs = 192, kFillRegs = 88, kMmaRegs = 40;
-static_assert(2 * kRowRegs + kFillRegs + kMmaRegs == 4 * 128, "register split");
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int BN = 64;  // keys of a block
 
 template <int DP>
 struct Shape {
   static constexpr int TILES = DP <= 128 ? 2 : 1;
-  static constexpr int BN = DP <= 128 ? 128 : 64;  // keys of a block
-  static constexpr int CHUNKS = DP / 64;           // 128-byte columns of fp16
+  static constexpr int STAGES = DP <= 128 ? 4 : 2;  // blocks of keys, and of values
   static constexpr int Q_TILE = 128 * DP * 2;
   static constexpr int STAGE = BN * DP * 2;
-  static constexpr int KS = 0;                     // two stages of keys, two of values, then the queries
-  static constexpr int VS = 2 * STAGE;
-  static constexpr int QS = 4 * STAGE;
+  static constexpr int KS = 0;
+  static constexpr int VS = STAGES * STAGE;
+  static constexpr int QS = 2 * STAGES * STAGE;
   static constexpr int BARS = QS + TILES * Q_TILE;
-  static constexpr int SMEM = BARS + 256 + 1024;   // 1024: what alignment may take
-  static constexpr int FILL = DP * BN / 128;       // values of a filling thread: a part of a row
-  static constexpr int O_COL = 256;                // TMEM: S at 0 and 128, then O
+  static constexpr int SMEM = BARS + 256 + 1024;  // 1024: what alignment may take
+  static constexpr int FILL = DP / 2;             // values of a filling thread: half of a row
+  static constexpr int O_COL = 256;               // TMEM: four buffers of S, then O
 };
 
 // mbarriers, eight bytes each
-enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPFull = 10, kOFull = 12, kPvDone = 14, kDrain = 15 };
+enum Bar { kKFull = 0, kKEmpty = 4, kVFull = 8, kVEmpty = 12, kSFull = 16, kPFull = 20, kPvDone = 24, kOFull = 26, kDrain = 28 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -85,7 +84,7 @@ constexpr uint32_t idesc_f16(int N, bool b_rows) {
 }
 // A whole warp comes to these and its leader issues: without a branch around them the descriptors
 // stay in uniform registers.  (Issued from inside `if (lane == 0)`, with descriptors formed for each
-// product, one took 88 clocks where the tensor core takes 64: prompts 755 us instead of 560.)
+// product, one took 88 clocks where the tensor core takes 64.)
 __device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
   asm volatile(
       "{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
@@ -119,16 +118,12 @@ __device__ __forceinline__ void st_x16(uint32_t taddr, const uint32_t* r) {
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-__device__ __forceinline__ void st_x32(uint32_t taddr, const uint32_t* r) {
+__device__ __forceinline__ void ld_x16(uint32_t taddr, uint32_t* r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,"
-      "%31,%32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
 }
 
 // One thread's part of a key or value row: FILL values as codes and scales.
@@ -163,7 +158,7 @@ __device__ __forceinline__ void store_raw(uint8_t* stage, int row, int first, in
       uint32_t h[4];
       codes8(w[k], h);
       const int piece = (first + 32 * i) / 8 + k;
-      *reinterpret_cast<uint4*>(stage + piece / 8 * (Shape<DP>::BN * 128) + row * 128 + ((piece % 8) ^ (row & 7)) * 16) =
+      *reinterpret_cast<uint4*>(stage + piece / 8 * (BN * 128) + row * 128 + ((piece % 8) ^ (row & 7)) * 16) =
           make_uint4(h2_mul(h[0], f), h2_mul(h[1], f), h2_mul(h[2], f), h2_mul(h[3], f));
     }
   }
@@ -178,7 +173,7 @@ __device__ __forceinline__ int64_t tiles_of(const AttendArgs& a, int rows_per_bl
 template <int DP, bool FULL>
 __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
   using S = Shape<DP>;
-  constexpr int ROWS = 128 * S::TILES, BN = S::BN;
+  constexpr int ROWS = 128 * S::TILES;
   extern __shared__ uint8_t dyn[];
   __shared__ Line line;
   __shared__ uint32_t tmem_slot;
@@ -194,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
       [&](int64_t) { return (int64_t)blockIdx.x; });
   if ((int64_t)blockIdx.x >= line.total) return;
 
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, b = line.sequence, D = FULL ? DP : c.dim;
+  const int tid = threadIdx.x, warp = tid / 32, b = line.sequence, D = FULL ? DP : c.dim;
   uint8_t* sm = dyn + (1024 - smem_u32(dyn) % 1024) % 1024;
   const uint32_t base = smem_u32(sm), bars = base + S::BARS;
   auto bar = [&](int i) { return bars + 8 * i; };
@@ -206,19 +201,21 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
   const int rows = (int)min((int64_t)ROWS, (int64_t)seq.rows * a.group - row0);
   const int nt = rows > 128 ? 2 : 1;
   const Keys<BN> keys = rows_keys<BN, uint64_t>(a, seq, (uint64_t)row0, rows);
-  const int nb = keys.count, jobs = nt * nb;
+  const int nb = keys.count;
 
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       tma::mbar_init(bar(kKFull + i), 32 * kFillWarps);
       tma::mbar_init(bar(kVFull + i), 32 * kFillWarps);
       tma::mbar_init(bar(kKEmpty + i), 1);
       tma::mbar_init(bar(kVEmpty + i), 1);
       tma::mbar_init(bar(kSFull + i), 1);
       tma::mbar_init(bar(kPFull + i), 128);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tma::mbar_init(bar(kPvDone + i), 1);
       tma::mbar_init(bar(kOFull + i), 1);
     }
-    tma::mbar_init(bar(kPvDone), 1);
     tma::mbar_init(bar(kDrain), 1);
     tma::fence_barrier_init();
     stop = 0;
@@ -284,22 +281,20 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
   const bool holes = bad_page != 0;
 
   if (warp < kRowWarps) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
     if (is_row) {
       const uint32_t at = tmem + ((uint32_t)(warp % 4 * 32) << 16), o_at = at + S::O_COL + tile * D;
       float m = -INFINITY;
       float2 l0 = make_float2(0.0f, 0.0f), l1 = l0;
       const int hi = a.causal ? min(p, seq.length - 1) : seq.length - 1;  // the last key that this row sees
       const int64_t lo = a.causal && a.window ? (int64_t)p - a.window : -1;  // keys up to this one lie before the window
-      int n = nt == 2 ? tile : 0;
-      for (int i = 0; i < nb && !stopped(stop); ++i, n += nt) {
-        const int buf = n & 1;
-        if (!warp_wait(bar(kSFull + buf), (n >> 1) & 1)) {
+      for (int i = 0; i < nb && !stopped(stop); ++i) {
+        const int buf = 2 * tile + (i & 1);
+        if (!warp_wait(bar(kSFull + buf), (i >> 1) & 1)) {
           stop = 1;
           break;
         }
         tc5::fence_after_thread_sync();
-        const uint32_t s_at = at + 128 * buf;
+        const uint32_t s_at = at + BN * buf;
         const int key = keys.chunk(i) * BN;
         const bool part = !keys.all_visible(key);
         // columns up to last, of them those behind before and those below first
@@ -335,19 +330,21 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
           if (up) m = high;
           l0 = mul2(l0, make_float2(d, d));
           l1 = mul2(l1, make_float2(d, d));
-          if (i > 0) {  // what O holds of the blocks before; with two tiles S comes after that product
-            if (nt == 1 && !warp_wait(bar(kPvDone), (i - 1) & 1)) {
+          if (i > 0) {  // what O holds of the blocks before, once the last of them is in
+            // (parity tells that phase from its neighbours alone: S came after the product before it)
+            if (!warp_wait(bar(kPvDone + tile), (i - 1) & 1)) {
               stop = 1;
               break;
             }
             tc5::fence_after_thread_sync();
-            for (int x = 0; x < D; x += 32) {
-              uint32_t o[32];
-              tc5::ld_32x32b_x32(o_at + x, o);
+#pragma unroll 1
+            for (int x = 0; x < D; x += 16) {
+              uint32_t o[16];
+              ld_x16(o_at + x, o);
               tc5::wait_ld();
 #pragma unroll
-              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * d);
-              st_x32(o_at + x, o);
+              for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * d);
+              st_x16(o_at + x, o);
             }
           }
         }
@@ -386,6 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
       const bool vec = rows_at_16(a.o);
       for (int x = 0; x < D; x += 32) {
         uint32_t o[32];
+        __syncwarp();  // lanes without a row have not stored
         if (got) {
           tc5::ld_32x32b_x32(o_at + x, o);
           tc5::wait_ld();
@@ -416,9 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
       }
     }
   } else if (warp < kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFillRegs));
-    constexpr int PARTS = 128 / BN;  // threads of a row
-    const int t = tid - 32 * kRowWarps, r = t / PARTS, first = t % PARTS * S::FILL;
+    const int t = tid - 32 * kRowWarps, r = t / 2, first = t % 2 * S::FILL;
     const int64_t hc = (int64_t)head * c.ch + first / 2, hs = (int64_t)head * c.sh + first / 16;
     // Keys of the next block are on their way while this block's values are unpacked, then its values;
     // its page is looked up a block before.
@@ -446,8 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
       if (nb > 1) look(1);
     }
     for (int i = 0; i < nb && !stopped(stop); ++i) {
-      const int st = i & 1;
-      if (i >= 2 && !warp_wait(bar(kKEmpty + st), ((i >> 1) - 1) & 1)) {
+      const int st = i % S::STAGES, round = i / S::STAGES;
+      if (round > 0 && !warp_wait(bar(kKEmpty + st), (round - 1) & 1)) {
         stop = 1;
         break;
       }
@@ -458,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
         on = place();
         load_raw<DP>(c.kc + co, c.ks + so, on, first, D, k);
       }
-      if (i >= 2 && !warp_wait(bar(kVEmpty + st), ((i >> 1) - 1) & 1)) {
+      if (round > 0 && !warp_wait(bar(kVEmpty + st), (round - 1) & 1)) {
         stop = 1;
         break;
       }
@@ -471,8 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
-    if (warp == kMmaWarp && jobs > 0) {
+    if (nb > 0) {
       const uint32_t leader = elected();
       constexpr uint32_t qk = idesc_f16(BN, false);
       const uint32_t pv = FULL ? idesc_f16(DP, true) : idesc_f16(D, true);
@@ -481,37 +476,41 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
       const uint64_t q0 = tc5::smem_desc(base + S::QS, 16, 1024, tc5::kLayoutSwizzle128B);
       const uint64_t k0 = tc5::smem_desc(base + S::KS, 16, 1024, tc5::kLayoutSwizzle128B);
       const uint64_t v0 = tc5::smem_desc(base + S::VS, BN * 128, 1024, tc5::kLayoutSwizzle128B);
-      auto product_qk = [&](int n) {
-        const int i = nt == 2 ? n >> 1 : n, t = nt == 2 ? n & 1 : 0, st = i & 1;
-        if (t == 0 && !warp_wait(bar(kKFull + st), (i >> 1) & 1)) return false;
+      auto product_qk = [&](int i, int t) {
+        const int st = i % S::STAGES;
+        if (t == 0 && !warp_wait(bar(kKFull + st), (i / S::STAGES) & 1)) return false;
         tc5::fence_after_thread_sync();
         const uint64_t qd = q0 + t * (S::Q_TILE / 16), kd = k0 + st * (S::STAGE / 16);
-        const uint32_t to = tmem + 128 * (n & 1);
+        const int buf = 2 * t + (i & 1);
 #pragma unroll
         for (int x = 0; x < DP / 16; ++x)
           if (FULL || x < steps)
-            mma_ss(leader, to, qd + (x / 4 * (128 * 128) + x % 4 * 32) / 16, kd + (x / 4 * (BN * 128) + x % 4 * 32) / 16, qk, x > 0);
-        commit(leader, bar(kSFull + (n & 1)));
+            mma_ss(leader, tmem + BN * buf, qd + (x / 4 * (128 * 128) + x % 4 * 32) / 16, kd + (x / 4 * (BN * 128) + x % 4 * 32) / 16,
+                   qk, x > 0);
+        commit(leader, bar(kSFull + buf));
         if (t == nt - 1) commit(leader, bar(kKEmpty + st));
         return true;
       };
-      auto product_pv = [&](int n) {
-        const int i = nt == 2 ? n >> 1 : n, t = nt == 2 ? n & 1 : 0, st = i & 1;
-        if (t == 0 && !warp_wait(bar(kVFull + st), (i >> 1) & 1)) return false;
-        if (!warp_wait(bar(kPFull + (n & 1)), (n >> 1) & 1)) return false;
+      auto product_pv = [&](int i, int t) {
+        const int st = i % S::STAGES, buf = 2 * t + (i & 1);
+        if (t == 0 && !warp_wait(bar(kVFull + st), (i / S::STAGES) & 1)) return false;
+        if (!warp_wait(bar(kPFull + buf), (i >> 1) & 1)) return false;
         tc5::fence_after_thread_sync();
         const uint64_t vd = v0 + st * (S::STAGE / 16);
-        const uint32_t to = tmem + S::O_COL + t * D, from = tmem + 128 * (n & 1);
 #pragma unroll
-        for (int x = 0; x < BN / 16; ++x) mma_ts(leader, to, from + 8 * x, vd + x * (2048 / 16), pv, i > 0 || x > 0);
-        if (t == nt - 1) commit(leader, bar(kVEmpty + st));
-        if (nt == 1) commit(leader, bar(kPvDone));
+        for (int x = 0; x < BN / 16; ++x)
+          mma_ts(leader, tmem + S::O_COL + t * D, tmem + BN * buf + 8 * x, vd + x * (2048 / 16), pv, i > 0 || x > 0);
+        commit(leader, bar(kPvDone + t));
         if (i == nb - 1) commit(leader, bar(kOFull + t));
+        if (t == nt - 1) commit(leader, bar(kVEmpty + st));
         return true;
       };
-      bool ok = product_qk(0);
-      for (int n = 1; ok && n < jobs && !stopped(stop); ++n) ok = product_qk(n) && product_pv(n - 1);
-      if (ok && !stopped(stop)) ok = product_pv(jobs - 1);
+      // a buffer of S is free for the block after next once its P has been used: products run in order
+      bool ok = true;
+      for (int i = 0; i < 2 && i < nb; ++i)
+        for (int t = 0; ok && t < nt; ++t) ok = product_qk(i, t);
+      for (int i = 0; ok && i < nb && !stopped(stop); ++i)
+        for (int t = 0; ok && t < nt; ++t) ok = product_pv(i, t) && (i + 2 >= nb || product_qk(i + 2, t));
       commit(leader, bar(kDrain));
       if (!warp_wait(bar(kDrain), 0) || !ok) stop = 1;
     }
@@ -527,12 +526,8 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
 template <int DP, bool FULL>
 cudaError_t launch(const AttendArgs& a, cudaStream_t s) {
   using S = Shape<DP>;
-  cudaError_t e = cudaFuncSetAttribute(many_kernel<DP, FULL>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+  const cudaError_t e = cudaFuncSetAttribute(many_kernel<DP, FULL>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
   if (e != cudaSuccess) return e;
-  // the register split draws on what the block is launched with: less than that would wait forever
-  cudaFuncAttributes attr;
-  if ((e = cudaFuncGetAttributes(&attr, many_kernel<DP, FULL>)) != cudaSuccess) return e;
-  if (attr.numRegs != 128) return cudaErrorInvalidConfiguration;
   // as many blocks as the batch can have tiles: one more for each sequence of more than kFewRows rows
   const int64_t rows = (int64_t)a.c.T * a.group, sequences = rows / (kFewRows + 1);
   const int64_t tiles = rows / (128 * S::TILES) + (sequences < a.c.sequences ? sequences : a.c.sequences);
