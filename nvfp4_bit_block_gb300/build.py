@@ -159,16 +159,15 @@ def _link_ext(o: str, ext: str, lib: str, stamp: str, force: bool, verbose: bool
 def build(force: bool = False, verbose: bool = False) -> str:
     """The product libraries and their bindings, side by side; returns the path of libnvfp4.so."""
     with ThreadPoolExecutor(max_workers=5) as ex:
+        exts = [(ex.submit(_build_ext, source, where, stamp, force, verbose), ext, lib, stamp)
+                for source, where, stamp, ext, lib in (
+                    ("layer_binding.cpp", LAYER_BUILD, EXT_STAMP, LAYER_EXT, LAYER_LIB),
+                    ("attention_binding.cpp", ATTENTION_BUILD, ATTENTION_STAMP, ATTENTION_EXT, ATTENTION_LIB))]
         libs = [ex.submit(_build_lib, [os.path.join(CSRC, s) for s in sources], where, lib, force, verbose, flags)
                 for sources, where, lib, flags in ((SOURCES, BUILD, LIB, NVCC_FLAGS),
                                                    (LAYER_SOURCES, LAYER_BUILD, LAYER_LIB, LAYER_NVCC_FLAGS),
                                                    (ATTENTION_SOURCES, ATTENTION_BUILD, ATTENTION_LIB,
                                                     LAYER_NVCC_FLAGS))]
-        import torch.utils.cpp_extension  # noqa: F401  (here: two threads that import it at once can wait for each other)
-        exts = [(ex.submit(_build_ext, source, where, stamp, force, verbose), ext, lib, stamp)
-                for source, where, stamp, ext, lib in (
-                    ("layer_binding.cpp", LAYER_BUILD, EXT_STAMP, LAYER_EXT, LAYER_LIB),
-                    ("attention_binding.cpp", ATTENTION_BUILD, ATTENTION_STAMP, ATTENTION_EXT, ATTENTION_LIB))]
         for lib in libs:
             lib.result()
         for made, ext, lib, stamp in exts:
