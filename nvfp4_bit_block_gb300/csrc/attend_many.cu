@@ -42,7 +42,7 @@ struct Shape {
   static constexpr int QS = 2 * STAGES * STAGE;
   static constexpr int BARS = QS + TILES * Q_TILE;
   static constexpr int SMEM = BARS + 256 + 1024;  // 1024: what alignment may take
-  static constexpr int FILL = DP / 2;             // values of a filling thread: half of a row
+  static constexpr int UNITS = DP / 64;           // units of 32 values of a filling thread: every other one of a row
   static constexpr int O_COL = 256;               // TMEM: four buffers of S, then O
 };
 
@@ -55,27 +55,22 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
 __device__ __forceinline__ void arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// The wait of tma.cuh, asleep between its looks: eight warps that poll take issue slots from those
-// that compute.
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
+// A warp's wait on a barrier: the same answer in every lane, false once the block has given up or
+// after about a second.  What is there already costs a look and a vote: the warp that issues the
+// products does little else, and with a clock read in each of its waits it was what bounded a block.
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* stop) {
   const uint64_t t0 = tma::globaltimer();
   for (uint32_t i = 0; i < tma::kWaitLimitPolls; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(20000u)  // ns
-        : "memory");
-    if (ok) return true;
-    if (tma::globaltimer() - t0 > tma::kWaitLimitNs) return false;
+    const bool ok = tma::try_wait(bar, parity);
+    if (__all_sync(0xFFFFFFFFu, ok)) return true;
+    if ((i & 15u) == 15u && __any_sync(0xFFFFFFFFu, *stop != 0 || tma::globaltimer() - t0 > tma::kWaitLimitNs)) break;
   }
+  *stop = 1;
   return false;
 }
-// A warp's wait and its look at whether the block has given up: the same answer in every lane.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
-  return __all_sync(0xFFFFFFFFu, wait(bar, parity));
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* stop) {
+  return __all_sync(0xFFFFFFFFu, tma::try_wait(bar, parity)) || wait_long(bar, parity, stop);
 }
-__device__ __forceinline__ bool stopped(const volatile int& stop) { return __any_sync(0xFFFFFFFFu, stop != 0); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // fp16 operands, fp32 sums: A (128 rows) and B with K contiguous, or B with its rows contiguous.
@@ -126,38 +121,40 @@ __device__ __forceinline__ void ld_x16(uint32_t taddr, uint32_t* r) {
       : "r"(taddr));
 }
 
-// One thread's part of a key or value row: FILL values as codes and scales.
+// One thread's part of a key or value row: units half, half + 2, .. of 32 values, as codes and scales.
 template <int DP>
 struct Raw {
-  uint4 codes[Shape<DP>::FILL / 32];
-  uint32_t scales[Shape<DP>::FILL / 32];  // two bytes of each
+  uint4 codes[Shape<DP>::UNITS];
+  uint32_t scales[Shape<DP>::UNITS];  // two bytes of each
 };
 
 template <int DP>
-__device__ __forceinline__ void load_raw(const uint8_t* codes, const uint8_t* scales, bool on, int first, int D, Raw<DP>& r) {
+__device__ __forceinline__ void load_raw(const uint8_t* codes, const uint8_t* scales, bool on, int half, int D, Raw<DP>& r) {
 #pragma unroll
-  for (int i = 0; i < Shape<DP>::FILL / 32; ++i) {
-    const bool in = on && first + 32 * i < D;
-    r.codes[i] = in ? *reinterpret_cast<const uint4*>(codes + 16 * i) : make_uint4(0, 0, 0, 0);
-    r.scales[i] = in ? *reinterpret_cast<const uint16_t*>(scales + 2 * i) : 0;
+  for (int i = 0; i < Shape<DP>::UNITS; ++i) {
+    const int u = half + 2 * i;
+    const bool in = on && 32 * u < D;
+    r.codes[i] = in ? *reinterpret_cast<const uint4*>(codes + 16 * u) : make_uint4(0, 0, 0, 0);
+    r.scales[i] = in ? *reinterpret_cast<const uint16_t*>(scales + 2 * u) : 0;
   }
 }
 
 // .. and as fp16 in shared memory: row `row` of columns of 64 values, 16-byte pieces in the
 // 128-byte swizzle.
 template <int DP>
-__device__ __forceinline__ void store_raw(uint8_t* stage, int row, int first, int D, const Raw<DP>& r) {
+__device__ __forceinline__ void store_raw(uint8_t* stage, int row, int half, int D, const Raw<DP>& r) {
 #pragma unroll
-  for (int i = 0; i < Shape<DP>::FILL / 32; ++i) {
-    if (first + 32 * i >= D) continue;
+  for (int i = 0; i < Shape<DP>::UNITS; ++i) {
+    const int u = half + 2 * i;
+    if (32 * u >= D) continue;
     const uint32_t w[4] = {r.codes[i].x, r.codes[i].y, r.codes[i].z, r.codes[i].w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const uint32_t byte = r.scales[i] >> (8 * (k / 2)) & 0xFFu;
-      const uint32_t f = scales2(byte | byte << 8);
+      const uint32_t f = scales2(byte * 0x101u);
       uint32_t h[4];
       codes8(w[k], h);
-      const int piece = (first + 32 * i) / 8 + k;
+      const int piece = 4 * u + k;  // the two threads of a row write to different banks
       *reinterpret_cast<uint4*>(stage + piece / 8 * (BN * 128) + row * 128 + ((piece % 8) ^ (row & 7)) * 16) =
           make_uint4(h2_mul(h[0], f), h2_mul(h[1], f), h2_mul(h[2], f), h2_mul(h[3], f));
     }
@@ -287,12 +284,10 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
       float2 l0 = make_float2(0.0f, 0.0f), l1 = l0;
       const int hi = a.causal ? min(p, seq.length - 1) : seq.length - 1;  // the last key that this row sees
       const int64_t lo = a.causal && a.window ? (int64_t)p - a.window : -1;  // keys up to this one lie before the window
-      for (int i = 0; i < nb && !stopped(stop); ++i) {
+      bool got = nb > 0;
+      for (int i = 0; i < nb; ++i) {
         const int buf = 2 * tile + (i & 1);
-        if (!warp_wait(bar(kSFull + buf), (i >> 1) & 1)) {
-          stop = 1;
-          break;
-        }
+        if (!(got = warp_wait(bar(kSFull + buf), (i >> 1) & 1, &stop))) break;
         tc5::fence_after_thread_sync();
         const uint32_t s_at = at + BN * buf;
         const int key = keys.chunk(i) * BN;
@@ -332,10 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
           l1 = mul2(l1, make_float2(d, d));
           if (i > 0) {  // what O holds of the blocks before, once the last of them is in
             // (parity tells that phase from its neighbours alone: S came after the product before it)
-            if (!warp_wait(bar(kPvDone + tile), (i - 1) & 1)) {
-              stop = 1;
-              break;
-            }
+            if (!(got = warp_wait(bar(kPvDone + tile), (i - 1) & 1, &stop))) break;
             tc5::fence_after_thread_sync();
 #pragma unroll 1
             for (int x = 0; x < D; x += 16) {
@@ -373,11 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
       const float l = (l0.x + l0.y) + (l1.x + l1.y);
       const float share = l != 0.0f ? c.alpha[1] / l : 0.0f;
       if (on && a.lse) a.lse[token * a.Hq + qh] = row_lse(m, l);
-      bool got = nb > 0 && !stopped(stop);
-      if (got && !warp_wait(bar(kOFull + tile), 0)) {
-        stop = 1;
-        got = false;
-      }
+      got = got && warp_wait(bar(kOFull + tile), 0, &stop);
       tc5::fence_after_thread_sync();
       bf16* out = static_cast<bf16*>(a.o.p) + token * a.o.ts + (int64_t)qh * a.o.hs;
       const bool vec = rows_at_16(a.o);
@@ -414,8 +402,8 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
       }
     }
   } else if (warp < kMmaWarp) {
-    const int t = tid - 32 * kRowWarps, r = t / 2, first = t % 2 * S::FILL;
-    const int64_t hc = (int64_t)head * c.ch + first / 2, hs = (int64_t)head * c.sh + first / 16;
+    const int t = tid - 32 * kRowWarps, r = t / 2, half = t % 2;
+    const int64_t hc = (int64_t)head * c.ch, hs = (int64_t)head * c.sh;
     // Keys of the next block are on their way while this block's values are unpacked, then its values;
     // its page is looked up a block before.
     Raw<DP> k, v;
@@ -437,32 +425,26 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
     if (nb > 0) {
       look(0);
       on = place();
-      load_raw<DP>(c.kc + co, c.ks + so, on, first, D, k);
-      load_raw<DP>(c.vc + co, c.vs + so, on, first, D, v);
+      load_raw<DP>(c.kc + co, c.ks + so, on, half, D, k);
+      load_raw<DP>(c.vc + co, c.vs + so, on, half, D, v);
       if (nb > 1) look(1);
     }
-    for (int i = 0; i < nb && !stopped(stop); ++i) {
+    for (int i = 0; i < nb; ++i) {
       const int st = i % S::STAGES, round = i / S::STAGES;
-      if (round > 0 && !warp_wait(bar(kKEmpty + st), (round - 1) & 1)) {
-        stop = 1;
-        break;
-      }
-      store_raw<DP>(sm + S::KS + st * S::STAGE, r, first, D, k);
+      if (round > 0 && !warp_wait(bar(kKEmpty + st), (round - 1) & 1, &stop)) break;
+      store_raw<DP>(sm + S::KS + st * S::STAGE, r, half, D, k);
       fence_async_smem();
       arrive(bar(kKFull + st));
       if (i + 1 < nb) {
         on = place();
-        load_raw<DP>(c.kc + co, c.ks + so, on, first, D, k);
+        load_raw<DP>(c.kc + co, c.ks + so, on, half, D, k);
       }
-      if (round > 0 && !warp_wait(bar(kVEmpty + st), (round - 1) & 1)) {
-        stop = 1;
-        break;
-      }
-      store_raw<DP>(sm + S::VS + st * S::STAGE, r, first, D, v);
+      if (round > 0 && !warp_wait(bar(kVEmpty + st), (round - 1) & 1, &stop)) break;
+      store_raw<DP>(sm + S::VS + st * S::STAGE, r, half, D, v);
       fence_async_smem();
       arrive(bar(kVFull + st));
       if (i + 1 < nb) {
-        load_raw<DP>(c.vc + co, c.vs + so, on, first, D, v);
+        load_raw<DP>(c.vc + co, c.vs + so, on, half, D, v);
         if (i + 2 < nb) look(i + 2);
       }
     }
@@ -476,43 +458,55 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
       const uint64_t q0 = tc5::smem_desc(base + S::QS, 16, 1024, tc5::kLayoutSwizzle128B);
       const uint64_t k0 = tc5::smem_desc(base + S::KS, 16, 1024, tc5::kLayoutSwizzle128B);
       const uint64_t v0 = tc5::smem_desc(base + S::VS, BN * 128, 1024, tc5::kLayoutSwizzle128B);
-      auto product_qk = [&](int i, int t) {
-        const int st = i % S::STAGES;
-        if (t == 0 && !warp_wait(bar(kKFull + st), (i / S::STAGES) & 1)) return false;
+      // Four blocks in a row are written out, so that stages, buffers and most parities are constants:
+      // u is a block's number modulo 4, fours that of the fours before it modulo 2.
+      auto product_qk = [&](int t, int u, uint32_t fours) {
+        const int st = u % S::STAGES, buf = 2 * t + (u & 1);
+        if (t == 0 && !warp_wait(bar(kKFull + st), S::STAGES == 4 ? fours : u >> 1, &stop)) return false;
         tc5::fence_after_thread_sync();
-        const uint64_t qd = q0 + t * (S::Q_TILE / 16), kd = k0 + st * (S::STAGE / 16);
-        const int buf = 2 * t + (i & 1);
 #pragma unroll
         for (int x = 0; x < DP / 16; ++x)
           if (FULL || x < steps)
-            mma_ss(leader, tmem + BN * buf, qd + (x / 4 * (128 * 128) + x % 4 * 32) / 16, kd + (x / 4 * (BN * 128) + x % 4 * 32) / 16,
-                   qk, x > 0);
+            mma_ss(leader, tmem + BN * buf, q0 + (t * S::Q_TILE + x / 4 * (128 * 128) + x % 4 * 32) / 16,
+                   k0 + (st * S::STAGE + x / 4 * (BN * 128) + x % 4 * 32) / 16, qk, x > 0);
         commit(leader, bar(kSFull + buf));
         if (t == nt - 1) commit(leader, bar(kKEmpty + st));
         return true;
       };
-      auto product_pv = [&](int i, int t) {
-        const int st = i % S::STAGES, buf = 2 * t + (i & 1);
-        if (t == 0 && !warp_wait(bar(kVFull + st), (i / S::STAGES) & 1)) return false;
-        if (!warp_wait(bar(kPFull + buf), (i >> 1) & 1)) return false;
+      auto product_pv = [&](int t, int u, uint32_t fours, bool first, bool last) {
+        const int st = u % S::STAGES, buf = 2 * t + (u & 1);
+        if (t == 0 && !warp_wait(bar(kVFull + st), S::STAGES == 4 ? fours : u >> 1, &stop)) return false;
+        if (!warp_wait(bar(kPFull + buf), u >> 1, &stop)) return false;
         tc5::fence_after_thread_sync();
-        const uint64_t vd = v0 + st * (S::STAGE / 16);
 #pragma unroll
         for (int x = 0; x < BN / 16; ++x)
-          mma_ts(leader, tmem + S::O_COL + t * D, tmem + BN * buf + 8 * x, vd + x * (2048 / 16), pv, i > 0 || x > 0);
+          mma_ts(leader, tmem + S::O_COL + t * D, tmem + BN * buf + 8 * x, v0 + (st * S::STAGE + x * 2048) / 16, pv,
+                 !first || x > 0);
         commit(leader, bar(kPvDone + t));
-        if (i == nb - 1) commit(leader, bar(kOFull + t));
+        if (last) commit(leader, bar(kOFull + t));
         if (t == nt - 1) commit(leader, bar(kVEmpty + st));
         return true;
       };
       // a buffer of S is free for the block after next once its P has been used: products run in order
       bool ok = true;
-      for (int i = 0; i < 2 && i < nb; ++i)
-        for (int t = 0; ok && t < nt; ++t) ok = product_qk(i, t);
-      for (int i = 0; ok && i < nb && !stopped(stop); ++i)
-        for (int t = 0; ok && t < nt; ++t) ok = product_pv(i, t) && (i + 2 >= nb || product_qk(i + 2, t));
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (ok && u < nb && t < nt) ok = product_qk(t, u, 0);
+      uint32_t fours = 0;
+      for (int i = 0; ok && i < nb; i += 4, fours ^= 1) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            if (ok && i + u < nb && t < nt) {
+              ok = product_pv(t, u, fours, i + u == 0, i + u == nb - 1);
+              if (ok && i + u + 2 < nb) ok = product_qk(t, (u + 2) % 4, u < 2 ? fours : fours ^ 1);
+            }
+      }
       commit(leader, bar(kDrain));
-      if (!warp_wait(bar(kDrain), 0) || !ok) stop = 1;
+      warp_wait(bar(kDrain), 0, &stop);
     }
   }
   __syncwarp();
