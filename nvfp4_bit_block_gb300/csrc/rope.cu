@@ -3,7 +3,8 @@
 // For each token and head y = turn(x * rsqrt(mean(x^2) + eps) * gamma): read once and
 // written once, HBM bounds it.  A block walks over groups of a few tokens: their angles go to
 // shared memory once for all heads, and a thread keeps those of its pairs for all heads of its
-// token.  The next heads' loads are on their way while these are turned, the next group's too.
+// token.  The next heads' loads are on their way while these are turned, the next group's too.  Queries
+// first, then keys: one set of weights at a time.
 #include <cmath>
 
 #include "rope_common.cuh"
@@ -22,69 +23,62 @@ __global__ void __launch_bounds__(kThreads, 2) rope_kernel(RopeArgs a, int lanes
   const Deal at(lanes, tokens);
   const Slots<V, SLOTS, INTER> s(at.lane, lanes, a.D, a.rotated);
   const float share = 1.0f / (float)a.D;
-  const int H = a.Hq + a.Hk;
-  RawHead<V, SLOTS, TI> raw[U];
-  auto fetch = [&](int64_t t, int h0) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * at.per;
-      const TI* p = h < a.Hq ? static_cast<const TI*>(a.q.p) + t * a.q.ts + (int64_t)h * a.q.hs
-                             : static_cast<const TI*>(a.k.p) + t * a.k.ts + (int64_t)(h - a.Hq) * a.k.hs;
-      raw[u].load(s, t < a.T && h < H, p);
-    }
-  };
   const int64_t step = (int64_t)gridDim.x * tokens;
-  fetch((int64_t)blockIdx.x * tokens + at.token, at.head);
   for (int i = threadIdx.x; i < a.rotated; i += kThreads) turns[i] = turns_of(a.inv_freq[i]);
-  __syncthreads();
-  float gamma[SLOTS][2 * V];
-  int of = -1;  // whose weights these are: queries' (0) or keys' (1)
-  for (int64_t t0 = (int64_t)blockIdx.x * tokens; t0 < a.T; t0 += step) {
-    const int here = (int)(a.T - t0 < tokens ? a.T - t0 : tokens);
-    for (int i = threadIdx.x; i < here * a.rotated; i += kThreads)
-      cs[i] = angle(a.positions[t0 + i / a.rotated], turns[i % a.rotated], a.turn);
-    __syncthreads();
-    const int64_t tt = t0 + at.token;
-    const bool there = tt < a.T;
-    float2 t[SLOTS][V];
-    load_angles(s, cs + (there ? at.token * a.rotated : 0), t);
-    cs = cs == angles ? cs + tokens * a.rotated : angles;
 #pragma unroll 1
-    for (int h0 = at.head; h0 - at.head < H; h0 += U * at.per) {  // whole warps: lanes of a head share sums
-      RawHead<V, SLOTS, TI> now[U];
+  for (int keys = blockIdx.y; keys < 2; keys += gridDim.y) {
+    const int H = keys ? a.Hk : a.Hq;
+    const Tokens in = keys ? a.k : a.q, out = keys ? a.ok : a.oq;
+    RawHead<V, SLOTS, TI> raw[U];
+    auto fetch = [&](int64_t t, int h0) {
+      const TI* p = static_cast<const TI*>(in.p) + t * in.ts + (int64_t)h0 * in.hs;
 #pragma unroll
-      for (int u = 0; u < U; ++u) now[u] = raw[u];
-      const int next = h0 + U * at.per;
-      if (next - at.head < H)
-        fetch(tt, next);
-      else
-        fetch(tt + step, at.head);
+      for (int u = 0; u < U; ++u) raw[u].load(s, t < a.T && h0 + u * at.per < H, p + (int64_t)(u * at.per) * in.hs);
+    };
+    if (H > 0) fetch((int64_t)blockIdx.x * tokens + at.token, at.head);
+    float gamma[SLOTS][2 * V];
+    if (a.norm) load_gamma(s, keys ? a.gamma_k : a.gamma_q, a.w_bf16, gamma_vec, gamma);
+    __syncthreads();
+    for (int64_t t0 = (int64_t)blockIdx.x * tokens; H > 0 && t0 < a.T; t0 += step) {
+      const int here = (int)(a.T - t0 < tokens ? a.T - t0 : tokens);
+      for (int i = threadIdx.x; i < here * a.rotated; i += kThreads)
+        cs[i] = angle(a.positions[t0 + i / a.rotated], turns[i % a.rotated], a.turn);
+      __syncthreads();
+      const int64_t tt = t0 + at.token;
+      const bool there = tt < a.T;
+      Angles<V, SLOTS> t;
+      t.load(s, cs + (there ? at.token * a.rotated : 0));
+      cs = cs == angles ? cs + tokens * a.rotated : angles;
+#pragma unroll 1
+      for (int h0 = at.head; h0 - at.head < H; h0 += U * at.per) {  // whole warps: lanes of a head share sums
+        RawHead<V, SLOTS, TI> now[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = h0 + u * at.per;
-        float x[SLOTS][2 * V];
-        now[u].widen(x);
-        if (a.norm) {
-          if (of != (h < a.Hq ? 0 : 1)) {
-            of = h < a.Hq ? 0 : 1;
-            load_gamma(s, of ? a.gamma_k : a.gamma_q, a.w_bf16, gamma_vec, gamma);
+        for (int u = 0; u < U; ++u) now[u] = raw[u];
+        if (h0 + U * at.per - at.head < H)
+          fetch(tt, h0 + U * at.per);
+        else
+          fetch(tt + step, at.head);
+        TO* to = static_cast<TO*>(out.p) + tt * out.ts + (int64_t)h0 * out.hs;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float x[SLOTS][2 * V];
+          now[u].widen(x);
+          if (a.norm) {
+            float2 q = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < SLOTS; ++i)
+#pragma unroll
+              for (int e = 0; e < 2 * V; e += 2) q = fma2(two(x[i] + e), two(x[i] + e), q);
+            const float r = rsqrtf(fmaf(lanes_sum(q.x + q.y, lanes), share, a.eps));
+#pragma unroll
+            for (int i = 0; i < SLOTS; ++i)
+#pragma unroll
+              for (int e = 0; e < 2 * V; e += 2)
+                put(x[i] + e, mul2(two(x[i] + e), mul2(two(gamma[i] + e), make_float2(r, r))));
           }
-          float r = 0.0f;
-#pragma unroll
-          for (int i = 0; i < SLOTS; ++i)
-#pragma unroll
-            for (int e = 0; e < 2 * V; ++e) r = fmaf(x[i][e], x[i][e], r);
-          r = rsqrtf(fmaf(lanes_sum(r, lanes), share, a.eps));
-#pragma unroll
-          for (int i = 0; i < SLOTS; ++i)
-#pragma unroll
-            for (int e = 0; e < 2 * V; ++e) x[i][e] *= r * gamma[i][e];
+          turn_pairs<V, SLOTS, INTER>(t, x);
+          if (there && h0 + u * at.per < H) store_head(s, to + (int64_t)(u * at.per) * out.hs, x);
         }
-        turn_pairs(s, t, x);
-        if (there && h < H)
-          store_head(s, h < a.Hq ? static_cast<TO*>(a.oq.p) + tt * a.oq.ts + (int64_t)h * a.oq.hs
-                                 : static_cast<TO*>(a.ok.p) + tt * a.ok.ts + (int64_t)(h - a.Hq) * a.ok.hs,
-                     x);
       }
     }
   }
@@ -95,7 +89,7 @@ cudaError_t launch(const RopeArgs& a, cudaStream_t s) {
   const int lanes = lanes_of(V, a.D, a.rotated), tokens = tokens_of(a.T);
   const int64_t groups = (a.T + tokens - 1) / tokens;
   const int smem = a.rotated * (8 + 2 * tokens * (int)sizeof(float2));
-  return launch_early(rope_kernel<V, INTER, TI, TO>, dim3((unsigned)(groups < kBlocks ? groups : kBlocks)), kThreads, smem,
+  return launch_early(rope_kernel<V, INTER, TI, TO>, dim3((unsigned)(groups < kBlocks ? groups : kBlocks), passes_apart(groups)), kThreads, smem,
                       s, a, lanes, tokens, gamma_vectors(a, V));
 }
 

@@ -30,7 +30,7 @@ __global__ void __launch_bounds__(kThreads, 2) rope_grad_kernel(RopeGradArgs b, 
   const float share = 1.0f / (float)a.D;
   // queries, then keys: one set of weights and sums at a time
 #pragma unroll 1
-  for (int keys = 0; keys < 2; ++keys) {
+  for (int keys = blockIdx.y; keys < 2; keys += gridDim.y) {
     const int H = keys ? a.Hk : a.Hq;
     const Tokens in = keys ? a.k : a.q, out = keys ? a.ok : a.oq, xin = keys ? b.xk : b.xq;
     float gamma[SLOTS][2 * V], dg[SLOTS][2 * V] = {};
@@ -53,8 +53,8 @@ __global__ void __launch_bounds__(kThreads, 2) rope_grad_kernel(RopeGradArgs b, 
       __syncthreads();
       const int64_t tt = t0 + at.token;
       const bool there = tt < a.T;
-      float2 t[SLOTS][V];
-      load_angles(s, cs + (there ? at.token * a.rotated : 0), t);
+      Angles<V, SLOTS> t;
+      t.load(s, cs + (there ? at.token * a.rotated : 0));
       cs = cs == angles ? cs + tokens * a.rotated : angles;
 #pragma unroll 1
       for (int h = at.head; h - at.head < H; h += at.per) {  // whole warps: lanes of a head share sums
@@ -68,26 +68,27 @@ __global__ void __launch_bounds__(kThreads, 2) rope_grad_kernel(RopeGradArgs b, 
           else
             fetch(tt + step, at.head);
         }
-        turn_pairs(s, t, g);
-        float q = 0.0f, p = 0.0f;
+        turn_pairs<V, SLOTS, INTER>(t, g);
+        float2 q2 = make_float2(0.0f, 0.0f), p2 = q2;
 #pragma unroll
         for (int i = 0; i < SLOTS; ++i)
 #pragma unroll
-          for (int e = 0; e < 2 * V; ++e) {
-            q = fmaf(x[i][e], x[i][e], q);
-            p = fmaf(g[i][e] * gamma[i][e], x[i][e], p);
+          for (int e = 0; e < 2 * V; e += 2) {
+            const float2 y = two(x[i] + e);
+            q2 = fma2(y, y, q2);
+            p2 = fma2(mul2(two(g[i] + e), two(gamma[i] + e)), y, p2);
           }
-        q = lanes_sum(q, lanes);
-        p = lanes_sum(p, lanes);
+        const float q = lanes_sum(q2.x + q2.y, lanes), p = lanes_sum(p2.x + p2.y, lanes);
         const float rstd = rsqrtf(fmaf(q, share, a.eps));
-        const float along = p * share * rstd * rstd;
         if (there && h < H) {
+          const float2 r = make_float2(rstd, rstd), along = make_float2(-p * share * rstd * rstd, -p * share * rstd * rstd);
 #pragma unroll
           for (int i = 0; i < SLOTS; ++i)
 #pragma unroll
-            for (int e = 0; e < 2 * V; ++e) {
-              dg[i][e] = fmaf(g[i][e], x[i][e] * rstd, dg[i][e]);
-              x[i][e] = rstd * (g[i][e] * gamma[i][e] - x[i][e] * along);
+            for (int e = 0; e < 2 * V; e += 2) {
+              const float2 y = two(x[i] + e), z = two(g[i] + e);
+              put(dg[i] + e, fma2(z, mul2(y, r), two(dg[i] + e)));
+              put(x[i] + e, mul2(r, fma2(y, along, mul2(z, two(gamma[i] + e)))));
             }
           store_head(s, static_cast<TX*>(out.p) + tt * out.ts + (int64_t)h * out.hs, x);
         }
@@ -130,7 +131,7 @@ cudaError_t launch(const RopeGradArgs& b, cudaStream_t s) {
   const int sums = b.dgamma_q || b.dgamma_k, tokens = tokens_of(a.T);
   const int64_t blocks = blocks_of(a.T, std::max(a.Hq, a.Hk));
   const int smem = a.rotated * 8 + std::max(2 * tokens * a.rotated * (int)sizeof(float2), 8 * a.D * (int)sizeof(float));
-  const cudaError_t e = launch_early(rope_grad_kernel<V, INTER, TG, TX>, dim3((unsigned)blocks), kThreads, smem, s, b,
+  const cudaError_t e = launch_early(rope_grad_kernel<V, INTER, TG, TX>, dim3((unsigned)blocks, passes_apart((a.T + tokens - 1) / tokens)), kThreads, smem, s, b,
                                      lanes_of(V, a.D, a.rotated), tokens, gamma_vectors(a, V), sums);
   if (e != cudaSuccess || !sums) return e;
   return colsum::launch_join<2>(b.ws, (int)blocks, a.D, b.dgamma_q, b.dgamma_k, s);

@@ -225,25 +225,45 @@ struct Deal {
 };
 
 // The cosines and sines of a lane's pairs: V of each slot.
-template <int V, int SLOTS, bool INTER>
-__device__ __forceinline__ void load_angles(const Slots<V, SLOTS, INTER>& s, const float2* cs, float2 t[SLOTS][V]) {
+template <int V, int SLOTS>
+struct Angles {
+  float c[SLOTS][V], s[SLOTS][V];
+  template <bool INTER>
+  __device__ __forceinline__ void load(const Slots<V, SLOTS, INTER>& at, const float2* cs) {
 #pragma unroll
-  for (int i = 0; i < SLOTS; ++i)
+    for (int i = 0; i < SLOTS; ++i)
 #pragma unroll
-    for (int e = 0; e < V; ++e) t[i][e] = s.pair[i] >= 0 ? cs[s.pair[i] + e] : make_float2(1.0f, 0.0f);
+      for (int e = 0; e < V; ++e) {
+        const float2 t = at.pair[i] >= 0 ? cs[at.pair[i] + e] : make_float2(1.0f, 0.0f);  // passes
+        c[i][e] = t.x;
+        s[i][e] = t.y;
+      }
+  }
+};
+// The arithmetic goes two values at a time (packed fp32): with one it kept the issue slots 53 %
+// busy and HBM at 70 %.
+__device__ __forceinline__ float2 two(const float* x) { return make_float2(x[0], x[1]); }
+__device__ __forceinline__ void put(float* x, float2 v) {
+  x[0] = v.x;
+  x[1] = v.y;
 }
 template <int V, int SLOTS, bool INTER>
-__device__ __forceinline__ void turn_pairs(const Slots<V, SLOTS, INTER>& s, const float2 t[SLOTS][V],
-                                           float x[SLOTS][2 * V]) {
+__device__ __forceinline__ void turn_pairs(const Angles<V, SLOTS>& t, float x[SLOTS][2 * V]) {
 #pragma unroll
   for (int i = 0; i < SLOTS; ++i) {
-    if (s.pair[i] < 0) continue;
+    if constexpr (INTER || V == 1) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const int ia = INTER ? 2 * e : e, ib = INTER ? 2 * e + 1 : V + e;
-      const float a = x[i][ia], b = x[i][ib];
-      x[i][ia] = a * t[i][e].x - b * t[i][e].y;
-      x[i][ib] = b * t[i][e].x + a * t[i][e].y;
+      for (int e = 0; e < V; ++e) {
+        const float2 a = two(x[i] + 2 * e), c = make_float2(t.c[i][e], t.c[i][e]), s = make_float2(t.s[i][e], t.s[i][e]);
+        put(x[i] + 2 * e, fma2(make_float2(-a.y, a.x), s, mul2(a, c)));
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; e += 2) {
+        const float2 a = two(x[i] + e), b = two(x[i] + V + e), c = two(t.c[i] + e), s = two(t.s[i] + e);
+        put(x[i] + e, fma2(make_float2(-b.x, -b.y), s, mul2(a, c)));
+        put(x[i] + V + e, fma2(a, s, mul2(b, c)));
+      }
     }
   }
 }
@@ -268,14 +288,17 @@ inline int lanes_of(int V, int D, int rotated) {
   while (L < slots && L < 32) L *= 2;
   return L;
 }
-// Tokens that a block takes at a time: eight, so that a thread of 8 lanes has every fourth head
-// and several on their way; few tokens are spread out.
+// Tokens that a block takes at a time: up to eight, so that a thread of 8 lanes has every fourth
+// head and several on their way; few tokens are spread out, so that no block has two groups.  Where
+// few blocks do that, queries and keys go to blocks of their own (515 tokens x 12 heads of 96 fp32,
+// backward: 13.5 us one after the other in blocks of one token).
 constexpr int kBlocks = 152 * 2;
 inline int tokens_of(int64_t T) {
-  int n = 8;
-  while (n > 1 && T < (int64_t)n * kBlocks) n /= 2;
+  int n = 1;
+  while (n < 8 && T > (int64_t)n * kBlocks) n *= 2;
   return n;
 }
+inline unsigned passes_apart(int64_t groups) { return groups <= kBlocks ? 2 : 1; }
 inline bool gamma_vectors(const RopeArgs& a, int V) {
   const uintptr_t n = a.w_bf16 ? 2 * V : 16;
   return reinterpret_cast<uintptr_t>(a.gamma_q) % n == 0 && reinterpret_cast<uintptr_t>(a.gamma_k) % n == 0;
