@@ -10,9 +10,10 @@
 * nvfp4_bit_block_gb300/_build/libnvfp4_attention.so and _nvfp4_attention.so --
   the attention operators (the C ABI of include/nvfp4_attention.h) and their
   binding, likewise;
-* tests/selftest/_build/libnvfp4_selftest.so and libnvfp4_layer_selftest.so --
-  device self-checks used only by the tests (build_selftest,
-  build_layer_selftest); they hold no product entry point.
+* tests/selftest/_build/libnvfp4_selftest.so, libnvfp4_layer_selftest.so and
+  libnvfp4_attention_selftest.so -- device self-checks used only by the tests
+  (build_selftest, build_layer_selftest, build_attention_selftest); they hold no
+  product entry point.
 
 Translation units compile in parallel; the CUDA runtime is linked statically.
 """
@@ -38,6 +39,7 @@ SELFTEST_DIR = os.path.join(ROOT, "tests", "selftest")
 SELFTEST_BUILD = os.path.join(SELFTEST_DIR, "_build")
 SELFTEST_LIB = os.path.join(SELFTEST_BUILD, "libnvfp4_selftest.so")
 LAYER_SELFTEST_LIB = os.path.join(SELFTEST_BUILD, "libnvfp4_layer_selftest.so")
+ATTENTION_SELFTEST_LIB = os.path.join(SELFTEST_BUILD, "libnvfp4_attention_selftest.so")
 
 SOURCES = ["api.cu", "tmap.cu", "amax.cu", "quant1d.cu", "quant1d_sr.cu", "quant1d_46mae.cu", "quant1d_46mse.cu", "quant1d_46max.cu",
            "quant2d.cu", "dequant.cu", "analysis.cu", "gemm.cu"]
@@ -184,6 +186,13 @@ def build_layer_selftest(force: bool = False, verbose: bool = False) -> str:
                       [*LAYER_NVCC_FLAGS, "-DNVFP4_TEST_NO_COPIES"])
 
 
+def build_attention_selftest(force: bool = False, verbose: bool = False) -> str:
+    """The test-only build of the attention kernel for many rows whose keys never come; returns its path."""
+    srcs = [os.path.join(SELFTEST_DIR, "nvfp4_attention_selftest.cu"), os.path.join(CSRC, "attend_many.cu")]
+    return _build_lib(srcs, os.path.join(SELFTEST_BUILD, "attention"), ATTENTION_SELFTEST_LIB, force, verbose,
+                      [*LAYER_NVCC_FLAGS, "-DNVFP4_TEST_NO_COPIES"])
+
+
 def build_selftest(force: bool = False, verbose: bool = False) -> str:
     """The test-only self-check library (its own copy of the tensor-map
     helper); returns its path."""
@@ -195,3 +204,4 @@ if __name__ == "__main__":
     print(build(verbose=True))
     print(build_selftest(verbose=True))
     print(build_layer_selftest(verbose=True))
+    print(build_attention_selftest(verbose=True))

@@ -773,3 +773,171 @@ def test_empty_batches():
     r = nv.nvfp4_cache_attention(rand((2, 4, 64), BF, 88), w.cache, ints([0, 2]), ints([0]),
                                  torch.empty((1, 0), dtype=torch.int32, device="cuda"), out=out, want_lse=True, status=st)
     assert st.item() == 0 and bool((out == 0).all()) and bool((r.lse == -math.inf).all())
+
+
+# ---------------------------------------------------------------- together, and around the calls
+
+
+def example():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "attention_block.py")
+    spec = importlib.util.spec_from_file_location("attention_block", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (40, 4)])
+def test_an_attention_block(window, sinks):
+    """The example: prompts and then tokens one at a time.  Each NVFP4 operand is off by about 0.1 of its norm, so a
+    product by 0.14; two products and the cached values in a row: 0.25."""
+    far = example().run(640, 10, 2, [150, 33, 70], dim=64, window=window, sinks=sinks)
+    assert all(v <= 0.35 for v in far.values()), far
+
+
+def test_the_calls_together_match_the_formulas():
+    """Rotation, write and attention as a decoder makes them, for a prompt and the tokens behind it, against the
+    formulas on what the calls before left."""
+    Hq, Hk, D, page = 6, 2, 96, 48
+    f, g = freqs(48), rand((D,), F32, 90, 0.1, 1.0)
+    pages = ints([[3, 0, 2, 5]])
+    cache = nv.nvfp4_kv_cache(6, Hk, page, D, (2.0 ** -5, 2.0 ** -5))
+    length = 0
+    for n in (130, 1, 1, 7, 40):
+        qkv = rand((n, Hq + 2 * Hk, D), BF, 91 + n)
+        q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hk], qkv[:, Hq + Hk:]
+        pos = torch.arange(length, length + n, device="cuda", dtype=torch.int32)
+        length += n
+        q0, k0 = q.clone(), k.clone()
+        r = nv.nvfp4_qk_rope(q, k, pos, f, g, g, out_q=q, out_k=k)
+        check_rope(q0, r.q, pos, f, g, 1e-6, True, False, "q")
+        check_rope(k0, r.k, pos, f, g, 1e-6, True, False, "k")
+        batch = (ints([0, n]), ints([length]), pages)
+        nv.nvfp4_cache_write(r.k, v, cache, *batch)
+        c = nv.nvfp4_cache_read(cache, *batch, tokens=n, out_dtype=F32)
+        for x, y in ((r.k, c.k), (v, c.v)):  # half a step of E2M1 at most, of the block's largest value / 6
+            top = x.float().unflatten(-1, (-1, 16)).abs().amax(-1, keepdim=True).expand(-1, -1, -1, 16).flatten(-2)
+            assert bool(((x.float() - y).abs() <= top * (1 / 6 + 2.0 ** -4) + 1e-3).all())
+        o = nv.nvfp4_cache_attention(r.q, cache, *batch, want_lse=True)
+        w = type("W", (), dict(cache=cache, starts=batch[0], lengths=batch[1], table=pages))()
+        check_attention(w, r.q, o)
+
+
+def test_workspaces_are_not_overrun():
+    """Guard bytes around a workspace of exactly the size that the C ABI asks for, for one and many rows."""
+    import ctypes
+    from nvfp4_bit_block_gb300.attention import Batch, Cache, Tokens
+    L = nv.attention_lib()
+    for news, dim, group in (([1, 1, 1], 64, 5), ([3, 1, 1], 128, 5), ([1, 1, 1], 256, 2), ([2, 30, 90], 128, 4), ([1, 1, 1], 96, 20)):
+        w = Work([700, 90, 333], news, 2, dim, 16, seed=92)
+        w.fill()
+        Hq = 2 * group
+        q = rand((w.T, Hq, dim), BF, 93)
+        want = nv.nvfp4_cache_attention(q, w.cache, *w.batch).o
+        n = L.nvfp4_cache_attention_workspace(w.T, Hq, 2, dim, 3)
+        ws = torch.full((n + 512,), 0xA5, dtype=torch.uint8, device="cuda")
+        o = torch.empty_like(q)
+        c, kc, sc = w.cache, w.cache.k_codes, w.cache.k_scales
+        cache = Cache(c.k_codes.data_ptr(), c.k_scales.data_ptr(), c.v_codes.data_ptr(), c.v_scales.data_ptr(),
+                      c.alpha.data_ptr(), kc.shape[0], 2, 16, dim, *kc.stride()[:3], *sc.stride()[:3])
+        batch = Batch(w.starts.data_ptr(), w.lengths.data_ptr(), w.table.data_ptr(), 3, w.table.shape[1], w.table.stride(0))
+        tok = lambda t: ctypes.byref(Tokens(t.data_ptr(), t.stride(0), t.stride(1)))
+        st = L.nvfp4_cache_attention(tok(q), w.T, Hq, ctypes.byref(cache), ctypes.byref(batch), dim ** -0.5, 1, 0, 0, tok(o),
+                                     None, ws.data_ptr() + 256, n, None, torch.cuda.current_stream().cuda_stream)
+        assert st == 0 and torch.equal(o, want)
+        assert bool((ws[:256] == 0xA5).all()) and bool((ws[256 + n:] == 0xA5).all())
+
+
+def test_a_wait_that_runs_out_is_reported():
+    """A build whose keys never come: the kernel for many rows gives up after about a second, says so, frees what it
+    holds and leaves the context usable."""
+    import ctypes
+    from nvfp4_bit_block_gb300.build import build_attention_selftest
+    L = ctypes.CDLL(build_attention_selftest())
+    w = Work([300], [200], 1, 64, 16, seed=94)
+    w.fill()
+    q, st = rand((200, 2, 64), BF, 95), ints([0])
+    o, p, c = torch.zeros_like(q), ctypes.c_void_p, w.cache
+    args = [p(t.data_ptr()) for t in (q, o, c.k_codes, c.k_scales, c.v_codes, c.v_scales, c.alpha, w.starts, w.lengths, w.table)]
+    torch.cuda.synchronize()
+    assert L.nvfp4_selftest_attend_many(*args, 200, 1, 2, 64, 16, w.table.shape[1], p(st.data_ptr())) == 0
+    torch.cuda.synchronize()
+    assert st.item() == -8
+    r = nv.nvfp4_cache_attention(q, c, *w.batch, want_lse=True)
+    check_attention(w, q, r)
+
+
+@pytest.mark.parametrize("news", [[1, 1, 1, 1], [20, 1, 300, 2]])
+def test_attention_on_two_streams_at_once(news):
+    """Calls that run at the same time have workspaces of their own."""
+    w = Work([800, 300, 500, 64], news, 2, 128, 32, seed=96)
+    w.fill()
+    qs = [rand((w.T, 10, 128), BF, 97 + i) for i in range(4)]
+    want = [nv.nvfp4_cache_attention(q, w.cache, *w.batch).o for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in qs]
+    got = [None] * 4
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i] = nv.nvfp4_cache_attention(qs[i], w.cache, *w.batch).o
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_two_captured_graphs_share_the_cache():
+    """Write and attention captured together, replayed with other tokens and lengths; two graphs in turn."""
+    w = Work([64, 40], [1, 1], 1, 64, 16, seed=98)
+    w.fill()
+    k, v, q = rand((2, 1, 64), BF, 99), rand((2, 1, 64), BF, 100), rand((2, 3, 64), BF, 101)
+    graphs = []
+    torch.cuda.synchronize()
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            nv.nvfp4_cache_write(k, v, w.cache, *w.batch)
+            o = nv.nvfp4_cache_attention(q, w.cache, *w.batch, want_lse=True)
+        graphs.append((g, o))
+    for step in range(6):
+        w.lengths.copy_(ints([50 + step, 30 + step]))
+        for t, s in ((k, 200), (v, 300), (q, 400)):
+            t.copy_(rand(t.shape, BF, s + step))
+        g, o = graphs[step % 2]
+        g.replay()
+        w.lens, w.news = [50 + step, 30 + step], [1, 1]
+        check_attention(w, q, o)
+
+
+def test_long_contexts_and_many_sequences():
+    """A sequence of 100000 keys among short ones, and 3000 sequences."""
+    w = Work([100000, 5, 40000], [1, 1, 2], 1, 64, 64, seed=102)
+    w.fill()
+    attend(w, 4)
+    w = Work([(i * 37) % 90 for i in range(3000)], [1 if i % 7 else 0 for i in range(3000)], 1, 32, 16, seed=103)
+    w.lens = [max(n, m) for n, m in zip(w.lens, w.news)]
+    w = Work(w.lens, w.news, 1, 32, 16, seed=103)
+    w.fill()
+    attend(w, 2)
+
+
+def test_offsets_beyond_32_bits():
+    """Pages that lie more than 2^32 bytes from the first."""
+    P = 70000
+    kc = torch.zeros((P, 1, 512, 128), dtype=torch.uint8, device="cuda")  # 4.6 GB
+    vc = kc  # the same bytes serve as values
+    sc = torch.full((P, 1, 512, 16), 0x38, dtype=torch.uint8, device="cuda")
+    cache = nv.KVCache(kc, sc, vc, sc, torch.ones(2, dtype=F32, device="cuda"))
+    far = [69999, 67001, 65537]
+    for i, p in enumerate(far):
+        kc[p] = torch.randint(0, 256, kc[p].shape, generator=gen(104 + i), device="cuda", dtype=torch.uint8)
+    near = nv.KVCache(*(t[far].contiguous() for t in (kc, sc, kc, sc)), cache.alpha)
+    for m in (1, 70):
+        batch = (ints([0, m]), ints([1300]))
+        q = rand((m, 2, 256), BF, 108, 0.1)
+        a = nv.nvfp4_cache_attention(q, cache, *batch, ints([far]))
+        b = nv.nvfp4_cache_attention(q, near, *batch, ints([[0, 1, 2]]))
+        assert torch.equal(a.o, b.o)
+        x = nv.nvfp4_cache_read(cache, *batch, ints([far]), tokens=m)
+        y = nv.nvfp4_cache_read(near, *batch, ints([[0, 1, 2]]), tokens=m)
+        assert torch.equal(x.k, y.k)
