@@ -161,8 +161,8 @@ __device__ __forceinline__ uint2 quantize16(const Block16<T>& r, float alpha, ui
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) write_kernel(CacheCopyArgs a, int tokens, bool vec) {
-  constexpr int U = sizeof(T) == 2 ? 4 : 2;  // blocks on their way
+__global__ void __launch_bounds__(kThreads, 4) write_kernel(CacheCopyArgs a, int tokens, bool vec) {
+  constexpr int U = sizeof(T) == 2 ? 2 : 1;  // blocks on their way
   __shared__ Place places[kMaxTokens];
   const CacheView& c = a.c;
   after_previous();
