@@ -11,10 +11,15 @@
 //   warps 0-7   a thread for each row: S from TMEM, exponentials, P back to TMEM as fp16 in
 //               the columns that S had.
 // Each tile has two buffers of S: the next block's scores are formed while this one's rows are at
-// their exponentials, so that these never wait for a product.  (128 keys at a time leave TMEM for one
-// buffer; a row's next scores then had to wait for both products, 1800 of 4200 clocks.)  The running
-// maximum moves only where a score passes it by more than 2^8, so that O in TMEM is rarely touched
-// between products.
+// their exponentials.  (128 keys at a time leave TMEM for one buffer and want registers moved to the
+// rows: a row's next scores then wait for both products, and the three prompts of the largest measured
+// case took as long.)  The running maximum moves only where a score passes it by more than 2^8, so that
+// O in TMEM is rarely touched between products.
+//
+// Measured: prompts of 2731, 1818 and 905 tokens that end caches of 8192, 5454 and 2716 keys, 40 query
+// heads on 8 of 128 values: 547 us, 1.08 PFLOP/s (56 % of the measured bf16 rate).  For each 64 keys a
+// row takes about 1200 clocks and its block 2360: what is left is the way from P's arrival to the
+// issuing warp (270 clocks) and from the product's end back, twice for each block.
 #include <cmath>
 
 #include "attend.cuh"
@@ -79,19 +84,24 @@ constexpr uint32_t idesc_f16(int N, bool b_rows) {
 }
 // A whole warp comes to these and its leader issues: without a branch around them the descriptors
 // stay in uniform registers.  (Issued from inside `if (lane == 0)`, with descriptors formed for each
-// product, one took 88 clocks where the tensor core takes 64.)
-__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+// product, one took 88 clocks where the tensor core takes 64.)  A descriptor's upper half is the same
+// for all tiles of a kind; the lower one counts addresses in 16 bytes.
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t upper, uint32_t idesc,
+                                       uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(leader)
+      "{\n .reg .pred p, q;\n .reg .b64 x, y;\n setp.ne.u32 p, %5, 0;\n setp.ne.u32 q, %6, 0;\n"
+      " mov.b64 x, {%1, %3};\n mov.b64 y, {%2, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(upper), "r"(idesc), "r"(accumulate), "r"(leader)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t upper, uint32_t idesc,
+                                       uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(leader)
+      "{\n .reg .pred p, q;\n .reg .b64 y;\n setp.ne.u32 p, %5, 0;\n setp.ne.u32 q, %6, 0;\n"
+      " mov.b64 y, {%2, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(upper), "r"(idesc), "r"(accumulate), "r"(leader)
       : "memory");
 }
 __device__ __forceinline__ void commit(uint32_t leader, uint32_t bar) {
@@ -469,8 +479,8 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
 #pragma unroll
         for (int x = 0; x < DP / 16; ++x)
           if (FULL || x < steps)
-            mma_ss(leader, tmem + BN * buf, q0 + (t * S::Q_TILE + x / 4 * (128 * 128) + x % 4 * 32) / 16,
-                   k0 + (st * S::STAGE + x / 4 * (BN * 128) + x % 4 * 32) / 16, qk, x > 0);
+            mma_ss(leader, tmem + BN * buf, (uint32_t)q0 + (t * S::Q_TILE + x / 4 * (128 * 128) + x % 4 * 32) / 16,
+                   (uint32_t)k0 + (st * S::STAGE + x / 4 * (BN * 128) + x % 4 * 32) / 16, (uint32_t)(q0 >> 32), qk, x > 0);
         commit(leader, bar(kSFull + buf));
         if (t == nt - 1) commit(leader, bar(kKEmpty + st));
         return true;
@@ -482,8 +492,8 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
         tc5::fence_after_thread_sync();
 #pragma unroll
         for (int x = 0; x < BN / 16; ++x)
-          mma_ts(leader, tmem + S::O_COL + t * D, tmem + BN * buf + 8 * x, v0 + (st * S::STAGE + x * 2048) / 16, pv,
-                 !first || x > 0);
+          mma_ts(leader, tmem + S::O_COL + t * D, tmem + BN * buf + 8 * x, (uint32_t)v0 + (st * S::STAGE + x * 2048) / 16,
+                 (uint32_t)(v0 >> 32), pv, !first || x > 0);
         commit(leader, bar(kPvDone + t));
         if (last) commit(leader, bar(kOFull + t));
         if (t == nt - 1) commit(leader, bar(kVEmpty + st));
