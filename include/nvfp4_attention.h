@@ -99,11 +99,11 @@ typedef struct {
  * positions[t] * inv_freq[i]:  (a, b) -> (a cos - b sin, b cos + a sin).  Pair i is
  * values (i, i + rotated), or (2i, 2i + 1) with interleaved = 1; the other values pass.
  * The angle is the product of the two numbers as they are, reduced in 64 bits: far
- * positions lose nothing.
+ * positions lose nothing (off by |position| max(1, |inv_freq|) 2^-53 turns).
  *
  *   q, k          T x q_heads x D and T x k_heads x D, x's type;  heads 0..65535
  *   D             a multiple of 2, 2..512;  rotated 0..D/2 (number of pairs)
- *   positions_dev int32[T];  inv_freq_dev  float[rotated]
+ *   positions_dev int32[T];  inv_freq_dev  float[rotated], finite
  *   norm          1 or 0;  eps finite and >= 0 (used with norm)
  *   gamma_q_dev, gamma_k_dev  D weights or NULL (ones), fp32 (w_is_bf16 = 0) or bf16;
  *                 both NULL without norm
@@ -191,7 +191,7 @@ NVFP4_API int nvfp4_cache_read(const nvfp4_tokens* k, const nvfp4_tokens* v, int
  *   q         T x q_heads x dim, bf16;  q_heads a multiple of heads, at most 65535
  *   o         as q;  may be q itself (same strides)
  *   lse_dev   T x q_heads floats (natural logarithm) or NULL
- *   scale     finite
+ *   scale     finite; scale * alpha * (a row's largest query) stays finite in fp32
  *   window    0 (no window) .. 2^31 - 1;  sinks 0 .. 2^31 - 1, 0 without a window
  *   workspace_dev  nvfp4_cache_attention_workspace(T, q_heads, heads, dim, sequences) bytes
  * The products take bf16 queries (scaled by a power of two per row into fp16) and the

@@ -152,8 +152,8 @@ def nvfp4_kv_cache(pages: int, heads: int, page_size: int, dim: int, alpha=(2.0 
                    device="cuda") -> KVCache:
     """An empty cache of `pages` pages of `page_size` tokens (a multiple of 16), `dim` values a
     head (a multiple of 32, at most 256).  alpha: the tensor scales of keys and values, best
-    powers of two: values up to 2688 alpha are held, and blocks of 16 whose largest value is
-    below alpha / 171 are held with fewer bits, those below alpha / 171 * 0.5 as zeros."""
+    powers of two: values up to 2688 alpha are held; blocks of 16 whose largest value is below
+    0.094 alpha have scales of fewer bits, and at or below alpha / 171 they become zeros."""
     import torch
     new = lambda *s: torch.zeros(s, dtype=torch.uint8, device=device)
     k, v = new(pages, heads, page_size, dim // 2), new(pages, heads, page_size, dim // 2)

@@ -5,9 +5,26 @@
 // rows to a key head are bound by the cache's bytes (attend_few.cu), those with many by their
 // products (attend_many.cu).  The lengths are on the device: where a batch may hold both, both
 // kernels run, and each leaves the other's sequences alone.
+//
+// What counts as few.  The kernel for many gives 256 rows of a key head to one SM and does not split
+// their keys; the one for few takes tiles of 16 rows and deals the keys of all of them out to all SMs,
+// at a seventh of the rate for a full 256 rows.  So it is ahead while the tiles,
+// over all key heads, are fewer than about 2.1 for each SM.  Measured, few against many, 40 query heads on 8
+// of 128 values: one sequence of 65536 keys and 130 rows to a key head 210 and 989 us, 520 rows 714 and 977, 750
+// rows 999 and 1000, 1040 rows 1402 and 978; four of 16384 keys and 130 rows each 209 and 266, 180 rows 272 and
+// 268, 260 rows 387 and 261; 64 of 4096 keys and 30 rows 213 and 279, 40 rows 290 and 279.  How the rows are spread over
+// the sequences only the device knows: if those beyond one token of each make more tiles than that, a sequence
+// is few by its even share of the tiles, two at least.
 #include "attend.cuh"
 
 namespace nvfp4 {
+
+int attend_few_rows(int64_t T, int group, int heads, int64_t sequences) {
+  constexpr int64_t kTiles = 320;  // 2.1 * 152
+  int64_t tiles = kTiles / heads;
+  if (((T - sequences) * group + 15) / 16 * heads > kTiles) tiles = kTiles / (heads * sequences);
+  return 16 * (int)(tiles > 2 ? tiles : 2);
+}
 
 int64_t attend_workspace(int64_t T, int Hq, int heads, int dim, int64_t sequences) {
   return attend_few_workspace(T, Hq / heads, dim, sequences);
@@ -15,7 +32,7 @@ int64_t attend_workspace(int64_t T, int Hq, int heads, int dim, int64_t sequence
 
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t s) {
   const cudaError_t e = launch_attend_few(a, s);
-  if (e != cudaSuccess || a.c.T <= 1 || (int64_t)a.c.T * a.group <= attention::kFewRows) return e;
+  if (e != cudaSuccess || a.c.T <= 1 || (int64_t)a.c.T * a.group <= a.few_rows) return e;
   return launch_attend_many(a, s);
 }
 

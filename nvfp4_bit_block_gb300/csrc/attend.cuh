@@ -13,12 +13,10 @@ using bf16 = __nv_bfloat16;
 using layer::after_previous;
 using layer::launch_early;
 
-// Sequences with at most this many rows (new tokens times the query heads of a key head) are
-// attend_few.cu's, and those with one token; the others go to the kernel for many.
-constexpr int kFewRows = 64;
-
+// Sequences with one new token and those with at most a.few_rows rows (new tokens times the query
+// heads of a key head) are attend_few.cu's, the others go to the kernel for many (attend.cu).
 __device__ __forceinline__ bool is_few(const AttendArgs& a, const Sequence& s) {
-  return s.rows <= 1 || (int64_t)s.rows * a.group <= kFewRows;
+  return s.rows <= 1 || (int64_t)s.rows * a.group <= a.few_rows;
 }
 
 // Whether the query at position p sees key j (0 <= j).

@@ -294,6 +294,7 @@ int nvfp4_cache_attention(const nvfp4_tokens* q, int64_t T, int q_heads, const n
   a.causal = causal ? 1 : 0;
   a.window = (int)window;
   a.sinks = (int)sinks;
+  a.few_rows = nvfp4::attend_few_rows(T, a.group, cache->heads, batch->sequences);
   return launch_status(nvfp4::launch_attend(a, static_cast<cudaStream_t>(stream)));
 }
 

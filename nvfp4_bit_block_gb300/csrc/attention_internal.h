@@ -65,9 +65,11 @@ struct AttendArgs {
   float scale;
   int causal;
   int window, sinks;
+  int few_rows;  // the most rows of a sequence that the kernel for few takes
 };
 
 int64_t rope_grad_workspace(int64_t T, int Hq, int Hk, int D);
+int attend_few_rows(int64_t T, int group, int heads, int64_t sequences);
 int64_t attend_workspace(int64_t T, int Hq, int heads, int dim, int64_t sequences);
 
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s);

@@ -283,7 +283,8 @@ static bool vectors(const CacheCopyArgs& a) {
   return true;
 }
 
-// Tokens of a block: as many as leave two blocks for each SM.
+// Tokens of a block: as many as leave two blocks for each SM.  (At most 4, 8, 16 and 32: four prompts written
+// and read back 69, 60, 58 and 62 us, 65536 tokens read 81, 67, 62 and 62.)
 static int tokens_of(const CacheView& c) {
   int n = kMaxTokens;
   while (n > 1 && c.T < n * 2 * 152) n /= 2;

@@ -474,6 +474,48 @@ def attend(w, Hq, seed=60, scale=1.0, **kw):
     return q, r
 
 
+def among_rows(t, T):
+    """t (tokens, heads, values) as the first of T tokens, its strides (where tokens or heads come first) and the alignment
+    of its address kept."""
+    n, H, D = t.shape
+    ts, hs = (t.stride(0) if n > 1 else H * D), (t.stride(1) if H > 1 else D)
+    if H > 1 and n > 1 and hs > ts:
+        hs = T * ts
+    off = t.data_ptr() % 16 // t.element_size()
+    base = torch.zeros(off + (T - 1) * ts + (H - 1) * hs + D, dtype=t.dtype, device="cuda")
+    v = base.as_strided((T, H, D), (ts, hs, 1), off)
+    v[:n] = t
+    return v
+
+
+@pytest.fixture(params=["alone", "crowded"])
+def company(request, monkeypatch):
+    """Which kernel takes a sequence depends on the whole batch (few hundred tiles of 16 rows over all key heads are few):
+    each call as it is, and with so many rows behind the last sequence and so many empty ones that sequences of more than
+    32 rows to a key head go to the kernel for many."""
+    call = nv.nvfp4_cache_attention
+
+    def crowded(q, cache, starts, lengths, pages, *args, out=None, **kw):
+        n, heads, B = q.shape[0], cache.k_codes.shape[1], lengths.shape[0]
+        more = 183 // heads + 1
+        T = n + B + more + 366 * 16 * heads // q.shape[1] + 1
+        starts = torch.cat([starts, starts[-1:].expand(more)])
+        lengths = torch.cat([lengths, lengths.new_zeros(more)])
+        pages = torch.cat([pages, pages.new_zeros(more, pages.shape[1])])
+        rows = among_rows(q, T)
+        o = among_rows(out, T) if out is not None and out is not q else rows if out is q else None
+        r = call(rows, cache, starts, lengths, pages, *args, out=o, **kw)
+        if out is not None:
+            out.copy_(r.o[:n])
+        return nv.AttentionOut(out if out is not None else r.o[:n], None if r.lse is None else r.lse[:n])
+
+    if request.param == "crowded":
+        monkeypatch.setattr(nv, "nvfp4_cache_attention", crowded)
+
+
+both_kernels = pytest.mark.usefixtures("company")
+
+
 # lengths, new tokens, key heads, queries to each, dim, page
 ATTEND = [([1], [1], 1, 1, 32, 16), ([17], [1], 2, 5, 128, 16), ([700], [1], 8, 5, 128, 16), ([64, 65, 63, 1], [1] * 4, 2, 8, 64, 32),
           ([300, 5, 0, 999], [1, 1, 0, 1], 3, 7, 96, 48), ([513], [1], 1, 16, 256, 64), ([90, 200], [1, 1], 1, 20, 160, 16),
@@ -482,6 +524,7 @@ ATTEND = [([1], [1], 1, 1, 32, 16), ([17], [1], 2, 5, 128, 16), ([700], [1], 8, 
           ([260, 129], [257, 128], 1, 2, 256, 128), ([5000], [2], 1, 3, 64, 64), ([30] * 70, [1] * 70, 2, 2, 32, 16)]
 
 
+@both_kernels
 @pytest.mark.parametrize("lens,news,heads,group,dim,page", ATTEND)
 def test_attention(lens, news, heads, group, dim, page):
     w = Work(lens, news, heads, dim, page, seed=61, behind=2)
@@ -497,6 +540,7 @@ def test_attention(lens, news, heads, group, dim, page):
     attend(w, heads * group, scale=0.3)
 
 
+@both_kernels
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (16, 4), (100, 4), (37, 17), (128, 1000), (10 ** 6, 3), (2 ** 31 - 1, 0)])
 @pytest.mark.parametrize("lens,news,heads,group,dim,page", [
     ([500, 3, 170], [1, 1, 1], 2, 5, 128, 16), ([300, 64], [4, 9], 1, 8, 64, 48), ([270, 130], [200, 130], 2, 2, 96, 32),
@@ -507,6 +551,7 @@ def test_attention_window_and_sinks(lens, news, heads, group, dim, page, window,
     attend(w, heads * group, window=window, sinks=sinks)
 
 
+@both_kernels
 def test_attention_rows_that_see_nothing():
     """More new tokens than the sequence holds: the first rows lie before its beginning; lengths of zero."""
     for lens, news in (([3, 0, 40], [5, 2, 41]), ([0], [1]), ([2], [300]), ([0, 0], [200, 1])):
@@ -524,6 +569,7 @@ def test_attention_rows_that_see_nothing():
         attend(w, 4, causal=False)
 
 
+@both_kernels
 @pytest.mark.parametrize("news", [[1, 1, 1], [6, 1, 30], [150, 90, 200]])
 def test_attention_ignores_what_it_must_not_see(news):
     """Bytes behind a sequence's end, in other pages and in later tokens change no row that does not see them."""
@@ -556,6 +602,7 @@ def test_attention_ignores_what_it_must_not_see(news):
     check_attention(w, q, other)
 
 
+@both_kernels
 @pytest.mark.parametrize("news", [[1, 1], [9, 30], [150, 180]])
 def test_attention_odd_queries(news):
     """Large and tiny queries, zeros, and NaN and Inf that stay in their rows."""
@@ -579,6 +626,7 @@ def test_attention_odd_queries(news):
     assert torch.equal(got.o[keep], r.o[keep]) and torch.equal(got.lse[keep], r.lse[keep])
 
 
+@both_kernels
 @pytest.mark.parametrize("news", [[1, 1, 1], [8, 1, 100]])
 def test_attention_rising_and_falling_scores(news):
     """Scores that climb over the whole sequence (the running maximum moves all the time) and that fall."""
@@ -596,6 +644,7 @@ def test_attention_rising_and_falling_scores(news):
         check_attention(w, q, r)
 
 
+@both_kernels
 @pytest.mark.parametrize("order", ["pshd", "hpsd"])
 @pytest.mark.parametrize("news", [[1, 1], [5, 140]])
 def test_attention_layouts(order, news):
@@ -617,6 +666,7 @@ def test_attention_layouts(order, news):
     assert torch.equal(q, want)
 
 
+@both_kernels
 @pytest.mark.parametrize("news", [[1, 1, 1], [4, 170, 1]])
 def test_attention_bad_pages(news):
     """Pages out of range hide their tokens; sequences with bad numbers keep their rows as they were."""
@@ -796,6 +846,7 @@ def test_an_attention_block(window, sinks):
     assert all(v <= 0.35 for v in far.values()), far
 
 
+@both_kernels
 def test_the_calls_together_match_the_formulas():
     """Rotation, write and attention as a decoder makes them, for a prompt and the tokens behind it, against the
     formulas on what the calls before left."""
@@ -868,6 +919,7 @@ def test_a_wait_that_runs_out_is_reported():
     check_attention(w, q, r)
 
 
+@both_kernels
 @pytest.mark.parametrize("news", [[1, 1, 1, 1], [20, 1, 300, 2]])
 def test_attention_on_two_streams_at_once(news):
     """Calls that run at the same time have workspaces of their own."""
