@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
   __shared__ volatile int stop;
   __shared__ int bad_page;
   const CacheView& c = a.c;
-  after_previous();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   find_line<kThreads>(
       c, line, [&](int b) {
         Sequence s;
@@ -271,6 +271,9 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
   tc5::fence_before_thread_sync();
   __syncthreads();
   tc5::fence_after_thread_sync();
+  // Only now may the next kernel begin: one that takes TMEM in its setup, before it waits for this one,
+  // would otherwise hold on an SM what this block still has to get there, and each would wait for the other.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // pages out of range, all of them before any key is used: their keys are hidden
   {
     bool bad = false;

@@ -919,6 +919,27 @@ def test_a_wait_that_runs_out_is_reported():
     check_attention(w, q, r)
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("M", [1, 16, 300])
+def test_a_linear_layer_right_behind(M, dim):
+    """A call whose kernel takes tensor memory before it waits for the attention's: 20 of them, back to back."""
+    w = Work([900, 700, 1100], [900, 513, 700], 2, dim, 16, seed=104)
+    w.fill()
+    q = rand((w.T, 8, dim), BF, 105)
+    want = nv.nvfp4_cache_attention(q, w.cache, *w.batch).o
+    flags = nv.ROWWISE | nv.SF_SWIZZLED
+    operands = []
+    for m, seed in ((M, 106), (256, 107)):
+        x = rand((m, 256), BF, seed)
+        z = nv.nvfp4_quantize(x, nv.nvfp4_amax(x, flags), flags)
+        operands += [z.q_row, z.s_row, z.alpha[0:1]]
+    lin = lambda: nv.nvfp4_linear(*operands).d
+    d = lin().clone()
+    for _ in range(20):
+        o, e = nv.nvfp4_cache_attention(q, w.cache, *w.batch).o, lin()
+    assert torch.equal(o, want) and torch.equal(e, d)
+
+
 @both_kernels
 @pytest.mark.parametrize("news", [[1, 1, 1, 1], [20, 1, 300, 2]])
 def test_attention_on_two_streams_at_once(news):
