@@ -284,6 +284,7 @@ __global__ void __launch_bounds__(kThreadsFew, Few<DP, NT>::PER_SM) few_kernel(A
   __shared__ Line line;
   const CacheView& c = a.c;
   after_previous();
+  const float alpha_v = c.alpha[1], scale = a.scale * c.alpha[0] * layer::kLog2e;  // on their way with the lengths
   if (blockIdx.x == 0) check_batch(c);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, q = lane % 4;
   float* os = reinterpret_cast<float*>(sm);          // [warps][ROWS][O_ROW]
@@ -311,7 +312,6 @@ __global__ void __launch_bounds__(kThreadsFew, Few<DP, NT>::PER_SM) few_kernel(A
   int b = line.sequence;
   load_few(a, b, seq);
   int64_t base = line.base;  // where sequence b begins on the line
-  const float alpha_v = c.alpha[1], scale = a.scale * c.alpha[0] * layer::kLog2e;
   const bool vec = rows_at_16(a.q);
   const bool o_pairs = reinterpret_cast<uintptr_t>(a.o.p) % 4 == 0 && a.o.ts % 2 == 0 && a.o.hs % 2 == 0;
   const bool dense = c.sr == c.dim / 16 &&
@@ -338,43 +338,7 @@ __global__ void __launch_bounds__(kThreadsFew, Few<DP, NT>::PER_SM) few_kernel(A
     const int s_begin = (int)(w - u0), s_end = (int)((w_end < u1 ? w_end : u1) - u0);
     const int rows = min(ROWS, seq.rows * a.group - ROWS * r);
 
-    // queries: rows g of each eight; scores and o: rows 2q and 2q + 1
-    uint32_t qf[NT][F::KW * 4];
-    float f[NT][2];
-    int p[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int row = ROWS * r + 8 * n + g;
-      const bool on = 8 * n + g < rows;
-      const float up = load_query<DP>(a, vec, on, (int64_t)seq.first + (on ? row / a.group : 0),
-                                      h * a.group + (on ? row % a.group : 0), scale < 0.0f, qf[n]);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        // scores to base 2 are f * S with f > 0: the scale's sign is in the queries, and where it vanishes
-        // f is the smallest number, so that -Inf stays -Inf
-        f[n][e] = fmaxf(fabsf(scale) * __shfl_sync(0xFFFFFFFFu, up, 8 * q + 4 * e), 0x1p-126f);
-        const int x = 8 * n + 2 * q + e;
-        p[n][e] = seq.length - seq.rows + (x < rows ? (ROWS * r + x) / a.group : 0);
-      }
-    }
     __syncthreads();  // the part before is read
-    if constexpr (F::Q_SHARED) {
-      if (warp == 0)
-#pragma unroll
-        for (int x = 0; x < F::KW; ++x)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-            qs[(x * NT + n) * 32 + lane] = make_uint4(qf[n][4 * x], qf[n][4 * x + 1], qf[n][4 * x + 2], qf[n][4 * x + 3]);
-      __syncthreads();
-    }
-
-    float o[F::VN / 2][NT][4] = {};
-    float m[NT][2], z[NT][2], l[NT][2];  // z: -m, 0 while nothing is seen
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      m[n][0] = m[n][1] = -INFINITY;
-      z[n][0] = z[n][1] = l[n][0] = l[n][1] = 0.0f;
-    }
     // This warp's chunks are those of i, i + 4, ..; the copies are STAGES - 1 of them ahead, the
     // page of the next to be copied one more.
     const int per_page = c.page_size / 16, i_end = min(keys.count, 4 * s_end);
@@ -409,6 +373,42 @@ __global__ void __launch_bounds__(kThreadsFew, Few<DP, NT>::PER_SM) few_kernel(A
     };
 #pragma unroll
     for (int x = 0; x < F::STAGES - 1; ++x) copy();
+    // queries: rows g of each eight; scores and o: rows 2q and 2q + 1
+    uint32_t qf[NT][F::KW * 4];
+    float f[NT][2];
+    int p[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int row = ROWS * r + 8 * n + g;
+      const bool on = 8 * n + g < rows;
+      const float up = load_query<DP>(a, vec, on, (int64_t)seq.first + (on ? row / a.group : 0),
+                                      h * a.group + (on ? row % a.group : 0), scale < 0.0f, qf[n]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        // scores to base 2 are f * S with f > 0: the scale's sign is in the queries, and where it vanishes
+        // f is the smallest number, so that -Inf stays -Inf
+        f[n][e] = fmaxf(fabsf(scale) * __shfl_sync(0xFFFFFFFFu, up, 8 * q + 4 * e), 0x1p-126f);
+        const int x = 8 * n + 2 * q + e;
+        p[n][e] = seq.length - seq.rows + (x < rows ? (ROWS * r + x) / a.group : 0);
+      }
+    }
+    if constexpr (F::Q_SHARED) {
+      if (warp == 0)
+#pragma unroll
+        for (int x = 0; x < F::KW; ++x)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            qs[(x * NT + n) * 32 + lane] = make_uint4(qf[n][4 * x], qf[n][4 * x + 1], qf[n][4 * x + 2], qf[n][4 * x + 3]);
+      __syncthreads();
+    }
+
+    float o[F::VN / 2][NT][4] = {};
+    float m[NT][2], z[NT][2], l[NT][2];  // z: -m, 0 while nothing is seen
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      z[n][0] = z[n][1] = l[n][0] = l[n][1] = 0.0f;
+    }
     int get = 0;
     for (int i = 4 * s_begin + warp; i < i_end; i += kWarps) {
       const int first = 16 * keys.chunk(i);
