@@ -14,7 +14,10 @@
 // rows 999 and 1000, 1040 rows 1402 and 978; four of 16384 keys and 130 rows each 209 and 266, 180 rows 272 and
 // 268, 260 rows 387 and 261; 64 of 4096 keys and 30 rows 213 and 279, 40 rows 290 and 279.  How the rows are spread over
 // the sequences only the device knows: if those beyond one token of each make more tiles than that, a sequence
-// is few by its even share of the tiles, two at least.
+// is few by its even share of the tiles, two at least.  On short contexts the tiles' own cost (about half a
+// microsecond for one, to find its place among all) counts more than the keys: with one key head and 2048 rows few
+// takes 90 us and many 38 on 1256 keys, with eight and 500 rows 47 and 37 on 1100, 320 rows 36 and 37 on 1064, 520 rows
+// 79 and 80 on 4096.
 #include "attend.cuh"
 
 namespace nvfp4 {
@@ -32,7 +35,7 @@ int64_t attend_workspace(int64_t T, int Hq, int heads, int dim, int64_t sequence
 
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t s) {
   const cudaError_t e = launch_attend_few(a, s);
-  if (e != cudaSuccess || a.c.T <= 1 || (int64_t)a.c.T * a.group <= a.few_rows) return e;
+  if (e != cudaSuccess || a.c.T <= 1 || (int64_t)a.c.T * a.group <= attention::surely_few(a)) return e;
   return launch_attend_many(a, s);
 }
 

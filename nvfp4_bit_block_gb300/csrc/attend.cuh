@@ -13,11 +13,15 @@ using bf16 = __nv_bfloat16;
 using layer::after_previous;
 using layer::launch_early;
 
-// Sequences with one new token and those with at most a.few_rows rows (new tokens times the query
-// heads of a key head) are attend_few.cu's, the others go to the kernel for many (attend.cu).
+// Sequences with one new token and those with few rows (new tokens times the query heads of a key
+// head) are attend_few.cu's, the others go to the kernel for many.  Few are at most a.few_rows, and on a
+// short context at most kFewShort and a row more for each 16 keys (attend.cu has the reasons).
+constexpr int kFewShort = 256;
 __device__ __forceinline__ bool is_few(const AttendArgs& a, const Sequence& s) {
-  return s.rows <= 1 || (int64_t)s.rows * a.group <= a.few_rows;
+  return s.rows <= 1 || (int64_t)s.rows * a.group <= min(a.few_rows, kFewShort + s.length / 16);
 }
+// What is few by its rows at any length.
+inline int64_t surely_few(const AttendArgs& a) { return a.few_rows < kFewShort ? a.few_rows : kFewShort; }
 
 // Whether the query at position p sees key j (0 <= j).
 __device__ __forceinline__ bool visible(const AttendArgs& a, const Sequence& s, int p, int j) {

@@ -24,8 +24,8 @@
 // The running maximum moves only where a score passes it by more than 2^8: weights stay below
 // 256, where fp16 holds them as well as below 1, and most steps leave o alone.
 //
-// Measured: the next token of 48 sequences of up to 16384 keys, 40 query heads on 8 of 128 values: 137 us
-// for 509 MB, 3.7 TB/s (55 % of the copy rate).  Issue slots bound it: about 430 instructions for 16
+// Measured: the next token of 48 sequences of up to 16384 keys, 40 query heads on 8 of 128 values: 132 us
+// for 509 MB, 3.9 TB/s (57 % of the copy rate).  Issue slots bound it: about 430 instructions for 16
 // keys, 60 % of the slots busy.  Half of them unpack: 72 conversions and 64 products by scales, two
 // clocks each.  One token of 700 keys: 12 us with its host side.
 #include <cmath>

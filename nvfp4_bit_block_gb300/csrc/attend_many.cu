@@ -537,8 +537,8 @@ cudaError_t launch(const AttendArgs& a, cudaStream_t s) {
   using S = Shape<DP>;
   const cudaError_t e = cudaFuncSetAttribute(many_kernel<DP, FULL>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
   if (e != cudaSuccess) return e;
-  // as many blocks as the batch can have tiles: one more for each sequence of more than few_rows rows
-  const int64_t rows = (int64_t)a.c.T * a.group, sequences = rows / (a.few_rows + 1);
+  // as many blocks as the batch can have tiles: one more for each sequence that is not surely few
+  const int64_t rows = (int64_t)a.c.T * a.group, sequences = rows / (surely_few(a) + 1);
   const int64_t tiles = rows / (128 * S::TILES) + (sequences < a.c.sequences ? sequences : a.c.sequences);
   const int64_t blocks = tiles * a.c.heads;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
