@@ -84,6 +84,10 @@ __device__ __forceinline__ void mma(float* d, uint32_t a0, uint32_t a1, uint32_t
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void put2(float* x, float2 v) {
+  x[0] = v.x;
+  x[1] = v.y;
+}
 // An 8 x 8 matrix of fp16, two of row lane / 4 in each lane, to its transpose.
 __device__ __forceinline__ uint32_t turned(uint32_t v) {
   uint32_t r;
@@ -456,15 +460,20 @@ __global__ void __launch_bounds__(kThreadsFew, Few<DP, NT>::PER_SM) few_kernel(A
 #pragma unroll
         for (int t = 0; t < 4; ++t) rv.s[t] = first + 8 * (t / 2) + 2 * q + t % 2 < seq.length ? rv.s[t] : 0;
       }
+      // scores are rounded before the maximum is taken off (not in one step with it): what is left of them
+      // is then 8 at most, whatever their size
       bool up = false;
       float x[NT][2];
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n) {
+        put2(sc[n], mul2(make_float2(sc[n][0], sc[n][1]), make_float2(f[n][0], f[n][1])));
+        put2(sc[n] + 2, mul2(make_float2(sc[n][2], sc[n][3]), make_float2(f[n][0], f[n][1])));
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          x[n][e] = fmaxf(sc[n][e], sc[n][2 + e]) * f[n][e];
-          up |= x[n][e] > m[n][e] + 8.0f;
+          x[n][e] = fmaxf(sc[n][e], sc[n][2 + e]);
+          up |= x[n][e] - m[n][e] > 8.0f;
         }
+      }
       if (__any_sync(0xFFFFFFFFu, up)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -489,8 +498,10 @@ __global__ void __launch_bounds__(kThreadsFew, Few<DP, NT>::PER_SM) few_kernel(A
       uint32_t pf[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
+        put2(sc[n], add2(make_float2(sc[n][0], sc[n][1]), make_float2(z[n][0], z[n][1])));
+        put2(sc[n] + 2, add2(make_float2(sc[n][2], sc[n][3]), make_float2(z[n][0], z[n][1])));
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[n][e] = layer::ex2(fmaf(sc[n][e], f[n][e & 1], z[n][e & 1]));
+        for (int e = 0; e < 4; ++e) sc[n][e] = layer::ex2(sc[n][e]);
         l[n][0] += sc[n][0] + sc[n][2];
         l[n][1] += sc[n][1] + sc[n][3];
         pf[n][0] = turned(pack_h2(sc[n][0], sc[n][1]));

@@ -1,0 +1,100 @@
+"""The attention operators where they are easily wrong: sizes of scores, weights and queries far apart,
+long contexts, infinities beside what passes.
+
+Tolerances.  A score is held to d = 2^-16 of sum |q k| |scale|, as in test_gpu_attention.py.  A
+weight is rounded to fp16 where it meets the values: 2^-11 of itself, or half of fp16's smallest
+step, 2^-25, where it is small; the row's largest stands there at 2^7 or above, so that this is
+2^-32 of it, whatever the number of keys.  With the exponential (2^-14) o is held to
+u |o| + (2^-11 + 2^-14 + 2 d) sum w |v| + 2^-32 sum |v| / sum exp(s - max), u = 2^-8 for bf16.
+"""
+import math
+
+import pytest
+import torch
+
+import nvfp4_bit_block_gb300 as nv
+from attention_oracle import rope64, sequence64, visible
+from test_gpu_attention import (BF, F32, T_SCORE, T_WEIGHT, U_OUT, Work, both_kernels, built, company, freqs, gen, ints,  # noqa: F401
+                                placed, rand, within)
+
+pytestmark = pytest.mark.gpu
+T_SMALL = 2.0 ** -32
+
+
+def check(w, q, r, scale=None, causal=True, window=0, sinks=0):
+    """o and lse of every row of the batch against the formula in 64 bits."""
+    scale = w.dim ** -0.5 if scale is None else scale
+    G = q.shape[1] // w.heads
+    at = 0
+    for b, (n, m) in enumerate(zip(w.lens, w.news)):
+        if m == 0:
+            continue
+        k, v = (t.transpose(0, 1) for t in sequence64(w.cache, w.table, b, n))  # heads, keys, values
+        see = visible(n, m, causal, window, sinks, q.device)
+        for h in range(q.shape[1]):
+            x, kh, vh = q[at:at + m, h].double(), k[h // G], v[h // G]
+            s = (x @ kh.t() * scale).masked_fill(~see, -math.inf)
+            top = s.amax(-1, keepdim=True).clamp(min=-1e300)
+            e = torch.exp(s - top)
+            total = e.sum(-1, keepdim=True)
+            d = T_SCORE * (x.abs() @ kh.abs().t() * abs(scale)).masked_fill(~see, 0.0).amax(-1, keepdim=True)
+            some = total > 0
+            total = torch.where(some, total, torch.ones_like(total))
+            o, lse = e @ vh / total, torch.where(some, top + total.log(), torch.full_like(top, -math.inf))
+            bar = U_OUT[BF] * o.abs() + (T_WEIGHT + 2 * d) * (e @ vh.abs() / total) + T_SMALL * (see.double() @ vh.abs() / total)
+            within(r.o[at:at + m, h], o, bar, f"o, sequence {b}, head {h}")
+            if r.lse is not None:
+                within(r.lse[at:at + m, h], lse[:, 0], (d + 2.0 ** -17 + 2.0 ** -23 * lse.abs().nan_to_num(0.0, posinf=0.0))[:, 0],
+                       f"lse, sequence {b}, head {h}")
+        at += m
+
+
+def attend(w, q, **kw):
+    st = ints([0])
+    r = nv.nvfp4_cache_attention(q, w.cache, *w.batch, want_lse=True, status=st, **kw)
+    assert st.item() == 0
+    check(w, q, r, **kw)
+    return r
+
+
+def put(w, k, v):
+    """Keys and values of every position of every sequence."""
+    starts = [0]
+    for n in w.lens:
+        starts.append(starts[-1] + n)
+    nv.nvfp4_cache_write(k, v, w.cache, ints(starts), w.lengths, w.table)
+
+
+# ---------------------------------------------------------------- attention
+
+
+SHAPES = [([300, 64, 1], [1, 1, 1], 2, 5, 128, 16), ([150, 90], [9, 30], 1, 3, 64, 16), ([270, 130], [200, 130], 2, 2, 96, 32),
+          ([400], [333], 1, 3, 256, 64)]
+
+
+@both_kernels
+@pytest.mark.parametrize("news", [[1, 1], [9, 30], [150, 180]])
+def test_scores_beyond_what_a_float_resolves(news):
+    """Scores of 2^20 and far more that differ by a few: whatever is left of their differences, the weights are none
+    that a sum of ones would show."""
+    w = Work([1500, 700], news, 1, 64, 16, (2.0 ** -5, 2.0 ** -5), seed=6)
+    k = torch.zeros((sum(w.lens), 1, 64), device="cuda")
+    k[..., 0] = 6.0
+    near = torch.tensor([0.0, 1.0, 2.0, 3.0, 4.0, 6.0], device="cuda")
+    put(w, k, torch.ones_like(k))
+    held = sequence64(w.cache, w.table, 0, 1)[1]  # what the cache has for 1, the same everywhere
+    for p in range(18, 100, 3):
+        k[..., 16] = near[torch.randint(0, 6, (sum(w.lens),), generator=gen(p), device="cuda")][:, None]
+        put(w, k, torch.ones_like(k))
+        q = torch.zeros((w.T, 3, 64), device="cuda")
+        q[..., 0] = torch.tensor([1.0, -1.5, 1.25], device="cuda") * 2.0 ** p
+        q[..., 16] = torch.tensor([1.0, 2.0, 4.0], device="cuda")
+        for f in (1.0, 2.0 ** min(p - 24, 8)):
+            q[..., 16] *= f
+            r = nv.nvfp4_cache_attention(q.to(BF), w.cache, *w.batch, scale=1.0, want_lse=True)
+            within(r.o, held.expand(r.o.shape), (U_OUT[BF] + T_WEIGHT) * held, f"2^{p}")
+            want = q[:, :, 0].double() * 6
+            within(r.lse, want, 2.0 ** -21 * want.abs() + 24 * q[..., 16].double() + 20, f"lse, 2^{p}")
+
+
+# ---------------------------------------------------------------- norm and rotation
