@@ -66,10 +66,18 @@ __device__ __forceinline__ Keys<CH> rows_keys(const AttendArgs& a, const Sequenc
   k.count = k.sinks + max(0, (int)(((uint32_t)max(end, 0) + (CH - 1)) / CH) - k.first);
   return k;
 }
-// lse of one row from its maximum and sum to base 2, both -Inf and 0 where it sees nothing.
-__device__ __forceinline__ float row_lse(float top, float l) {
+
+// Weights are 2^(s - m) with an offset m of the row's own.  m is 7 below the largest score when it moves, and
+// moves only where a score passes it by more than 15: weights lie below 2^15, where fp16 still holds them, and
+// most steps leave o alone.  As high as that, weights keep their digits down to 2^-21 of the largest and are
+// held to 2^-32 of it below; with the maximum itself as m a row with one key far above 65535 others, whose
+// value is zero, lost 3 % of its result at e^-17 and all of it at e^-20.
+constexpr float kLift = 7.0f, kMoves = 15.0f;
+
+// lse of one row from m and the sum of its weights, -Inf and 0 where it sees nothing.
+__device__ __forceinline__ float row_lse(float m, float l) {
   if (l == 0.0f) return -INFINITY;
-  return top == -INFINITY ? l : (top + log2f(l)) * 0.6931471805599453f;  // NaN leaves the maximum alone
+  return m == -INFINITY ? l : (m + log2f(l)) * 0.6931471805599453f;  // NaN leaves the maximum alone
 }
 // ---- fp16 products --------------------------------------------------------------------------
 

@@ -21,9 +21,6 @@
 // 9 + 2q the g-th eighth.  P leaves its product with keys along g and rows along q and enters the
 // next one the other way round: movmatrix turns it.
 //
-// The running maximum moves only where a score passes it by more than 2^8: weights stay below
-// 256, where fp16 holds them as well as below 1, and most steps leave o alone.
-//
 // Measured: the next token of 48 sequences of up to 16384 keys, 40 query heads on 8 of 128 values: 132 us
 // for 509 MB, 3.9 TB/s (57 % of the copy rate).  Issue slots bound it: about 430 instructions for 16
 // keys, 60 % of the slots busy.  Half of them unpack: 72 conversions and 64 products by scales, two
@@ -461,17 +458,17 @@ __global__ void __launch_bounds__(kThreadsFew, Few<DP, NT>::PER_SM) few_kernel(A
         for (int t = 0; t < 4; ++t) rv.s[t] = first + 8 * (t / 2) + 2 * q + t % 2 < seq.length ? rv.s[t] : 0;
       }
       // scores are rounded before the maximum is taken off (not in one step with it): what is left of them
-      // is then 8 at most, whatever their size
+      // is then kMoves at most, whatever their size
       bool up = false;
       float x[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        put2(sc[n], mul2(make_float2(sc[n][0], sc[n][1]), make_float2(f[n][0], f[n][1])));
-        put2(sc[n] + 2, mul2(make_float2(sc[n][2], sc[n][3]), make_float2(f[n][0], f[n][1])));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[n][e] = __fmul_rn(sc[n][e], f[n][e & 1]);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           x[n][e] = fmaxf(sc[n][e], sc[n][2 + e]);
-          up |= x[n][e] - m[n][e] > 8.0f;
+          up |= x[n][e] - m[n][e] > kMoves;
         }
       }
       if (__any_sync(0xFFFFFFFFu, up)) {
@@ -483,7 +480,7 @@ __global__ void __launch_bounds__(kThreadsFew, Few<DP, NT>::PER_SM) few_kernel(A
             float top = x[n][e];
 #pragma unroll
             for (int s = 4; s < 32; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, s));
-            top = fmaxf(top, m[n][e]);
+            top = fmaxf(top - kLift, m[n][e]);
             d[e] = top == m[n][e] ? 1.0f : layer::ex2(m[n][e] - top);
             m[n][e] = top;
             z[n][e] = top == -INFINITY ? 0.0f : -top;
@@ -498,10 +495,8 @@ __global__ void __launch_bounds__(kThreadsFew, Few<DP, NT>::PER_SM) few_kernel(A
       uint32_t pf[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        put2(sc[n], add2(make_float2(sc[n][0], sc[n][1]), make_float2(z[n][0], z[n][1])));
-        put2(sc[n] + 2, add2(make_float2(sc[n][2], sc[n][3]), make_float2(z[n][0], z[n][1])));
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[n][e] = layer::ex2(sc[n][e]);
+        for (int e = 0; e < 4; ++e) sc[n][e] = layer::ex2(__fadd_rn(sc[n][e], z[n][e & 1]));
         l[n][0] += sc[n][0] + sc[n][2];
         l[n][1] += sc[n][1] + sc[n][3];
         pf[n][0] = turned(pack_h2(sc[n][0], sc[n][1]));

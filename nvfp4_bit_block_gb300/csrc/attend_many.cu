@@ -13,8 +13,7 @@
 // Each tile has two buffers of S: the next block's scores are formed while this one's rows are at
 // their exponentials.  (128 keys at a time leave TMEM for one buffer and want registers moved to the
 // rows: a row's next scores then wait for both products, and the three prompts of the largest measured
-// case took as long.)  The running maximum moves only where a score passes it by more than 2^8, so that
-// O in TMEM is rarely touched between products.
+// case took as long.)
 //
 // Measured: prompts of 2731, 1818 and 905 tokens that end caches of 8192, 5454 and 2716 keys, 40 query
 // heads on 8 of 128 values: 547 us, 1.08 PFLOP/s (56 % of the measured bf16 rate).  For each 64 keys a
@@ -333,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
         float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * f, g = f;
         // A score times f and what is taken off it are one rounding, the maximum has one of its own: where
         // a step of that is no longer small, the row's scores are rounded alike, so that no weight passes
-        // 2^8.  (Always so, the largest measured case takes 570 us and not 548.)
+        // 2^15.  (Always so, the largest measured case takes 570 us and not 548.)
         const bool coarse = fabsf(high) > 0x1p20f && fabsf(high) < INFINITY;
         if (__any_sync(0xFFFFFFFFu, coarse)) {
           g = coarse ? 1.0f : f;
@@ -341,10 +340,10 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
 #pragma unroll
           for (int x = 0; x < BN; ++x) s[x] *= once;
         }
-        const bool up = high - m > 8.0f;
+        const bool up = high - m > kMoves;
         if (__any_sync(0xFFFFFFFFu, up)) {
-          const float d = up ? layer::ex2(m - high) : 1.0f;
-          if (up) m = high;
+          const float d = up ? layer::ex2(m - (high - kLift)) : 1.0f;
+          if (up) m = high - kLift;
           l0 = mul2(l0, make_float2(d, d));
           l1 = mul2(l1, make_float2(d, d));
           if (i > 0) {  // what O holds of the blocks before, once the last of them is in

@@ -68,8 +68,41 @@ def put(w, k, v):
 # ---------------------------------------------------------------- attention
 
 
+@both_kernels
+@pytest.mark.parametrize("gap", [8.0, 11.0, 13.5, 15.0, 17.0])
+@pytest.mark.parametrize("B,n,m,dim", [(16, 2048, 40, 64), (2, 9000, 40, 128), (3, 2500, 1, 256), (160, 900, 1, 32)])
+def test_one_key_outweighs_the_others(B, n, m, dim, gap):
+    """The first key's score lies `gap` above all others and its value is zero: the result is made of weights that are
+    e^-gap of the largest."""
+    w = Work([n - 7 * b % 300 for b in range(B)], [m] * B, 8 if B < 100 else 2, dim, 16, (2.0 ** -5, 2.0 ** -5), seed=1)
+    k = torch.zeros((sum(w.lens), w.heads, dim), device="cuda")
+    v = 1 + 0.25 * rand(k.shape, F32, 2)
+    at = 0
+    for length in w.lens:
+        k[at, :, 0] = 6.0
+        v[at] = 0.0
+        at += length
+    put(w, k, v)
+    q = rand((w.T, w.heads, dim), BF, 3)
+    q[..., 0] = gap / 6
+    attend(w, q, scale=1.0)
+
+
 SHAPES = [([300, 64, 1], [1, 1, 1], 2, 5, 128, 16), ([150, 90], [9, 30], 1, 3, 64, 16), ([270, 130], [200, 130], 2, 2, 96, 32),
           ([400], [333], 1, 3, 256, 64)]
+
+
+@both_kernels
+@pytest.mark.parametrize("scale", [0.3, -0.2, 1.7, 0.0, -0.0, 1e-6, -1e-30, 1e-38, 2.0 ** -149])
+@pytest.mark.parametrize("lens,news,heads,group,dim,page", SHAPES)
+def test_scales(lens, news, heads, group, dim, page, scale):
+    """Any factor of the scores: negative ones, none, and those that vanish; hidden keys stay hidden."""
+    w = Work(lens, news, heads, dim, page, seed=4)
+    w.fill()
+    q = rand((w.T, heads * group, dim), BF, 5)
+    attend(w, q, scale=scale)
+    attend(w, q, scale=scale, causal=False)
+    attend(w, q, scale=scale, window=37, sinks=5)
 
 
 @both_kernels
@@ -95,6 +128,24 @@ def test_scores_beyond_what_a_float_resolves(news):
             within(r.o, held.expand(r.o.shape), (U_OUT[BF] + T_WEIGHT) * held, f"2^{p}")
             want = q[:, :, 0].double() * 6
             within(r.lse, want, 2.0 ** -21 * want.abs() + 24 * q[..., 16].double() + 20, f"lse, 2^{p}")
+
+
+@both_kernels
+@pytest.mark.parametrize("lens,news,group,dim", [([100000, 5, 40000], [1, 1, 2], 4, 64), ([100000], [40], 2, 64),
+                                                 ([30000, 20000], [70, 1], 1, 128)])
+def test_long_contexts_with_few_keys_that_count(lens, news, group, dim):
+    """The weight sits on some forty keys, all along each sequence: none of its pieces can be lost or counted twice."""
+    w = Work(lens, news, 1, dim, 64, (2.0 ** -5, 2.0 ** -6), seed=11)
+    k, v = 0.1 * rand((sum(lens), 1, dim), F32, 12), rand((sum(lens), 1, dim), F32, 13)
+    at = 0
+    for n in lens:
+        for i in torch.linspace(0, max(n - max(news) - 1, 0), min(n, 41)).long().unique().tolist():
+            k[at + i, 0, 0] = 6.0
+        at += n
+    put(w, k, v)
+    q = rand((w.T, group, dim), BF, 14)
+    q[..., 0] = 3.0
+    attend(w, q, scale=1.0)
 
 
 # ---------------------------------------------------------------- norm and rotation
