@@ -194,10 +194,11 @@ NVFP4_API int nvfp4_cache_read(const nvfp4_tokens* k, const nvfp4_tokens* v, int
  *   scale     finite; scale * alpha * (a row's largest query) stays finite in fp32
  *   window    0 (no window) .. 2^31 - 1;  sinks 0 .. 2^31 - 1, 0 without a window
  *   workspace_dev  nvfp4_cache_attention_workspace(T, q_heads, heads, dim, sequences) bytes
- * The products take bf16 queries (scaled by a power of two per row into fp16) and the
- * cache's values exactly; sums are fp32; a weight is rounded to fp16 where it meets the
- * values (half a step: 2^-11 of the weight, or 2^-32 of the row's largest weight where
- * that is more), not where it is summed.
+ * The products take bf16 queries (scaled by a power of two per row into fp16: exactly down
+ * to 2^-31 of the row's largest, within 2^-39 of it below) and the cache's values exactly;
+ * sums are fp32.  A weight is rounded to fp16 where it meets the values (half a step: 2^-11
+ * of the weight, or 2^-32 of the row's largest weight where that is more), not where it is
+ * summed.
  * NaN or Inf in a query makes that row NaN (or whatever their formula gives) and touches no other.
  * Errors: SHAPE, NULL, ALIGN, FLAGS (scale; window or sinks without causal; sinks without
  * a window; negative ones), CUDA.

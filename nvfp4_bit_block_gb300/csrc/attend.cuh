@@ -105,15 +105,12 @@ __device__ __forceinline__ uint32_t scales2(uint32_t two) {  // two scale bytes 
   return r;
 }
 // Queries go to fp16 scaled by a power of two per row.  From the bits of the row's largest
-// magnitude (they order as the numbers do, NaN above all): what brings it below 4, and what
-// undoes that.
-__device__ __forceinline__ float query_down(uint32_t top) {
-  const int e = min(max((int)(top >> 23), 1), 253);
-  return __int_as_float((254 - e) << 23);
-}
-__device__ __forceinline__ float query_up(uint32_t top) {
-  return __int_as_float(min(max((int)(top >> 23), 1), 253) << 23);
-}
+// magnitude (they order as the numbers do, NaN above all): what brings it to 2^14 .. 2^15 (bf16's last binade to
+// below 2^16, which fp16 holds), and what undoes that.  So high, all eight bits of a value are there down
+// to 2^-31 of the largest; with the largest below 4 they went from 2^-18 on.
+__device__ __forceinline__ uint32_t query_exponent(uint32_t top) { return min(max(top >> 23, 15u), 253u); }
+__device__ __forceinline__ float query_down(uint32_t top) { return __uint_as_float((268u - query_exponent(top)) << 23); }
+__device__ __forceinline__ float query_up(uint32_t top) { return __uint_as_float((query_exponent(top) - 14u) << 23); }
 __device__ __forceinline__ uint32_t larger_magnitude(uint32_t top, uint32_t two_bf16) {
   return max(top, max(two_bf16 << 16 & 0x7FFF0000u, two_bf16 & 0x7FFF0000u));
 }

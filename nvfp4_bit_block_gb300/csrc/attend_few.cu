@@ -81,10 +81,6 @@ __device__ __forceinline__ void mma(float* d, uint32_t a0, uint32_t a1, uint32_t
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void put2(float* x, float2 v) {
-  x[0] = v.x;
-  x[1] = v.y;
-}
 // An 8 x 8 matrix of fp16, two of row lane / 4 in each lane, to its transpose.
 __device__ __forceinline__ uint32_t turned(uint32_t v) {
   uint32_t r;

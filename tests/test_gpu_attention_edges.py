@@ -131,6 +131,21 @@ def test_scores_beyond_what_a_float_resolves(news):
 
 
 @both_kernels
+@pytest.mark.parametrize("news", [[1, 1], [9, 30], [150, 180]])
+@pytest.mark.parametrize("down", [10, 17, 22, 27])
+def test_queries_whose_values_lie_far_apart(news, down):
+    """A query's largest value meets zeros only: the scores are those of values 2^-down of it, which keep their digits."""
+    w = Work([400, 200], news, 2, 64, 16, seed=7)
+    k, v = rand((600, 2, 64), F32, 8), rand((600, 2, 64), F32, 9)
+    k[..., :16] = 0.0
+    put(w, k, v)
+    for size in (1.0, 2.0 ** 100, 2.0 ** -90):
+        q = rand((w.T, 6, 64), F32, 10) * size
+        q[..., 3] = 2.0 ** down * size
+        attend(w, q.to(BF), scale=0.125 / size)
+
+
+@both_kernels
 @pytest.mark.parametrize("lens,news,group,dim", [([100000, 5, 40000], [1, 1, 2], 4, 64), ([100000], [40], 2, 64),
                                                  ([30000, 20000], [70, 1], 1, 128)])
 def test_long_contexts_with_few_keys_that_count(lens, news, group, dim):
