@@ -5,9 +5,10 @@
 // shared memory once for all heads, and a thread keeps those of its pairs for all heads of its
 // token.  The next heads' loads are on their way while these are turned, the next group's too.  Queries
 // first, then keys: one set of weights at a time.
-// Measured: 16384 tokens x 48 heads x 128 values bf16 74.6 us, 5.4 TB/s (80 % of the copy rate).  Four
+// Measured: 16384 tokens x 48 heads x 128 values bf16 74.2 us, 5.4 TB/s (80 % of the copy rate).  Four
 // heads on their way by asynchronous copies through shared memory change nothing (75.3): instructions bound it.
 #include <cmath>
+#include <type_traits>
 
 #include "rope_common.cuh"
 
@@ -61,26 +62,32 @@ __global__ void __launch_bounds__(kThreads, 2) rope_kernel(RopeArgs a, int lanes
         else
           fetch(tt + step, at.head);
         TO* to = static_cast<TO*>(out.p) + tt * out.ts + (int64_t)h0 * out.hs;
+        auto finish = [&](auto ALL) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          float x[SLOTS][2 * V];
-          now[u].widen(x);
-          if (a.norm) {
-            float2 q = make_float2(0.0f, 0.0f);
+          for (int u = 0; u < U; ++u) {
+            float x[SLOTS][2 * V];
+            now[u].widen(x);
+            if (a.norm) {
+              float2 q = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int i = 0; i < SLOTS; ++i)
+              for (int i = 0; i < SLOTS; ++i)
 #pragma unroll
-              for (int e = 0; e < 2 * V; e += 2) q = fma2(two(x[i] + e), two(x[i] + e), q);
-            const float r = rsqrtf(fmaf(lanes_sum(q.x + q.y, lanes), share, a.eps));
+                for (int e = 0; e < 2 * V; e += 2) q = fma2(two(x[i] + e), two(x[i] + e), q);
+              const float r = rsqrtf(fmaf(lanes_sum(q.x + q.y, lanes), share, a.eps));
 #pragma unroll
-            for (int i = 0; i < SLOTS; ++i)
+              for (int i = 0; i < SLOTS; ++i)
 #pragma unroll
-              for (int e = 0; e < 2 * V; e += 2)
-                put(x[i] + e, mul2(two(x[i] + e), mul2(two(gamma[i] + e), make_float2(r, r))));
+                for (int e = 0; e < 2 * V; e += 2)
+                  put(x[i] + e, mul2(two(x[i] + e), mul2(two(gamma[i] + e), make_float2(r, r))));
+            }
+            turn_pairs<ALL.value>(s, t, x);
+            if (there && h0 + u * at.per < H) store_head(s, to + (int64_t)(u * at.per) * out.hs, x);
           }
-          turn_pairs<V, SLOTS, INTER>(t, x);
-          if (there && h0 + u * at.per < H) store_head(s, to + (int64_t)(u * at.per) * out.hs, x);
-        }
+        };
+        if (2 * a.rotated == a.D)
+          finish(std::true_type());
+        else
+          finish(std::false_type());
       }
     }
   }

@@ -71,7 +71,10 @@ __global__ void __launch_bounds__(kThreads, 2) rope_grad_kernel(RopeGradArgs b, 
           else
             fetch(tt + step, at.head);
         }
-        turn_pairs<V, SLOTS, INTER>(t, g);
+        if (2 * a.rotated == a.D)
+          turn_pairs<true>(s, t, g);
+        else
+          turn_pairs<false>(s, t, g);
         float2 q2 = make_float2(0.0f, 0.0f), p2 = q2;
 #pragma unroll
         for (int i = 0; i < SLOTS; ++i)

@@ -234,7 +234,7 @@ struct Angles {
     for (int i = 0; i < SLOTS; ++i)
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float2 t = at.pair[i] >= 0 ? cs[at.pair[i] + e] : make_float2(1.0f, 0.0f);  // passes
+        const float2 t = at.pair[i] >= 0 ? cs[at.pair[i] + e] : make_float2(1.0f, 0.0f);
         c[i][e] = t.x;
         s[i][e] = t.y;
       }
@@ -248,24 +248,31 @@ __device__ __forceinline__ void put(float* x, float2 v) {
   x[1] = v.y;
 }
 template <int V, int SLOTS, bool INTER>
-__device__ __forceinline__ void turn_pairs(const Angles<V, SLOTS>& t, float x[SLOTS][2 * V]) {
+__device__ __forceinline__ void turn_slot(const Angles<V, SLOTS>& t, int i, float x[2 * V]) {
+  if constexpr (INTER || V == 1) {
 #pragma unroll
-  for (int i = 0; i < SLOTS; ++i) {
-    if constexpr (INTER || V == 1) {
+    for (int e = 0; e < V; ++e) {
+      const float2 a = two(x + 2 * e), c = make_float2(t.c[i][e], t.c[i][e]), s = make_float2(t.s[i][e], t.s[i][e]);
+      put(x + 2 * e, fma2(make_float2(-a.y, a.x), s, mul2(a, c)));
+    }
+  } else {
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float2 a = two(x[i] + 2 * e), c = make_float2(t.c[i][e], t.c[i][e]), s = make_float2(t.s[i][e], t.s[i][e]);
-        put(x[i] + 2 * e, fma2(make_float2(-a.y, a.x), s, mul2(a, c)));
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < V; e += 2) {
-        const float2 a = two(x[i] + e), b = two(x[i] + V + e), c = two(t.c[i] + e), s = two(t.s[i] + e);
-        put(x[i] + e, fma2(make_float2(-b.x, -b.y), s, mul2(a, c)));
-        put(x[i] + V + e, fma2(a, s, mul2(b, c)));
-      }
+    for (int e = 0; e < V; e += 2) {
+      const float2 a = two(x + e), b = two(x + V + e), c = two(t.c[i] + e), s = two(t.s[i] + e);
+      put(x + e, fma2(make_float2(-b.x, -b.y), s, mul2(a, c)));
+      put(x + V + e, fma2(a, s, mul2(b, c)));
     }
   }
+}
+// What passes is left alone: turned by nothing, an infinity in it would reach the value beside it.
+// ALL: nothing passes, the same for the whole kernel.  (A lane's own question in every slot costs
+// the gradient of 16384 tokens 5 %.)
+template <bool ALL, int V, int SLOTS, bool INTER>
+__device__ __forceinline__ void turn_pairs(const Slots<V, SLOTS, INTER>& at, const Angles<V, SLOTS>& t,
+                                           float x[SLOTS][2 * V]) {
+#pragma unroll
+  for (int i = 0; i < SLOTS; ++i)
+    if (ALL || at.pair[i] >= 0) turn_slot<V, SLOTS, INTER>(t, i, x[i]);
 }
 
 // Values per vector at these sizes and this alignment: every vector of a slot begins at a

@@ -164,3 +164,61 @@ def test_long_contexts_with_few_keys_that_count(lens, news, group, dim):
 
 
 # ---------------------------------------------------------------- norm and rotation
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("xt,yt", [(BF, BF), (F32, F32), (F32, BF), (BF, F32)])
+@pytest.mark.parametrize("D,R,tp,hp,off", [(128, 32, 0, 0, 0), (96, 24, 4, 4, 4), (64, 10, 2, 2, 2), (66, 9, 1, 1, 1),
+                                           (128, 0, 0, 0, 0), (34, 17, 0, 0, 0)])
+def test_what_passes_is_what_came(D, R, tp, hp, off, xt, yt, inter):
+    """Values outside the rotated part come out as they went in, infinities and NaN beside them or not; in the rotated
+    part such a value reaches its pair alone."""
+    T, H = 5, 3
+    x = rand((T, H, D), xt, 15)
+    odd = [float("inf"), float("nan"), float("-inf")]
+    for t in range(T):
+        for h in range(H):
+            for c in range(2 * R, D, 5 + t):
+                x[t, h, c] = odd[(t + h + c) % 3]
+    if R:
+        x[1, 1, 1 if inter else 0] = float("inf")
+        x[2, 0, 2 * R - 1] = float("nan")
+    pos, f = ints([0, 1, 7, 900, 123456]), freqs(R)
+    q = placed(x, tp, hp, off)[1]
+    out = placed(torch.zeros((T, H, D), dtype=yt, device="cuda"), tp, hp, off)[1]
+    for back in (False, True):
+        if back:
+            got = nv.nvfp4_qk_rope_backward(q, q, None, None, pos, f, norm=False, interleaved=inter,
+                                            out_q=out if xt is yt else None).dq
+            turn = -f
+        else:
+            got = nv.nvfp4_qk_rope(q, q, pos, f, norm=False, interleaved=inter, out_q=out, out_dtype=yt).q
+            turn = f
+        want = x[..., 2 * R:].to(got.dtype)
+        passed = got[..., 2 * R:]
+        assert bool(((passed == want) | (passed.isnan() & want.isnan())).all())
+        clean = torch.where(x.isfinite(), x, torch.zeros_like(x))
+        ref, size = rope64(clean, pos, turn, None, 0, False, inter)
+        keep = torch.ones((T, H, D), dtype=torch.bool, device="cuda")
+        keep[..., 2 * R:] = False
+        if R:
+            for t, h, i in ((1, 1, 0), (2, 0, R - 1)):
+                keep[t, h, (2 * i if inter else i)] = keep[t, h, (2 * i + 1 if inter else i + R)] = False
+        within(got[keep], ref[keep], U_OUT[got.dtype] * ref[keep].abs() + 2.0 ** -18 * size[keep], "turned")
+
+
+@pytest.mark.parametrize("D,R,hp", [(128, 32, 0), (96, 24, 1), (64, 10, 2)])
+def test_an_infinite_gradient_reaches_its_own_weight_alone(D, R, hp):
+    """Of the gradient of the norm's weights, where what passes holds an infinity."""
+    T, H = 9, 2
+    x, dy = placed(rand((T, H, D), F32, 16), 0, hp, 0)[1], placed(rand((T, H, D), F32, 17), 0, hp, 0)[1]
+    pos, f = torch.arange(T, device="cuda", dtype=torch.int32), freqs(R)
+    want = nv.nvfp4_qk_rope_backward(dy, dy, x, x, pos, f).dgamma_q
+    for c in (2 * R, D - 1):
+        odd = dy.clone()
+        odd[4, 1, c] = float("inf")
+        odd = placed(odd, 0, hp, 0)[1]
+        got = nv.nvfp4_qk_rope_backward(odd, dy, x, x, pos, f).dgamma_q
+        assert bool(got[c].isinf())
+        got[c] = want[c]
+        assert torch.equal(got, want)
