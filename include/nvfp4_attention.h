@@ -61,7 +61,7 @@ typedef struct {
  *   codes and their strides: multiples of 16 bytes; scales and theirs: of 2 bytes;
  *   no stride may be less than what it steps over makes necessary for rows not to
  *   overlap: any order of page, head and row is accepted; strides of pages and rows are
- *   below 2^32.
+ *   below 2^32, those of heads at most 2^45.
  */
 typedef struct {
   uint8_t *k_codes, *k_scales, *v_codes, *v_scales;

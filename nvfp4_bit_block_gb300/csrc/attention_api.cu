@@ -17,8 +17,9 @@ uintptr_t elem(int is_bf16) { return is_bf16 ? 2 : 4; }
 int launch_status(cudaError_t e) { return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA; }
 
 // Sizes are bounded so that token and head counts fit 32 bits; offsets are formed in
-// 64 bits everywhere, and a stride times a count stays far below 2^63.
-constexpr int64_t kMaxStride = INT64_MAX / 8 / INT32_MAX;
+// 64 bits everywhere, and a stride times a count stays far below 2^63.  A cache's heads are at
+// most 65535, so they may lie further apart than tokens.
+constexpr int64_t kMaxStride = INT64_MAX / 8 / INT32_MAX, kMaxHeadStride = (int64_t)1 << 45;
 bool bad_tokens(const nvfp4_tokens* t) {
   return t->token_stride < 0 || t->head_stride < 0 || t->token_stride > kMaxStride || t->head_stride > kMaxStride;
 }
@@ -71,7 +72,7 @@ int check_cache(const nvfp4_kv_cache* c, const nvfp4_batch* b, int64_t T, const 
   for (int k = 0; k < 2; ++k) {
     int o[3] = {0, 1, 2};  // by stride, smallest first; axes of one entry are not stepped over
     for (int i = 0; i < 3; ++i)  // pages and rows are stepped over in the kernels' loops
-      if (strides[k][i] < 0 || strides[k][i] > (i == 1 ? kMaxStride : (int64_t)UINT32_MAX)) return NVFP4_ERR_SHAPE;
+      if (strides[k][i] < 0 || strides[k][i] > (i == 1 ? kMaxHeadStride : (int64_t)UINT32_MAX)) return NVFP4_ERR_SHAPE;
     for (int i = 0; i < 2; ++i)
       for (int j = 0; j < 2 - i; ++j)
         if (strides[k][o[j]] > strides[k][o[j + 1]]) {
@@ -79,9 +80,9 @@ int check_cache(const nvfp4_kv_cache* c, const nvfp4_batch* b, int64_t T, const 
           o[j] = o[j + 1];
           o[j + 1] = x;
         }
-    int64_t below = k == 0 ? c->dim / 2 : c->dim / 16;
+    uint64_t below = k == 0 ? c->dim / 2 : c->dim / 16;  // at most 2^48 + 2^61 + 2^63
     for (int i = 0; i < 3; ++i) {
-      const int64_t n = counts[o[i]], st = strides[k][o[i]];
+      const uint64_t n = (uint64_t)counts[o[i]], st = (uint64_t)strides[k][o[i]];
       if (n <= 1) continue;
       if (st < below) return NVFP4_ERR_SHAPE;
       below += (n - 1) * st;

@@ -163,6 +163,34 @@ def test_long_contexts_with_few_keys_that_count(lens, news, group, dim):
     attend(w, q, scale=1.0)
 
 
+def test_heads_that_lie_far_apart():
+    """Heads first, 2^32 bytes and more from one to the next."""
+    H, D = 3, 128
+    w = Work([200, 90], [70, 1], H, D, 64, seed=18, order="hpsd")
+    w.fill()
+
+    def apart(t, step):
+        P, H, S, n = t.shape
+        base = torch.empty((H - 1) * step + P * S * n, dtype=torch.uint8, device="cuda")
+        v = base.as_strided((P, H, S, n), (S * n, step, n, 1))
+        v.copy_(t)
+        return v
+    c = w.cache
+    far = nv.KVCache(apart(c.k_codes, 2 ** 32 + 4096), apart(c.k_scales, 2 ** 31 + 1024), apart(c.v_codes, 2 ** 32 + 4096),
+                     apart(c.v_scales, 2 ** 31 + 1024), c.alpha)
+    q = rand((w.T, 2 * H, D), BF, 19)
+    for batch in (w.batch, (w.starts[1:] - w.starts[1], w.lengths[1:], w.table[1:])):
+        m = int(batch[0][-1])
+        want, got = (nv.nvfp4_cache_attention(q[:m], x, *batch, want_lse=True) for x in (c, far))
+        assert torch.equal(got.o, want.o) and torch.equal(got.lse, want.lse)
+        a, b = (nv.nvfp4_cache_read(x, *batch, tokens=m) for x in (c, far))
+        assert torch.equal(a.k, b.k) and torch.equal(a.v, b.v)
+    k, v = rand((w.T, H, D), BF, 20), rand((w.T, H, D), BF, 21)
+    for x in (c, far):
+        nv.nvfp4_cache_write(k, v, x, *w.batch)
+    assert all(torch.equal(a, b) for a, b in zip(c.tensors(), far.tensors()))
+
+
 # ---------------------------------------------------------------- norm and rotation
 
 
