@@ -187,7 +187,7 @@ def build_layer_selftest(force: bool = False, verbose: bool = False) -> str:
 
 
 def build_attention_selftest(force: bool = False, verbose: bool = False) -> str:
-    """The test-only build of the attention kernel for many rows whose keys never come; returns its path."""
+    """The test-only build of the attention kernel for many rows whose keys stop coming; returns its path."""
     srcs = [os.path.join(SELFTEST_DIR, "nvfp4_attention_selftest.cu"), os.path.join(CSRC, "attend_many.cu")]
     return _build_lib(srcs, os.path.join(SELFTEST_BUILD, "attention"), ATTENTION_SELFTEST_LIB, force, verbose,
                       [*LAYER_NVCC_FLAGS, "-DNVFP4_TEST_NO_COPIES"])

@@ -455,9 +455,10 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
       if (round > 0 && !warp_wait(bar(kKEmpty + st), (round - 1) & 1, &stop)) break;
       store_raw<DP>(sm + S::KS + st * S::STAGE, r, half, D, k);
       fence_async_smem();
-#ifndef NVFP4_TEST_NO_COPIES  // the test build's keys never come
-      arrive(bar(kKFull + st));
+#ifdef NVFP4_TEST_NO_COPIES  // the test build's keys come no more from the fifth block on
+      if (i < 4)
 #endif
+        arrive(bar(kKFull + st));
       if (i + 1 < nb) {
         on = place();
         load_raw<DP>(c.kc + co, c.ks + so, on, half, D, k);
@@ -528,8 +529,10 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(AttendArgs a) {
               if (ok && i + u + 2 < nb) ok = product_qk(t, (u + 2) % 4, u < 2 ? fours : fours ^ 1);
             }
       }
+      // What has been issued is waited for also where the block has given up: the tensor memory that it
+      // writes is freed behind this.
       commit(leader, bar(kDrain));
-      warp_wait(bar(kDrain), 0, &stop);
+      if (!tma::wait(bar(kDrain), 0)) stop = 1;
     }
   }
   __syncwarp();

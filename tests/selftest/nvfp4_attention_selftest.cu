@@ -1,5 +1,5 @@
 // nvfp4_attention_selftest.cu -- test-only entry of the attention kernel for many rows in a
-// build whose filling warps never report a block (NVFP4_TEST_NO_COPIES): its waits run out.
+// build whose filling warps report four blocks of keys and no more (NVFP4_TEST_NO_COPIES): its waits run out.
 #include <cuda_runtime.h>
 
 #include "attend.cuh"

@@ -7,12 +7,14 @@ step, 2^-25, where it is small; the row's largest stands there at 2^7 or above, 
 2^-32 of it, whatever the number of keys.  With the exponential (2^-14) o is held to
 u |o| + (2^-11 + 2^-14 + 2 d) sum w |v| + 2^-32 sum |v| / sum exp(s - max), u = 2^-8 for bf16.
 """
+import ctypes
 import math
 
 import pytest
 import torch
 
 import nvfp4_bit_block_gb300 as nv
+from nvfp4_bit_block_gb300.build import build_attention_selftest
 from attention_oracle import rope64, sequence64, visible
 from test_gpu_attention import (BF, F32, T_SCORE, T_WEIGHT, U_OUT, Work, both_kernels, built, company, freqs, gen, ints,  # noqa: F401
                                 placed, rand, within)
@@ -189,6 +191,28 @@ def test_heads_that_lie_far_apart():
     for x in (c, far):
         nv.nvfp4_cache_write(k, v, x, *w.batch)
     assert all(torch.equal(a, b) for a, b in zip(c.tensors(), far.tensors()))
+
+
+@pytest.mark.parametrize("n,m,dim", [(900, 200, 128), (321, 300, 256)])
+def test_blocks_that_give_up_with_products_behind_them(n, m, dim):
+    """A build whose keys stop coming after four blocks: what was issued is waited for before the tensor memory is freed,
+    and the calls behind it, one of them another user of that memory, have all of it."""
+    L = ctypes.CDLL(build_attention_selftest())
+    w = Work([n], [m], 2, dim, 16, seed=22)
+    w.fill()
+    q, st = rand((m, 4, dim), BF, 23), ints([0])
+    o, p, c = torch.zeros_like(q), ctypes.c_void_p, w.cache
+    flags = nv.ROWWISE | nv.SF_SWIZZLED
+    x = rand((300, 256), BF, 24)
+    z = nv.nvfp4_quantize(x, nv.nvfp4_amax(x, flags), flags)
+    linear = lambda: nv.nvfp4_linear(z.q_row, z.s_row, z.alpha[0:1], z.q_row, z.s_row, z.alpha[0:1]).d
+    want = linear().clone()
+    args = [p(t.data_ptr()) for t in (q, o, c.k_codes, c.k_scales, c.v_codes, c.v_scales, c.alpha, w.starts, w.lengths, w.table)]
+    torch.cuda.synchronize()
+    assert L.nvfp4_selftest_attend_many(*args, m, 2, 2, dim, 16, w.table.shape[1], p(st.data_ptr())) == 0
+    d = linear()
+    assert st.item() == -8 and torch.equal(d, want)
+    check(w, q, nv.nvfp4_cache_attention(q, c, *w.batch, want_lse=True))
 
 
 # ---------------------------------------------------------------- norm and rotation
