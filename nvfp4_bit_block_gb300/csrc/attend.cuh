@@ -59,7 +59,7 @@ __device__ __forceinline__ Keys<CH> rows_keys(const AttendArgs& a, const Sequenc
       const int low = (int)max((int64_t)0, (int64_t)p0 - a.window + 1);
       k.all_from = (int)max((int64_t)0, (int64_t)p1 - a.window + 1);
       k.all_sinks = a.sinks;
-      k.sinks = (max(0, min(min(a.sinks, low), end)) + (CH - 1)) / CH;
+      k.sinks = (int)(((uint32_t)max(0, min(min(a.sinks, low), end)) + (CH - 1)) / CH);
       k.first = max(low / CH, k.sinks);
     }
   }

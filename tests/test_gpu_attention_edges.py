@@ -193,6 +193,46 @@ def test_heads_that_lie_far_apart():
     assert all(torch.equal(a, b) for a, b in zip(c.tensors(), far.tensors()))
 
 
+@pytest.mark.parametrize("length", [2 ** 31 - 1, 2 ** 31 - 40, 2 ** 31 - 65])
+@pytest.mark.parametrize("window,sinks", [(1, 2 ** 31 - 1), (40, 2 ** 31 - 70), (2 ** 31 - 1, 5), (100, 100)])
+def test_the_longest_contexts(length, window, sinks):
+    """Positions up to the last that 32 bits hold, on one page again and again.  2^31 equal rounds of the page's weights
+    are summed in fp32, at most 2^17 of them one after another in a lane (2^27 chunks of 16 keys in 4 x 760 warps):
+    off by 2^-7 where the roundings all go one way."""
+    page, D = 65536, 32
+    w = Work([page], [1], 1, D, page, seed=25)
+    w.fill()
+    q = rand((1, 2, D), BF, 26)
+    table = w.table[:, :1].expand(1, 32768).contiguous()
+    st = ints([0])
+    r = nv.nvfp4_cache_attention(q, w.cache, w.starts, ints([length]), table, window=window, sinks=sinks, want_lse=True, status=st)
+    assert st.item() == 0
+    k, v = (t[:, 0] for t in sequence64(w.cache, w.table, 0, page))
+    # how often each of the page's keys is visible
+    often = torch.zeros(page, dtype=torch.float64, device="cuda")
+
+    def count(a, b):  # positions a .. b - 1
+        if b <= a:
+            return
+        first, last = a // page, (b - 1) // page
+        if first == last:
+            often[a % page:(b - 1) % page + 1] += 1
+        else:
+            often[a % page:] += 1
+            often[:(b - 1) % page + 1] += 1
+            often.add_(last - first - 1)
+    low = max(0, length - window)
+    count(low, length)
+    count(0, min(sinks, low))
+    s = q[0].double() @ k.t() * D ** -0.5
+    e = torch.exp(s - s.amax(-1, keepdim=True)) * often
+    total = e.sum(-1, keepdim=True)
+    long = 2.0 ** -7 if length - low + min(sinks, low) > 2 ** 20 else 0.0
+    o = e @ v / total
+    within(r.o[0], o, U_OUT[BF] * o.abs() + (T_WEIGHT + 2.0 ** -12 + 2 * long) * (e @ v.abs() / total), "o")
+    within(r.lse[0], (s.amax(-1, keepdim=True) + total.log())[:, 0], 2.0 ** -13 + long, "lse")
+
+
 @pytest.mark.parametrize("n,m,dim", [(900, 200, 128), (321, 300, 256)])
 def test_blocks_that_give_up_with_products_behind_them(n, m, dim):
     """A build whose keys stop coming after four blocks: what was issued is waited for before the tensor memory is freed,
