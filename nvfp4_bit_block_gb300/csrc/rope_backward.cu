@@ -123,10 +123,20 @@ __global__ void __launch_bounds__(kThreads, 2) rope_grad_kernel(RopeGradArgs b, 
   }
 }
 
+// Tokens that a block takes at a time: up to four, so that the blocks of queries and those of keys are all on the GPU
+// at once, as far as four will do, and eight of many.  (515 tokens x 12 heads of 96 fp32: 9.3 us; by two, as
+// the forward pass takes them, 516 blocks follow each other in two rounds, 11.3.  1000 tokens by eight 11.0 and
+// not 13.4, but 700 x 48 heads of 128 bf16 17.0 and not 14.4.)
+static int grad_tokens_of(int64_t T) {
+  int n = 1;
+  while (n < 4 && 2 * T > (int64_t)n * kBlocks) n *= 2;
+  return T > 4 * kBlocks ? 8 : n;
+}
+
 // Blocks: enough to fill the GPU, and so many that a thread adds at most 512 heads one after
 // another.
 static int64_t blocks_of(int64_t T, int H) {
-  const int tokens = tokens_of(T);
+  const int tokens = grad_tokens_of(T);
   const int64_t groups = (T + tokens - 1) / tokens, per_group = H;
   return std::min(groups, std::max<int64_t>(kBlocks, (groups * per_group + 511) / 512));
 }
@@ -134,7 +144,7 @@ static int64_t blocks_of(int64_t T, int H) {
 template <int V, bool INTER, typename TG, typename TX>
 cudaError_t launch(const RopeGradArgs& b, cudaStream_t s) {
   const RopeArgs& a = b.r;
-  const int sums = b.dgamma_q || b.dgamma_k, tokens = tokens_of(a.T);
+  const int sums = b.dgamma_q || b.dgamma_k, tokens = grad_tokens_of(a.T);
   const int64_t blocks = blocks_of(a.T, std::max(a.Hq, a.Hk));
   const int smem = a.rotated * 8 + std::max(2 * tokens * a.rotated * (int)sizeof(float2), 8 * a.D * (int)sizeof(float));
   const cudaError_t e = launch_early(rope_grad_kernel<V, INTER, TG, TX>, dim3((unsigned)blocks, passes_apart((a.T + tokens - 1) / tokens)), kThreads, smem, s, b,

@@ -297,8 +297,8 @@ inline int lanes_of(int V, int D, int rotated) {
 }
 // Tokens that a block takes at a time: up to eight, so that a thread of 8 lanes has every fourth
 // head and several on their way; few tokens are spread out, so that no block has two groups.  Where
-// few blocks do that, queries and keys go to blocks of their own (515 tokens x 12 heads of 96 fp32,
-// backward: 13.5 us one after the other in blocks of one token).
+// few blocks do that, queries and keys go to blocks of their own.  (The gradient, which leaves a row of
+// sums for each block, has its own number of tokens.)
 constexpr int kBlocks = 152 * 2;
 inline int tokens_of(int64_t T) {
   int n = 1;

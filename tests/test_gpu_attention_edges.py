@@ -14,9 +14,10 @@ import pytest
 import torch
 
 import nvfp4_bit_block_gb300 as nv
+from nvfp4_bit_block_gb300.attention import Tokens
 from nvfp4_bit_block_gb300.build import build_attention_selftest
 from attention_oracle import rope64, sequence64, visible
-from test_gpu_attention import (BF, F32, T_SCORE, T_WEIGHT, U_OUT, Work, both_kernels, built, company, freqs, gen, ints,  # noqa: F401
+from test_gpu_attention import (BF, F32, T_SCORE, T_WEIGHT, U_OUT, Work, both_kernels, built, check_rope_grad, company, freqs, gen, ints,  # noqa: F401
                                 placed, rand, within)
 
 pytestmark = pytest.mark.gpu
@@ -314,3 +315,26 @@ def test_an_infinite_gradient_reaches_its_own_weight_alone(D, R, hp):
         assert bool(got[c].isinf())
         got[c] = want[c]
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("T", [151, 152, 153, 304, 305, 515, 608, 609, 1216, 1217])
+def test_gradients_where_blocks_take_more_tokens(T):
+    """Numbers of tokens around those at which a block takes two, four and eight; guard bytes around a workspace of exactly
+    the size that the C ABI asks for."""
+    Hq, Hk, D, R = 5, 2, 64, 32
+    q, k, dq, dk = (rand((T, h, D), F32, 27 + i) for i, h in enumerate((Hq, Hk, Hq, Hk)))
+    g, pos, f = rand((D,), F32, 31, 0.2, 1.0), torch.arange(T, device="cuda", dtype=torch.int32), freqs(R)
+    r = nv.nvfp4_qk_rope_backward(dq, dk, q, k, pos, f, g, g)
+    check_rope_grad(dq, q, r.dq, r.dgamma_q, pos, f, g, 1e-6, True, False, "q")
+    check_rope_grad(dk, k, r.dk, r.dgamma_k, pos, f, g, 1e-6, True, False, "k")
+    L = nv.attention_lib()
+    n = L.nvfp4_qk_rope_backward_workspace(T, Hq, Hk, D)
+    ws = torch.full((n + 512,), 0xA5, dtype=torch.uint8, device="cuda")
+    oq, ok, gq, gk = torch.empty_like(q), torch.empty_like(k), torch.empty(D, device="cuda"), torch.empty(D, device="cuda")
+    tok = lambda t: ctypes.byref(Tokens(t.data_ptr(), t.stride(0), t.stride(1)))
+    assert L.nvfp4_qk_rope_backward(tok(dq), tok(dk), 0, tok(q), tok(k), 0, T, Hq, Hk, D, R, 0, pos.data_ptr(), f.data_ptr(), 1,
+                                    1e-6, g.data_ptr(), g.data_ptr(), 0, tok(oq), tok(ok), gq.data_ptr(), gk.data_ptr(),
+                                    ws.data_ptr() + 256, n, torch.cuda.current_stream().cuda_stream) == 0
+    for a, b in ((oq, r.dq), (ok, r.dk), (gq, r.dgamma_q), (gk, r.dgamma_k)):
+        assert torch.equal(a, b)
+    assert bool((ws[:256] == 0xA5).all()) and bool((ws[256 + n:] == 0xA5).all())
