@@ -108,8 +108,9 @@ typedef struct {
  *   gamma_q_dev, gamma_k_dev  D weights or NULL (ones), fp32 (w_is_bf16 = 0) or bf16;
  *                 both NULL without norm
  *   out_q, out_k  as q and k, y's type; may be q and k themselves (same type and strides)
- * A NaN or Inf in a head of a token touches no other; the sum of squares of a head is
- * formed in fp32 and has to stay finite.
+ * A NaN or Inf in a head of a token touches no other, and without the norm no other pair or
+ * passing value; the sum of squares of a head is formed in fp32 and has to stay finite (and
+ * above 0 where eps is 0).
  * Errors: SHAPE, NULL, ALIGN, FLAGS (eps, gammas without norm), CUDA.
  */
 NVFP4_API int nvfp4_qk_rope(const nvfp4_tokens* q, const nvfp4_tokens* k, int x_is_bf16, int64_t T, int q_heads,
@@ -191,7 +192,7 @@ NVFP4_API int nvfp4_cache_read(const nvfp4_tokens* k, const nvfp4_tokens* v, int
  *   q         T x q_heads x dim, bf16;  q_heads a multiple of heads, at most 65535
  *   o         as q;  may be q itself (same strides)
  *   lse_dev   T x q_heads floats (natural logarithm) or NULL
- *   scale     finite; scale * alpha * (a row's largest query) stays finite in fp32
+ *   scale     finite; scale * alpha, and that times a row's largest query, stay finite in fp32
  *   window    0 (no window) .. 2^31 - 1;  sinks 0 .. 2^31 - 1, 0 without a window
  *   workspace_dev  nvfp4_cache_attention_workspace(T, q_heads, heads, dim, sequences) bytes
  * The products take bf16 queries (scaled by a power of two per row into fp16: exactly down

@@ -17,7 +17,9 @@
 // is few by its even share of the tiles, two at least.  On short contexts the tiles' own cost (about half a
 // microsecond for one, to find its place among all) counts more than the keys: with one key head and 2048 rows few
 // takes 90 us and many 38 on 1256 keys, with eight and 500 rows 47 and 37 on 1100, 320 rows 36 and 37 on 1064, 520 rows
-// 79 and 80 on 4096.
+// 79 and 80 on 4096.  All of T counts, rows behind the last sequence and empty ones too: padding a batch can move a
+// sequence to the other kernel, whose roundings differ in their order.  In a batch of next tokens and one long part
+// the part is not few and follows the tokens (64 tokens of up to 4096 keys 64 us, 512 on 32768 505, together 589).
 #include "attend.cuh"
 
 namespace nvfp4 {

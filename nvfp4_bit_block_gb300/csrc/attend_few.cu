@@ -22,8 +22,8 @@
 // next one the other way round: movmatrix turns it.
 //
 // Measured: the next token of 48 sequences of up to 16384 keys, 40 query heads on 8 of 128 values: 132 us
-// for 509 MB, 3.9 TB/s (57 % of the copy rate).  Issue slots bound it: about 430 instructions for 16
-// keys, 60 % of the slots busy.  Half of them unpack: 72 conversions and 64 products by scales, two
+// for 509 MB, 3.9 TB/s (57 % of the copy rate).  About 430 instructions for 16 keys, 60 % of the issue
+// slots busy with 16 warps on an SM.  Half of them unpack: 72 conversions and 64 products by scales, two
 // clocks each.  One token of 700 keys: 12 us with its host side.
 #include <cmath>
 

@@ -16,9 +16,12 @@
 // case took as long.)
 //
 // Measured: prompts of 2731, 1818 and 905 tokens that end caches of 8192, 5454 and 2716 keys, 40 query
-// heads on 8 of 128 values: 547 us, 1.08 PFLOP/s (56 % of the measured bf16 rate).  For each 64 keys a
-// row takes about 1200 clocks and its block 2360: what is left is the way from P's arrival to the
-// issuing warp (270 clocks) and from the product's end back, twice for each block.
+// heads on 8 of 128 values: 550 us, 1.08 PFLOP/s (56 % of the measured bf16 rate).  For each 64 keys a
+// row takes about 1200 clocks, its block's products 1550 and the block 2360.  A product of 64 columns with
+// both operands in shared memory takes the tensor core as long as one of 128, 64 clocks: 16 of S and 8 of O
+// are 1536 where products of 128 columns throughout would be 1024.  The rest is the way from P's arrival to
+// the issuing warp (270 clocks) and from the product's end back, twice for each block.  Keys of D 64 take
+// 443 us (35 % of the rate), D 256 1421 (43 %: one tile, nothing to alternate with).
 #include <cmath>
 
 #include "attend.cuh"
