@@ -25,8 +25,8 @@
  * they may.
  *
  * Token tensors (T tokens x H heads x D values) have D contiguous and any stride, in
- * elements, from token to token and from head to head (0 <= stride); outputs must
- * not overlap themselves.  Any base address aligned to the element is accepted;
+ * elements, from token to token and from head to head (0 <= stride, and at most 2^58 from the
+ * first to the last); outputs must not overlap themselves.  Any base address aligned to the element is accepted;
  * heads that begin at 16 bytes are faster.
  */
 #ifndef NVFP4_ATTENTION_H

@@ -17,11 +17,11 @@ uintptr_t elem(int is_bf16) { return is_bf16 ? 2 : 4; }
 int launch_status(cudaError_t e) { return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA; }
 
 // Sizes are bounded so that token and head counts fit 32 bits; offsets are formed in
-// 64 bits everywhere, and a stride times a count stays far below 2^63.  A cache's heads are at
-// most 65535, so they may lie further apart than tokens.
-constexpr int64_t kMaxStride = INT64_MAX / 8 / INT32_MAX, kMaxHeadStride = (int64_t)1 << 45;
-bool bad_tokens(const nvfp4_tokens* t) {
-  return t->token_stride < 0 || t->head_stride < 0 || t->token_stride > kMaxStride || t->head_stride > kMaxStride;
+// 64 bits everywhere, and a stride times what it is stepped over stays far below 2^63.
+constexpr int64_t kMaxExtent = (int64_t)1 << 58, kMaxHeadStride = (int64_t)1 << 45;
+bool bad_stride(int64_t stride, int64_t n) { return stride < 0 || (n > 1 && stride > kMaxExtent / (n - 1)); }
+bool bad_tokens(const nvfp4_tokens* t, int64_t T, int heads) {
+  return bad_stride(t->token_stride, T) || bad_stride(t->head_stride, heads);
 }
 nvfp4::Tokens view(const nvfp4_tokens* t) { return {t->data, t->token_stride, t->head_stride}; }
 
@@ -46,7 +46,7 @@ int check_rope(const nvfp4_tokens* const* t, const uintptr_t* es, int n, int64_t
   if (bad_rope_sizes(T, Hq, Hk, D, rotated)) return NVFP4_ERR_SHAPE;
   for (int i = 0; i < n; ++i) {
     if (!t[i]) return NVFP4_ERR_NULL;
-    if (bad_tokens(t[i])) return NVFP4_ERR_SHAPE;
+    if (bad_tokens(t[i], T, i % 2 ? Hk : Hq)) return NVFP4_ERR_SHAPE;
   }
   if (norm ? (!(eps >= 0.0f) || std::isinf(eps)) : (gq || gk)) return NVFP4_ERR_FLAGS;
   const bool empty = T == 0 || Hq + Hk == 0;
@@ -89,7 +89,7 @@ int check_cache(const nvfp4_kv_cache* c, const nvfp4_batch* b, int64_t T, const 
     }
   }
   if (b->sequences < 0 || b->sequences > INT32_MAX - 1 || b->table_width < 0 || b->table_width > INT32_MAX ||
-      b->table_stride < 0 || b->table_stride > kMaxStride)
+      bad_stride(b->table_stride, b->sequences))
     return NVFP4_ERR_SHAPE;
   if (T > 0 && b->sequences > 0) {
     if (!b->starts || !b->lengths || (b->table_width > 0 && !b->table) || !c->alpha_dev) return NVFP4_ERR_NULL;
@@ -237,7 +237,7 @@ int nvfp4_cache_write(const nvfp4_tokens* k, const nvfp4_tokens* v, int x_is_bf1
   if (!k || !v) return NVFP4_ERR_NULL;
   const int st = check_cache(cache, batch, T, status_dev);
   if (st) return st;
-  if (bad_tokens(k) || bad_tokens(v)) return NVFP4_ERR_SHAPE;
+  if (bad_tokens(k, T, cache->heads) || bad_tokens(v, T, cache->heads)) return NVFP4_ERR_SHAPE;
   const bool empty = T == 0 || batch->sequences == 0;
   if (!empty && (!k->data || !v->data)) return NVFP4_ERR_NULL;
   if (!aligned(k->data, elem(x_is_bf16)) || !aligned(v->data, elem(x_is_bf16))) return NVFP4_ERR_ALIGN;
@@ -251,7 +251,7 @@ int nvfp4_cache_read(const nvfp4_tokens* k, const nvfp4_tokens* v, int y_is_bf16
   if (!k || !v) return NVFP4_ERR_NULL;
   const int st = check_cache(cache, batch, T, status_dev);
   if (st) return st;
-  if (bad_tokens(k) || bad_tokens(v)) return NVFP4_ERR_SHAPE;
+  if (bad_tokens(k, T, cache->heads) || bad_tokens(v, T, cache->heads)) return NVFP4_ERR_SHAPE;
   if (!aligned(k->data, elem(y_is_bf16)) || !aligned(v->data, elem(y_is_bf16))) return NVFP4_ERR_ALIGN;
   if (T == 0 || batch->sequences == 0 || (!k->data && !v->data)) return NVFP4_OK;
   const nvfp4::CacheCopyArgs a = {view(cache, batch, T, status_dev), view(k), view(v), y_is_bf16 ? 1 : 0};
@@ -272,7 +272,8 @@ int nvfp4_cache_attention(const nvfp4_tokens* q, int64_t T, int q_heads, const n
   if (!q || !o) return NVFP4_ERR_NULL;
   const int st = check_cache(cache, batch, T, status_dev);
   if (st) return st;
-  if (bad_tokens(q) || bad_tokens(o) || q_heads < 1 || q_heads > 65535 || q_heads % cache->heads) return NVFP4_ERR_SHAPE;
+  if (q_heads < 1 || q_heads > 65535 || q_heads % cache->heads || bad_tokens(q, T, q_heads) || bad_tokens(o, T, q_heads))
+    return NVFP4_ERR_SHAPE;
   if (std::isnan(scale) || std::isinf(scale) || window < 0 || window > INT32_MAX || sinks < 0 || sinks > INT32_MAX ||
       (!causal && window > 0) || (window == 0 && sinks > 0))
     return NVFP4_ERR_FLAGS;

@@ -9,12 +9,13 @@ u |o| + (2^-11 + 2^-14 + 2 d) sum w |v| + 2^-32 sum |v| / sum exp(s - max), u = 
 """
 import ctypes
 import math
+import threading
 
 import pytest
 import torch
 
 import nvfp4_bit_block_gb300 as nv
-from nvfp4_bit_block_gb300.attention import Tokens
+from nvfp4_bit_block_gb300.attention import Batch, Cache, Tokens
 from nvfp4_bit_block_gb300.build import build_attention_selftest
 from attention_oracle import rope64, sequence64, visible
 from test_gpu_attention import (BF, F32, T_SCORE, T_WEIGHT, U_OUT, Work, both_kernels, built, check_rope_grad, company, freqs, gen, ints,  # noqa: F401
@@ -254,6 +255,100 @@ def test_blocks_that_give_up_with_products_behind_them(n, m, dim):
     d = linear()
     assert st.item() == -8 and torch.equal(d, want)
     check(w, q, nv.nvfp4_cache_attention(q, c, *w.batch, want_lse=True))
+
+
+@both_kernels
+@pytest.mark.parametrize("lens,news,heads,group,dim", [([300], [1], 1, 5000, 32), ([90, 33], [2, 1], 1, 1500, 64),
+                                                       ([40], [3], 300, 2, 32), ([17, 5, 0], [1, 1, 0], 3000, 1, 32)])
+def test_very_many_heads(lens, news, heads, group, dim):
+    w = Work(lens, news, heads, dim, 16, seed=32)
+    w.fill()
+    q = rand((w.T, heads * group, dim), BF, 33)
+    r = attend(w, q)
+    again = nv.nvfp4_cache_attention(q, w.cache, *w.batch, want_lse=True)
+    assert torch.equal(again.o, r.o) and torch.equal(again.lse, r.lse)
+
+
+def spread(t, step):
+    """t (T, H, D) with `step` elements from token to token."""
+    T, H, D = t.shape
+    v = torch.empty((T - 1) * step + H * D, dtype=t.dtype, device="cuda").as_strided((T, H, D), (step, D, 1))
+    v.copy_(t)
+    return v
+
+
+@pytest.mark.parametrize("m", [2, 3])
+def test_tokens_that_lie_far_apart(m):
+    """2^31 elements and more from token to token, of queries, keys, values and results of each call."""
+    step, H, D = 2 ** 31 + 64, 2, 64
+    w = Work([40 + m], [m], H, D, 16, seed=34)
+    w.fill()
+    q, k, v = (rand((m, h, D), BF, 35 + h) for h in (20, H, H))
+    pos, f = torch.arange(40, 40 + m, device="cuda", dtype=torch.int32), freqs(32)
+    a = nv.nvfp4_qk_rope(q, k, pos, f)
+    b = nv.nvfp4_qk_rope(spread(q, step), k, pos, f, out_q=spread(q, step))
+    assert torch.equal(a.q, b.q) and torch.equal(a.k, b.k)
+    far = b.q
+    ga = nv.nvfp4_qk_rope_backward(q, k, a.q, a.k, pos, f)
+    gb = nv.nvfp4_qk_rope_backward(q, k, far, a.k, pos, f, out_q=far)
+    assert torch.equal(ga.dq, gb.dq) and torch.equal(ga.dgamma_q, gb.dgamma_q)
+    del far, b, gb
+    nv.nvfp4_cache_write(k, v, w.cache, *w.batch)
+    before = [t.clone() for t in w.cache.tensors()]
+    far = spread(v, step)
+    w.cache.v_codes.zero_()
+    nv.nvfp4_cache_write(k, far, w.cache, *w.batch)
+    pages, rows = (torch.tensor(x, device="cuda") for x in zip(*w.slots()))
+    assert torch.equal(w.cache.v_codes[pages, :, rows], before[2][pages, :, rows])
+    far.zero_()
+    r = nv.nvfp4_cache_read(w.cache, *w.batch, out_v=far, want_k=False)
+    assert torch.equal(r.v, nv.nvfp4_cache_read(w.cache, *w.batch, tokens=m).v)
+    del far, r
+    w.cache.v_codes.copy_(before[2])
+    o = attend(w, q).o
+    far = spread(q, step)
+    assert torch.equal(nv.nvfp4_cache_attention(far, w.cache, *w.batch, out=far).o, o)
+
+
+def test_host_threads_at_once():
+    """C callers launch from several threads, heads of different sizes, few rows and many; no thread's launch may depend on
+    what another has just asked for."""
+    L = nv.attention_lib()
+    jobs, faults = [], []
+    for i, (dim, news) in enumerate([(64, [1, 1]), (128, [3, 2]), (256, [1, 4]), (96, [90, 70]), (128, [150, 200]), (256, [80, 1])]):
+        w = Work([300, 210], news, 2, dim, 16, seed=40 + i)
+        w.fill()
+        q = rand((w.T, 8, dim), BF, 50 + i)
+        want = nv.nvfp4_cache_attention(q, w.cache, *w.batch).o
+        c, kc, sc = w.cache, w.cache.k_codes, w.cache.k_scales
+        cache = Cache(c.k_codes.data_ptr(), c.k_scales.data_ptr(), c.v_codes.data_ptr(), c.v_scales.data_ptr(), c.alpha.data_ptr(),
+                      kc.shape[0], 2, 16, dim, *kc.stride()[:3], *sc.stride()[:3])
+        batch = Batch(w.starts.data_ptr(), w.lengths.data_ptr(), w.table.data_ptr(), 2, w.table.shape[1], w.table.stride(0))
+        n = L.nvfp4_cache_attention_workspace(w.T, 8, 2, dim, 2)
+        ws, o = torch.empty(n, dtype=torch.uint8, device="cuda"), torch.zeros_like(q)
+        tq, to = (Tokens(t.data_ptr(), t.stride(0), t.stride(1)) for t in (q, o))
+        jobs.append((lambda s, tq=tq, to=to, w=w, cache=cache, batch=batch, ws=ws, n=n, dim=dim, q=q: L.nvfp4_cache_attention(
+            ctypes.byref(tq), w.T, 8, ctypes.byref(cache), ctypes.byref(batch), dim ** -0.5, 1, 0, 0, ctypes.byref(to), None,
+            ws.data_ptr(), n, None, s), o, want))
+    torch.cuda.synchronize()
+    start = threading.Barrier(len(jobs))
+
+    def work(call):
+        s = torch.cuda.Stream()
+        start.wait()
+        for _ in range(200):
+            if status := call(s.cuda_stream):
+                faults.append(status)
+        s.synchronize()
+    threads = [threading.Thread(target=work, args=(j[0],)) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not faults
+    for _, o, want in jobs:
+        assert torch.equal(o, want)
 
 
 # ---------------------------------------------------------------- norm and rotation
